@@ -48,7 +48,7 @@ extern "C" {
 typedef enum {
   SSM_OK = 0,
   SSM_ERR_INVALID_ARG = 1,  /* null required pointer, negative size, misalignment, aliasing */
-  SSM_ERR_UNSUPPORTED = 2,  /* N outside [1, 64], unknown dtype or variant */
+  SSM_ERR_UNSUPPORTED = 2,  /* N outside [1, 64], unknown dtype or variant, a size past an entry point's limits */
   SSM_ERR_HIP = 3,          /* no usable device, launch failure, or missing gfx950 code */
   SSM_ERR_TOO_LARGE = 4     /* the call needs more scratch than the allocation-free entry point holds */
 } ssm_status;
@@ -450,6 +450,151 @@ ssm_status ssm_ssd_scan_fwd_noalloc(
     const float *Dskip, const float *dt_bias, int dt_softplus,
     const float *initial_state, void *y, float *final_state,
     int64_t batch, int64_t L, int64_t H, int64_t P, int64_t N, ssm_dtype dtype, void *stream);
+
+/*
+ * Linear attention with a constant decay per head, prompt form.  For batch row b, token
+ * t and head h, with lam_h = exp(log_decay[h]) and the K x V state S:
+ *
+ *   S_t = lam S_{t-1} + k_t v_t^T        o_t = scale * q_t S_t
+ *
+ * computed chunk by chunk on the matrix cores.
+ *
+ *   q            : [batch][L][Hq][K] act, k : [batch][L][Hk][K], v : [batch][L][Hv][V];
+ *                  each of Hq, Hk, Hv divides H, and state head h uses head h / (H / Hx)
+ *                  (shared heads).  Unlike the packed tensors, these three may be views:
+ *                  q_strides etc. give the element strides of their batch, token and head
+ *                  axes (NULL: packed); the last axis is contiguous.  Strides are >= 0.
+ *   log_decay    : [H] float32: the logarithm of the decay, <= 0 in the models (-inf is a
+ *                  decay of 0); a constant of the model (no gradient)
+ *   lengths      : [batch] int32 or NULL (= L): tokens t >= lengths[b] are absent: they do
+ *                  not touch the state, their outputs and gradients are 0, and what their
+ *                  q, k and v hold (NaN included) does not matter.  Values outside [0, L]
+ *                  are clamped.
+ *   initial_state: [batch][H][K][V] float32 or NULL (= 0)
+ *   out          : [batch][L][H][V] act, packed
+ *   final_state  : [batch][H][K][V] float32 or NULL: the state after the last token that is
+ *                  there; may be the initial_state pointer (in place) but must not
+ *                  otherwise overlap it
+ *   K, V         : 1..SSM_LA_MAX_DIM, any; L < 2^30; batch * H <= 2^20
+ *   workspace    : >= ssm_linear_attention_workspace_size(...) bytes of device memory, 16-byte
+ *                  aligned, owned by the caller (NULL where that is 0); contents irrelevant
+ *
+ * With float32 activations every product is in float32.  With bfloat16 the products are
+ * bfloat16 with float32 accumulation: q, k and v enter as they are, the masked scores and
+ * the state as two bfloat16 terms (16 bits); the state is float32 throughout.  16-byte aligned rows (K and V
+ * multiples of 8, strides multiples of 16 bytes) move as vectors; other layouts run slower
+ * with the same results.  A NaN or infinity in a token that is there reaches every later
+ * output of its row and head, and may reach earlier outputs within 63 tokens of it.
+ *
+ * ssm_linear_attention_bwd: the gradients of sum(dout * out) + sum(dfinal_state * final_state).
+ *   dout          : [batch][L][H][V] act, a view as q is (dout_strides)
+ *   dfinal_state  : [batch][H][K][V] float32 or NULL (= 0)
+ *   dq, dk, dv    : out, act, packed in the shapes of q, k and v (summed over the state heads
+ *                   that share a head)
+ *   dinitial_state: out [batch][H][K][V] float32 or NULL
+ * Errors of both: SSM_ERR_INVALID_ARG for a NULL required pointer, a negative size or stride,
+ * a head count that does not divide H, misalignment, a workspace that is too small, or an
+ * output overlapping an input, another output or the workspace; SSM_ERR_UNSUPPORTED for a
+ * bad dtype, K or V outside [1, SSM_LA_MAX_DIM] or sizes past the limits above; SSM_ERR_HIP
+ * when no device is usable or a launch fails.  Deterministic.
+ */
+#define SSM_LA_MAX_DIM 128
+
+size_t ssm_linear_attention_workspace_size(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V, ssm_dtype dt);
+
+ssm_status ssm_linear_attention_fwd(
+    const void *q, const void *k, const void *v, const int64_t *q_strides, const int64_t *k_strides,
+    const int64_t *v_strides, const float *log_decay, float scale, const int32_t *lengths,
+    const float *initial_state, void *out, float *final_state,
+    int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv, int64_t K, int64_t V, ssm_dtype dt,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+size_t ssm_linear_attention_bwd_workspace_size(int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv,
+                                               int64_t K, int64_t V, ssm_dtype dt);
+
+ssm_status ssm_linear_attention_bwd(
+    const void *q, const void *k, const void *v, const void *dout, const int64_t *q_strides, const int64_t *k_strides,
+    const int64_t *v_strides, const int64_t *dout_strides, const float *log_decay, float scale, const int32_t *lengths,
+    const float *initial_state, const float *dfinal_state, void *dq, void *dk, void *dv, float *dinitial_state,
+    int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv, int64_t K, int64_t V, ssm_dtype dt,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of the same attention (the recurrent form): advances the state of `batch`
+ * sequences by one token and reads it out.
+ *
+ *   state_in, state_out : [states][H][K][V] float32; state_out may equal state_in (in
+ *                  place) but must not partially overlap it
+ *   q, k, v      : [batch][Hq][K], [batch][Hk][K], [batch][Hv][V] act; *_strides give the
+ *                  element strides of their batch and head axes (NULL: packed)
+ *   slots        : [batch] int32 or NULL.  Sequence b's state is number slots[b] of the pool;
+ *                  a slot outside [0, states) marks an idle row: its output is 0 and no
+ *                  state is touched.  Two rows of one call must not name the same slot.
+ *                  NULL: sequence b's state is number b (states >= batch).
+ *   out          : [batch][H][V] act
+ * States that no row names are not touched (state_out keeps what it held).  float32
+ * arithmetic.  Limits and errors as above; batch * H <= 2^22; a pool without slots that is smaller than the
+ * batch is SSM_ERR_INVALID_ARG.
+ */
+ssm_status ssm_linear_attention_step(
+    const float *state_in, float *state_out, const void *q, const void *k, const void *v, const int64_t *q_strides,
+    const int64_t *k_strides, const int64_t *v_strides, const float *log_decay, float scale, const int32_t *slots,
+    void *out, int64_t batch, int64_t states, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv, int64_t K, int64_t V,
+    ssm_dtype dt, void *stream);
+
+/*
+ * The norms around a block, fused with its gate, residual and residual scale.  For each
+ * row of D columns:
+ *
+ *   n = post_weight * x * rsqrt(mean over x's column group of x^2 + eps)   (post_weight NULL: n = x)
+ *   t = n * silu(gate)                                                     (gate NULL: t = n)
+ *   h = residual + res_scale * t                                           (either NULL: without it)
+ *   y = pre_weight * h * rsqrt(mean over the row of h^2 + eps)             (pre_weight NULL: no y)
+ *
+ * The gated norm of a mixer's heads before its output projection, the residual add with the
+ * next block's norm, both norms of a block at once, or a plain norm are all this call.
+ *
+ *   x, gate      : [rows][D] act with row strides x_row_stride, gate_row_stride >= D (elements)
+ *   residual, h  : [rows][D] of residual_dtype: SSM_F32, or dt
+ *   y            : [rows][D] act
+ *   post_weight, res_scale, pre_weight : [D] float32 or NULL
+ *   h            : out, or NULL (not stored); y : out, NULL exactly when pre_weight is
+ *   groups       : column groups of the first norm; divides D, and D / groups is a multiple
+ *                  of 8 unless groups is 1
+ *   D            : 1..SSM_NORM_MAX_D; eps >= 0; rows <= 2^22
+ * y is formed from h before its rounding.  h may be the residual pointer (in place).
+ *
+ * ssm_block_norm_bwd: gradients of sum(dy * y) + sum(dh * h).
+ *   h            : what the forward pass returned (NULL only without pre_weight)
+ *   dy           : [rows][D] act, NULL exactly when pre_weight is; dh : [rows][D] of
+ *                  residual_dtype or NULL (= 0)
+ *   dx           : out [rows][D] act; dgate : out [rows][D] act, NULL exactly when gate is
+ *   dresidual    : out [rows][D] of residual_dtype or NULL; may be the dh pointer (in place)
+ *   dpost_weight, dres_scale, dpre_weight : out [D] float32, each NULL exactly when its weight is
+ * Sums are float32 in a fixed order.  Workspace: >= ssm_block_norm_bwd_workspace_size(...)
+ * bytes, 16-byte aligned.
+ * Errors: SSM_ERR_INVALID_ARG for a NULL required pointer, a gradient without its input, a
+ * negative size, a row stride below D, groups that do not divide D, eps < 0 or NaN,
+ * misalignment, a small workspace or an overlap other than the two named; SSM_ERR_UNSUPPORTED
+ * for a bad dtype (residual_dtype neither SSM_F32 nor dt), D or rows past the limits, or
+ * group widths that are not a multiple of 8; SSM_ERR_HIP when no device is usable or a
+ * launch fails.
+ */
+#define SSM_NORM_MAX_D 16384
+
+ssm_status ssm_block_norm_fwd(
+    const void *x, int64_t x_row_stride, const void *residual, const void *gate, int64_t gate_row_stride,
+    const float *post_weight, const float *res_scale, const float *pre_weight, void *h, void *y,
+    int64_t rows, int64_t D, int64_t groups, float eps, ssm_dtype dt, ssm_dtype residual_dtype, void *stream);
+
+size_t ssm_block_norm_bwd_workspace_size(int64_t rows, int64_t D);
+
+ssm_status ssm_block_norm_bwd(
+    const void *x, int64_t x_row_stride, const void *h, const void *dy, const void *dh, const void *gate,
+    int64_t gate_row_stride, const float *post_weight, const float *res_scale, const float *pre_weight,
+    void *dx, void *dgate, void *dresidual, float *dpost_weight, float *dres_scale, float *dpre_weight,
+    int64_t rows, int64_t D, int64_t groups, float eps, ssm_dtype dt, ssm_dtype residual_dtype,
+    void *workspace, size_t workspace_bytes, void *stream);
 
 /* Static, human-readable text for a status code (never NULL). */
 const char *ssm_status_string(ssm_status s);

@@ -31,6 +31,7 @@ _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _sz = ctypes.c_size_t
+_f32 = ctypes.c_float
 
 # name -> (restype, argtypes); mirrors include/ssm.h and include/ssm_calib.h
 SIGNATURES = {
@@ -66,6 +67,16 @@ SIGNATURES = {
                                 _i64, _i64, _i64, _i64, _i64, _int, _vp, _sz, _vp]),
     "ssm_ssd_scan_fwd_noalloc": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp,
                                         _i64, _i64, _i64, _i64, _i64, _int, _vp]),
+    "ssm_linear_attention_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i64, _int]),
+    "ssm_linear_attention_fwd": (_int, [_vp] * 7 + [_f32, _vp, _vp, _vp, _vp] + [_i64] * 8 + [_int, _vp, _sz, _vp]),
+    "ssm_linear_attention_bwd_workspace_size": (_sz, [_i64] * 8 + [_int]),
+    "ssm_linear_attention_bwd": (_int, [_vp] * 9 + [_f32] + [_vp] * 7 + [_i64] * 8 + [_int, _vp, _sz, _vp]),
+    "ssm_linear_attention_step": (_int, [_vp] * 9 + [_f32, _vp, _vp] + [_i64] * 8 + [_int, _vp]),
+    "ssm_block_norm_fwd": (_int, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _f32, _int,
+                                  _int, _vp]),
+    "ssm_block_norm_bwd_workspace_size": (_sz, [_i64, _i64]),
+    "ssm_block_norm_bwd": (_int, [_vp, _i64] + [_vp] * 4 + [_i64] + [_vp] * 9 + [_i64, _i64, _i64, _f32, _int, _int,
+                                                                                _vp, _sz, _vp]),
     "ssm_status_string": (ctypes.c_char_p, [_int]),
     "ssm_calib_copy": (_int, [_vp, _vp, _sz, _vp]),
     "ssm_calib_alu": (_int, [_int, _vp, _i64, _int, _vp]),

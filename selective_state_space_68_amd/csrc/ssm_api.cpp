@@ -3,36 +3,23 @@
 // synchronisation, no global mutable state beyond a cached device probe.
 #include <hip/hip_runtime.h>
 
-#include <atomic>
 #include <cstdint>
 
 #include "../../include/ssm.h"
+#include "host_common.hpp"
 #include "kernels.hpp"
 
 namespace {
 
+using ssm::aligned;
+using ssm::from_hip;
+using ssm::mul_ok;
+using ssm::overlaps;
+using ssm::probe_device;
+using ssm::Span;
+using ssm::span;
+
 constexpr int kVersion = 30100;  // 3.1.0: + allocation-free SSD entry point (ssm_ssd_scan_fwd_noalloc)
-
-struct Span {
-  uintptr_t lo = 0, hi = 0;  // [lo, hi); empty when lo == hi
-  bool empty() const { return lo == hi; }
-};
-
-Span span(const void* p, uint64_t bytes) {
-  Span s;
-  s.lo = reinterpret_cast<uintptr_t>(p);
-  s.hi = s.lo + (p ? bytes : 0);
-  return s;
-}
-
-bool overlaps(const Span& a, const Span& b) {
-  if (a.empty() || b.empty()) return false;
-  return a.lo < b.hi && b.lo < a.hi;
-}
-
-bool mul_ok(uint64_t a, uint64_t b, uint64_t* out) { return !__builtin_mul_overflow(a, b, out); }
-
-bool aligned(const void* p, uintptr_t a) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Bytes of the saved chunk states: [batch][D][ceil(L / 512)][N] float32 (sizes already
 // checked by check_scan, so the product does not overflow).
@@ -40,23 +27,6 @@ uint64_t chunk_states_bytes(int64_t batch, int64_t L, int64_t D, int64_t N) {
   const uint64_t nck = (static_cast<uint64_t>(L) + ssm::kSaveChunk - 1) / ssm::kSaveChunk;
   return static_cast<uint64_t>(batch) * static_cast<uint64_t>(D) * nck * static_cast<uint64_t>(N) * sizeof(float);
 }
-
-// 1 = a device is usable, 0 = none; probed once per process.
-std::atomic<int> g_device_state{-1};
-
-ssm_status probe_device() {
-  int st = g_device_state.load(std::memory_order_relaxed);
-  if (st == 1) return SSM_OK;
-  if (st == 0) return SSM_ERR_HIP;
-  int count = 0;
-  const hipError_t e = hipGetDeviceCount(&count);
-  st = (e == hipSuccess && count > 0) ? 1 : 0;
-  if (e != hipSuccess) (void)hipGetLastError();
-  g_device_state.store(st, std::memory_order_relaxed);
-  return st ? SSM_OK : SSM_ERR_HIP;
-}
-
-ssm_status from_hip(hipError_t e) { return e == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
 
 struct ScanSizes {
   uint64_t act_bytes = 0, bc_bytes = 0, a_bytes = 0, vec_bytes = 0, state_bytes = 0;
