@@ -475,7 +475,7 @@ ssm_status ssm_ssd_scan_fwd_noalloc(
  *   final_state  : [batch][H][K][V] float32 or NULL: the state after the last token that is
  *                  there; may be the initial_state pointer (in place) but must not
  *                  otherwise overlap it
- *   K, V         : 1..SSM_LA_MAX_DIM, any; L < 2^30; batch * H <= 2^20
+ *   K, V         : 1..SSM_LA_MAX_DIM, any; L < 2^30; H <= 2^16; batch * H <= 2^20
  *   workspace    : >= ssm_linear_attention_workspace_size(...) bytes of device memory, 16-byte
  *                  aligned, owned by the caller (NULL where that is 0); contents irrelevant
  *

@@ -18,9 +18,11 @@
 // 16 x 16 tile four consecutive rows of column c, and since the order of a product's
 // summation index is free, the rows of each tile are assigned (kperm below) so that the
 // two tiles of a pair leave a lane 8 consecutive indices: what one operand needs.  q, k and
-// v go through LDS row by row; operands that sum over tokens (k^T, v^T) come out of the same
-// rows by transposing LDS reads.  P goes through LDS (each wave forms 16 rows of it).  The
-// next chunk's rows are loaded into registers while the current chunk computes.
+// v go from memory straight into LDS row by row (16 bytes a lane, no registers); operands that sum over tokens
+// (k^T, v^T) come out of the same rows by transposing LDS reads.  P goes through LDS (each
+// wave forms 16 rows of it).  A chunk's rows are asked for as soon as every wave has done with
+// the tiles of the chunk before, and arrive during its P v product and, the workgroups of a CU being
+// independent, during another workgroup's chunk.
 //
 // Roundings (bfloat16 activations; float32 activations use float32 products throughout):
 // the decayed v of the state update is split into three bfloat16 terms, which carry all 24
@@ -30,6 +32,8 @@
 // When the (batch row, head) pairs are too few to fill the chip the sequence is cut into
 // segments: a pre-pass forms each segment's own state sum, a small kernel chains them, and
 // the main pass runs every segment from its entering E.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "lm_kernels.hpp"
 #include "scan_common.hpp"
@@ -44,6 +48,17 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
+// Place of byte `byte` of a row in an LDS tile of RB-byte rows.  Rows are packed (the loads
+// into LDS leave no room for padding); the 16-byte slots of a row are exchanged within
+// groups of 8 by its number, so that the rows one read instruction touches lie in different
+// banks: 8 consecutive rows, the rows {0..3, 8..11} of the permuted tiles, and two
+// neighbouring slots of 4 consecutive rows (the transposing reads) are all apart.
+__device__ __forceinline__ constexpr int swizzle(int row) { return ((row & 3) << 1) | (((row >> 2) ^ (row >> 3)) & 1); }
+template <int RB>
+__device__ __forceinline__ constexpr int tile_at(int row, int byte) {
+  return row * RB + (byte ^ (swizzle(row) << 4));
+}
+
 // ---- eight values of one lane: a matrix operand (one v_mfma_f32_16x16x32_bf16, lane
 // (g, c) holding row/column c and summation indices 8g..8g+7; or eight
 // v_mfma_f32_16x16x4_f32, lane group g holding index g of each)
@@ -54,7 +69,7 @@ template <>
 struct Op<ActBF16> {
   using elem = uint16_t;
   using piece = uint4;
-  static constexpr int kPad = 8;     // elements of row padding in LDS (16 bytes)
+  static constexpr int kPad = 8;     // elements of row padding of P (16 bytes)
   static __device__ __forceinline__ f32x4_t mma(const piece& a, const piece& b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
                                                    c, 0, 0, 0);
@@ -85,16 +100,21 @@ struct Op<ActBF16> {
       }
     }
   }
-  // Values [row0 + 8g + e][col(c)], e = 0..7, of a row-major LDS tile, col(c) = col0 + step (c / 4) + c % 4:
+  // Values [row0 + 8g + e][col(c)], e = 0..7, of a tile, col(c) = col0 + step (c / 4) + c % 4:
   // two transposing reads of 4 rows each.  Lane i of a 16-lane group gives the address
   // of 4 columns (piece i % 4) of row i / 4 and receives column i of the 4 rows.
-  static __device__ __forceinline__ piece column(const elem* tile, int stride, int row0, int col0, int step, int lane) {
-    const int g = lane >> 4, i = lane & 15;
-    const elem* a = tile + (row0 + 8 * g + (i >> 2)) * stride + col0 + step * (i & 3);
-    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(a));
-    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(a + 4 * stride));
+  template <int RB>
+  static __device__ __forceinline__ piece column(const char* tile, int row0, int col0, int step, int lane) {
+    const int row = row0 + 8 * (lane >> 4) + ((lane & 15) >> 2), byte = 2 * (col0 + step * (lane & 3));
+    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(tile + tile_at<RB>(row, byte)));
+    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(tile + tile_at<RB>(row + 4, byte)));
     const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
     return make_uint4(l.x, l.y, h.x, h.y);
+  }
+  // Columns col..col + 7 of a row.
+  template <int RB>
+  static __device__ __forceinline__ piece row(const char* tile, int row, int col) {
+    return *reinterpret_cast<const uint4*>(tile + tile_at<RB>(row, 2 * col));
   }
 };
 
@@ -132,11 +152,18 @@ struct Op<ActF32> {
     static_assert(TERMS == 1, "float32 operands are exact");
     p[0] = pack(v);
   }
-  static __device__ __forceinline__ piece column(const elem* tile, int stride, int row0, int col0, int step, int lane) {
-    const int g = lane >> 4, c = lane & 15;
-    const elem* a = tile + (row0 + 8 * g) * stride + col0 + step * (c >> 2) + (c & 3);
-    return F8{make_float4(a[0], a[stride], a[2 * stride], a[3 * stride]),
-              make_float4(a[4 * stride], a[5 * stride], a[6 * stride], a[7 * stride])};
+  template <int RB>
+  static __device__ __forceinline__ piece column(const char* tile, int row0, int col0, int step, int lane) {
+    const int row = row0 + 8 * (lane >> 4), byte = 4 * (col0 + step * ((lane & 15) >> 2) + (lane & 3));
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = *reinterpret_cast<const float*>(tile + tile_at<RB>(row + e, byte));
+    return pack(v);
+  }
+  template <int RB>
+  static __device__ __forceinline__ piece row(const char* tile, int row, int col) {
+    return F8{*reinterpret_cast<const float4*>(tile + tile_at<RB>(row, 4 * col)),
+              *reinterpret_cast<const float4*>(tile + tile_at<RB>(row, 4 * col + 16))};
   }
 };
 
@@ -167,52 +194,104 @@ __device__ __forceinline__ int row_length(const LaArgs& p, int64_t b) {
   return n < 0 ? 0 : (n > L ? L : n);
 }
 
-// A tile row's 8 elements starting at column col of a row of `cols` elements (zeros past it).
-template <typename ACT>
-__device__ __forceinline__ typename Op<ACT>::piece load_piece(const typename Op<ACT>::elem* row, int col, int cols,
-                                                              int vec) {
-  using P = typename Op<ACT>::piece;
-  if (vec) {
-    const int c = col < cols ? col : cols - 8;        // (a whole vector: cols is a multiple of 8)
-    P r = *reinterpret_cast<const P*>(row + c);
-    return col < cols ? r : Op<ACT>::zero();
-  }
-  typename Op<ACT>::elem e[8];
+// Rows of a [64][cols] block of elements into an LDS tile of RB-byte rows, by one workgroup.
+// Row r is at base + r * step elements; rows past `last` repeat it (they are cleared
+// afterwards), and columns past `cols` are left as they are (zeros, from the start).
+typedef __attribute__((address_space(1))) const void global_void_t;
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+template <typename ELEM, int RB>
+__device__ __forceinline__ void load_tile(char* tile, const ELEM* base, int64_t step, int last, int cols, int w,
+                                          int lane) {
+  constexpr int kSlots = RB / 16, kRows = 64 / kSlots;              // slots of a row, rows of an instruction
+  constexpr int kInstr = kQ / kRows / 4;                            // instructions of a wave
+  const int lane_row = lane / kSlots;
+  const int lane_slot = (lane % kSlots) ^ swizzle(lane_row);        // (the swizzle is linear in the row's bits)
+  if (last == kQ - 1 && cols * static_cast<int>(sizeof(ELEM)) == RB) {
+    // a whole tile: a uniform address of each instruction's lowest row plus the lane's offset from it
+    const int64_t bytes = step * static_cast<int64_t>(sizeof(ELEM));
+    const bool up = bytes >= 0;
+    const uint32_t row_off = static_cast<uint32_t>(up ? lane_row : kRows - 1 - lane_row) *
+                             static_cast<uint32_t>(up ? bytes : -bytes);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) e[i] = col + i < cols ? row[col + i] : typename Op<ACT>::elem(0);
-  return *reinterpret_cast<const P*>(e);
+    for (int i = 0; i < kInstr; ++i) {
+      const int row0 = (w * kInstr + i) * kRows;
+      const char* src = reinterpret_cast<const char*>(base) + (row0 + (up ? 0 : kRows - 1)) * bytes;
+      const uint32_t off = row_off + static_cast<uint32_t>((lane_slot ^ swizzle(i * kRows)) * 16);
+      __builtin_amdgcn_global_load_lds((global_void_t*)(src + off), (lds_void_t*)(tile + row0 * RB), 16, 0, 0);
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < kInstr; ++i) {
+      const int row0 = (w * kInstr + i) * kRows, row = row0 + lane_row, slot = lane_slot ^ swizzle(i * kRows);
+      const int r = row < last ? row : last;
+      const char* src = reinterpret_cast<const char*>(base + r * step) + slot * 16;
+      if (slot * 16 < cols * static_cast<int>(sizeof(ELEM)))
+        __builtin_amdgcn_global_load_lds((global_void_t*)src, (lds_void_t*)(tile + row0 * RB), 16, 0, 0);
+    }
+  }
+}
+
+// Clears rows n.. of the slots that this wave's load_tile filled.
+template <int RB>
+__device__ __forceinline__ void clear_tile(char* tile, int n, int w, int lane) {
+  constexpr int kSlots = RB / 16, kInstr = kQ * RB / 1024 / 4;
+#pragma unroll 1
+  for (int i = 0; i < kInstr; ++i) {
+    const int s = (w * kInstr + i) * 64 + lane;
+    if (s / kSlots >= n) *reinterpret_cast<uint4*>(tile + s * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// The same element by element, for rows that do not move as 16-byte vectors (rows past `last` as zeros).
+template <typename ELEM, int RB>
+__device__ __forceinline__ void load_tile_scalar(char* tile, const ELEM* base, int64_t step, int last, int cols, int tid) {
+  constexpr int kCols = RB / sizeof(ELEM);
+  for (int i = tid; i < kQ * kCols; i += 256) {
+    const int row = i / kCols, col = i % kCols;
+    ELEM x = ELEM(0);
+    if (row <= last && col < cols) x = base[row * step + col];
+    *reinterpret_cast<ELEM*>(tile + tile_at<RB>(row, col * static_cast<int>(sizeof(ELEM)))) = x;
+  }
 }
 
 // STATE_ONLY: the pre-pass, which leaves each segment's own sum (its state after its last
 // token, from zero) in role.seg.  Otherwise the whole of the segment's output.
-template <typename ACT, int KD, int VT, bool STATE_ONLY>
-__global__ __launch_bounds__(256) void la_kernel(LaArgs p) {
+template <typename ACT, int KD, int VT, bool VEC, bool STATE_ONLY>
+__global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
   using O = Op<ACT>;
   using elem = typename O::elem;
   using piece = typename O::piece;
   constexpr bool kF32 = sizeof(elem) == 4;
   constexpr int VD = 64 * VT;
-  constexpr int RK = KD + O::kPad, RV = VD + O::kPad, RS = kQ + O::kPad;
+  constexpr int RK = KD * static_cast<int>(sizeof(elem)), RV = VD * static_cast<int>(sizeof(elem));   // row bytes
+  constexpr int RS = kQ + O::kPad;
   constexpr int KT = KD / 32;                       // pairs of state tiles along K
-  constexpr int NK = KD / 32, NV = VD / 32;         // 8-element pieces per thread of a k (q) and v tile
   constexpr int WT = kF32 ? 1 : 3;                  // operand terms of the decayed v
   constexpr int ET = kF32 ? 1 : 2;                  // operand terms of E and of P
-  __shared__ __attribute__((aligned(16))) elem sQ[STATE_ONLY ? 16 : kQ * RK];
-  __shared__ __attribute__((aligned(16))) elem sK[kQ * RK];
-  __shared__ __attribute__((aligned(16))) elem sV[kQ * RV];
+  __shared__ __attribute__((aligned(16))) char sQ[STATE_ONLY ? 16 : kQ * RK];
+  __shared__ __attribute__((aligned(16))) char sK[kQ * RK];
+  __shared__ __attribute__((aligned(16))) char sV[kQ * RV];
   __shared__ __attribute__((aligned(16))) elem sP[ET][STATE_ONLY ? 16 : kQ * RS];   // P [j][i]
 
-  const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6);
-  const int g = lane >> 4, c16 = lane & 15;
-  const LaRole& r = p.role[blockIdx.y];
+  const int tid = threadIdx.x, lane0 = tid & 63, w = uniform_int(tid >> 6);
+  // Workgroup ids go round the 8 XCDs: the roles of one (batch row, head, segment), which
+  // read the same rows, are 8 ids apart, on one XCD and its L2 at about the same time.
   const int nseg = p.nseg;
-  const int64_t bh = blockIdx.x / nseg;
-  const int seg = static_cast<int>(blockIdx.x % nseg);
+  const int64_t per_role = static_cast<int64_t>(p.batch) * p.H * nseg;
+  const int64_t group = blockIdx.x / (8 * p.nroles) * 8;
+  const int in_group = static_cast<int>(blockIdx.x % (8 * p.nroles));
+  const int64_t item = group + in_group % 8;
+  if (item >= per_role) return;
+  const LaRole& r = p.role[in_group / 8];
+  const int64_t bh = item / nseg;
+  const int seg = static_cast<int>(item % nseg);
+  if (STATE_ONLY && seg + 1 == nseg && !r.fin) return;   // (its sum would be read by nobody)
   const int64_t b = bh / p.H;
   const int h = static_cast<int>(bh % p.H);
   const int L = static_cast<int>(p.L);
   const int len = row_length(p, b);
-  const int K = r.K, V = r.V, vec = r.vec, reverse = r.reverse;
+  const int K = r.K, V = r.V, reverse = r.reverse;
   const int nchunks = (L + kQ - 1) / kQ;
   const int live = (len + kQ - 1) / kQ;             // chunks that hold a token
   const int c_begin = seg * static_cast<int>(p.seg_chunks);
@@ -230,6 +309,7 @@ __global__ __launch_bounds__(256) void la_kernel(LaArgs p) {
   const elem* vg = static_cast<const elem*>(r.v) + b * r.vs[0] + (h / r.vdiv) * r.vs[2] + t_first * r.vs[1];
   const int64_t qstep = r.qs[1] * t_step, kstep = r.ks[1] * t_step, vstep = r.vs[1] * t_step;
 
+  const int g = lane0 >> 4, c16 = lane0 & 15;
   // E[vt][t][u][e] is the entry k = 32 t + 8 g + 4 u + e, v = 16 (VT w + vt) + c16
   f32x4_t E[VT][KT][2];
   const float* src = nullptr;
@@ -250,61 +330,90 @@ __global__ __launch_bounds__(256) void la_kernel(LaArgs p) {
         for (int e = 0; e < 4; ++e) {
           const int kk = 32 * t + 8 * g + 4 * u + e, vv = 16 * (VT * w + vt) + c16;
           float x = 0.0f;
-          if (src && kk < K && vv < V) {
-            x = src[static_cast<int64_t>(kk) * r.sk + static_cast<int64_t>(vv) * r.sv];
-            if (!decayed) x *= lam1;
+          if (src) {                                // (uniform; the loads themselves sit behind no branch)
+            const bool in = kk < K && vv < V;
+            x = src[static_cast<int64_t>(in ? kk : 0) * r.sk + static_cast<int64_t>(in ? vv : 0) * r.sv];
+            x = in ? (decayed ? x : x * lam1) : 0.0f;
           }
           E[vt][t][u][e] = x;
         }
 
-  piece rq[STATE_ONLY ? 1 : NK], rk[NK], rv[NV];
-  // The rows of chunk c into registers; rows past its n tokens reload its last one (zeroed on the way to LDS).
-  auto fetch = [&](int c) __attribute__((always_inline)) {
-    const int r0 = c * kQ;
-    const int lim = len - 1 - r0 < kQ - 1 ? len - 1 - r0 : kQ - 1;
+  // Decay factors.  lam^(j-i) of P splits into a lane's lam^(j - 32t - 8g - 7) and the uniform
+  // lam^(7 - (4u + e)); the first may exceed 1 near the diagonal, so heads that decay by more
+  // than 2^16 a token (lam^7 near float32's end) take the exponent of each element instead.
+  const bool steep = !(g2 >= -16.0f);
+  float pw[8];
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int v = tid + 256 * i, row = v / (KD / 8), col = v % (KD / 8) * 8;
-      const int64_t t = r0 + (row < lim ? row : lim);
-      rk[i] = load_piece<ACT>(kg + t * kstep, col, K, vec);
-      if constexpr (!STATE_ONLY) rq[i] = load_piece<ACT>(qg + t * qstep, col, K, vec);
-    }
+  for (int e = 0; e < 8; ++e) pw[e] = exp2_hw(g2 * static_cast<float>(7 - e));
+  const float io_scale = r.in_scale * r.out_scale;
+  float pl[2], wl[2];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = tid + 256 * i, row = v / (VD / 8), col = v % (VD / 8) * 8;
-      const int64_t t = r0 + (row < lim ? row : lim);
-      rv[i] = load_piece<ACT>(vg + t * vstep, col, V, vec);
-    }
-  };
-  auto stage = [&](int n) __attribute__((always_inline)) {
+  for (int t = 0; t < 2; ++t) {
+    const int j = 16 * w + c16;
+    pl[t] = exp2_hw(g2 * static_cast<float>(j - 32 * t - 8 * g - 7)) * io_scale;
+    wl[t] = exp2_hw(g2 * static_cast<float>(kQ - 32 * t - 8 * g - 7)) * r.in_scale;   // (of a whole chunk)
+  }
+  float fj[4];
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int v = tid + 256 * i, row = v / (KD / 8), col = v % (KD / 8) * 8;
-      *reinterpret_cast<piece*>(&sK[row * RK + col]) = row < n ? rk[i] : O::zero();
-      if constexpr (!STATE_ONLY) *reinterpret_cast<piece*>(&sQ[row * RK + col]) = row < n ? rq[i] : O::zero();
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = tid + 256 * i, row = v / (VD / 8), col = v % (VD / 8) * 8;
-      *reinterpret_cast<piece*>(&sV[row * RV + col]) = row < n ? rv[i] : O::zero();
-    }
-  };
+  for (int jt = 0; jt < 4; ++jt) fj[jt] = exp2_hw(g2 * static_cast<float>(16 * jt + c16)) * r.out_scale;
 
-  if (c_begin < c_live) fetch(c_begin);
+  // Asks for the rows of chunk c.
+  auto load = [&](int c, int lane) __attribute__((always_inline)) {
+    const int64_t r0 = static_cast<int64_t>(c) * kQ;
+    const int last = len - 1 - c * kQ < kQ - 1 ? len - 1 - c * kQ : kQ - 1;
+    if constexpr (VEC) {
+      load_tile<elem, RK>(sK, kg + r0 * kstep, kstep, last, K, w, lane);
+      if constexpr (!STATE_ONLY) load_tile<elem, RK>(sQ, qg + r0 * qstep, qstep, last, K, w, lane);
+      load_tile<elem, RV>(sV, vg + r0 * vstep, vstep, last, V, w, lane);
+    } else {
+      load_tile_scalar<elem, RK>(sK, kg + r0 * kstep, kstep, last, K, tid);
+      if constexpr (!STATE_ONLY) load_tile_scalar<elem, RK>(sQ, qg + r0 * qstep, qstep, last, K, tid);
+      load_tile_scalar<elem, RV>(sV, vg + r0 * vstep, vstep, last, V, tid);
+    }
+  };
+  // Waits for this wave's part of them (and for its stores of the chunk before); n: the tokens of
+  // the chunk asked for.
+  auto arrived = [&](int n, int lane) __attribute__((always_inline)) {
+    if constexpr (VEC) {
+      __builtin_amdgcn_s_waitcnt(0x0f70);           // vmcnt(0); expcnt and lgkmcnt as they are
+      if (n < kQ) {
+        clear_tile<RK>(sK, n, w, lane);
+        if constexpr (!STATE_ONLY) clear_tile<RK>(sQ, n, w, lane);
+        clear_tile<RV>(sV, n, w, lane);
+      }
+    }
+  };
+  auto present = [&](int c) { return len - c * kQ < kQ ? len - c * kQ : kQ; };
+  if constexpr (VEC) {
+    if (K < KD || V < VD) {                         // columns that the loads leave alone
+      clear_tile<RK>(sK, 0, w, lane0);
+      if constexpr (!STATE_ONLY) clear_tile<RK>(sQ, 0, w, lane0);
+      clear_tile<RV>(sV, 0, w, lane0);
+      __builtin_amdgcn_s_waitcnt(0xc07f);           // lgkmcnt(0): before the loads into the same slots
+    }
+  }
+
+  if (c_begin < c_live) {
+    load(c_begin, lane0);
+    arrived(present(c_begin), lane0);
+  }
   for (int c = c_begin; c < c_live; ++c) {
-    const int n = len - c * kQ < kQ ? len - c * kQ : kQ;
+    const int n = present(c);
     // the last chunk of the sequence (of the segment, in the pre-pass) forwards leaves S, not lam S
     const int shift = (STATE_ONLY || !reverse) && c + 1 == c_live && (STATE_ONLY || c_live == live) ? 1 : 0;
-    stage(n);
-    if (c + 1 < c_live) fetch(c + 1);
-    barrier_lds();
+    // (opaque, so that the chunk's many LDS and memory addresses are formed here from the lane's
+    // number: kept in registers over the loop they crowd out the state)
+    int lane = lane0;
+    asm volatile("" : "+v"(lane));
+    const int g = lane >> 4, c16 = lane & 15;
+    barrier_lds();                                  // the tiles of chunk c are complete
 
     // ---- P rows j = 16 w + c16: tiles of k q^T, rows i = 32 t + 8 g + 4 u + e
     if constexpr (!STATE_ONLY) {
       const int j = 16 * w + c16;
       piece qf[KT];
 #pragma unroll
-      for (int x = 0; x < KT; ++x) qf[x] = *reinterpret_cast<const piece*>(&sQ[j * RK + 32 * x + 8 * g]);
+      for (int x = 0; x < KT; ++x) qf[x] = O::template row<RK>(sQ, j, 32 * x + 8 * g);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         float pv[8];
@@ -317,12 +426,13 @@ __global__ __launch_bounds__(256) void la_kernel(LaArgs p) {
             const int krow = 32 * t + 8 * (c16 >> 2) + 4 * u + (c16 & 3);
 #pragma unroll
             for (int x = 0; x < KT; ++x)
-              s = O::mma(*reinterpret_cast<const piece*>(&sK[krow * RK + 32 * x + 8 * g]), qf[x], s);
+              s = O::mma(O::template row<RK>(sK, krow, 32 * x + 8 * g), qf[x], s);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int off = j - (32 * t + 8 * g + 4 * u + e);
-              const float d = exp2_hw(g2 * static_cast<float>(off > 0 ? off : 0)) * (r.in_scale * r.out_scale);
-              pv[4 * u + e] = off >= 0 ? s[e] * d : 0.0f;
+              float x = s[e] * (pl[t] * pw[4 * u + e]);
+              if (steep) x = s[e] * (exp2_hw(g2 * static_cast<float>(off > 0 ? off : 0)) * io_scale);
+              pv[4 * u + e] = off >= 0 ? x : 0.0f;
             }
           }
         }
@@ -338,7 +448,7 @@ __global__ __launch_bounds__(256) void la_kernel(LaArgs p) {
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) vf[vt][t] = O::column(sV, RV, 32 * t, 16 * (VT * w + vt), 4, lane);
+      for (int t = 0; t < 2; ++t) vf[vt][t] = O::template column<RV>(sV, 32 * t, 16 * (VT * w + vt), 4, lane);
 
     // ---- output from the carried state, transposed: acc[vt][jt] = rows v, column j = 16 jt + c16
     f32x4_t acc[VT][4];
@@ -358,7 +468,7 @@ __global__ __launch_bounds__(256) void la_kernel(LaArgs p) {
         }
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) {
-          const piece q = *reinterpret_cast<const piece*>(&sQ[(16 * jt + c16) * RK + 32 * t + 8 * g]);
+          const piece q = O::template row<RK>(sQ, 16 * jt + c16, 32 * t + 8 * g);
 #pragma unroll
           for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
@@ -382,9 +492,13 @@ __global__ __launch_bounds__(256) void la_kernel(LaArgs p) {
     for (int t = 0; t < 2; ++t) {
       float wgt[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int left = n - shift - (32 * t + 8 * g + e);
-        wgt[e] = exp2_hw(g2 * static_cast<float>(left > 0 ? left : 0)) * r.in_scale;
+      for (int e = 0; e < 8; ++e) wgt[e] = wl[t] * pw[e];
+      if (n - shift != kQ) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int left = n - shift - (32 * t + 8 * g + e);
+          wgt[e] = exp2_hw(g2 * static_cast<float>(left > 0 ? left : 0)) * r.in_scale;
+        }
       }
       piece wv[VT][WT];
 #pragma unroll
@@ -399,7 +513,7 @@ __global__ __launch_bounds__(256) void la_kernel(LaArgs p) {
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const piece kf = O::column(sK, RK, 32 * t, 32 * kt + 4 * u, 8, lane);
+          const piece kf = O::template column<RK>(sK, 32 * t, 32 * kt + 4 * u, 8, lane);
 #pragma unroll
           for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
@@ -407,57 +521,85 @@ __global__ __launch_bounds__(256) void la_kernel(LaArgs p) {
         }
     }
     barrier_lds();                                  // P complete; the tiles are free
+    if (c + 1 < c_live) load(c + 1, lane);
 
-    // ---- P v, transposed, on top; the output rows to memory
+    // ---- P v, transposed, on top
     if constexpr (!STATE_ONLY) {
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
         const int j = 16 * jt + c16;
-        const float f = exp2_hw(g2 * static_cast<float>(j)) * r.out_scale;
         piece pf[2][ET];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int m = 0; m < ET; ++m)
             if (t == 0 || jt >= 2) pf[t][m] = *reinterpret_cast<const piece*>(&sP[m][j * RS + 32 * t + 8 * g]);
-        const int64_t row = static_cast<int64_t>(c) * kQ + j;
-        const int64_t token = reverse ? (row < len ? len - 1 - row : row) : row;
-        const int64_t o0 = ((b * L + token) * p.H + h) * V;
 #pragma unroll
         for (int vt = 0; vt < VT; ++vt) {
-          f32x4_t a = acc[vt][jt];
+          f32x4_t& a = acc[vt][jt];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) a[e] *= f;
+          for (int e = 0; e < 4; ++e) a[e] *= fj[jt];
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int m = 0; m < ET; ++m)
               if (t == 0 || jt >= 2) a = O::mma(vf[vt][t], pf[t][m], a);
-          if (j >= n) a = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-          const int v0 = 16 * (VT * w + vt) + 4 * g;
-          if (row < L) {
-            if (r.o_f32 || kF32) {
-              float* o = static_cast<float*>(r.o) + o0 + v0;
-              if (vec) {
-                if (v0 < V) *reinterpret_cast<float4*>(o) = make_float4(a[0], a[1], a[2], a[3]);
-              } else {
+          if (n < kQ && j >= n) a = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+      }
+    }
+    // The rows of the next chunk are waited for before this chunk's stores are issued, so the
+    // wait never covers a store just made.  (Without a next chunk nothing is cleared.)
+    arrived(c + 1 < c_live ? present(c + 1) : kQ, lane);
+
+    // ---- the output rows to memory: lane (g, c) has 4 columns of row 16 jt + c of each tile
+    if constexpr (!STATE_ONLY) {
+      auto put = [&](auto* out) __attribute__((always_inline)) {
+        using OUT = std::remove_pointer_t<decltype(out)>;
+        auto four = [](const f32x4_t& a) __attribute__((always_inline)) {
+          if constexpr (sizeof(OUT) == 4) return make_float4(a[0], a[1], a[2], a[3]);
+          else return make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+        };
+        const int64_t row_stride = static_cast<int64_t>(p.H) * V;
+        const int r0 = c * kQ;
+        if (VEC && V == VD && n == kQ) {
+          // uniform addresses of 16 rows, the lane's place among them
+          const uint32_t off = static_cast<uint32_t>((reverse ? 15 - c16 : c16)) * static_cast<uint32_t>(row_stride) +
+                               static_cast<uint32_t>(16 * VT * w + 4 * g);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (v0 + e < V) o[e] = a[e];
-              }
+          for (int jt = 0; jt < 4; ++jt) {
+            const int64_t token = reverse ? len - 16 - (r0 + 16 * jt) : r0 + 16 * jt;
+            OUT* rows = out + (b * L + token) * row_stride + static_cast<int64_t>(h) * V;
+#pragma unroll
+            for (int vt = 0; vt < VT; ++vt)
+              *reinterpret_cast<decltype(four(acc[0][0]))*>(rows + off + 16 * vt) = four(acc[vt][jt]);
+          }
+          return;
+        }
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt) {
+          const int row = r0 + 16 * jt + c16;
+          if (row >= L) continue;
+          const int64_t token = reverse && row < len ? len - 1 - row : row;
+          OUT* o = out + (b * L + token) * row_stride + static_cast<int64_t>(h) * V;
+#pragma unroll
+          for (int vt = 0; vt < VT; ++vt) {
+            const int v0 = 16 * (VT * w + vt) + 4 * g;
+            if constexpr (VEC) {
+              if (v0 < V) *reinterpret_cast<decltype(four(acc[0][0]))*>(o + v0) = four(acc[vt][jt]);
             } else {
-              uint16_t* o = static_cast<uint16_t*>(r.o) + o0 + v0;
-              if (vec) {
-                if (v0 < V) *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
-              } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (v0 + e < V) o[e] = to_bf16(a[e]);
+              for (int e = 0; e < 4; ++e) {
+                if (v0 + e >= V) continue;
+                if constexpr (sizeof(OUT) == 4) o[v0 + e] = acc[vt][jt][e];
+                else o[v0 + e] = to_bf16(acc[vt][jt][e]);
               }
             }
           }
         }
-      }
+      };
+      if (kF32 || r.o_f32) put(static_cast<float*>(r.o));
+      else put(static_cast<uint16_t*>(r.o));
     }
   }
 
@@ -495,7 +637,7 @@ __global__ __launch_bounds__(256) void la_kernel(LaArgs p) {
 // Chains the segments' own sums T_s into the E entering each segment (written over T_s) and
 // the state after the last token.  One thread per state entry.
 __global__ __launch_bounds__(256) void la_chain_kernel(LaArgs p) {
-  const LaRole& r = p.role[0];
+  const LaRole& r = p.role[blockIdx.z];
   const int64_t bh = blockIdx.y;
   const int KV = r.K * r.V;
   const int i = blockIdx.x * 256 + threadIdx.x;
@@ -509,7 +651,8 @@ __global__ __launch_bounds__(256) void la_chain_kernel(LaArgs p) {
   auto times = [](const Pair& d, float x) { return __builtin_fmaf(d.hi, x, d.lo * x); };
   for (int k = 0; k < p.nseg; ++k, slot += KV) {
     const int left = len - k * seg_tokens, n = left < 0 ? 0 : (left < seg_tokens ? left : seg_tokens);
-    const float T = *slot;
+    const bool last = k + 1 == p.nseg;
+    const float T = last && !r.fin ? 0.0f : *slot;
     *slot = r.reverse ? s : times(l1, s);
     if (n == 0) continue;
     const Pair d = n == seg_tokens ? lS : decay_pair(p.log_decay, h, n);
@@ -537,47 +680,79 @@ __global__ __launch_bounds__(256) void la_copy_state_kernel(float* dst, const fl
 
 template <typename ACT, int KD, int VT>
 void launch_la_t(const LaArgs& a, bool state_only, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.batch * a.H * a.nseg), static_cast<unsigned>(a.nroles));
-  if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VT, true>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((la_kernel<ACT, KD, VT, false>), grid, dim3(256), 0, s, a);
+  const int64_t items = (a.batch * a.H * a.nseg + 7) / 8 * 8;
+  const dim3 grid(static_cast<unsigned>(items * a.nroles)), block(256);
+  if (a.role[0].vec) {
+    if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VT, true, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((la_kernel<ACT, KD, VT, true, false>), grid, block, 0, s, a);
+  } else {
+    if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VT, false, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((la_kernel<ACT, KD, VT, false, false>), grid, block, 0, s, a);
+  }
 }
 
-template <typename ACT>
-void launch_la_act(const LaArgs& a, bool state_only, hipStream_t s) {
+// One launch for all of `a`'s roles, which have one tile shape and one `vec`.
+void launch_la_roles(const LaArgs& a, Dt dt, bool state_only, hipStream_t s) {
   const bool k2 = a.role[0].K > 64, v2 = a.role[0].V > 64;
-  if (k2 && v2) launch_la_t<ACT, 128, 2>(a, state_only, s);
-  else if (k2) launch_la_t<ACT, 128, 1>(a, state_only, s);
-  else if (v2) launch_la_t<ACT, 64, 2>(a, state_only, s);
-  else launch_la_t<ACT, 64, 1>(a, state_only, s);
+  auto go = [&](auto act) {
+    using ACT = decltype(act);
+    if (k2 && v2) launch_la_t<ACT, 128, 2>(a, state_only, s);
+    else if (k2) launch_la_t<ACT, 128, 1>(a, state_only, s);
+    else if (v2) launch_la_t<ACT, 64, 2>(a, state_only, s);
+    else launch_la_t<ACT, 64, 1>(a, state_only, s);
+  };
+  if (dt == Dt::BF16) go(ActBF16{});
+  else go(ActF32{});
 }
 
 }  // namespace
 
-int la_segments(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V) {
-  (void)batch; (void)L; (void)H; (void)K; (void)V;
-  return 1;
+// Segments per sequence: enough that the (batch row, head, segment) workgroups fill the chip's
+// 2 a CU, each at least 4 chunks long.  The count is then derived back from the segment length,
+// so that no segment is without a chunk.
+int la_segments(int64_t batch, int64_t L, int64_t H) {
+  const int64_t pairs = batch * H, nch = (L + kQ - 1) / kQ, resident = 512;
+  int64_t s = resident / (pairs > 0 ? pairs : 1);
+  if (s > nch / 4) s = nch / 4;
+  if (s <= 1) return 1;
+  const int64_t per = (nch + s - 1) / s;
+  return static_cast<int>((nch + per - 1) / per);
 }
 
-// The roles of one call, each launched by itself (their tile shapes differ where K != V).
+// The roles of one call: the forward's one, or dq, dk and dv.  Roles of one tile shape go in one
+// launch.  With segments, a pre-pass leaves the states' sums of the forward walk (dq's
+// role) and of the backward walk (dv's; dk's is the same state with its axes exchanged, in the same
+// memory), and the chain kernel turns them into the states that enter the segments.
 hipError_t launch_la(const LaArgs& a, Dt dt, hipStream_t s) {
   const int64_t nchunks = (a.L + kQ - 1) / kQ;
-  for (int pass = a.nseg > 1 ? 0 : 1; pass < 2; ++pass) {
-    for (int i = 0; i < a.nroles; ++i) {
-      LaArgs one = a;
-      one.role[0] = a.role[i];
-      one.nroles = 1;
-      one.seg_chunks = (nchunks + a.nseg - 1) / a.nseg;
-      // (the roles of dk and dv share one set of segment states: role 2's)
-      if (pass == 0 && i == 1) continue;
-      if (dt == Dt::BF16) launch_la_act<ActBF16>(one, pass == 0, s);
-      else launch_la_act<ActF32>(one, pass == 0, s);
-      if (pass == 0) {
-        const dim3 grid(static_cast<unsigned>((one.role[0].K * one.role[0].V + 255) / 256),
-                        static_cast<unsigned>(a.batch * a.H), 1);
-        hipLaunchKernelGGL(la_chain_kernel, grid, dim3(256), 0, s, one);
-      }
+  LaArgs all = a;
+  all.seg_chunks = (nchunks + a.nseg - 1) / a.nseg;
+  // launches `n` of all's roles, together where they can
+  auto run = [&](const int* which, int n, bool state_only) {
+    LaArgs x = all;
+    bool same = true;
+    for (int i = 0; i < n; ++i) {
+      x.role[i] = all.role[which[i]];
+      same = same && (x.role[i].K > 64) == (x.role[0].K > 64) && (x.role[i].V > 64) == (x.role[0].V > 64) &&
+             x.role[i].vec == x.role[0].vec;
     }
+    x.nroles = same ? n : 1;
+    for (int i = 0; i < n; i += x.nroles) {
+      if (!same) x.role[0] = all.role[which[i]];
+      launch_la_roles(x, dt, state_only, s);
+    }
+  };
+  static constexpr int kAll[3] = {0, 1, 2}, kStates[2] = {0, 2};
+  if (a.nseg > 1) {
+    const int n = a.nroles > 1 ? 2 : 1;
+    run(kStates, n, true);
+    LaArgs x = all;
+    x.role[1] = all.role[2];
+    const dim3 grid(static_cast<unsigned>((a.role[0].K * a.role[0].V + 255) / 256), static_cast<unsigned>(a.batch * a.H),
+                    static_cast<unsigned>(n));
+    hipLaunchKernelGGL(la_chain_kernel, grid, dim3(256), 0, s, x);
   }
+  run(kAll, a.nroles, false);
   return hipGetLastError();
 }
 

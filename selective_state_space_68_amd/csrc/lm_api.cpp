@@ -21,6 +21,8 @@ using ssm::span;
 constexpr uint64_t kMaxBytes = uint64_t(1) << 62;
 constexpr int64_t kMaxL = int64_t(1) << 30;
 constexpr int64_t kMaxPairs = int64_t(1) << 20;      // batch * H of the prompt form
+constexpr int64_t kMaxHeads = int64_t(1) << 16;      // (16 rows of the output span less than 2^31 bytes)
+constexpr int64_t kMaxTokenStride = int64_t(1) << 26;  // ... and 8 rows of an input that moves as vectors
 constexpr int64_t kMaxStepPairs = int64_t(1) << 22;  // batch * H of the step
 constexpr int64_t kMaxRows = int64_t(1) << 22;
 
@@ -66,10 +68,10 @@ bool make_view(const int64_t* strides, const int64_t (&n)[DIMS], int64_t width, 
   return mul_ok(last, elem, &v->extent) && v->extent <= kMaxBytes;
 }
 
-// Whether every row of the tensor starts 16-byte aligned.
+// Whether every row of the tensor starts 16-byte aligned (and the rows of a tile lie near enough).
 template <int DIMS>
 bool rows_aligned(const void* p, const View<DIMS>& v, uint64_t elem) {
-  if (!aligned(p, 16)) return false;
+  if (!aligned(p, 16) || (DIMS == 3 && v.stride[1] > kMaxTokenStride)) return false;
   for (int i = 0; i < DIMS; ++i)
     if (static_cast<uint64_t>(v.stride[i]) * elem % 16) return false;
   return true;
@@ -97,7 +99,8 @@ ssm_status check_la_sizes(int64_t batch, int64_t L, int64_t H, int64_t Hq, int64
   if (H > 0 && (Hq < 1 || Hk < 1 || Hv < 1 || H % Hq || H % Hk || H % Hv)) return SSM_ERR_INVALID_ARG;
   uint64_t pairs;
   if (!mul_ok(static_cast<uint64_t>(batch), static_cast<uint64_t>(H), &pairs)) return SSM_ERR_INVALID_ARG;
-  if (pairs > static_cast<uint64_t>(max_pairs) || batch > max_pairs || H > max_pairs) return SSM_ERR_UNSUPPORTED;
+  if (pairs > static_cast<uint64_t>(max_pairs) || batch > max_pairs || H > kMaxHeads)
+    return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
 
@@ -111,7 +114,7 @@ struct LaPlan {
 
 bool la_plan(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V, int sets, const int64_t* share, LaPlan* p) {
   if (batch == 0 || L == 0 || H == 0) return true;
-  p->nseg = ssm::la_segments(batch, L, H, K, V);
+  p->nseg = ssm::la_segments(batch, L, H);
   if (p->nseg > 1 && !bytes_of(4, &p->seg_bytes, batch, H, p->nseg, K, V)) return false;
   p->total = up256(p->seg_bytes) * sets;
   const int64_t width[3] = {K, K, V};

@@ -45,7 +45,7 @@ struct LaArgs {
 constexpr int kLaMaxDim = 128;        // largest K and V
 
 // Segments per sequence and the floats of the segment states of one role.
-int la_segments(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V);
+int la_segments(int64_t batch, int64_t L, int64_t H);
 hipError_t launch_la(const LaArgs& a, Dt dt, hipStream_t s);
 
 // out[batch][L][heads][d] (act) = sum over the H / heads sharing heads of part[batch][L][H][d].
