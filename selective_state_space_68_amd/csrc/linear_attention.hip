@@ -20,9 +20,9 @@
 // two tiles of a pair leave a lane 8 consecutive indices: what one operand needs.  q, k and
 // v go from memory straight into LDS row by row (16 bytes a lane, no registers); operands that sum over tokens
 // (k^T, v^T) come out of the same rows by transposing LDS reads.  P goes through LDS (each
-// wave forms 16 rows of it).  A chunk's rows are asked for as soon as every wave has done with
-// the tiles of the chunk before, and arrive during its P v product and, the workgroups of a CU being
-// independent, during another workgroup's chunk.
+// wave forms 16 rows of it).  The next chunk's rows are asked for as early as the tiles allow: k, in
+// two buffers, at the chunk's start; q and v once P and the product with E are done, before
+// P v and the state's product.
 //
 // Roundings (bfloat16 activations; float32 activations use float32 products throughout):
 // the decayed v of the state update is split into three bfloat16 terms, which carry all 24
@@ -49,14 +49,21 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
 // Place of byte `byte` of a row in an LDS tile of RB-byte rows.  Rows are packed (the loads
-// into LDS leave no room for padding); the 16-byte slots of a row are exchanged within
-// groups of 8 by its number, so that the rows one read instruction touches lie in different
-// banks: 8 consecutive rows, the rows {0..3, 8..11} of the permuted tiles, and two
-// neighbouring slots of 4 consecutive rows (the transposing reads) are all apart.
-__device__ __forceinline__ constexpr int swizzle(int row) { return ((row & 3) << 1) | (((row >> 2) ^ (row >> 3)) & 1); }
-template <int RB>
+// into LDS leave no room for padding); the 16-byte slots of a row are exchanged by bits b of its number so
+// that the rows one read touches at a time lie in different banks: 16 consecutive rows and
+// the rows {0..3, 8..11, 16..19, 24..27} of the permuted tiles at 16 bytes a lane (in whose
+// phases lanes 4..11 of a 16-lane group go with the others of the next group, one slot
+// on), and two neighbouring slots of rows {0..3, 8..11} (the transposing reads).
+template <int RB, bool F32>
+__device__ __forceinline__ constexpr int swizzle(int row) {
+  const int b0 = row & 1, b1 = (row >> 1) & 1, b2 = (row >> 2) & 1, b3 = (row >> 3) & 1, b4 = (row >> 4) & 1;
+  if (F32) return b1 | (b0 << 1) | ((b2 ^ b4) << 2) | (b3 << 3);
+  if (RB == 128) return (b2 ^ b4) | (b1 << 1) | ((b2 ^ b3 ^ b4) << 2);
+  return (b2 ^ b4) | (b0 << 1) | (b1 << 2) | ((b2 ^ b3 ^ b4) << 3);
+}
+template <int RB, bool F32>
 __device__ __forceinline__ constexpr int tile_at(int row, int byte) {
-  return row * RB + (byte ^ (swizzle(row) << 4));
+  return row * RB + (byte ^ (swizzle<RB, F32>(row) << 4));
 }
 
 // ---- eight values of one lane: a matrix operand (one v_mfma_f32_16x16x32_bf16, lane
@@ -69,7 +76,6 @@ template <>
 struct Op<ActBF16> {
   using elem = uint16_t;
   using piece = uint4;
-  static constexpr int kPad = 8;     // elements of row padding of P (16 bytes)
   static __device__ __forceinline__ f32x4_t mma(const piece& a, const piece& b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
                                                    c, 0, 0, 0);
@@ -106,15 +112,19 @@ struct Op<ActBF16> {
   template <int RB>
   static __device__ __forceinline__ piece column(const char* tile, int row0, int col0, int step, int lane) {
     const int row = row0 + 8 * (lane >> 4) + ((lane & 15) >> 2), byte = 2 * (col0 + step * (lane & 3));
-    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(tile + tile_at<RB>(row, byte)));
-    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(tile + tile_at<RB>(row + 4, byte)));
+    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(tile + tile_at<RB, false>(row, byte)));
+    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(tile + tile_at<RB, false>(row + 4, byte)));
     const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
     return make_uint4(l.x, l.y, h.x, h.y);
   }
   // Columns col..col + 7 of a row.
   template <int RB>
   static __device__ __forceinline__ piece row(const char* tile, int row, int col) {
-    return *reinterpret_cast<const uint4*>(tile + tile_at<RB>(row, 2 * col));
+    return *reinterpret_cast<const uint4*>(tile + tile_at<RB, false>(row, 2 * col));
+  }
+  template <int RB>
+  static __device__ __forceinline__ void put(char* tile, int row, int col, const piece& p) {
+    *reinterpret_cast<uint4*>(tile + tile_at<RB, false>(row, 2 * col)) = p;
   }
 };
 
@@ -126,7 +136,6 @@ template <>
 struct Op<ActF32> {
   using elem = float;
   using piece = F8;
-  static constexpr int kPad = 4;
   static __device__ __forceinline__ f32x4_t mma(const piece& a, const piece& b, f32x4_t c) {
     c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.a.x, b.a.x, c, 0, 0, 0);
     c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.a.y, b.a.y, c, 0, 0, 0);
@@ -157,13 +166,18 @@ struct Op<ActF32> {
     const int row = row0 + 8 * (lane >> 4), byte = 4 * (col0 + step * ((lane & 15) >> 2) + (lane & 3));
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = *reinterpret_cast<const float*>(tile + tile_at<RB>(row + e, byte));
+    for (int e = 0; e < 8; ++e) v[e] = *reinterpret_cast<const float*>(tile + tile_at<RB, true>(row + e, byte));
     return pack(v);
   }
   template <int RB>
   static __device__ __forceinline__ piece row(const char* tile, int row, int col) {
-    return F8{*reinterpret_cast<const float4*>(tile + tile_at<RB>(row, 4 * col)),
-              *reinterpret_cast<const float4*>(tile + tile_at<RB>(row, 4 * col + 16))};
+    return F8{*reinterpret_cast<const float4*>(tile + tile_at<RB, true>(row, 4 * col)),
+              *reinterpret_cast<const float4*>(tile + tile_at<RB, true>(row, 4 * col + 16))};
+  }
+  template <int RB>
+  static __device__ __forceinline__ void put(char* tile, int row, int col, const piece& p) {
+    *reinterpret_cast<float4*>(tile + tile_at<RB, true>(row, 4 * col)) = p.a;
+    *reinterpret_cast<float4*>(tile + tile_at<RB, true>(row, 4 * col + 16)) = p.b;
   }
 };
 
@@ -197,8 +211,22 @@ __device__ __forceinline__ int row_length(const LaArgs& p, int64_t b) {
 // Rows of a [64][cols] block of elements into an LDS tile of RB-byte rows, by one workgroup.
 // Row r is at base + r * step elements; rows past `last` repeat it (they are cleared
 // afterwards), and columns past `cols` are left as they are (zeros, from the start).
-typedef __attribute__((address_space(1))) const void global_void_t;
-typedef __attribute__((address_space(3))) void lds_void_t;
+//
+// The load is written out (it has no result register; M0 holds the wave's LDS address, lane
+// l's 16 bytes go to M0 + 16 l): the compiler would wait for a load into one buffer of k
+// before reading the other.  Whoever reads the tile waits first (vmcnt(0), then a barrier).
+// (5 wait states lie between a vector write of an address's scalar register and its use.)
+typedef __attribute__((address_space(3))) char lds_char_t;
+__device__ __forceinline__ void load_to_lds(const char* tile, const char* base, uint32_t off) {
+  const uint32_t m0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char_t*)(tile)));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(m0), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void load_to_lds(const char* tile, const char* src) {
+  const uint32_t m0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char_t*)(tile)));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off"
+               :: "s"(m0), "v"(src) : "memory", "m0");
+}
 
 template <typename ELEM, int RB>
 __device__ __forceinline__ void load_tile(char* tile, const ELEM* base, int64_t step, int last, int cols, int w,
@@ -206,7 +234,8 @@ __device__ __forceinline__ void load_tile(char* tile, const ELEM* base, int64_t 
   constexpr int kSlots = RB / 16, kRows = 64 / kSlots;              // slots of a row, rows of an instruction
   constexpr int kInstr = kQ / kRows / 4;                            // instructions of a wave
   const int lane_row = lane / kSlots;
-  const int lane_slot = (lane % kSlots) ^ swizzle(lane_row);        // (the swizzle is linear in the row's bits)
+  constexpr bool kF32 = sizeof(ELEM) == 4;
+  const int lane_slot = (lane % kSlots) ^ swizzle<RB, kF32>(lane_row);   // (the swizzle is linear in the row's bits)
   if (last == kQ - 1 && cols * static_cast<int>(sizeof(ELEM)) == RB) {
     // a whole tile: a uniform address of each instruction's lowest row plus the lane's offset from it
     const int64_t bytes = step * static_cast<int64_t>(sizeof(ELEM));
@@ -217,17 +246,17 @@ __device__ __forceinline__ void load_tile(char* tile, const ELEM* base, int64_t 
     for (int i = 0; i < kInstr; ++i) {
       const int row0 = (w * kInstr + i) * kRows;
       const char* src = reinterpret_cast<const char*>(base) + (row0 + (up ? 0 : kRows - 1)) * bytes;
-      const uint32_t off = row_off + static_cast<uint32_t>((lane_slot ^ swizzle(i * kRows)) * 16);
-      __builtin_amdgcn_global_load_lds((global_void_t*)(src + off), (lds_void_t*)(tile + row0 * RB), 16, 0, 0);
+      const uint32_t off = row_off + static_cast<uint32_t>((lane_slot ^ swizzle<RB, kF32>(row0)) * 16);
+      load_to_lds(tile + row0 * RB, src, off);
     }
   } else {
 #pragma unroll 1
     for (int i = 0; i < kInstr; ++i) {
-      const int row0 = (w * kInstr + i) * kRows, row = row0 + lane_row, slot = lane_slot ^ swizzle(i * kRows);
+      const int row0 = (w * kInstr + i) * kRows, row = row0 + lane_row, slot = lane_slot ^ swizzle<RB, kF32>(row0);
       const int r = row < last ? row : last;
       const char* src = reinterpret_cast<const char*>(base + r * step) + slot * 16;
       if (slot * 16 < cols * static_cast<int>(sizeof(ELEM)))
-        __builtin_amdgcn_global_load_lds((global_void_t*)src, (lds_void_t*)(tile + row0 * RB), 16, 0, 0);
+        load_to_lds(tile + row0 * RB, src);
     }
   }
 }
@@ -251,7 +280,7 @@ __device__ __forceinline__ void load_tile_scalar(char* tile, const ELEM* base, i
     const int row = i / kCols, col = i % kCols;
     ELEM x = ELEM(0);
     if (row <= last && col < cols) x = base[row * step + col];
-    *reinterpret_cast<ELEM*>(tile + tile_at<RB>(row, col * static_cast<int>(sizeof(ELEM)))) = x;
+    *reinterpret_cast<ELEM*>(tile + tile_at<RB, sizeof(ELEM) == 4>(row, col * static_cast<int>(sizeof(ELEM)))) = x;
   }
 }
 
@@ -265,14 +294,14 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
   constexpr bool kF32 = sizeof(elem) == 4;
   constexpr int VD = 64 * VT;
   constexpr int RK = KD * static_cast<int>(sizeof(elem)), RV = VD * static_cast<int>(sizeof(elem));   // row bytes
-  constexpr int RS = kQ + O::kPad;
+  constexpr int RP = kQ * static_cast<int>(sizeof(elem));
   constexpr int KT = KD / 32;                       // pairs of state tiles along K
   constexpr int WT = kF32 ? 1 : 3;                  // operand terms of the decayed v
   constexpr int ET = kF32 ? 1 : 2;                  // operand terms of E and of P
   __shared__ __attribute__((aligned(16))) char sQ[STATE_ONLY ? 16 : kQ * RK];
-  __shared__ __attribute__((aligned(16))) char sK[kQ * RK];
+  __shared__ __attribute__((aligned(16))) char sKK[2][kQ * RK];                // k of this chunk and of the next
   __shared__ __attribute__((aligned(16))) char sV[kQ * RV];
-  __shared__ __attribute__((aligned(16))) elem sP[ET][STATE_ONLY ? 16 : kQ * RS];   // P [j][i]
+  __shared__ __attribute__((aligned(16))) char sP[ET][STATE_ONLY ? 16 : kQ * RP];   // P [j][i]
 
   const int tid = threadIdx.x, lane0 = tid & 63, w = uniform_int(tid >> 6);
   // Workgroup ids go round the 8 XCDs: the roles of one (batch row, head, segment), which
@@ -338,6 +367,21 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
           E[vt][t][u][e] = x;
         }
 
+  // E times (1 + chunks * lo / hi) of lam^kQ = hi + lo
+  const float fix = dQ.hi > 0.0f ? dQ.lo / dQ.hi : 0.0f;
+  int since = 0;
+  auto correct = [&](float chunks) __attribute__((always_inline)) {
+    const float f = fix * chunks;
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) E[vt][t][u][e] = __builtin_fmaf(f, E[vt][t][u][e], E[vt][t][u][e]);
+  };
+
   // Decay factors.  lam^(j-i) of P splits into a lane's lam^(j - 32t - 8g - 7) and the uniform
   // lam^(7 - (4u + e)); the first may exceed 1 near the diagonal, so heads that decay by more
   // than 2^16 a token (lam^7 near float32's end) take the exponent of each element instead.
@@ -357,27 +401,30 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
 #pragma unroll
   for (int jt = 0; jt < 4; ++jt) fj[jt] = exp2_hw(g2 * static_cast<float>(16 * jt + c16)) * r.out_scale;
 
-  // Asks for the rows of chunk c.
-  auto load = [&](int c, int lane) __attribute__((always_inline)) {
+  // Ask for the rows of k, or of q and v, of chunk c.
+  auto load_k = [&](int c, int lane) __attribute__((always_inline)) {
+    const int64_t r0 = static_cast<int64_t>(c) * kQ;
+    const int last = len - 1 - c * kQ < kQ - 1 ? len - 1 - c * kQ : kQ - 1;
+    if constexpr (VEC) load_tile<elem, RK>(sKK[c & 1], kg + r0 * kstep, kstep, last, K, w, lane);
+    else load_tile_scalar<elem, RK>(sKK[c & 1], kg + r0 * kstep, kstep, last, K, tid);
+  };
+  auto load_qv = [&](int c, int lane) __attribute__((always_inline)) {
     const int64_t r0 = static_cast<int64_t>(c) * kQ;
     const int last = len - 1 - c * kQ < kQ - 1 ? len - 1 - c * kQ : kQ - 1;
     if constexpr (VEC) {
-      load_tile<elem, RK>(sK, kg + r0 * kstep, kstep, last, K, w, lane);
       if constexpr (!STATE_ONLY) load_tile<elem, RK>(sQ, qg + r0 * qstep, qstep, last, K, w, lane);
       load_tile<elem, RV>(sV, vg + r0 * vstep, vstep, last, V, w, lane);
     } else {
-      load_tile_scalar<elem, RK>(sK, kg + r0 * kstep, kstep, last, K, tid);
       if constexpr (!STATE_ONLY) load_tile_scalar<elem, RK>(sQ, qg + r0 * qstep, qstep, last, K, tid);
       load_tile_scalar<elem, RV>(sV, vg + r0 * vstep, vstep, last, V, tid);
     }
   };
-  // Waits for this wave's part of them (and for its stores of the chunk before); n: the tokens of
-  // the chunk asked for.
-  auto arrived = [&](int n, int lane) __attribute__((always_inline)) {
+  // Waits for this wave's part of chunk c's rows (and for its stores of the chunk before).
+  auto arrived = [&](int c, int n, int lane) __attribute__((always_inline)) {
     if constexpr (VEC) {
       __builtin_amdgcn_s_waitcnt(0x0f70);           // vmcnt(0); expcnt and lgkmcnt as they are
       if (n < kQ) {
-        clear_tile<RK>(sK, n, w, lane);
+        clear_tile<RK>(sKK[c & 1], n, w, lane);
         if constexpr (!STATE_ONLY) clear_tile<RK>(sQ, n, w, lane);
         clear_tile<RV>(sV, n, w, lane);
       }
@@ -386,7 +433,8 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
   auto present = [&](int c) { return len - c * kQ < kQ ? len - c * kQ : kQ; };
   if constexpr (VEC) {
     if (K < KD || V < VD) {                         // columns that the loads leave alone
-      clear_tile<RK>(sK, 0, w, lane0);
+      clear_tile<RK>(sKK[0], 0, w, lane0);
+      clear_tile<RK>(sKK[1], 0, w, lane0);
       if constexpr (!STATE_ONLY) clear_tile<RK>(sQ, 0, w, lane0);
       clear_tile<RV>(sV, 0, w, lane0);
       __builtin_amdgcn_s_waitcnt(0xc07f);           // lgkmcnt(0): before the loads into the same slots
@@ -394,8 +442,9 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
   }
 
   if (c_begin < c_live) {
-    load(c_begin, lane0);
-    arrived(present(c_begin), lane0);
+    load_k(c_begin, lane0);
+    load_qv(c_begin, lane0);
+    arrived(c_begin, present(c_begin), lane0);
   }
   for (int c = c_begin; c < c_live; ++c) {
     const int n = present(c);
@@ -407,6 +456,8 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
     asm volatile("" : "+v"(lane));
     const int g = lane >> 4, c16 = lane & 15;
     barrier_lds();                                  // the tiles of chunk c are complete
+    const char* sK = sKK[c & 1];
+    if (c + 1 < c_live) load_k(c + 1, lane);
 
     // ---- P rows j = 16 w + c16: tiles of k q^T, rows i = 32 t + 8 g + 4 u + e
     if constexpr (!STATE_ONLY) {
@@ -439,7 +490,7 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
         piece ps[ET];
         O::template split<ET>(pv, ps);
 #pragma unroll
-        for (int m = 0; m < ET; ++m) *reinterpret_cast<piece*>(&sP[m][j * RS + 32 * t + 8 * g]) = ps[m];
+        for (int m = 0; m < ET; ++m) O::template put<RP>(sP[m], j, 32 * t + 8 * g, ps[m]);
       }
     }
 
@@ -477,51 +528,8 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
       }
     }
 
-    // ---- the state: E = lam^n E + k^T (lam^(n-i) v)
-    Pair dn = dQ;
-    if (n - shift != kQ) dn = decay_pair(p.log_decay, h, n - shift);
-#pragma unroll
-    for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) E[vt][t][u][e] = __builtin_fmaf(dn.hi, E[vt][t][u][e], dn.lo * E[vt][t][u][e]);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      float wgt[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) wgt[e] = wl[t] * pw[e];
-      if (n - shift != kQ) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int left = n - shift - (32 * t + 8 * g + e);
-          wgt[e] = exp2_hw(g2 * static_cast<float>(left > 0 ? left : 0)) * r.in_scale;
-        }
-      }
-      piece wv[VT][WT];
-#pragma unroll
-      for (int vt = 0; vt < VT; ++vt) {
-        float x[8];
-        O::unpack(vf[vt][t], x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= wgt[e];
-        O::template split<WT>(x, wv[vt]);
-      }
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const piece kf = O::template column<RK>(sK, 32 * t, 32 * kt + 4 * u, 8, lane);
-#pragma unroll
-          for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-            for (int m = 0; m < WT; ++m) E[vt][kt][u] = O::mma(kf, wv[vt][m], E[vt][kt][u]);
-        }
-    }
-    barrier_lds();                                  // P complete; the tiles are free
-    if (c + 1 < c_live) load(c + 1, lane);
+    barrier_lds();                                  // P complete; the tiles of q and v are free
+    if (c + 1 < c_live) load_qv(c + 1, lane);
 
     // ---- P v, transposed, on top
     if constexpr (!STATE_ONLY) {
@@ -533,7 +541,7 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int m = 0; m < ET; ++m)
-            if (t == 0 || jt >= 2) pf[t][m] = *reinterpret_cast<const piece*>(&sP[m][j * RS + 32 * t + 8 * g]);
+            if (t == 0 || jt >= 2) pf[t][m] = O::template row<RP>(sP[m], j, 32 * t + 8 * g);
 #pragma unroll
         for (int vt = 0; vt < VT; ++vt) {
           f32x4_t& a = acc[vt][jt];
@@ -548,10 +556,6 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
         }
       }
     }
-    // The rows of the next chunk are waited for before this chunk's stores are issued, so the
-    // wait never covers a store just made.  (Without a next chunk nothing is cleared.)
-    arrived(c + 1 < c_live ? present(c + 1) : kQ, lane);
-
     // ---- the output rows to memory: lane (g, c) has 4 columns of row 16 jt + c of each tile
     if constexpr (!STATE_ONLY) {
       auto put = [&](auto* out) __attribute__((always_inline)) {
@@ -601,7 +605,59 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
       if (kF32 || r.o_f32) put(static_cast<float*>(r.o));
       else put(static_cast<uint16_t*>(r.o));
     }
+
+    // ---- the state: E = lam^n E + k^T (lam^(n-i) v)
+    const bool whole = n - shift == kQ;
+    const Pair dn = whole ? dQ : decay_pair(p.log_decay, h, n - shift);
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) E[vt][t][u][e] *= dn.hi;
+    // what the rounding of lam^n to float32 left, for 16 chunks at a time (2^-20 by then)
+    if (whole && ++since == 16) {
+      correct(16.0f);
+      since = 0;
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      float wgt[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wgt[e] = wl[t] * pw[e];
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int left = n - shift - (32 * t + 8 * g + e);
+          wgt[e] = exp2_hw(g2 * static_cast<float>(left > 0 ? left : 0)) * r.in_scale;
+        }
+      }
+      piece wv[VT][WT];
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) {
+        float x[8];
+        O::unpack(vf[vt][t], x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= wgt[e];
+        O::template split<WT>(x, wv[vt]);
+      }
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const piece kf = O::template column<RK>(sK, 32 * t, 32 * kt + 4 * u, 8, lane);
+#pragma unroll
+          for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+            for (int m = 0; m < WT; ++m) E[vt][kt][u] = O::mma(kf, wv[vt][m], E[vt][kt][u]);
+        }
+    }
+    // (without a next chunk there is nothing to clear)
+    arrived(c + 1, c + 1 < c_live ? present(c + 1) : kQ, lane);
   }
+  if (since) correct(static_cast<float>(since));
 
   // chunks with no token: zeros
   if constexpr (!STATE_ONLY) {
