@@ -12,8 +12,8 @@
 // sequence is token n_tokens - 1 - r, and E before the first row is the gradient of the
 // final state.
 //
-// One workgroup of 4 waves walks the chunks of one (batch row, head, segment).  Wave w owns
-// columns v in [16 VT w, 16 VT (w + 1)) of E and of the output, so E is used as a matrix
+// One workgroup walks the chunks of one (batch row, head, segment).  Wave w owns columns
+// v in [16 w, 16 w + 16) of E and of the output, so E is used as a matrix
 // operand straight from the registers that accumulate it: a product leaves lane (g, c) of a
 // 16 x 16 tile four consecutive rows of column c, and since the order of a product's
 // summation index is free, the rows of each tile are assigned (kperm below) so that the
@@ -45,25 +45,37 @@ constexpr int kQ = 64;               // tokens per chunk
 constexpr float kMinLog2 = -1.0e4f;  // 2^kMinLog2 == 0 and kMinLog2 * 0 == 0: a decay of exactly 0 works like any other
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
-// Place of byte `byte` of a row in an LDS tile of RB-byte rows.  Rows are packed (the loads
-// into LDS leave no room for padding); the 16-byte slots of a row are exchanged by bits b of its number so
-// that the rows one read touches at a time lie in different banks: 16 consecutive rows and
-// the rows {0..3, 8..11, 16..19, 24..27} of the permuted tiles at 16 bytes a lane (in whose
-// phases lanes 4..11 of a 16-lane group go with the others of the next group, one slot
-// on), and two neighbouring slots of rows {0..3, 8..11} (the transposing reads).
-template <int RB, bool F32>
+// Place of byte `byte` of a row in an LDS tile of RB-byte rows: row RB + (byte ^ 16 swizzle(row)).
+// Rows are packed (the loads into LDS leave no room for padding); the 16-byte slots of a
+// row are exchanged by the bits of its number so that the rows one read touches at a time lie
+// in different banks: 16 consecutive rows and (PERM) the rows {0..3, 8..11, 16..19, 24..27} of the permuted
+// tiles at 16 bytes a lane (in whose phases lanes 4..11 of a 16-lane group go with the
+// others of the next group, one slot on), and two neighbouring slots of rows {0..3, 8..11}
+// (the transposing reads).  It is linear in the row's bits, so an address is one lane
+// part, exclusive-or'ed with constants, plus a constant offset.
+template <int RB, bool F32, bool PERM>
 __device__ __forceinline__ constexpr int swizzle(int row) {
-  const int b0 = row & 1, b1 = (row >> 1) & 1, b2 = (row >> 2) & 1, b3 = (row >> 3) & 1, b4 = (row >> 4) & 1;
+  const int b0 = row & 1, b1 = (row >> 1) & 1, b2 = (row >> 2) & 1, b3 = (row >> 3) & 1,
+            b4 = PERM ? (row >> 4) & 1 : 0;
   if (F32) return b1 | (b0 << 1) | ((b2 ^ b4) << 2) | (b3 << 3);
   if (RB == 128) return (b2 ^ b4) | (b1 << 1) | ((b2 ^ b3 ^ b4) << 2);
   return (b2 ^ b4) | (b0 << 1) | (b1 << 2) | ((b2 ^ b3 ^ b4) << 3);
 }
-template <int RB, bool F32>
-__device__ __forceinline__ constexpr int tile_at(int row, int byte) {
-  return row * RB + (byte ^ (swizzle<RB, F32>(row) << 4));
+typedef __attribute__((address_space(3))) char lds_char_t;
+__device__ __forceinline__ uint32_t lds_address(const char* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char_t*)(p)));
+}
+template <typename V>
+__device__ __forceinline__ V lds_read(uint32_t at) {
+  return *(const __attribute__((address_space(3))) V*)(static_cast<uintptr_t>(at));
+}
+template <typename V>
+__device__ __forceinline__ void lds_write(uint32_t at, const V& v) {
+  *(__attribute__((address_space(3))) V*)(static_cast<uintptr_t>(at)) = v;
 }
 
 // ---- eight values of one lane: a matrix operand (one v_mfma_f32_16x16x32_bf16, lane
@@ -98,34 +110,48 @@ struct Op<ActBF16> {
 #pragma unroll
     for (int t = 0; t < TERMS; ++t) {
       p[t] = pack(r);
-      if (t + 1 < TERMS) {
-        float q[8];
-        unpack(p[t], q);
+      if (t + 1 < TERMS) {                          // r - p, exact: one dot product of p's pair with (-1, 0) or (0, -1)
+        const uint32_t pw[4] = {p[t].x, p[t].y, p[t].z, p[t].w};
+        uint32_t low = 0x0000bf80u, high = 0xbf800000u;
+        asm("" : "+s"(low), "+s"(high));            // (scalar registers: as an immediate operand -1.0 is the pair's high half alone)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] -= q[e];
+        for (int e = 0; e < 8; ++e)
+          r[e] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, pw[e / 2]),
+                                                 __builtin_bit_cast(bf16x2_t, e % 2 ? high : low), r[e], false);
       }
     }
   }
-  // Values [row0 + 8g + e][col(c)], e = 0..7, of a tile, col(c) = col0 + step (c / 4) + c % 4:
-  // two transposing reads of 4 rows each.  Lane i of a 16-lane group gives the address
-  // of 4 columns (piece i % 4) of row i / 4 and receives column i of the 4 rows.
-  template <int RB>
-  static __device__ __forceinline__ piece column(const char* tile, int row0, int col0, int step, int lane) {
-    const int row = row0 + 8 * (lane >> 4) + ((lane & 15) >> 2), byte = 2 * (col0 + step * (lane & 3));
-    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(tile + tile_at<RB, false>(row, byte)));
-    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(tile + tile_at<RB, false>(row + 4, byte)));
+  static constexpr int kPiece = 16;                 // bytes of 8 elements
+  // A lane's part of the address of columns 8g.. of row `row`, and the 8 columns at it.
+  template <int RB, bool PERM>
+  static __device__ __forceinline__ uint32_t row_part(uint32_t tile, int row, int g) {
+    return tile + row * RB + ((16 * g) ^ (swizzle<RB, false, PERM>(row) << 4));
+  }
+  static __device__ __forceinline__ piece row(uint32_t at, int flip, int offset) {
+    return __builtin_bit_cast(piece, lds_read<u32x4_t>((at ^ flip) + offset));
+  }
+  static __device__ __forceinline__ void put(uint32_t at, int flip, int offset, const piece& p) {
+    lds_write<u32x4_t>((at ^ flip) + offset, __builtin_bit_cast(u32x4_t, p));
+  }
+  // Values [8g + e][col(c)], e = 0..7, col(c) = col0 + step (c / 4) + c % 4: two
+  // transposing reads of 4 rows each.  Lane i of a 16-lane group gives the address of 4
+  // columns (piece i % 4) of row i / 4 and receives column i of the 4 rows.
+  template <int RB, bool PERM>
+  static __device__ __forceinline__ uint32_t column_part(uint32_t tile, int col0, int step, int lane) {
+    const int row = 8 * (lane >> 4) + ((lane & 15) >> 2);
+    return tile + row * RB + ((2 * (col0 + step * (lane & 3))) ^ (swizzle<RB, false, PERM>(row) << 4));
+  }
+  template <int RB, bool PERM>
+  static __device__ __forceinline__ piece column(uint32_t at, int flip, int offset) {
+    const uint32_t a = (at ^ flip) + offset, b = (at ^ flip ^ (swizzle<RB, false, PERM>(4) << 4)) + offset + 4 * RB;
+    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(static_cast<uintptr_t>(a)));
+    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(static_cast<uintptr_t>(b)));
     const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
     return make_uint4(l.x, l.y, h.x, h.y);
   }
-  // Columns col..col + 7 of a row.
-  template <int RB>
-  static __device__ __forceinline__ piece row(const char* tile, int row, int col) {
-    return *reinterpret_cast<const uint4*>(tile + tile_at<RB, false>(row, 2 * col));
-  }
-  template <int RB>
-  static __device__ __forceinline__ void put(char* tile, int row, int col, const piece& p) {
-    *reinterpret_cast<uint4*>(tile + tile_at<RB, false>(row, 2 * col)) = p;
-  }
+  // The next 4 columns of a piece (u = 1): one half of a slot on.
+  static __device__ __forceinline__ constexpr int half_flip(int) { return 0; }
+  static __device__ __forceinline__ constexpr int half_offset(int u) { return 8 * u; }
 };
 
 struct F8 {
@@ -161,24 +187,34 @@ struct Op<ActF32> {
     static_assert(TERMS == 1, "float32 operands are exact");
     p[0] = pack(v);
   }
-  template <int RB>
-  static __device__ __forceinline__ piece column(const char* tile, int row0, int col0, int step, int lane) {
-    const int row = row0 + 8 * (lane >> 4), byte = 4 * (col0 + step * ((lane & 15) >> 2) + (lane & 3));
+  static constexpr int kPiece = 32;
+  template <int RB, bool PERM>
+  static __device__ __forceinline__ uint32_t row_part(uint32_t tile, int row, int g) {
+    return tile + row * RB + ((32 * g) ^ (swizzle<RB, true, PERM>(row) << 4));
+  }
+  static __device__ __forceinline__ piece row(uint32_t at, int flip, int offset) {
+    return F8{__builtin_bit_cast(float4, lds_read<f32x4_t>((at ^ flip) + offset)),
+              __builtin_bit_cast(float4, lds_read<f32x4_t>((at ^ flip ^ 16) + offset))};
+  }
+  static __device__ __forceinline__ void put(uint32_t at, int flip, int offset, const piece& p) {
+    lds_write<f32x4_t>((at ^ flip) + offset, __builtin_bit_cast(f32x4_t, p.a));
+    lds_write<f32x4_t>((at ^ flip ^ 16) + offset, __builtin_bit_cast(f32x4_t, p.b));
+  }
+  template <int RB, bool PERM>
+  static __device__ __forceinline__ uint32_t column_part(uint32_t tile, int col0, int step, int lane) {
+    const int row = 8 * (lane >> 4);
+    return tile + row * RB + ((4 * (col0 + step * ((lane & 15) >> 2) + (lane & 3))) ^ (swizzle<RB, true, PERM>(row) << 4));
+  }
+  template <int RB, bool PERM>
+  static __device__ __forceinline__ piece column(uint32_t at, int flip, int offset) {
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = *reinterpret_cast<const float*>(tile + tile_at<RB, true>(row + e, byte));
+    for (int e = 0; e < 8; ++e)
+      v[e] = lds_read<float>((at ^ flip ^ (swizzle<RB, true, PERM>(e) << 4)) + offset + e * RB);
     return pack(v);
   }
-  template <int RB>
-  static __device__ __forceinline__ piece row(const char* tile, int row, int col) {
-    return F8{*reinterpret_cast<const float4*>(tile + tile_at<RB, true>(row, 4 * col)),
-              *reinterpret_cast<const float4*>(tile + tile_at<RB, true>(row, 4 * col + 16))};
-  }
-  template <int RB>
-  static __device__ __forceinline__ void put(char* tile, int row, int col, const piece& p) {
-    *reinterpret_cast<float4*>(tile + tile_at<RB, true>(row, 4 * col)) = p.a;
-    *reinterpret_cast<float4*>(tile + tile_at<RB, true>(row, 4 * col + 16)) = p.b;
-  }
+  static __device__ __forceinline__ constexpr int half_flip(int u) { return 16 * u; }
+  static __device__ __forceinline__ constexpr int half_offset(int) { return 0; }
 };
 
 // log2(lam) of a head, kept finite at the bottom (NaN passes through).
@@ -187,24 +223,42 @@ __device__ __forceinline__ float decay_log2(const float* log_decay, int h) {
   return g < kMinLog2 ? kMinLog2 : g;
 }
 
-// lam^n as a float32 pair hi + lo.  A state passes through thousands of these products, so
-// the rounding of lam^n alone would grow to n_chunks * 2^-24 over the head's memory.
+// lam^n.  A state passes through thousands of these factors, so they are formed in float64
+// and applied as a float32 pair hi + lo: the rounding of lam^n alone would grow to
+// n_chunks * 2^-24 over the head's memory.
 struct Pair {
   float hi, lo;
 };
-__device__ __forceinline__ Pair decay_pair(const float* log_decay, int h, int n) {
-  double x = static_cast<double>(log_decay[h]) * n;
-  if (n == 0) x = 0.0;
-  const double d = exp(x);
+__device__ __forceinline__ double decay_power(const float* log_decay, int h, int n) {
+  return n == 0 ? 1.0 : exp(static_cast<double>(log_decay[h]) * n);
+}
+__device__ __forceinline__ Pair pair_of(double d) {
   const float hi = static_cast<float>(d);
   const float lo = static_cast<float>(d - static_cast<double>(hi));
   return Pair{hi, lo == lo ? lo : 0.0f};              // (inf - inf where lam^n overflows)
+}
+__device__ __forceinline__ Pair decay_pair(const float* log_decay, int h, int n) {
+  return pair_of(decay_power(log_decay, h, n));
+}
+
+__device__ __forceinline__ int lane_id() { return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)); }
+
+// A value that is the same in every lane, kept in a scalar register.
+__device__ __forceinline__ float uniform_float(float v) {
+  return __builtin_bit_cast(float, uniform_int(__builtin_bit_cast(int, v)));
+}
+
+__device__ __forceinline__ double uniform_double(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint64_t lo = static_cast<uint32_t>(uniform_int(static_cast<int>(u))),
+                 hi = static_cast<uint32_t>(uniform_int(static_cast<int>(u >> 32)));
+  return __builtin_bit_cast(double, lo | (hi << 32));
 }
 
 __device__ __forceinline__ int row_length(const LaArgs& p, int64_t b) {
   const int L = static_cast<int>(p.L);
   if (!p.lengths) return L;
-  const int n = p.lengths[b];
+  const int n = uniform_int(p.lengths[b]);
   return n < 0 ? 0 : (n > L ? L : n);
 }
 
@@ -215,27 +269,27 @@ __device__ __forceinline__ int row_length(const LaArgs& p, int64_t b) {
 // The load is written out (it has no result register; M0 holds the wave's LDS address, lane
 // l's 16 bytes go to M0 + 16 l): the compiler would wait for a load into one buffer of k
 // before reading the other.  Whoever reads the tile waits first (vmcnt(0), then a barrier).
-// (5 wait states lie between a vector write of an address's scalar register and its use.)
-typedef __attribute__((address_space(3))) char lds_char_t;
+// (5 wait states lie between a vector write of an address's scalar register and its use.  The
+// compiler has M0 reserved, and nothing else in these kernels uses it.)
 __device__ __forceinline__ void load_to_lds(const char* tile, const char* base, uint32_t off) {
-  const uint32_t m0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char_t*)(tile)));
+  const int m0 = uniform_int(static_cast<int>(lds_address(tile)));
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"(m0), "v"(off), "s"(base) : "memory", "m0");
+               :: "s"(m0), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void load_to_lds(const char* tile, const char* src) {
-  const uint32_t m0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char_t*)(tile)));
+  const int m0 = uniform_int(static_cast<int>(lds_address(tile)));
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off"
-               :: "s"(m0), "v"(src) : "memory", "m0");
+               :: "s"(m0), "v"(src) : "memory");
 }
 
-template <typename ELEM, int RB>
+template <typename ELEM, int RB, int NW, bool PERM>
 __device__ __forceinline__ void load_tile(char* tile, const ELEM* base, int64_t step, int last, int cols, int w,
                                           int lane) {
   constexpr int kSlots = RB / 16, kRows = 64 / kSlots;              // slots of a row, rows of an instruction
-  constexpr int kInstr = kQ / kRows / 4;                            // instructions of a wave
+  constexpr int kInstr = kQ / kRows / NW;                           // instructions of a wave
   const int lane_row = lane / kSlots;
   constexpr bool kF32 = sizeof(ELEM) == 4;
-  const int lane_slot = (lane % kSlots) ^ swizzle<RB, kF32>(lane_row);   // (the swizzle is linear in the row's bits)
+  const int lane_slot = (lane % kSlots) ^ swizzle<RB, kF32, PERM>(lane_row);   // (the swizzle is linear in the row's bits)
   if (last == kQ - 1 && cols * static_cast<int>(sizeof(ELEM)) == RB) {
     // a whole tile: a uniform address of each instruction's lowest row plus the lane's offset from it
     const int64_t bytes = step * static_cast<int64_t>(sizeof(ELEM));
@@ -246,13 +300,13 @@ __device__ __forceinline__ void load_tile(char* tile, const ELEM* base, int64_t 
     for (int i = 0; i < kInstr; ++i) {
       const int row0 = (w * kInstr + i) * kRows;
       const char* src = reinterpret_cast<const char*>(base) + (row0 + (up ? 0 : kRows - 1)) * bytes;
-      const uint32_t off = row_off + static_cast<uint32_t>((lane_slot ^ swizzle<RB, kF32>(row0)) * 16);
+      const uint32_t off = row_off + static_cast<uint32_t>((lane_slot ^ swizzle<RB, kF32, PERM>(row0)) * 16);
       load_to_lds(tile + row0 * RB, src, off);
     }
   } else {
 #pragma unroll 1
     for (int i = 0; i < kInstr; ++i) {
-      const int row0 = (w * kInstr + i) * kRows, row = row0 + lane_row, slot = lane_slot ^ swizzle<RB, kF32>(row0);
+      const int row0 = (w * kInstr + i) * kRows, row = row0 + lane_row, slot = lane_slot ^ swizzle<RB, kF32, PERM>(row0);
       const int r = row < last ? row : last;
       const char* src = reinterpret_cast<const char*>(base + r * step) + slot * 16;
       if (slot * 16 < cols * static_cast<int>(sizeof(ELEM)))
@@ -262,9 +316,9 @@ __device__ __forceinline__ void load_tile(char* tile, const ELEM* base, int64_t 
 }
 
 // Clears rows n.. of the slots that this wave's load_tile filled.
-template <int RB>
+template <int RB, int NW>
 __device__ __forceinline__ void clear_tile(char* tile, int n, int w, int lane) {
-  constexpr int kSlots = RB / 16, kInstr = kQ * RB / 1024 / 4;
+  constexpr int kSlots = RB / 16, kInstr = kQ * RB / 1024 / NW;
 #pragma unroll 1
   for (int i = 0; i < kInstr; ++i) {
     const int s = (w * kInstr + i) * 64 + lane;
@@ -273,35 +327,41 @@ __device__ __forceinline__ void clear_tile(char* tile, int n, int w, int lane) {
 }
 
 // The same element by element, for rows that do not move as 16-byte vectors (rows past `last` as zeros).
-template <typename ELEM, int RB>
+template <typename ELEM, int RB, int NW, bool PERM>
 __device__ __forceinline__ void load_tile_scalar(char* tile, const ELEM* base, int64_t step, int last, int cols, int tid) {
   constexpr int kCols = RB / sizeof(ELEM);
-  for (int i = tid; i < kQ * kCols; i += 256) {
+  for (int i = tid; i < kQ * kCols; i += 64 * NW) {
     const int row = i / kCols, col = i % kCols;
     ELEM x = ELEM(0);
     if (row <= last && col < cols) x = base[row * step + col];
-    *reinterpret_cast<ELEM*>(tile + tile_at<RB, sizeof(ELEM) == 4>(row, col * static_cast<int>(sizeof(ELEM)))) = x;
+    const int byte = col * static_cast<int>(sizeof(ELEM));
+    *reinterpret_cast<ELEM*>(tile + row * RB + (byte ^ (swizzle<RB, sizeof(ELEM) == 4, PERM>(row) << 4))) = x;
   }
 }
 
 // STATE_ONLY: the pre-pass, which leaves each segment's own sum (its state after its last
 // token, from zero) in role.seg.  Otherwise the whole of the segment's output.
-template <typename ACT, int KD, int VT, bool VEC, bool STATE_ONLY>
-__global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
+//
+// NW = VD / 16 waves.  Wider waves (32 columns each, 4 waves at VD = 128) halve the LDS reads but hold
+// twice the state, 256 registers: 2 waves a SIMD instead of 4, and the gradient at 8 x 2048 x
+// 32 heads of 128 took 637 us instead of @@.
+template <typename ACT, int KD, int VD, bool VEC, bool STATE_ONLY>
+__global__ __launch_bounds__(4 * VD, sizeof(typename Op<ACT>::elem) == 4 ? 2 : (VD == 128 ? 4 : 3))
+void la_kernel(LaArgs p) {
   using O = Op<ACT>;
   using elem = typename O::elem;
   using piece = typename O::piece;
   constexpr bool kF32 = sizeof(elem) == 4;
-  constexpr int VD = 64 * VT;
+  constexpr int NW = VD / 16;
   constexpr int RK = KD * static_cast<int>(sizeof(elem)), RV = VD * static_cast<int>(sizeof(elem));   // row bytes
   constexpr int RP = kQ * static_cast<int>(sizeof(elem));
   constexpr int KT = KD / 32;                       // pairs of state tiles along K
   constexpr int WT = kF32 ? 1 : 3;                  // operand terms of the decayed v
   constexpr int ET = kF32 ? 1 : 2;                  // operand terms of E and of P
-  __shared__ __attribute__((aligned(16))) char sQ[STATE_ONLY ? 16 : kQ * RK];
-  __shared__ __attribute__((aligned(16))) char sKK[2][kQ * RK];                // k of this chunk and of the next
-  __shared__ __attribute__((aligned(16))) char sV[kQ * RV];
-  __shared__ __attribute__((aligned(16))) char sP[ET][STATE_ONLY ? 16 : kQ * RP];   // P [j][i]
+  __shared__ __attribute__((aligned(512))) char sQ[STATE_ONLY ? 16 : kQ * RK];
+  __shared__ __attribute__((aligned(512))) char sKK[2][kQ * RK];                // k of this chunk and of the next
+  __shared__ __attribute__((aligned(512))) char sV[kQ * RV];
+  __shared__ __attribute__((aligned(512))) char sP[ET][STATE_ONLY ? 16 : kQ * RP];   // P [j][i]
 
   const int tid = threadIdx.x, lane0 = tid & 63, w = uniform_int(tid >> 6);
   // Workgroup ids go round the 8 XCDs: the roles of one (batch row, head, segment), which
@@ -328,7 +388,6 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
   const int c_end = c_stop < nchunks ? c_stop : nchunks;
   const int c_live = c_end < live ? c_end : live;
   const float g2 = decay_log2(p.log_decay, h);
-  const Pair dQ = decay_pair(p.log_decay, h, kQ);
 
   // row r of the sequence is token r forwards, len - 1 - r backwards
   const int64_t t_first = reverse ? len - 1 : 0;
@@ -338,9 +397,53 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
   const elem* vg = static_cast<const elem*>(r.v) + b * r.vs[0] + (h / r.vdiv) * r.vs[2] + t_first * r.vs[1];
   const int64_t qstep = r.qs[1] * t_step, kstep = r.ks[1] * t_step, vstep = r.vs[1] * t_step;
 
+  // Ask for the rows of k, or of q and v, of chunk c.
+  auto load_k = [&](int c, int lane) __attribute__((always_inline)) {
+    const int64_t r0 = static_cast<int64_t>(c) * kQ;
+    const int last = len - 1 - c * kQ < kQ - 1 ? len - 1 - c * kQ : kQ - 1;
+    if constexpr (VEC) load_tile<elem, RK, NW, true>(sKK[c & 1], kg + r0 * kstep, kstep, last, K, w, lane);
+    else load_tile_scalar<elem, RK, NW, true>(sKK[c & 1], kg + r0 * kstep, kstep, last, K, tid);
+  };
+  auto load_qv = [&](int c, int lane) __attribute__((always_inline)) {
+    const int64_t r0 = static_cast<int64_t>(c) * kQ;
+    const int last = len - 1 - c * kQ < kQ - 1 ? len - 1 - c * kQ : kQ - 1;
+    if constexpr (VEC) {
+      if constexpr (!STATE_ONLY) load_tile<elem, RK, NW, false>(sQ, qg + r0 * qstep, qstep, last, K, w, lane);
+      load_tile<elem, RV, NW, false>(sV, vg + r0 * vstep, vstep, last, V, w, lane);
+    } else {
+      if constexpr (!STATE_ONLY) load_tile_scalar<elem, RK, NW, false>(sQ, qg + r0 * qstep, qstep, last, K, tid);
+      load_tile_scalar<elem, RV, NW, false>(sV, vg + r0 * vstep, vstep, last, V, tid);
+    }
+  };
+  // Waits for this wave's part of chunk c's rows (and for its stores of the chunk before).
+  auto arrived = [&](int c, int n, int lane) __attribute__((always_inline)) {
+    if constexpr (VEC) {
+      __builtin_amdgcn_s_waitcnt(0x0f70);           // vmcnt(0); expcnt and lgkmcnt as they are
+      if (n < kQ) {
+        clear_tile<RK, NW>(sKK[c & 1], n, w, lane);
+        if constexpr (!STATE_ONLY) clear_tile<RK, NW>(sQ, n, w, lane);
+        clear_tile<RV, NW>(sV, n, w, lane);
+      }
+    }
+  };
+  auto present = [&](int c) { return len - c * kQ < kQ ? len - c * kQ : kQ; };
+  if constexpr (VEC) {
+    if (K < KD || V < VD) {                         // columns that the loads leave alone
+      clear_tile<RK, NW>(sKK[0], 0, w, lane0);
+      clear_tile<RK, NW>(sKK[1], 0, w, lane0);
+      if constexpr (!STATE_ONLY) clear_tile<RK, NW>(sQ, 0, w, lane0);
+      clear_tile<RV, NW>(sV, 0, w, lane0);
+      __builtin_amdgcn_s_waitcnt(0xc07f);           // lgkmcnt(0): before the loads into the same slots
+    }
+  }
+  if (c_begin < c_live) {
+    load_k(c_begin, lane0);
+    load_qv(c_begin, lane0);
+  }
+
   const int g = lane0 >> 4, c16 = lane0 & 15;
-  // E[vt][t][u][e] is the entry k = 32 t + 8 g + 4 u + e, v = 16 (VT w + vt) + c16
-  f32x4_t E[VT][KT][2];
+  // E[t][u][e] is the entry k = 32 t + 8 g + 4 u + e, v = 16 w + c16
+  f32x4_t E[KT][2];
   const float* src = nullptr;
   if (!STATE_ONLY) {
     if (nseg > 1) src = r.seg + (bh * nseg + seg) * static_cast<int64_t>(K) * V;
@@ -350,213 +453,187 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
   const float lam1 = exp2_hw(g2);
   const bool decayed = nseg > 1 || reverse || len == 0;
 #pragma unroll
-  for (int vt = 0; vt < VT; ++vt)
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int kk = 32 * t + 8 * g + 4 * u + e, vv = 16 * w + c16;
+        float x = 0.0f;
+        if (src) {                                  // (uniform; the loads themselves sit behind no branch)
+          const bool in = kk < K && vv < V;
+          x = src[static_cast<int64_t>(in ? kk : 0) * r.sk + static_cast<int64_t>(in ? vv : 0) * r.sv];
+          x = in ? (decayed ? x : x * lam1) : 0.0f;
+        }
+        E[t][u][e] = x;
+      }
+
+  // The registers hold the state divided by rho = lam^(64 a), a the chunks since the last time
+  // it was multiplied out: a chunk then adds lam^(64 - i) v / rho' instead of decaying
+  // every entry.  Past 2^30 the state is multiplied out, by rho as a float32 pair from
+  // float64, so that no rounding of lam^64 builds up over the thousands of chunks of a head's memory.
+  const double lam_q = uniform_double(decay_power(p.log_decay, h, kQ));
+  const double g2d = uniform_double(static_cast<double>(p.log_decay[h]) * 1.4426950408889634);
+  const float g_q = g2 * kQ;
+  int a = 0;
+  // lam^(64 chunks) to float32 accuracy, |its exponent| up to 2^7
+  auto power_q = [&](int chunks) __attribute__((always_inline)) {
+    if (chunks == 0) return 1.0f;
+    const double x = g2d * (kQ * chunks), whole = __builtin_floor(x);
+    return __builtin_ldexpf(exp2_hw(static_cast<float>(x - whole)), static_cast<int>(whole));
+  };
+  auto multiply_out = [&](double by) __attribute__((always_inline)) {      // by: the decay of the chunk just done
+    double base = lam_q;
+    for (int n = a; n > 0; n >>= 1, base *= base)
+      if (n & 1) by *= base;
+    const Pair d = pair_of(by);
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int kk = 32 * t + 8 * g + 4 * u + e, vv = 16 * (VT * w + vt) + c16;
-          float x = 0.0f;
-          if (src) {                                // (uniform; the loads themselves sit behind no branch)
-            const bool in = kk < K && vv < V;
-            x = src[static_cast<int64_t>(in ? kk : 0) * r.sk + static_cast<int64_t>(in ? vv : 0) * r.sv];
-            x = in ? (decayed ? x : x * lam1) : 0.0f;
-          }
-          E[vt][t][u][e] = x;
-        }
-
-  // E times (1 + chunks * lo / hi) of lam^kQ = hi + lo
-  const float fix = dQ.hi > 0.0f ? dQ.lo / dQ.hi : 0.0f;
-  int since = 0;
-  auto correct = [&](float chunks) __attribute__((always_inline)) {
-    const float f = fix * chunks;
-#pragma unroll
-    for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) E[vt][t][u][e] = __builtin_fmaf(f, E[vt][t][u][e], E[vt][t][u][e]);
+        for (int e = 0; e < 4; ++e) E[t][u][e] = __builtin_fmaf(d.hi, E[t][u][e], d.lo * E[t][u][e]);
+    a = 0;
   };
+  // The last chunk of the sequence (of the segment, in the pre-pass) forwards leaves S, not lam S,
+  // and may hold fewer tokens.
+  const int n_end = uniform_int(c_begin < c_live ? present(c_live - 1) : 0);
+  const int shift = uniform_int((STATE_ONLY || !reverse) && (STATE_ONLY || c_live == live) ? 1 : 0);
+  const double lam_end = uniform_double(decay_power(p.log_decay, h, n_end - shift > 0 ? n_end - shift : 0));
 
   // Decay factors.  lam^(j-i) of P splits into a lane's lam^(j - 32t - 8g - 7) and the uniform
   // lam^(7 - (4u + e)); the first may exceed 1 near the diagonal, so heads that decay by more
   // than 2^16 a token (lam^7 near float32's end) take the exponent of each element instead.
   const bool steep = !(g2 >= -16.0f);
+  constexpr int PT = NW == 8 ? 1 : 2;               // 32-token halves of it that the wave forms
+  const int t_p = NW == 8 ? w >> 2 : 0;             // the first of them
   float pw[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) pw[e] = exp2_hw(g2 * static_cast<float>(7 - e));
+  for (int e = 0; e < 8; ++e) pw[e] = uniform_float(exp2_hw(g2 * static_cast<float>(7 - e)));
   const float io_scale = r.in_scale * r.out_scale;
-  float pl[2], wl[2];
+  float pj[4];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int j = 16 * w + c16;
-    pl[t] = exp2_hw(g2 * static_cast<float>(j - 32 * t - 8 * g - 7)) * io_scale;
-    wl[t] = exp2_hw(g2 * static_cast<float>(kQ - 32 * t - 8 * g - 7)) * r.in_scale;   // (of a whole chunk)
-  }
-  float fj[4];
-#pragma unroll
-  for (int jt = 0; jt < 4; ++jt) fj[jt] = exp2_hw(g2 * static_cast<float>(16 * jt + c16)) * r.out_scale;
+  for (int jt = 0; jt < 4; ++jt) pj[jt] = uniform_float(exp2_hw(g2 * static_cast<float>(16 * jt)));
 
-  // Ask for the rows of k, or of q and v, of chunk c.
-  auto load_k = [&](int c, int lane) __attribute__((always_inline)) {
-    const int64_t r0 = static_cast<int64_t>(c) * kQ;
-    const int last = len - 1 - c * kQ < kQ - 1 ? len - 1 - c * kQ : kQ - 1;
-    if constexpr (VEC) load_tile<elem, RK>(sKK[c & 1], kg + r0 * kstep, kstep, last, K, w, lane);
-    else load_tile_scalar<elem, RK>(sKK[c & 1], kg + r0 * kstep, kstep, last, K, tid);
-  };
-  auto load_qv = [&](int c, int lane) __attribute__((always_inline)) {
-    const int64_t r0 = static_cast<int64_t>(c) * kQ;
-    const int last = len - 1 - c * kQ < kQ - 1 ? len - 1 - c * kQ : kQ - 1;
-    if constexpr (VEC) {
-      if constexpr (!STATE_ONLY) load_tile<elem, RK>(sQ, qg + r0 * qstep, qstep, last, K, w, lane);
-      load_tile<elem, RV>(sV, vg + r0 * vstep, vstep, last, V, w, lane);
-    } else {
-      if constexpr (!STATE_ONLY) load_tile_scalar<elem, RK>(sQ, qg + r0 * qstep, qstep, last, K, tid);
-      load_tile_scalar<elem, RV>(sV, vg + r0 * vstep, vstep, last, V, tid);
-    }
-  };
-  // Waits for this wave's part of chunk c's rows (and for its stores of the chunk before).
-  auto arrived = [&](int c, int n, int lane) __attribute__((always_inline)) {
-    if constexpr (VEC) {
-      __builtin_amdgcn_s_waitcnt(0x0f70);           // vmcnt(0); expcnt and lgkmcnt as they are
-      if (n < kQ) {
-        clear_tile<RK>(sKK[c & 1], n, w, lane);
-        if constexpr (!STATE_ONLY) clear_tile<RK>(sQ, n, w, lane);
-        clear_tile<RV>(sV, n, w, lane);
-      }
-    }
-  };
-  auto present = [&](int c) { return len - c * kQ < kQ ? len - c * kQ : kQ; };
-  if constexpr (VEC) {
-    if (K < KD || V < VD) {                         // columns that the loads leave alone
-      clear_tile<RK>(sKK[0], 0, w, lane0);
-      clear_tile<RK>(sKK[1], 0, w, lane0);
-      if constexpr (!STATE_ONLY) clear_tile<RK>(sQ, 0, w, lane0);
-      clear_tile<RV>(sV, 0, w, lane0);
-      __builtin_amdgcn_s_waitcnt(0xc07f);           // lgkmcnt(0): before the loads into the same slots
-    }
-  }
-
-  if (c_begin < c_live) {
-    load_k(c_begin, lane0);
-    load_qv(c_begin, lane0);
-    arrived(c_begin, present(c_begin), lane0);
-  }
+  if (c_begin < c_live) arrived(c_begin, present(c_begin), lane0);
   for (int c = c_begin; c < c_live; ++c) {
     const int n = present(c);
-    // the last chunk of the sequence (of the segment, in the pre-pass) forwards leaves S, not lam S
-    const int shift = (STATE_ONLY || !reverse) && c + 1 == c_live && (STATE_ONLY || c_live == live) ? 1 : 0;
     // (opaque, so that the chunk's many LDS and memory addresses are formed here from the lane's
     // number: kept in registers over the loop they crowd out the state)
-    int lane = lane0;
+    int lane = lane_id();
     asm volatile("" : "+v"(lane));
     const int g = lane >> 4, c16 = lane & 15;
     barrier_lds();                                  // the tiles of chunk c are complete
-    const char* sK = sKK[c & 1];
+    const uint32_t k_tile = lds_address(sKK[0]) + (c & 1) * (kQ * RK);
+    constexpr int PB = O::kPiece;
+    const uint32_t q_rows = O::template row_part<RK, false>(lds_address(sQ), c16, g);
+    const uint32_t p_rows = O::template row_part<RP, false>(lds_address(sP[0]), c16, g);
     if (c + 1 < c_live) load_k(c + 1, lane);
 
-    // ---- P rows j = 16 w + c16: tiles of k q^T, rows i = 32 t + 8 g + 4 u + e
+    // ---- P row jw: tiles of k q^T, rows i = 32 t + 8 g + 4 u + e
     if constexpr (!STATE_ONLY) {
-      const int j = 16 * w + c16;
       piece qf[KT];
 #pragma unroll
-      for (int x = 0; x < KT; ++x) qf[x] = O::template row<RK>(sQ, j, 32 * x + 8 * g);
+      for (int x = 0; x < KT; ++x) qf[x] = O::row(q_rows + (w & 3) * (16 * RK), 4 * PB * x, 0);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int tt = 0; tt < PT; ++tt) {
+        const int t = tt + t_p;
         float pv[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) pv[e] = 0.0f;
-        if (t == 0 || w >= 2) {                     // the block right of the diagonal is zero
+        if (t == 0 || (w & 3) >= 2) {               // the block right of the diagonal is zero
+          const uint32_t k_rows = O::template row_part<RK, true>(k_tile, 8 * (c16 >> 2) + (c16 & 3), g) + t * (32 * RK);
+          f32x4_t s[2];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
-            const int krow = 32 * t + 8 * (c16 >> 2) + 4 * u + (c16 & 3);
+          for (int u = 0; u < 2; ++u) s[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int x = 0; x < KT; ++x)
-              s = O::mma(O::template row<RK>(sK, krow, 32 * x + 8 * g), qf[x], s);
+          for (int x = 0; x < KT; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int off = j - (32 * t + 8 * g + 4 * u + e);
-              float x = s[e] * (pl[t] * pw[4 * u + e]);
-              if (steep) x = s[e] * (exp2_hw(g2 * static_cast<float>(off > 0 ? off : 0)) * io_scale);
-              pv[4 * u + e] = off >= 0 ? x : 0.0f;
+            for (int u = 0; u < 2; ++u)
+              s[u] = O::mma(O::row(k_rows, (4 * PB * x) ^ (swizzle<RK, kF32, true>(4 * u) << 4), 4 * u * RK), qf[x], s[u]);
+          const int off0 = 16 * (w & 3) + c16 - 32 * t - 8 * g;
+          const float pl = exp2_hw(g2 * static_cast<float>(off0 - 7)) * io_scale;
+          if (__builtin_expect(steep, 0)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int off = off0 - e;
+              pv[e] = s[e / 4][e % 4] * (exp2_hw(g2 * static_cast<float>(off > 0 ? off : 0)) * io_scale);
+              asm volatile("" : "+v"(pv[e]));       // (kept behind the branch)
             }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) pv[e] = s[e / 4][e % 4] * pl * pw[e];
           }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) pv[e] = off0 >= e ? pv[e] : 0.0f;
         }
         piece ps[ET];
         O::template split<ET>(pv, ps);
 #pragma unroll
-        for (int m = 0; m < ET; ++m) O::template put<RP>(sP[m], j, 32 * t + 8 * g, ps[m]);
+        for (int m = 0; m < ET; ++m) O::put((p_rows ^ (4 * PB * t)) + (w & 3) * (16 * RP), 0, m * (kQ * RP), ps[m]);
       }
     }
 
-    // ---- the wave's own columns of v: as they are (for P v) and decayed (for the state)
-    piece vf[VT][2];
+    // ---- the wave's own columns of v
+    piece vf[2];
 #pragma unroll
-    for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) vf[vt][t] = O::template column<RV>(sV, 32 * t, 16 * (VT * w + vt), 4, lane);
+    for (int t = 0; t < 2; ++t)
+      vf[t] = O::template column<RV, false>(O::template column_part<RV, false>(lds_address(sV), 16 * w, 4, lane), 0,
+                                            32 * t * RV);
 
-    // ---- output from the carried state, transposed: acc[vt][jt] = rows v, column j = 16 jt + c16
-    f32x4_t acc[VT][4];
+    // ---- output from the carried state, transposed: acc[jt] = rows v, column j = 16 jt + c16
+    f32x4_t acc[4];
     if constexpr (!STATE_ONLY) {
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-        for (int jt = 0; jt < 4; ++jt) acc[vt][jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int jt = 0; jt < 4; ++jt) acc[jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
-        piece ef[VT][ET];
+        piece ef[ET], q[4];
+        const float x[8] = {E[t][0][0], E[t][0][1], E[t][0][2], E[t][0][3],
+                            E[t][1][0], E[t][1][1], E[t][1][2], E[t][1][3]};
+        O::template split<ET>(x, ef);
 #pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-          const float x[8] = {E[vt][t][0][0], E[vt][t][0][1], E[vt][t][0][2], E[vt][t][0][3],
-                              E[vt][t][1][0], E[vt][t][1][1], E[vt][t][1][2], E[vt][t][1][3]};
-          O::template split<ET>(x, ef[vt]);
-        }
+        for (int jt = 0; jt < 4; ++jt) q[jt] = O::row(q_rows, 4 * PB * t, 16 * jt * RK);
 #pragma unroll
-        for (int jt = 0; jt < 4; ++jt) {
-          const piece q = O::template row<RK>(sQ, 16 * jt + c16, 32 * t + 8 * g);
+        for (int m = 0; m < ET; ++m)
 #pragma unroll
-          for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-            for (int m = 0; m < ET; ++m) acc[vt][jt] = O::mma(ef[vt][m], q, acc[vt][jt]);
-        }
+          for (int jt = 0; jt < 4; ++jt) acc[jt] = O::mma(ef[m], q[jt], acc[jt]);
       }
     }
-
     barrier_lds();                                  // P complete; the tiles of q and v are free
     if (c + 1 < c_live) load_qv(c + 1, lane);
 
     // ---- P v, transposed, on top
     if constexpr (!STATE_ONLY) {
+      const float f0 = exp2_hw(g2 * static_cast<float>(c16)) * (r.out_scale * power_q(a));
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
-        const int j = 16 * jt + c16;
-        piece pf[2][ET];
+        const float f = f0 * pj[jt];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int e = 0; e < 4; ++e) acc[jt][e] *= f;
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        piece pf[4][ET];
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
           for (int m = 0; m < ET; ++m)
-            if (t == 0 || jt >= 2) pf[t][m] = O::template row<RP>(sP[m], j, 32 * t + 8 * g);
+            if (t == 0 || jt >= 2) pf[jt][m] = O::row(p_rows, 4 * PB * t, 16 * jt * RP + m * (kQ * RP));
 #pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-          f32x4_t& a = acc[vt][jt];
+        for (int m = 0; m < ET; ++m)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) a[e] *= fj[jt];
+          for (int jt = 0; jt < 4; ++jt)
+            if (t == 0 || jt >= 2) acc[jt] = O::mma(vf[t], pf[jt][m], acc[jt]);
+      }
+      if (n < kQ) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int m = 0; m < ET; ++m)
-              if (t == 0 || jt >= 2) a = O::mma(vf[vt][t], pf[t][m], a);
-          if (n < kQ && j >= n) a = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        }
+        for (int jt = 0; jt < 4; ++jt)
+          if (16 * jt + c16 >= n) acc[jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
       }
     }
-    // ---- the output rows to memory: lane (g, c) has 4 columns of row 16 jt + c of each tile
+
+    // ---- the output rows to memory: lane (g, c) has 4 columns of row 16 jt + c
     if constexpr (!STATE_ONLY) {
       auto put = [&](auto* out) __attribute__((always_inline)) {
         using OUT = std::remove_pointer_t<decltype(out)>;
@@ -568,15 +645,13 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
         const int r0 = c * kQ;
         if (VEC && V == VD && n == kQ) {
           // uniform addresses of 16 rows, the lane's place among them
-          const uint32_t off = static_cast<uint32_t>((reverse ? 15 - c16 : c16)) * static_cast<uint32_t>(row_stride) +
-                               static_cast<uint32_t>(16 * VT * w + 4 * g);
+          const uint32_t off = static_cast<uint32_t>(reverse ? 15 - c16 : c16) * static_cast<uint32_t>(row_stride) +
+                               static_cast<uint32_t>(16 * w + 4 * g);
 #pragma unroll
           for (int jt = 0; jt < 4; ++jt) {
             const int64_t token = reverse ? len - 16 - (r0 + 16 * jt) : r0 + 16 * jt;
             OUT* rows = out + (b * L + token) * row_stride + static_cast<int64_t>(h) * V;
-#pragma unroll
-            for (int vt = 0; vt < VT; ++vt)
-              *reinterpret_cast<decltype(four(acc[0][0]))*>(rows + off + 16 * vt) = four(acc[vt][jt]);
+            *reinterpret_cast<decltype(four(acc[0]))*>(rows + off) = four(acc[jt]);
           }
           return;
         }
@@ -585,19 +660,16 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
           const int row = r0 + 16 * jt + c16;
           if (row >= L) continue;
           const int64_t token = reverse && row < len ? len - 1 - row : row;
+          const int v0 = 16 * w + 4 * g;
           OUT* o = out + (b * L + token) * row_stride + static_cast<int64_t>(h) * V;
+          if constexpr (VEC) {
+            if (v0 < V) *reinterpret_cast<decltype(four(acc[0]))*>(o + v0) = four(acc[jt]);
+          } else {
 #pragma unroll
-          for (int vt = 0; vt < VT; ++vt) {
-            const int v0 = 16 * (VT * w + vt) + 4 * g;
-            if constexpr (VEC) {
-              if (v0 < V) *reinterpret_cast<decltype(four(acc[0][0]))*>(o + v0) = four(acc[vt][jt]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (v0 + e >= V) continue;
-                if constexpr (sizeof(OUT) == 4) o[v0 + e] = acc[vt][jt][e];
-                else o[v0 + e] = to_bf16(acc[vt][jt][e]);
-              }
+            for (int e = 0; e < 4; ++e) {
+              if (v0 + e >= V) continue;
+              if constexpr (sizeof(OUT) == 4) o[v0 + e] = acc[jt][e];
+              else o[v0 + e] = to_bf16(acc[jt][e]);
             }
           }
         }
@@ -606,63 +678,52 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
       else put(static_cast<uint16_t*>(r.o));
     }
 
-    // ---- the state: E = lam^n E + k^T (lam^(n-i) v)
-    const bool whole = n - shift == kQ;
-    const Pair dn = whole ? dQ : decay_pair(p.log_decay, h, n - shift);
-#pragma unroll
-    for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) E[vt][t][u][e] *= dn.hi;
-    // what the rounding of lam^n to float32 left, for 16 chunks at a time (2^-20 by then)
-    if (whole && ++since == 16) {
-      correct(16.0f);
-      since = 0;
-    }
+    // ---- the state: lam^n E + k^T (lam^(n-i) v)
+    const bool whole = c + 1 < c_live || n - shift == kQ;
+    if (whole && fabsf(g_q * static_cast<float>(a + 1)) < 30.0f) ++a;
+    else multiply_out(whole ? lam_q : lam_end);
+    const float wc = exp2_hw(g2 * static_cast<float>(kQ - 32 - 8 * g - 7)) * (r.in_scale * power_q(-a));
+    const uint32_t k_cols = O::template column_part<RK, true>(k_tile, 0, 8, lane);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       float wgt[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) wgt[e] = wl[t] * pw[e];
+      for (int e = 0; e < 8; ++e) wgt[e] = (t == 0 ? wc * pj[2] : wc) * pw[e];
       if (!whole) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int left = n - shift - (32 * t + 8 * g + e);
           wgt[e] = exp2_hw(g2 * static_cast<float>(left > 0 ? left : 0)) * r.in_scale;
+          asm volatile("" : "+v"(wgt[e]));
         }
       }
-      piece wv[VT][WT];
+      piece wv[WT];
+      float x[8];
+      O::unpack(vf[t], x);
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) {
-        float x[8];
-        O::unpack(vf[vt][t], x);
+      for (int e = 0; e < 8; ++e) x[e] *= wgt[e];
+      O::template split<WT>(x, wv);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= wgt[e];
-        O::template split<WT>(x, wv[vt]);
+      for (int kt = 0; kt < KT; ++kt) {
+        piece kf[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          kf[u] = O::template column<RK, true>(k_cols, (4 * PB * kt) ^ O::half_flip(u), 32 * t * RK + O::half_offset(u));
+#pragma unroll
+        for (int m = 0; m < WT; ++m)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) E[kt][u] = O::mma(kf[u], wv[m], E[kt][u]);
       }
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const piece kf = O::template column<RK>(sK, 32 * t, 32 * kt + 4 * u, 8, lane);
-#pragma unroll
-          for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-            for (int m = 0; m < WT; ++m) E[vt][kt][u] = O::mma(kf, wv[vt][m], E[vt][kt][u]);
-        }
     }
     // (without a next chunk there is nothing to clear)
     arrived(c + 1, c + 1 < c_live ? present(c + 1) : kQ, lane);
   }
-  if (since) correct(static_cast<float>(since));
+  if (a) multiply_out(1.0);
 
   // chunks with no token: zeros
   if constexpr (!STATE_ONLY) {
     for (int64_t c = c_live > c_begin ? c_live : c_begin; c < c_end; ++c) {
-      for (int i = tid; i < kQ * V; i += 256) {
+      for (int i = tid; i < kQ * V; i += 64 * NW) {
         const int64_t token = c * kQ + i / V;
         if (token >= L) break;
         const int64_t o = ((b * L + token) * p.H + h) * V + i % V;
@@ -677,16 +738,14 @@ __global__ __launch_bounds__(256, 2) void la_kernel(LaArgs p) {
   else if (nseg == 1 && r.fin) dst = r.fin + bh * static_cast<int64_t>(K) * V;
   if (dst) {
 #pragma unroll
-    for (int vt = 0; vt < VT; ++vt)
+    for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int t = 0; t < KT; ++t)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int kk = 32 * t + 8 * g + 4 * u + e, vv = 16 * (VT * w + vt) + c16;
-            if (kk < K && vv < V) dst[static_cast<int64_t>(kk) * r.sk + static_cast<int64_t>(vv) * r.sv] = E[vt][t][u][e];
-          }
+        for (int e = 0; e < 4; ++e) {
+          const int kk = 32 * t + 8 * g + 4 * u + e, vv = 16 * w + c16;
+          if (kk < K && vv < V) dst[static_cast<int64_t>(kk) * r.sk + static_cast<int64_t>(vv) * r.sv] = E[t][u][e];
+        }
   }
 }
 
@@ -734,16 +793,16 @@ __global__ __launch_bounds__(256) void la_copy_state_kernel(float* dst, const fl
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) dst[i] = src ? src[i] : 0.0f;
 }
 
-template <typename ACT, int KD, int VT>
+template <typename ACT, int KD, int VD>
 void launch_la_t(const LaArgs& a, bool state_only, hipStream_t s) {
   const int64_t items = (a.batch * a.H * a.nseg + 7) / 8 * 8;
-  const dim3 grid(static_cast<unsigned>(items * a.nroles)), block(256);
+  const dim3 grid(static_cast<unsigned>(items * a.nroles)), block(4 * VD);
   if (a.role[0].vec) {
-    if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VT, true, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((la_kernel<ACT, KD, VT, true, false>), grid, block, 0, s, a);
+    if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VD, true, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((la_kernel<ACT, KD, VD, true, false>), grid, block, 0, s, a);
   } else {
-    if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VT, false, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((la_kernel<ACT, KD, VT, false, false>), grid, block, 0, s, a);
+    if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VD, false, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((la_kernel<ACT, KD, VD, false, false>), grid, block, 0, s, a);
   }
 }
 
@@ -752,10 +811,10 @@ void launch_la_roles(const LaArgs& a, Dt dt, bool state_only, hipStream_t s) {
   const bool k2 = a.role[0].K > 64, v2 = a.role[0].V > 64;
   auto go = [&](auto act) {
     using ACT = decltype(act);
-    if (k2 && v2) launch_la_t<ACT, 128, 2>(a, state_only, s);
-    else if (k2) launch_la_t<ACT, 128, 1>(a, state_only, s);
-    else if (v2) launch_la_t<ACT, 64, 2>(a, state_only, s);
-    else launch_la_t<ACT, 64, 1>(a, state_only, s);
+    if (k2 && v2) launch_la_t<ACT, 128, 128>(a, state_only, s);
+    else if (k2) launch_la_t<ACT, 128, 64>(a, state_only, s);
+    else if (v2) launch_la_t<ACT, 64, 128>(a, state_only, s);
+    else launch_la_t<ACT, 64, 64>(a, state_only, s);
   };
   if (dt == Dt::BF16) go(ActBF16{});
   else go(ActF32{});
