@@ -633,7 +633,48 @@ void la_kernel(LaArgs p) {
       }
     }
 
-    // ---- the output rows to memory: lane (g, c) has 4 columns of row 16 jt + c
+    // ---- the state: lam^n E + k^T (lam^(n-i) v)
+    const bool whole = c + 1 < c_live || n - shift == kQ;
+    if (whole && fabsf(g_q * static_cast<float>(a + 1)) < 30.0f) ++a;
+    else multiply_out(whole ? lam_q : lam_end);
+    const float wc = exp2_hw(g2 * static_cast<float>(kQ - 32 - 8 * g - 7)) * (r.in_scale * power_q(-a));
+    const uint32_t k_cols = O::template column_part<RK, true>(k_tile, 0, 8, lane);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      float wgt[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wgt[e] = (t == 0 ? wc * pj[2] : wc) * pw[e];
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int left = n - shift - (32 * t + 8 * g + e);
+          wgt[e] = exp2_hw(g2 * static_cast<float>(left > 0 ? left : 0)) * r.in_scale;
+          asm volatile("" : "+v"(wgt[e]));
+        }
+      }
+      piece wv[WT];
+      float x[8];
+      O::unpack(vf[t], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= wgt[e];
+      O::template split<WT>(x, wv);
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        piece kf[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          kf[u] = O::template column<RK, true>(k_cols, (4 * PB * kt) ^ O::half_flip(u), 32 * t * RK + O::half_offset(u));
+#pragma unroll
+        for (int m = 0; m < WT; ++m)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) E[kt][u] = O::mma(kf[u], wv[m], E[kt][u]);
+      }
+    }
+    // (without a next chunk there is nothing to clear)
+    arrived(c + 1, c + 1 < c_live ? present(c + 1) : kQ, lane);
+
+    // ---- the output rows to memory: lane (g, c) has 4 columns of row 16 jt + c.  They are issued after
+    // the wait for the next chunk's rows, so that a wait covers only the stores of the chunk before.
     if constexpr (!STATE_ONLY) {
       auto put = [&](auto* out) __attribute__((always_inline)) {
         using OUT = std::remove_pointer_t<decltype(out)>;
@@ -677,46 +718,6 @@ void la_kernel(LaArgs p) {
       if (kF32 || r.o_f32) put(static_cast<float*>(r.o));
       else put(static_cast<uint16_t*>(r.o));
     }
-
-    // ---- the state: lam^n E + k^T (lam^(n-i) v)
-    const bool whole = c + 1 < c_live || n - shift == kQ;
-    if (whole && fabsf(g_q * static_cast<float>(a + 1)) < 30.0f) ++a;
-    else multiply_out(whole ? lam_q : lam_end);
-    const float wc = exp2_hw(g2 * static_cast<float>(kQ - 32 - 8 * g - 7)) * (r.in_scale * power_q(-a));
-    const uint32_t k_cols = O::template column_part<RK, true>(k_tile, 0, 8, lane);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      float wgt[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) wgt[e] = (t == 0 ? wc * pj[2] : wc) * pw[e];
-      if (!whole) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int left = n - shift - (32 * t + 8 * g + e);
-          wgt[e] = exp2_hw(g2 * static_cast<float>(left > 0 ? left : 0)) * r.in_scale;
-          asm volatile("" : "+v"(wgt[e]));
-        }
-      }
-      piece wv[WT];
-      float x[8];
-      O::unpack(vf[t], x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= wgt[e];
-      O::template split<WT>(x, wv);
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        piece kf[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          kf[u] = O::template column<RK, true>(k_cols, (4 * PB * kt) ^ O::half_flip(u), 32 * t * RK + O::half_offset(u));
-#pragma unroll
-        for (int m = 0; m < WT; ++m)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) E[kt][u] = O::mma(kf[u], wv[m], E[kt][u]);
-      }
-    }
-    // (without a next chunk there is nothing to clear)
-    arrived(c + 1, c + 1 < c_live ? present(c + 1) : kQ, lane);
   }
   if (a) multiply_out(1.0);
 
@@ -750,30 +751,42 @@ void la_kernel(LaArgs p) {
 }
 
 // Chains the segments' own sums T_s into the E entering each segment (written over T_s) and
-// the state after the last token.  One thread per state entry.
+// the state after the last token.  A thread takes kChain entries 256 apart, so that the decays
+// (float64 exponentials) are a small part of its work.
+constexpr int kChain = 8;
 __global__ __launch_bounds__(256) void la_chain_kernel(LaArgs p) {
   const LaRole& r = p.role[blockIdx.z];
   const int64_t bh = blockIdx.y;
   const int KV = r.K * r.V;
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= KV) return;
+  const int i0 = blockIdx.x * (256 * kChain) + threadIdx.x;
   const int h = static_cast<int>(bh % p.H);
   const int len = row_length(p, bh / p.H);
   const int seg_tokens = static_cast<int>(p.seg_chunks) * kQ;
   const Pair l1 = decay_pair(p.log_decay, h, 1), lS = decay_pair(p.log_decay, h, seg_tokens);
-  float* slot = r.seg + bh * p.nseg * static_cast<int64_t>(KV) + i;
-  float s = r.carry ? r.carry[bh * static_cast<int64_t>(KV) + i] : 0.0f;
+  float* slot = r.seg + bh * p.nseg * static_cast<int64_t>(KV);
+  const float* carry = r.carry ? r.carry + bh * static_cast<int64_t>(KV) : nullptr;
+  float* fin = r.fin ? r.fin + bh * static_cast<int64_t>(KV) : nullptr;
+  float s[kChain], T[kChain];
+#pragma unroll
+  for (int x = 0; x < kChain; ++x) s[x] = carry && i0 + 256 * x < KV ? carry[i0 + 256 * x] : 0.0f;
   auto times = [](const Pair& d, float x) { return __builtin_fmaf(d.hi, x, d.lo * x); };
   for (int k = 0; k < p.nseg; ++k, slot += KV) {
     const int left = len - k * seg_tokens, n = left < 0 ? 0 : (left < seg_tokens ? left : seg_tokens);
-    const bool last = k + 1 == p.nseg;
-    const float T = last && !r.fin ? 0.0f : *slot;
-    *slot = r.reverse ? s : times(l1, s);
-    if (n == 0) continue;
+    const bool read = n > 0 && (k + 1 < p.nseg || fin);
+#pragma unroll
+    for (int x = 0; x < kChain; ++x) T[x] = read && i0 + 256 * x < KV ? slot[i0 + 256 * x] : 0.0f;
     const Pair d = n == seg_tokens ? lS : decay_pair(p.log_decay, h, n);
-    s = times(d, s) + (r.reverse ? times(l1, T) : T);
+#pragma unroll
+    for (int x = 0; x < kChain; ++x) {
+      if (i0 + 256 * x < KV) slot[i0 + 256 * x] = r.reverse ? s[x] : times(l1, s[x]);
+      if (n > 0) s[x] = times(d, s[x]) + (r.reverse ? times(l1, T[x]) : T[x]);
+    }
   }
-  if (r.fin) r.fin[bh * static_cast<int64_t>(KV) + i] = s;
+  if (fin) {
+#pragma unroll
+    for (int x = 0; x < kChain; ++x)
+      if (i0 + 256 * x < KV) fin[i0 + 256 * x] = s[x];
+  }
 }
 
 template <typename ACT>
@@ -822,12 +835,15 @@ void launch_la_roles(const LaArgs& a, Dt dt, bool state_only, hipStream_t s) {
 
 }  // namespace
 
-// Segments per sequence: enough that the (batch row, head, segment) workgroups fill the chip's
-// 2 a CU, each at least 4 chunks long.  The count is then derived back from the segment length,
-// so that no segment is without a chunk.
-int la_segments(int64_t batch, int64_t L, int64_t H) {
-  const int64_t pairs = batch * H, nch = (L + kQ - 1) / kQ, resident = 512;
-  int64_t s = resident / (pairs > 0 ? pairs : 1);
+// Segments per sequence.  Where every CU gets a workgroup, one: the pre-pass and the chaining that
+// segments need cost more than they gain (the gradient at 8 x 2048, 32 heads of 128, 768
+// workgroups: 415 us with one, 577 with two; 4 x 2048, 80 heads of 64: 145 and 152).  With fewer, 2 workgroups a CU
+// (131072 tokens, 20 heads of 128: 1618 us with 13, 1088 with 25, 1127 with 51), each at least 4 chunks long.  The
+// count is then derived back from the segment length, so that no segment is without a chunk.
+int la_segments(int64_t batch, int64_t L, int64_t H, int roles) {
+  const int64_t workgroups = batch * H * roles, nch = (L + kQ - 1) / kQ;
+  if (workgroups >= 256) return 1;
+  int64_t s = 512 / (workgroups > 0 ? workgroups : 1);
   if (s > nch / 4) s = nch / 4;
   if (s <= 1) return 1;
   const int64_t per = (nch + s - 1) / s;
@@ -863,7 +879,8 @@ hipError_t launch_la(const LaArgs& a, Dt dt, hipStream_t s) {
     run(kStates, n, true);
     LaArgs x = all;
     x.role[1] = all.role[2];
-    const dim3 grid(static_cast<unsigned>((a.role[0].K * a.role[0].V + 255) / 256), static_cast<unsigned>(a.batch * a.H),
+    const dim3 grid(static_cast<unsigned>((a.role[0].K * a.role[0].V + 256 * kChain - 1) / (256 * kChain)),
+                    static_cast<unsigned>(a.batch * a.H),
                     static_cast<unsigned>(n));
     hipLaunchKernelGGL(la_chain_kernel, grid, dim3(256), 0, s, x);
   }

@@ -114,7 +114,7 @@ struct LaPlan {
 
 bool la_plan(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V, int sets, const int64_t* share, LaPlan* p) {
   if (batch == 0 || L == 0 || H == 0) return true;
-  p->nseg = ssm::la_segments(batch, L, H);
+  p->nseg = ssm::la_segments(batch, L, H, sets == 1 ? 1 : 3);
   if (p->nseg > 1 && !bytes_of(4, &p->seg_bytes, batch, H, p->nseg, K, V)) return false;
   p->total = up256(p->seg_bytes) * sets;
   const int64_t width[3] = {K, K, V};

@@ -44,8 +44,8 @@ struct LaArgs {
 
 constexpr int kLaMaxDim = 128;        // largest K and V
 
-// Segments per sequence and the floats of the segment states of one role.
-int la_segments(int64_t batch, int64_t L, int64_t H);
+// Segments per sequence of a call with `roles` roles.
+int la_segments(int64_t batch, int64_t L, int64_t H, int roles);
 hipError_t launch_la(const LaArgs& a, Dt dt, hipStream_t s);
 
 // out[batch][L][heads][d] (act) = sum over the H / heads sharing heads of part[batch][L][H][d].
