@@ -9,29 +9,68 @@ last axis (slices of one projection's output); other tensors are contiguous.
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 from typing import Optional, Tuple
 
 import torch
 
 from . import _lib
-from .ops import _dt, _ptr, _shape, _stream, _workspace
+from .ops import _shape, _workspace
 
 F32 = torch.float32
+BF16 = torch.bfloat16
+_I32 = torch.int32
+_Tensor = torch.Tensor
+
+# The checks of a call run before every launch and are most of a small call's time on the
+# host, so the passing case is a few comparisons; a failing one goes on to say what is wrong.
+
+
+def _dt(dtype) -> int:
+    if dtype is BF16:
+        return _lib.SSM_BF16
+    if dtype is F32:
+        return _lib.SSM_F32
+    raise TypeError(f"activations must be float32 or bfloat16, got {dtype}")
 
 
 def _dims(t, name: str, n: int) -> None:
-    if not isinstance(t, torch.Tensor) or t.dim() != n:
+    if not isinstance(t, _Tensor) or t.dim() != n:
         raise ValueError(f"{name} must be a tensor of {n} dimensions")
 
 
-def _view(t: torch.Tensor, name: str, dtype, device):
-    """(pointer, strides) of a view with a contiguous last axis; strides is a ctypes array
-    of the element strides of the axes before it (None: packed)."""
+def _is(t, name: str, shape) -> None:
+    """_shape for a tuple of ints (None passes)."""
+    if t is not None and (not isinstance(t, _Tensor) or t.shape != shape):
+        _shape(t, name, shape)
+
+
+def _device(t, name: str, device) -> None:
     if not t.is_cuda:
         raise ValueError(f"{name} must live on the GPU")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
+
+
+def _ptr(t, name: str, dtype, device):
+    """Pointer of a contiguous tensor of the given type on the given device (None for None)."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.device != device:
+        _device(t, name, device)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _view(t, name: str, dtype, device):
+    """(pointer, strides) of a view with a contiguous last axis; strides is a ctypes array
+    of the element strides of the axes before it (None: packed)."""
+    if not t.is_cuda or t.device != device:
+        _device(t, name, device)
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.is_contiguous() or t.numel() == 0:
         return t.data_ptr(), None
@@ -40,37 +79,54 @@ def _view(t: torch.Tensor, name: str, dtype, device):
     return t.data_ptr(), (ctypes.c_int64 * (t.dim() - 1))(*t.stride()[:-1])
 
 
-def _attention_shapes(q, k, v, log_decay, lead, L):
-    """Shapes of q, k, v [*lead, heads, width]; returns (H, Hq, Hk, Hv, K, V)."""
-    n = len(lead) + (L is not None) + 2
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _dims(t, name, n)
-    _dims(log_decay, "log_decay", 1)
-    H = log_decay.shape[0]
-    head = tuple(lead) + (() if L is None else (L,))
-    K, V = q.shape[-1], v.shape[-1]
-    _shape(q, "q", head + (q.shape[-2], K))
-    _shape(k, "k", head + (k.shape[-2], K))
-    _shape(v, "v", head + (v.shape[-2], V))
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        if t.shape[-2] < 1 or H % t.shape[-2]:
-            raise ValueError(f"{name} has {t.shape[-2]} heads, which does not divide log_decay's {H}")
-    return H, q.shape[-2], k.shape[-2], v.shape[-2], K, V
+def _run(fn, device, stream, *args) -> None:
+    """Calls fn on `stream` (the device's current one when None), with `device` current."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() != device.index:
+        with torch.cuda.device(device):
+            status = fn(*args, int(stream))
+    else:
+        status = fn(*args, int(stream))
+    if status:
+        _lib.check(status)
 
 
-def linear_attention_workspace_size(batch, L, H, K, V, dtype=torch.bfloat16) -> int:
+@lru_cache(maxsize=None)
+def _entry(name: str):
+    return getattr(_lib.load_library(), name)
+
+
+def _attention_shapes(q, k, v, log_decay, n: int):
+    """Checks q, k, v [..., heads, width] of n dimensions; returns (lead shape, H, Hq, Hk, Hv, K, V)."""
+    if not (isinstance(q, _Tensor) and isinstance(k, _Tensor) and isinstance(v, _Tensor) and
+            isinstance(log_decay, _Tensor) and q.dim() == k.dim() == v.dim() == n and log_decay.dim() == 1):
+        for t, name in ((q, "q"), (k, "k"), (v, "v")):
+            _dims(t, name, n)
+        _dims(log_decay, "log_decay", 1)
+    *lead, Hq, K = q.shape
+    Hk, (Hv, V), H = k.shape[-2], v.shape[-2:], log_decay.shape[0]
+    _is(k, "k", (*lead, Hk, K))
+    _is(v, "v", (*lead, Hv, V))
+    for heads, name in ((Hq, "q"), (Hk, "k"), (Hv, "v")):
+        if heads < 1 or H % heads:
+            raise ValueError(f"{name} has {heads} heads, which does not divide log_decay's {H}")
+    return lead, H, Hq, Hk, Hv, K, V
+
+
+@lru_cache(maxsize=4096)
+def linear_attention_workspace_size(batch, L, H, K, V, dtype=BF16) -> int:
     """Bytes of device workspace linear_attention_fwd needs for this shape (0: none)."""
-    lib = _lib.load_library()
-    dt = _lib.SSM_BF16 if dtype == torch.bfloat16 else _lib.SSM_F32
-    return int(lib.ssm_linear_attention_workspace_size(int(batch), int(L), int(H), int(K), int(V), dt))
+    return int(_entry("ssm_linear_attention_workspace_size")(int(batch), int(L), int(H), int(K), int(V), _dt(dtype)))
 
 
-def linear_attention_bwd_workspace_size(batch, L, H, K, V, dtype=torch.bfloat16, *, Hq=None, Hk=None, Hv=None) -> int:
+@lru_cache(maxsize=4096)
+def linear_attention_bwd_workspace_size(batch, L, H, K, V, dtype=BF16, *, Hq=None, Hk=None, Hv=None) -> int:
     """Bytes of device workspace linear_attention_bwd needs (Hq, Hk, Hv: heads of q, k and v, H when None)."""
-    lib = _lib.load_library()
-    dt = _lib.SSM_BF16 if dtype == torch.bfloat16 else _lib.SSM_F32
-    return int(lib.ssm_linear_attention_bwd_workspace_size(int(batch), int(L), int(H), int(Hq or H), int(Hk or H),
-                                                           int(Hv or H), int(K), int(V), dt))
+    return int(_entry("ssm_linear_attention_bwd_workspace_size")(
+        int(batch), int(L), int(H), int(Hq or H), int(Hk or H), int(Hv or H), int(K), int(V), _dt(dtype)))
 
 
 def linear_attention_fwd(q, k, v, log_decay, scale=None, *, initial_state=None, lengths=None, out=None,
@@ -87,26 +143,25 @@ def linear_attention_fwd(q, k, v, log_decay, scale=None, *, initial_state=None, 
     least linear_attention_workspace_size(...) bytes, or None (allocated here).
     Returns (out [batch, L, H, V], final_state or None).
     """
-    lib = _lib.load_library()
-    _dims(q, "q", 4)
-    batch, L = q.shape[:2]
-    H, Hq, Hk, Hv, K, V = _attention_shapes(q, k, v, log_decay, (batch,), L)
-    _shape(lengths, "lengths", (batch,))
-    _shape(initial_state, "initial_state", (batch, H, K, V))
-    _shape(out, "out", (batch, L, H, V))
-    _shape(final_state, "final_state", (batch, H, K, V))
+    (batch, L), H, Hq, Hk, Hv, K, V = _attention_shapes(q, k, v, log_decay, 4)
+    states = (batch, H, K, V)
+    _is(lengths, "lengths", (batch,))
+    _is(initial_state, "initial_state", states)
+    _is(out, "out", (batch, L, H, V))
+    _is(final_state, "final_state", states)
     act, dev = q.dtype, q.device
-    (qp, qs), (kp, ks), (vp, vs) = (_view(t, n, act, dev) for t, n in ((q, "q"), (k, "k"), (v, "v")))
+    dt = _dt(act)
+    (qp, qs), (kp, ks), (vp, vs) = _view(q, "q", act, dev), _view(k, "k", act, dev), _view(v, "v", act, dev)
     if out is None:
         out = torch.empty((batch, L, H, V), dtype=act, device=dev)
     if final_state is None and return_final_state:
-        final_state = torch.empty((batch, H, K, V), dtype=F32, device=dev)
+        final_state = torch.empty(states, dtype=F32, device=dev)
     ws_ptr, ws_bytes = _workspace(workspace, linear_attention_workspace_size(batch, L, H, K, V, act), dev)
-    _lib.check(lib.ssm_linear_attention_fwd(
-        qp, kp, vp, qs, ks, vs, _ptr(log_decay, "log_decay", F32, dev), float(K ** -0.5 if scale is None else scale),
-        _ptr(lengths, "lengths", torch.int32, dev), _ptr(initial_state, "initial_state", F32, dev),
-        _ptr(out, "out", act, dev), _ptr(final_state, "final_state", F32, dev), batch, L, H, Hq, Hk, Hv, K, V, _dt(q),
-        ws_ptr, ws_bytes, _stream(stream)))
+    _run(_entry("ssm_linear_attention_fwd"), dev, stream,
+         qp, kp, vp, qs, ks, vs, _ptr(log_decay, "log_decay", F32, dev), K ** -0.5 if scale is None else float(scale),
+         _ptr(lengths, "lengths", _I32, dev), _ptr(initial_state, "initial_state", F32, dev),
+         _ptr(out, "out", act, dev), _ptr(final_state, "final_state", F32, dev), batch, L, H, Hq, Hk, Hv, K, V, dt,
+         ws_ptr, ws_bytes)
     return out, final_state
 
 
@@ -121,31 +176,29 @@ def linear_attention_bwd(q, k, v, log_decay, dout, scale=None, *, initial_state=
     `workspace`: a device tensor of at least linear_attention_bwd_workspace_size(...)
     bytes, or None (allocated here); `out` may hold preallocated outputs under the same keys.
     """
-    lib = _lib.load_library()
-    _dims(q, "q", 4)
-    batch, L = q.shape[:2]
-    H, Hq, Hk, Hv, K, V = _attention_shapes(q, k, v, log_decay, (batch,), L)
-    _shape(dout, "dout", (batch, L, H, V))
-    if not isinstance(dout, torch.Tensor):
+    (batch, L), H, Hq, Hk, Hv, K, V = _attention_shapes(q, k, v, log_decay, 4)
+    states = (batch, H, K, V)
+    if not isinstance(dout, _Tensor):
         raise TypeError("dout must be a torch.Tensor")
-    _shape(lengths, "lengths", (batch,))
-    _shape(initial_state, "initial_state", (batch, H, K, V))
-    _shape(dfinal_state, "dfinal_state", (batch, H, K, V))
+    _is(dout, "dout", (batch, L, H, V))
+    _is(lengths, "lengths", (batch,))
+    _is(initial_state, "initial_state", states)
+    _is(dfinal_state, "dfinal_state", states)
     act, dev = q.dtype, q.device
+    dt = _dt(act)
     (qp, qs), (kp, ks), (vp, vs), (dp, ds) = (
         _view(t, n, act, dev) for t, n in ((q, "q"), (k, "k"), (v, "v"), (dout, "dout")))
     want = initial_state is not None if want_dinitial_state is None else want_dinitial_state
     g = _outputs(out, dev, {"dq": ((batch, L, Hq, K), act, True), "dk": ((batch, L, Hk, K), act, True),
-                            "dv": ((batch, L, Hv, V), act, True), "dinitial_state": ((batch, H, K, V), F32, want)})
+                            "dv": ((batch, L, Hv, V), act, True), "dinitial_state": (states, F32, want)})
     ws_ptr, ws_bytes = _workspace(
         workspace, linear_attention_bwd_workspace_size(batch, L, H, K, V, act, Hq=Hq, Hk=Hk, Hv=Hv), dev)
-    _lib.check(lib.ssm_linear_attention_bwd(
-        qp, kp, vp, dp, qs, ks, vs, ds, _ptr(log_decay, "log_decay", F32, dev),
-        float(K ** -0.5 if scale is None else scale), _ptr(lengths, "lengths", torch.int32, dev),
-        _ptr(initial_state, "initial_state", F32, dev), _ptr(dfinal_state, "dfinal_state", F32, dev),
-        _ptr(g["dq"], "dq", act, dev), _ptr(g["dk"], "dk", act, dev), _ptr(g["dv"], "dv", act, dev),
-        _ptr(g["dinitial_state"], "dinitial_state", F32, dev), batch, L, H, Hq, Hk, Hv, K, V, _dt(q),
-        ws_ptr, ws_bytes, _stream(stream)))
+    _run(_entry("ssm_linear_attention_bwd"), dev, stream,
+         qp, kp, vp, dp, qs, ks, vs, ds, _ptr(log_decay, "log_decay", F32, dev),
+         K ** -0.5 if scale is None else float(scale), _ptr(lengths, "lengths", _I32, dev),
+         _ptr(initial_state, "initial_state", F32, dev), _ptr(dfinal_state, "dfinal_state", F32, dev),
+         _ptr(g["dq"], "dq", act, dev), _ptr(g["dk"], "dk", act, dev), _ptr(g["dv"], "dv", act, dev),
+         _ptr(g["dinitial_state"], "dinitial_state", F32, dev), batch, L, H, Hq, Hk, Hv, K, V, dt, ws_ptr, ws_bytes)
     return g
 
 
@@ -159,28 +212,25 @@ def linear_attention_step(state, q_t, k_t, v_t, log_decay, scale=None, *, slots=
     is outside [0, states) is idle (output 0, no state touched).  No two rows may name one
     slot.  None: row b's state is number b.
     """
-    lib = _lib.load_library()
+    (batch,), H, Hq, Hk, Hv, K, V = _attention_shapes(q_t, k_t, v_t, log_decay, 3)
     _dims(state, "state", 4)
-    _dims(q_t, "q_t", 3)
-    batch, states = q_t.shape[0], state.shape[0]
-    H, Hq, Hk, Hv, K, V = _attention_shapes(q_t, k_t, v_t, log_decay, (batch,), None)
-    _shape(state, "state", (states, H, K, V))
-    _shape(slots, "slots", (batch,))
-    _shape(out_state, "out_state", (states, H, K, V))
-    _shape(out, "out", (batch, H, V))
+    states = state.shape[0]
+    _is(state, "state", (states, H, K, V))
+    _is(slots, "slots", (batch,))
+    _is(out_state, "out_state", state.shape)
+    _is(out, "out", (batch, H, V))
     if slots is None and states < batch:
         raise ValueError(f"{batch} rows need as many states, got {states}")
     act, dev = q_t.dtype, state.device
-    (qp, qs), (kp, ks), (vp, vs) = (_view(t, n, act, dev) for t, n in ((q_t, "q_t"), (k_t, "k_t"), (v_t, "v_t")))
-    if out_state is None:
-        out_state = state
+    dt = _dt(act)
+    (qp, qs), (kp, ks), (vp, vs) = _view(q_t, "q_t", act, dev), _view(k_t, "k_t", act, dev), _view(v_t, "v_t", act, dev)
+    state_ptr = _ptr(state, "state", F32, dev)
     if out is None:
         out = torch.empty((batch, H, V), dtype=act, device=dev)
-    _lib.check(lib.ssm_linear_attention_step(
-        _ptr(state, "state", F32, dev), _ptr(out_state, "out_state", F32, dev), qp, kp, vp, qs, ks, vs,
-        _ptr(log_decay, "log_decay", F32, dev), float(K ** -0.5 if scale is None else scale),
-        _ptr(slots, "slots", torch.int32, dev), _ptr(out, "out", act, dev), batch, states, H, Hq, Hk, Hv, K, V,
-        _dt(q_t), _stream(stream)))
+    _run(_entry("ssm_linear_attention_step"), dev, stream,
+         state_ptr, state_ptr if out_state is None else _ptr(out_state, "out_state", F32, dev), qp, kp, vp, qs, ks, vs,
+         _ptr(log_decay, "log_decay", F32, dev), K ** -0.5 if scale is None else float(scale),
+         _ptr(slots, "slots", _I32, dev), _ptr(out, "out", act, dev), batch, states, H, Hq, Hk, Hv, K, V, dt)
     return out
 
 
@@ -190,7 +240,7 @@ def _outputs(given, dev, spec) -> dict:
     for name, (shape, dtype, computed) in spec.items():
         t = (given or {}).get(name)
         if t is not None and computed:
-            _shape(t, f"out[{name!r}]", shape)
+            _is(t, f"out[{name!r}]", tuple(shape))
             if t.dtype != dtype:
                 raise TypeError(f"out[{name!r}] must be {dtype}")
             got[name] = t
@@ -218,33 +268,31 @@ def _rows(t, name: str, D: int):
 
 
 def _norm_inputs(x, gate, post_weight, res_scale, pre_weight, groups):
-    """Checked (rows shape, D, residual-independent pointers) of a block norm's inputs."""
-    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+    """Checks a block norm's inputs; returns (rows, D, device)."""
+    if not isinstance(x, _Tensor) or x.dim() < 1:
         raise ValueError("expected x [..., D]")
     D = x.shape[-1]
-    for t, name in ((post_weight, "post_weight"), (res_scale, "res_scale"), (pre_weight, "pre_weight")):
-        _shape(t, name, (D,))
-    _shape(gate, "gate", x.shape)
+    _is(post_weight, "post_weight", (D,))
+    _is(res_scale, "res_scale", (D,))
+    _is(pre_weight, "pre_weight", (D,))
+    _is(gate, "gate", x.shape)
     if int(groups) < 1 or D % int(groups):
         raise ValueError(f"groups ({groups}) must divide D ({D})")
     dev = x.device
-    for t, name in ((x, "x"), (gate, "gate")):
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must live on the GPU")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
-        if t.dtype != x.dtype:
-            raise TypeError(f"{name} must be {x.dtype}, got {t.dtype}")
+    if not x.is_cuda:
+        raise ValueError("x must live on the GPU")
+    if gate is not None:
+        _device(gate, "gate", dev)
+        if gate.dtype != x.dtype:
+            raise TypeError(f"gate must be {x.dtype}, got {gate.dtype}")
     return x.numel() // D if D else 0, D, dev
 
 
 def _residual_dtype(dtype, x) -> Tuple[torch.dtype, int]:
     dtype = x.dtype if dtype is None else dtype
-    if dtype not in (F32, x.dtype):
+    if dtype is not F32 and dtype is not x.dtype:
         raise TypeError(f"the residual stream must be float32 or {x.dtype}, got {dtype}")
-    return dtype, _lib.SSM_F32 if dtype == F32 else _lib.SSM_BF16
+    return dtype, _dt(dtype)
 
 
 def block_norm_fwd(x, residual=None, gate=None, post_weight=None, res_scale=None, pre_weight=None, *, groups=1,
@@ -262,31 +310,33 @@ def block_norm_fwd(x, residual=None, gate=None, post_weight=None, res_scale=None
     residual (updated in place).  Returns (h, y): h None when return_h is False and no h is
     given, y None without pre_weight.
     """
-    lib = _lib.load_library()
+    shape = x.shape if isinstance(x, _Tensor) else None
+    _is(residual, "residual", shape)
+    _is(h, "h", shape)
+    _is(y, "y", shape)
     rows, D, dev = _norm_inputs(x, gate, post_weight, res_scale, pre_weight, groups)
-    _shape(residual, "residual", x.shape)
-    _shape(h, "h", x.shape)
-    _shape(y, "y", x.shape)
     if residual_dtype is None and (residual is not None or h is not None):
         residual_dtype = (residual if residual is not None else h).dtype
     rdtype, rdt = _residual_dtype(residual_dtype, x)
     if pre_weight is None and y is not None:
         raise ValueError("y is computed only with pre_weight")
     if h is None and (return_h or pre_weight is None):
-        h = torch.empty(x.shape, dtype=rdtype, device=dev)
+        h = torch.empty(shape, dtype=rdtype, device=dev)
     if y is None and pre_weight is not None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        y = torch.empty(shape, dtype=x.dtype, device=dev)
     (xp, xs), (gp, gs) = _rows(x, "x", D), _rows(gate, "gate", D)
-    _lib.check(lib.ssm_block_norm_fwd(
-        xp, xs, _ptr(residual, "residual", rdtype, dev), gp, gs, _ptr(post_weight, "post_weight", F32, dev),
-        _ptr(res_scale, "res_scale", F32, dev), _ptr(pre_weight, "pre_weight", F32, dev), _ptr(h, "h", rdtype, dev),
-        _ptr(y, "y", x.dtype, dev), rows, D, int(groups), float(eps), _dt(x), rdt, _stream(stream)))
+    act = x.dtype
+    _run(_entry("ssm_block_norm_fwd"), dev, stream,
+         xp, xs, _ptr(residual, "residual", rdtype, dev), gp, gs, _ptr(post_weight, "post_weight", F32, dev),
+         _ptr(res_scale, "res_scale", F32, dev), _ptr(pre_weight, "pre_weight", F32, dev), _ptr(h, "h", rdtype, dev),
+         _ptr(y, "y", act, dev), rows, D, int(groups), float(eps), _dt(act), rdt)
     return h, y
 
 
+@lru_cache(maxsize=4096)
 def block_norm_bwd_workspace_size(rows, D) -> int:
     """Bytes of device workspace block_norm_bwd needs."""
-    return int(_lib.load_library().ssm_block_norm_bwd_workspace_size(int(rows), int(D)))
+    return int(_entry("ssm_block_norm_bwd_workspace_size")(int(rows), int(D)))
 
 
 def block_norm_bwd(x, h=None, dy=None, dh=None, gate=None, post_weight=None, res_scale=None, pre_weight=None, *,
@@ -299,10 +349,11 @@ def block_norm_bwd(x, h=None, dy=None, dh=None, gate=None, post_weight=None, res
     computed), else None.  Returns a dict with dx, dgate, dresidual, dpost_weight, dres_scale
     and dpre_weight (None where the input is absent).  out["dresidual"] may be dh itself.
     """
-    lib = _lib.load_library()
+    shape = x.shape if isinstance(x, _Tensor) else None
+    _is(h, "h", shape)
+    _is(dy, "dy", shape)
+    _is(dh, "dh", shape)
     rows, D, dev = _norm_inputs(x, gate, post_weight, res_scale, pre_weight, groups)
-    for t, name in ((h, "h"), (dy, "dy"), (dh, "dh")):
-        _shape(t, name, x.shape)
     if (pre_weight is None) != (dy is None):
         raise ValueError("dy is given exactly when pre_weight is")
     if pre_weight is not None and h is None:
@@ -319,11 +370,11 @@ def block_norm_bwd(x, h=None, dy=None, dh=None, gate=None, post_weight=None, res
     ws_ptr, ws_bytes = _workspace(workspace, block_norm_bwd_workspace_size(rows, D), dev)
     (xp, xs), (gp, gs) = _rows(x, "x", D), _rows(gate, "gate", D)
     act = x.dtype
-    _lib.check(lib.ssm_block_norm_bwd(
-        xp, xs, _ptr(h, "h", rdtype, dev), _ptr(dy, "dy", act, dev), _ptr(dh, "dh", rdtype, dev), gp, gs,
-        _ptr(post_weight, "post_weight", F32, dev), _ptr(res_scale, "res_scale", F32, dev),
-        _ptr(pre_weight, "pre_weight", F32, dev), _ptr(g["dx"], "dx", act, dev), _ptr(g["dgate"], "dgate", act, dev),
-        _ptr(g["dresidual"], "dresidual", rdtype, dev), _ptr(g["dpost_weight"], "dpost_weight", F32, dev),
-        _ptr(g["dres_scale"], "dres_scale", F32, dev), _ptr(g["dpre_weight"], "dpre_weight", F32, dev),
-        rows, D, int(groups), float(eps), _dt(x), rdt, ws_ptr, ws_bytes, _stream(stream)))
+    _run(_entry("ssm_block_norm_bwd"), dev, stream,
+         xp, xs, _ptr(h, "h", rdtype, dev), _ptr(dy, "dy", act, dev), _ptr(dh, "dh", rdtype, dev), gp, gs,
+         _ptr(post_weight, "post_weight", F32, dev), _ptr(res_scale, "res_scale", F32, dev),
+         _ptr(pre_weight, "pre_weight", F32, dev), _ptr(g["dx"], "dx", act, dev), _ptr(g["dgate"], "dgate", act, dev),
+         _ptr(g["dresidual"], "dresidual", rdtype, dev), _ptr(g["dpost_weight"], "dpost_weight", F32, dev),
+         _ptr(g["dres_scale"], "dres_scale", F32, dev), _ptr(g["dpre_weight"], "dpre_weight", F32, dev),
+         rows, D, int(groups), float(eps), _dt(act), rdt, ws_ptr, ws_bytes)
     return g
