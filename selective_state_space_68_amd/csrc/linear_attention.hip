@@ -12,8 +12,8 @@
 // sequence is token n_tokens - 1 - r, and E before the first row is the gradient of the
 // final state.
 //
-// One workgroup walks the chunks of one (batch row, head, segment).  Wave w owns columns
-// v in [16 w, 16 w + 16) of E and of the output, so E is used as a matrix
+// One workgroup walks the chunks of one (batch row, head, segment).  A wave owns 16 or 32
+// columns v of E and of the output, so E is used as a matrix
 // operand straight from the registers that accumulate it: a product leaves lane (g, c) of a
 // 16 x 16 tile four consecutive rows of column c, and since the order of a product's
 // summation index is free, the rows of each tile are assigned (kperm below) so that the
@@ -342,17 +342,20 @@ __device__ __forceinline__ void load_tile_scalar(char* tile, const ELEM* base, i
 // STATE_ONLY: the pre-pass, which leaves each segment's own sum (its state after its last
 // token, from zero) in role.seg.  Otherwise the whole of the segment's output.
 //
-// NW = VD / 16 waves.  Wider waves (32 columns each, 4 waves at VD = 128) halve the LDS reads but hold
-// twice the state, 256 registers: 2 waves a SIMD instead of 4, and the gradient at 8 x 2048 x
-// 32 heads of 128 took 637 us instead of @@.
+// A wave owns 16 VT columns.  VT = 2 at bfloat16, V > 64: half the waves, each LDS read and
+// address used for two columns' tiles, at 256 registers and 2 waves a SIMD (@@).
+template <typename ACT, int VD>
+constexpr int kColumnTiles = sizeof(typename Op<ACT>::elem) == 2 && VD == 128 ? 2 : 1;
+
 template <typename ACT, int KD, int VD, bool VEC, bool STATE_ONLY>
-__global__ __launch_bounds__(4 * VD, sizeof(typename Op<ACT>::elem) == 4 ? 2 : (VD == 128 ? 4 : 3))
+__global__ __launch_bounds__((4 * VD / kColumnTiles<ACT, VD>), VD == 128 || sizeof(typename Op<ACT>::elem) == 4 ? 2 : 3)
 void la_kernel(LaArgs p) {
+  constexpr int VT = kColumnTiles<ACT, VD>;
   using O = Op<ACT>;
   using elem = typename O::elem;
   using piece = typename O::piece;
   constexpr bool kF32 = sizeof(elem) == 4;
-  constexpr int NW = VD / 16;
+  constexpr int NW = VD / 16 / VT;
   constexpr int RK = KD * static_cast<int>(sizeof(elem)), RV = VD * static_cast<int>(sizeof(elem));   // row bytes
   constexpr int RP = kQ * static_cast<int>(sizeof(elem));
   constexpr int KT = KD / 32;                       // pairs of state tiles along K
@@ -442,8 +445,8 @@ void la_kernel(LaArgs p) {
   }
 
   const int g = lane0 >> 4, c16 = lane0 & 15;
-  // E[t][u][e] is the entry k = 32 t + 8 g + 4 u + e, v = 16 w + c16
-  f32x4_t E[KT][2];
+  // E[vt][t][u][e] is the entry k = 32 t + 8 g + 4 u + e, v = 16 (VT w + vt) + c16
+  f32x4_t E[VT][KT][2];
   const float* src = nullptr;
   if (!STATE_ONLY) {
     if (nseg > 1) src = r.seg + (bh * nseg + seg) * static_cast<int64_t>(K) * V;
@@ -453,20 +456,22 @@ void la_kernel(LaArgs p) {
   const float lam1 = exp2_hw(g2);
   const bool decayed = nseg > 1 || reverse || len == 0;
 #pragma unroll
-  for (int t = 0; t < KT; ++t)
+  for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int kk = 32 * t + 8 * g + 4 * u + e, vv = 16 * w + c16;
-        float x = 0.0f;
-        if (src) {                                  // (uniform; the loads themselves sit behind no branch)
-          const bool in = kk < K && vv < V;
-          x = src[static_cast<int64_t>(in ? kk : 0) * r.sk + static_cast<int64_t>(in ? vv : 0) * r.sv];
-          x = in ? (decayed ? x : x * lam1) : 0.0f;
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int kk = 32 * t + 8 * g + 4 * u + e, vv = 16 * (VT * w + vt) + c16;
+          float x = 0.0f;
+          if (src) {                                // (uniform; the loads themselves sit behind no branch)
+            const bool in = kk < K && vv < V;
+            x = src[static_cast<int64_t>(in ? kk : 0) * r.sk + static_cast<int64_t>(in ? vv : 0) * r.sv];
+            x = in ? (decayed ? x : x * lam1) : 0.0f;
+          }
+          E[vt][t][u][e] = x;
         }
-        E[t][u][e] = x;
-      }
 
   // The registers hold the state divided by rho = lam^(64 a), a the chunks since the last time
   // it was multiplied out: a chunk then adds lam^(64 - i) v / rho' instead of decaying
@@ -488,11 +493,13 @@ void la_kernel(LaArgs p) {
       if (n & 1) by *= base;
     const Pair d = pair_of(by);
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+    for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) E[t][u][e] = __builtin_fmaf(d.hi, E[t][u][e], d.lo * E[t][u][e]);
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) E[vt][t][u][e] = __builtin_fmaf(d.hi, E[vt][t][u][e], d.lo * E[vt][t][u][e]);
     a = 0;
   };
   // The last chunk of the sequence (of the segment, in the pre-pass) forwards leaves S, not lam S,
@@ -575,29 +582,37 @@ void la_kernel(LaArgs p) {
     }
 
     // ---- the wave's own columns of v
-    piece vf[2];
+    piece vf[VT][2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-      vf[t] = O::template column<RV, false>(O::template column_part<RV, false>(lds_address(sV), 16 * w, 4, lane), 0,
-                                            32 * t * RV);
+    for (int vt = 0; vt < VT; ++vt) {
+      const uint32_t v_cols = O::template column_part<RV, false>(lds_address(sV), 16 * (VT * w + vt), 4, lane);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) vf[vt][t] = O::template column<RV, false>(v_cols, 0, 32 * t * RV);
+    }
 
-    // ---- output from the carried state, transposed: acc[jt] = rows v, column j = 16 jt + c16
-    f32x4_t acc[4];
+    // ---- output from the carried state, transposed: acc[vt][jt] = rows v, column j = 16 jt + c16
+    f32x4_t acc[VT][4];
     if constexpr (!STATE_ONLY) {
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt) acc[jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt) acc[vt][jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
-        piece ef[ET], q[4];
-        const float x[8] = {E[t][0][0], E[t][0][1], E[t][0][2], E[t][0][3],
-                            E[t][1][0], E[t][1][1], E[t][1][2], E[t][1][3]};
-        O::template split<ET>(x, ef);
+        piece q[4];
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) q[jt] = O::row(q_rows, 4 * PB * t, 16 * jt * RK);
 #pragma unroll
-        for (int m = 0; m < ET; ++m)
+        for (int vt = 0; vt < VT; ++vt) {
+          piece ef[ET];
+          const float x[8] = {E[vt][t][0][0], E[vt][t][0][1], E[vt][t][0][2], E[vt][t][0][3],
+                              E[vt][t][1][0], E[vt][t][1][1], E[vt][t][1][2], E[vt][t][1][3]};
+          O::template split<ET>(x, ef);
 #pragma unroll
-          for (int jt = 0; jt < 4; ++jt) acc[jt] = O::mma(ef[m], q[jt], acc[jt]);
+          for (int m = 0; m < ET; ++m)
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt) acc[vt][jt] = O::mma(ef[m], q[jt], acc[vt][jt]);
+        }
       }
     }
     barrier_lds();                                  // P complete; the tiles of q and v are free
@@ -610,7 +625,9 @@ void la_kernel(LaArgs p) {
       for (int jt = 0; jt < 4; ++jt) {
         const float f = f0 * pj[jt];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[jt][e] *= f;
+        for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[vt][jt][e] *= f;
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -623,13 +640,18 @@ void la_kernel(LaArgs p) {
 #pragma unroll
         for (int m = 0; m < ET; ++m)
 #pragma unroll
-          for (int jt = 0; jt < 4; ++jt)
-            if (t == 0 || jt >= 2) acc[jt] = O::mma(vf[t], pf[jt][m], acc[jt]);
+          for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt)
+              if (t == 0 || jt >= 2) acc[vt][jt] = O::mma(vf[vt][t], pf[jt][m], acc[vt][jt]);
       }
       if (n < kQ) {
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt)
-          if (16 * jt + c16 >= n) acc[jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+          if (16 * jt + c16 >= n) {
+#pragma unroll
+            for (int vt = 0; vt < VT; ++vt) acc[vt][jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+          }
       }
     }
 
@@ -652,12 +674,15 @@ void la_kernel(LaArgs p) {
           asm volatile("" : "+v"(wgt[e]));
         }
       }
-      piece wv[WT];
-      float x[8];
-      O::unpack(vf[t], x);
+      piece wv[VT][WT];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= wgt[e];
-      O::template split<WT>(x, wv);
+      for (int vt = 0; vt < VT; ++vt) {
+        float x[8];
+        O::unpack(vf[vt][t], x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= wgt[e];
+        O::template split<WT>(x, wv[vt]);
+      }
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         piece kf[2];
@@ -667,7 +692,9 @@ void la_kernel(LaArgs p) {
 #pragma unroll
         for (int m = 0; m < WT; ++m)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) E[kt][u] = O::mma(kf[u], wv[m], E[kt][u]);
+          for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) E[vt][kt][u] = O::mma(kf[u], wv[vt][m], E[vt][kt][u]);
       }
     }
     // (without a next chunk there is nothing to clear)
@@ -687,12 +714,14 @@ void la_kernel(LaArgs p) {
         if (VEC && V == VD && n == kQ) {
           // uniform addresses of 16 rows, the lane's place among them
           const uint32_t off = static_cast<uint32_t>(reverse ? 15 - c16 : c16) * static_cast<uint32_t>(row_stride) +
-                               static_cast<uint32_t>(16 * w + 4 * g);
+                               static_cast<uint32_t>(16 * VT * w + 4 * g);
 #pragma unroll
           for (int jt = 0; jt < 4; ++jt) {
             const int64_t token = reverse ? len - 16 - (r0 + 16 * jt) : r0 + 16 * jt;
             OUT* rows = out + (b * L + token) * row_stride + static_cast<int64_t>(h) * V;
-            *reinterpret_cast<decltype(four(acc[0]))*>(rows + off) = four(acc[jt]);
+#pragma unroll
+            for (int vt = 0; vt < VT; ++vt)
+              *reinterpret_cast<decltype(four(acc[0][0]))*>(rows + off + 16 * vt) = four(acc[vt][jt]);
           }
           return;
         }
@@ -701,16 +730,19 @@ void la_kernel(LaArgs p) {
           const int row = r0 + 16 * jt + c16;
           if (row >= L) continue;
           const int64_t token = reverse && row < len ? len - 1 - row : row;
-          const int v0 = 16 * w + 4 * g;
           OUT* o = out + (b * L + token) * row_stride + static_cast<int64_t>(h) * V;
-          if constexpr (VEC) {
-            if (v0 < V) *reinterpret_cast<decltype(four(acc[0]))*>(o + v0) = four(acc[jt]);
-          } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (v0 + e >= V) continue;
-              if constexpr (sizeof(OUT) == 4) o[v0 + e] = acc[jt][e];
-              else o[v0 + e] = to_bf16(acc[jt][e]);
+          for (int vt = 0; vt < VT; ++vt) {
+            const int v0 = 16 * (VT * w + vt) + 4 * g;
+            if constexpr (VEC) {
+              if (v0 < V) *reinterpret_cast<decltype(four(acc[0][0]))*>(o + v0) = four(acc[vt][jt]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (v0 + e >= V) continue;
+                if constexpr (sizeof(OUT) == 4) o[v0 + e] = acc[vt][jt][e];
+                else o[v0 + e] = to_bf16(acc[vt][jt][e]);
+              }
             }
           }
         }
@@ -739,14 +771,16 @@ void la_kernel(LaArgs p) {
   else if (nseg == 1 && r.fin) dst = r.fin + bh * static_cast<int64_t>(K) * V;
   if (dst) {
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+    for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int kk = 32 * t + 8 * g + 4 * u + e, vv = 16 * w + c16;
-          if (kk < K && vv < V) dst[static_cast<int64_t>(kk) * r.sk + static_cast<int64_t>(vv) * r.sv] = E[t][u][e];
-        }
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int kk = 32 * t + 8 * g + 4 * u + e, vv = 16 * (VT * w + vt) + c16;
+            if (kk < K && vv < V) dst[static_cast<int64_t>(kk) * r.sk + static_cast<int64_t>(vv) * r.sv] = E[vt][t][u][e];
+          }
   }
 }
 
@@ -809,7 +843,7 @@ __global__ __launch_bounds__(256) void la_copy_state_kernel(float* dst, const fl
 template <typename ACT, int KD, int VD>
 void launch_la_t(const LaArgs& a, bool state_only, hipStream_t s) {
   const int64_t items = (a.batch * a.H * a.nseg + 7) / 8 * 8;
-  const dim3 grid(static_cast<unsigned>(items * a.nroles)), block(4 * VD);
+  const dim3 grid(static_cast<unsigned>(items * a.nroles)), block(4 * VD / kColumnTiles<ACT, VD>);
   if (a.role[0].vec) {
     if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VD, true, true>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((la_kernel<ACT, KD, VD, true, false>), grid, block, 0, s, a);
