@@ -713,15 +713,23 @@ void la_kernel(LaArgs p) {
         const int r0 = c * kQ;
         if (VEC && V == VD && n == kQ) {
           // uniform addresses of 16 rows, the lane's place among them
-          const uint32_t off = static_cast<uint32_t>(reverse ? 15 - c16 : c16) * static_cast<uint32_t>(row_stride) +
-                               static_cast<uint32_t>(16 * VT * w + 4 * g);
+          const uint32_t off = static_cast<uint32_t>(reverse ? 15 - c16 : c16) * static_cast<uint32_t>(row_stride);
 #pragma unroll
           for (int jt = 0; jt < 4; ++jt) {
             const int64_t token = reverse ? len - 16 - (r0 + 16 * jt) : r0 + 16 * jt;
-            OUT* rows = out + (b * L + token) * row_stride + static_cast<int64_t>(h) * V;
+            OUT* rows = out + (b * L + token) * row_stride + static_cast<int64_t>(h) * V + 16 * VT * w;
+            if constexpr (VT == 2 && sizeof(OUT) == 2) {
+              // lane groups 2x and 2x + 1 exchange halves: 8 columns a lane, 64 bytes of a row an instruction
+              const uint2 a0 = four(acc[0][jt]), a1 = four(acc[1][jt]);
+              const auto lo = __builtin_amdgcn_permlane16_swap(a0.x, a1.x, false, false);
+              const auto hi = __builtin_amdgcn_permlane16_swap(a0.y, a1.y, false, false);
+              const uint32_t col = (g & 1) * 16 + (g >> 1) * 8;
+              *reinterpret_cast<uint4*>(rows + (off + col)) = make_uint4(lo[0], hi[0], lo[1], hi[1]);
+            } else {
 #pragma unroll
-            for (int vt = 0; vt < VT; ++vt)
-              *reinterpret_cast<decltype(four(acc[0][0]))*>(rows + off + 16 * vt) = four(acc[vt][jt]);
+              for (int vt = 0; vt < VT; ++vt)
+                *reinterpret_cast<decltype(four(acc[0][0]))*>(rows + (off + 4 * g + 16 * vt)) = four(acc[vt][jt]);
+            }
           }
           return;
         }
