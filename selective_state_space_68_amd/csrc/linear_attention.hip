@@ -262,58 +262,75 @@ __device__ __forceinline__ int row_length(const LaArgs& p, int64_t b) {
   return n < 0 ? 0 : (n > L ? L : n);
 }
 
-// Rows of a [64][cols] block of elements into an LDS tile of RB-byte rows, by one workgroup.
-// Row r is at base + r * step elements; rows past `last` repeat it (they are cleared
-// afterwards), and columns past `cols` are left as they are (zeros, from the start).
-//
 // The load is written out (it has no result register; M0 holds the wave's LDS address, lane
 // l's 16 bytes go to M0 + 16 l): the compiler would wait for a load into one buffer of k
 // before reading the other.  Whoever reads the tile waits first (vmcnt(0), then a barrier).
 // (5 wait states lie between a vector write of an address's scalar register and its use.  The
 // compiler has M0 reserved, and nothing else in these kernels uses it.)
-__device__ __forceinline__ void load_to_lds(const char* tile, const char* base, uint32_t off) {
-  const int m0 = uniform_int(static_cast<int>(lds_address(tile)));
+__device__ __forceinline__ void load_to_lds(uint32_t tile, const char* base, uint32_t off) {
+  const int m0 = uniform_int(static_cast<int>(tile));
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
                :: "s"(m0), "v"(off), "s"(base) : "memory");
 }
-__device__ __forceinline__ void load_to_lds(const char* tile, const char* src) {
-  const int m0 = uniform_int(static_cast<int>(lds_address(tile)));
+__device__ __forceinline__ void load_to_lds(uint32_t tile, const char* src) {
+  const int m0 = uniform_int(static_cast<int>(tile));
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off"
                :: "s"(m0), "v"(src) : "memory");
 }
 
+// One tensor's rows into its LDS tile.  Whole chunks take the short way: a uniform address that moves
+// on by a chunk, and for each of the wave's instructions (1024 bytes, 64 lanes of 16) the lane's offset,
+// formed once.  Scalar work inside the loop costs a chunk dearly (at 64 x 64 the addresses of
+// its loads and stores, formed there, were 2800 of its 7300 cycles).
 template <typename ELEM, int RB, int NW, bool PERM>
-__device__ __forceinline__ void load_tile(char* tile, const ELEM* base, int64_t step, int last, int cols, int w,
-                                          int lane) {
-  constexpr int kSlots = RB / 16, kRows = 64 / kSlots;              // slots of a row, rows of an instruction
-  constexpr int kInstr = kQ / kRows / NW;                           // instructions of a wave
-  const int lane_row = lane / kSlots;
-  constexpr bool kF32 = sizeof(ELEM) == 4;
-  const int lane_slot = (lane % kSlots) ^ swizzle<RB, kF32, PERM>(lane_row);   // (the swizzle is linear in the row's bits)
-  if (last == kQ - 1 && cols * static_cast<int>(sizeof(ELEM)) == RB) {
-    // a whole tile: a uniform address of each instruction's lowest row plus the lane's offset from it
+struct TileLoad {
+  static constexpr bool kF32 = sizeof(ELEM) == 4;
+  static constexpr int kSlots = RB / 16, kRows = 64 / kSlots;       // slots of a row, rows of an instruction
+  static constexpr int kInstr = kQ / kRows / NW;                    // instructions of a wave
+  const char* next;                   // lowest address of the chunk to load next
+  int64_t move;                       // bytes from a chunk to the next
+  uint32_t off[kInstr];
+  bool narrow;                        // columns past `cols` are left as they are (zeros, from the start)
+
+  static __device__ __forceinline__ int slot_of(int row, int lane) {   // (the swizzle is linear in the row's bits)
+    return (lane % kSlots) ^ swizzle<RB, kF32, PERM>(row);
+  }
+  // step: elements from a row to the next (negative: backwards)
+  __device__ __forceinline__ void start(const ELEM* base, int64_t step, int chunk, int cols, int w, int lane) {
     const int64_t bytes = step * static_cast<int64_t>(sizeof(ELEM));
-    const bool up = bytes >= 0;
-    const uint32_t row_off = static_cast<uint32_t>(up ? lane_row : kRows - 1 - lane_row) *
-                             static_cast<uint32_t>(up ? bytes : -bytes);
+    move = kQ * bytes;
+    next = reinterpret_cast<const char*>(base) + chunk * move + (bytes < 0 ? (kQ - 1) * bytes : 0);
+    narrow = cols * static_cast<int>(sizeof(ELEM)) < RB;
 #pragma unroll
     for (int i = 0; i < kInstr; ++i) {
-      const int row0 = (w * kInstr + i) * kRows;
-      const char* src = reinterpret_cast<const char*>(base) + (row0 + (up ? 0 : kRows - 1)) * bytes;
-      const uint32_t off = row_off + static_cast<uint32_t>((lane_slot ^ swizzle<RB, kF32, PERM>(row0)) * 16);
-      load_to_lds(tile + row0 * RB, src, off);
-    }
-  } else {
-#pragma unroll 1
-    for (int i = 0; i < kInstr; ++i) {
-      const int row0 = (w * kInstr + i) * kRows, row = row0 + lane_row, slot = lane_slot ^ swizzle<RB, kF32, PERM>(row0);
-      const int r = row < last ? row : last;
-      const char* src = reinterpret_cast<const char*>(base + r * step) + slot * 16;
-      if (slot * 16 < cols * static_cast<int>(sizeof(ELEM)))
-        load_to_lds(tile + row0 * RB, src);
+      const int row = (w * kInstr + i) * kRows + lane / kSlots;
+      off[i] = static_cast<uint32_t>(bytes < 0 ? kQ - 1 - row : row) * static_cast<uint32_t>(bytes < 0 ? -bytes : bytes) +
+               static_cast<uint32_t>(slot_of(row, lane) * 16);
     }
   }
-}
+  __device__ __forceinline__ void whole(uint32_t tile, int cols, int w, int lane) {
+    if (!narrow) {
+#pragma unroll
+      for (int i = 0; i < kInstr; ++i) load_to_lds(tile + (w * kInstr + i) * 1024, next, off[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kInstr; ++i)
+        if (slot_of((w * kInstr + i) * kRows + lane / kSlots, lane) * 16 < cols * static_cast<int>(sizeof(ELEM)))
+          load_to_lds(tile + (w * kInstr + i) * 1024, next, off[i]);
+    }
+    next += move;
+  }
+  // The last chunk: rows past `last` repeat it (they are cleared afterwards).
+  static __device__ __forceinline__ void part(uint32_t tile, const ELEM* base, int64_t step, int last, int cols, int w,
+                                              int lane) {
+#pragma unroll 1
+    for (int i = 0; i < kInstr; ++i) {
+      const int row = (w * kInstr + i) * kRows + lane / kSlots, slot = slot_of(row, lane), r = row < last ? row : last;
+      if (slot * 16 < cols * static_cast<int>(sizeof(ELEM)))
+        load_to_lds(tile + (w * kInstr + i) * 1024, reinterpret_cast<const char*>(base + r * step) + slot * 16);
+    }
+  }
+};
 
 // Clears rows n.. of the slots that this wave's load_tile filled.
 template <int RB, int NW>
@@ -400,19 +417,37 @@ void la_kernel(LaArgs p) {
   const elem* vg = static_cast<const elem*>(r.v) + b * r.vs[0] + (h / r.vdiv) * r.vs[2] + t_first * r.vs[1];
   const int64_t qstep = r.qs[1] * t_step, kstep = r.ks[1] * t_step, vstep = r.vs[1] * t_step;
 
-  // Ask for the rows of k, or of q and v, of chunk c.
+  // Ask for the rows of k, or of q and v, of chunk c (in order, from c_begin).
+  TileLoad<elem, RK, NW, true> k_load;
+  TileLoad<elem, RK, NW, false> q_load;
+  TileLoad<elem, RV, NW, false> v_load;
+  if constexpr (VEC) {
+    k_load.start(kg, kstep, c_begin, K, w, lane0);
+    if constexpr (!STATE_ONLY) q_load.start(qg, qstep, c_begin, K, w, lane0);
+    v_load.start(vg, vstep, c_begin, V, w, lane0);
+  }
   auto load_k = [&](int c, int lane) __attribute__((always_inline)) {
+    const int last = len - 1 - c * kQ;
     const int64_t r0 = static_cast<int64_t>(c) * kQ;
-    const int last = len - 1 - c * kQ < kQ - 1 ? len - 1 - c * kQ : kQ - 1;
-    if constexpr (VEC) load_tile<elem, RK, NW, true>(sKK[c & 1], kg + r0 * kstep, kstep, last, K, w, lane);
-    else load_tile_scalar<elem, RK, NW, true>(sKK[c & 1], kg + r0 * kstep, kstep, last, K, tid);
+    if constexpr (VEC) {
+      const uint32_t tile = lds_address(sKK[0]) + (c & 1) * (kQ * RK);
+      if (last >= kQ - 1) k_load.whole(tile, K, w, lane);
+      else k_load.part(tile, kg + r0 * kstep, kstep, last, K, w, lane);
+    } else {
+      load_tile_scalar<elem, RK, NW, true>(sKK[c & 1], kg + r0 * kstep, kstep, last, K, tid);
+    }
   };
   auto load_qv = [&](int c, int lane) __attribute__((always_inline)) {
+    const int last = len - 1 - c * kQ;
     const int64_t r0 = static_cast<int64_t>(c) * kQ;
-    const int last = len - 1 - c * kQ < kQ - 1 ? len - 1 - c * kQ : kQ - 1;
     if constexpr (VEC) {
-      if constexpr (!STATE_ONLY) load_tile<elem, RK, NW, false>(sQ, qg + r0 * qstep, qstep, last, K, w, lane);
-      load_tile<elem, RV, NW, false>(sV, vg + r0 * vstep, vstep, last, V, w, lane);
+      if (last >= kQ - 1) {
+        if constexpr (!STATE_ONLY) q_load.whole(lds_address(sQ), K, w, lane);
+        v_load.whole(lds_address(sV), V, w, lane);
+      } else {
+        if constexpr (!STATE_ONLY) q_load.part(lds_address(sQ), qg + r0 * qstep, qstep, last, K, w, lane);
+        v_load.part(lds_address(sV), vg + r0 * vstep, vstep, last, V, w, lane);
+      }
     } else {
       if constexpr (!STATE_ONLY) load_tile_scalar<elem, RK, NW, false>(sQ, qg + r0 * qstep, qstep, last, K, tid);
       load_tile_scalar<elem, RV, NW, false>(sV, vg + r0 * vstep, vstep, last, V, tid);
@@ -521,6 +556,21 @@ void la_kernel(LaArgs p) {
   float pj[4];
 #pragma unroll
   for (int jt = 0; jt < 4; ++jt) pj[jt] = uniform_float(exp2_hw(g2 * static_cast<float>(16 * jt)));
+
+  // where the output rows of a whole chunk go: backwards, row r of the chunk is 63 - r rows up
+  const bool o_f32 = kF32 || r.o_f32;
+  char* o_next = nullptr;
+  int64_t o_move = 0;
+  uint32_t o_off = 0, o_rows = 0;
+  if constexpr (!STATE_ONLY && VEC) {
+    const int esz = o_f32 ? 4 : 2;
+    const int64_t bytes = static_cast<int64_t>(p.H) * V * esz, r0 = static_cast<int64_t>(c_begin) * kQ;
+    o_next = static_cast<char*>(r.o) + (b * L + (reverse ? len - kQ - r0 : r0)) * bytes + static_cast<int64_t>(h) * V * esz;
+    o_move = (reverse ? -kQ : kQ) * bytes;
+    const int col = VT == 2 && esz == 2 ? 16 * VT * w + (g & 1) * 16 + (g >> 1) * 8 : 16 * VT * w + 4 * g;
+    o_rows = static_cast<uint32_t>(reverse ? -16 * bytes : 16 * bytes);
+    o_off = static_cast<uint32_t>((reverse ? kQ - 1 - c16 : c16) * bytes + col * esz);
+  }
 
   if (c_begin < c_live) arrived(c_begin, present(c_begin), lane0);
   for (int c = c_begin; c < c_live; ++c) {
@@ -709,30 +759,28 @@ void la_kernel(LaArgs p) {
           if constexpr (sizeof(OUT) == 4) return make_float4(a[0], a[1], a[2], a[3]);
           else return make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
         };
-        const int64_t row_stride = static_cast<int64_t>(p.H) * V;
-        const int r0 = c * kQ;
-        if (VEC && V == VD && n == kQ) {
-          // uniform addresses of 16 rows, the lane's place among them
-          const uint32_t off = static_cast<uint32_t>(reverse ? 15 - c16 : c16) * static_cast<uint32_t>(row_stride);
+        if (VEC && n == kQ && V == VD) {
+          // a uniform address that moves on by a chunk, the lane's offset in 16 rows, 16 rows' bytes
 #pragma unroll
           for (int jt = 0; jt < 4; ++jt) {
-            const int64_t token = reverse ? len - 16 - (r0 + 16 * jt) : r0 + 16 * jt;
-            OUT* rows = out + (b * L + token) * row_stride + static_cast<int64_t>(h) * V + 16 * VT * w;
+            char* rows = o_next + (o_off + static_cast<uint32_t>(jt) * o_rows);
             if constexpr (VT == 2 && sizeof(OUT) == 2) {
               // lane groups 2x and 2x + 1 exchange halves: 8 columns a lane, 64 bytes of a row an instruction
               const uint2 a0 = four(acc[0][jt]), a1 = four(acc[1][jt]);
               const auto lo = __builtin_amdgcn_permlane16_swap(a0.x, a1.x, false, false);
               const auto hi = __builtin_amdgcn_permlane16_swap(a0.y, a1.y, false, false);
-              const uint32_t col = (g & 1) * 16 + (g >> 1) * 8;
-              *reinterpret_cast<uint4*>(rows + (off + col)) = make_uint4(lo[0], hi[0], lo[1], hi[1]);
+              *reinterpret_cast<uint4*>(rows) = make_uint4(lo[0], hi[0], lo[1], hi[1]);
             } else {
 #pragma unroll
               for (int vt = 0; vt < VT; ++vt)
-                *reinterpret_cast<decltype(four(acc[0][0]))*>(rows + (off + 4 * g + 16 * vt)) = four(acc[vt][jt]);
+                *reinterpret_cast<decltype(four(acc[0][0]))*>(rows + 16 * vt * sizeof(OUT)) = four(acc[vt][jt]);
             }
           }
+          o_next += o_move;
           return;
         }
+        const int64_t row_stride = static_cast<int64_t>(p.H) * V;
+        const int r0 = c * kQ;
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) {
           const int row = r0 + 16 * jt + c16;
@@ -755,7 +803,7 @@ void la_kernel(LaArgs p) {
           }
         }
       };
-      if (kF32 || r.o_f32) put(static_cast<float*>(r.o));
+      if (o_f32) put(static_cast<float*>(r.o));
       else put(static_cast<uint16_t*>(r.o));
     }
   }

@@ -21,8 +21,8 @@ using ssm::span;
 constexpr uint64_t kMaxBytes = uint64_t(1) << 62;
 constexpr int64_t kMaxL = int64_t(1) << 30;
 constexpr int64_t kMaxPairs = int64_t(1) << 20;      // batch * H of the prompt form
-constexpr int64_t kMaxHeads = int64_t(1) << 16;      // (16 rows of the output span less than 2^31 bytes)
-constexpr int64_t kMaxTokenStride = int64_t(1) << 26;  // ... and 8 rows of an input that moves as vectors
+constexpr int64_t kMaxHeads = int64_t(1) << 16;      // (64 rows of the output span less than 2^32 bytes)
+constexpr int64_t kMaxTokenStride = int64_t(1) << 23;  // ... and 64 rows of an input that moves as vectors
 constexpr int64_t kMaxStepPairs = int64_t(1) << 22;  // batch * H of the step
 constexpr int64_t kMaxRows = int64_t(1) << 22;
 
