@@ -842,8 +842,9 @@ void la_kernel(LaArgs p) {
 
 // Chains the segments' own sums T_s into the E entering each segment (written over T_s) and
 // the state after the last token.  A thread takes kChain entries 256 apart, so that the decays
-// (float64 exponentials) are a small part of its work.
-constexpr int kChain = 8;
+// (float64 exponentials) are a small part of its work, and reads kAhead segments' sums at a time:
+// only the arithmetic is a chain.
+constexpr int kChain = 4, kAhead = 8;
 __global__ __launch_bounds__(256) void la_chain_kernel(LaArgs p) {
   const LaRole& r = p.role[blockIdx.z];
   const int64_t bh = blockIdx.y;
@@ -852,24 +853,42 @@ __global__ __launch_bounds__(256) void la_chain_kernel(LaArgs p) {
   const int h = static_cast<int>(bh % p.H);
   const int len = row_length(p, bh / p.H);
   const int seg_tokens = static_cast<int>(p.seg_chunks) * kQ;
-  const Pair l1 = decay_pair(p.log_decay, h, 1), lS = decay_pair(p.log_decay, h, seg_tokens);
   float* slot = r.seg + bh * p.nseg * static_cast<int64_t>(KV);
   const float* carry = r.carry ? r.carry + bh * static_cast<int64_t>(KV) : nullptr;
   float* fin = r.fin ? r.fin + bh * static_cast<int64_t>(KV) : nullptr;
-  float s[kChain], T[kChain];
+  auto tokens = [&](int k) {
+    const int left = len - k * seg_tokens;
+    return left < 0 ? 0 : (left < seg_tokens ? left : seg_tokens);
+  };
+  float s[kChain], T[kAhead][kChain];
 #pragma unroll
   for (int x = 0; x < kChain; ++x) s[x] = carry && i0 + 256 * x < KV ? carry[i0 + 256 * x] : 0.0f;
   auto times = [](const Pair& d, float x) { return __builtin_fmaf(d.hi, x, d.lo * x); };
-  for (int k = 0; k < p.nseg; ++k, slot += KV) {
-    const int left = len - k * seg_tokens, n = left < 0 ? 0 : (left < seg_tokens ? left : seg_tokens);
-    const bool read = n > 0 && (k + 1 < p.nseg || fin);
+  Pair l1, lS;
+  for (int k0 = 0; k0 < p.nseg; k0 += kAhead) {
 #pragma unroll
-    for (int x = 0; x < kChain; ++x) T[x] = read && i0 + 256 * x < KV ? slot[i0 + 256 * x] : 0.0f;
-    const Pair d = n == seg_tokens ? lS : decay_pair(p.log_decay, h, n);
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = k0 + u;
+      const bool read = k < p.nseg && tokens(k) > 0 && (k + 1 < p.nseg || fin);   // (the others were not written)
 #pragma unroll
-    for (int x = 0; x < kChain; ++x) {
-      if (i0 + 256 * x < KV) slot[i0 + 256 * x] = r.reverse ? s[x] : times(l1, s[x]);
-      if (n > 0) s[x] = times(d, s[x]) + (r.reverse ? times(l1, T[x]) : T[x]);
+      for (int x = 0; x < kChain; ++x)
+        T[u][x] = read && i0 + 256 * x < KV ? slot[static_cast<int64_t>(k) * KV + i0 + 256 * x] : 0.0f;
+    }
+    if (k0 == 0) {                                  // (while the first sums are on their way)
+      l1 = decay_pair(p.log_decay, h, 1);
+      lS = decay_pair(p.log_decay, h, seg_tokens);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = k0 + u;
+      if (k >= p.nseg) break;
+      const int n = tokens(k);
+      const Pair d = n == seg_tokens ? lS : decay_pair(p.log_decay, h, n);
+#pragma unroll
+      for (int x = 0; x < kChain; ++x) {
+        if (i0 + 256 * x < KV) slot[static_cast<int64_t>(k) * KV + i0 + 256 * x] = r.reverse ? s[x] : times(l1, s[x]);
+        if (n > 0) s[x] = times(d, s[x]) + (r.reverse ? times(l1, T[u][x]) : T[u][x]);
+      }
     }
   }
   if (fin) {

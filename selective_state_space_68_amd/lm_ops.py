@@ -45,19 +45,19 @@ def _is(t, name: str, shape) -> None:
         _shape(t, name, shape)
 
 
-def _device(t, name: str, device) -> None:
+def _device(t, name: str, index: int) -> None:
     if not t.is_cuda:
         raise ValueError(f"{name} must live on the GPU")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _ptr(t, name: str, dtype, device):
-    """Pointer of a contiguous tensor of the given type on the given device (None for None)."""
+def _ptr(t, name: str, dtype, index: int):
+    """Pointer of a contiguous tensor of the given type on GPU `index` (None for None)."""
     if t is None:
         return None
-    if not t.is_cuda or t.device != device:
-        _device(t, name, device)
+    if t.get_device() != index or index < 0:
+        _device(t, name, index)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
@@ -65,33 +65,40 @@ def _ptr(t, name: str, dtype, device):
     return t.data_ptr()
 
 
-def _view(t, name: str, dtype, device):
-    """(pointer, strides) of a view with a contiguous last axis; strides is a ctypes array
-    of the element strides of the axes before it (None: packed)."""
-    if not t.is_cuda or t.device != device:
-        _device(t, name, device)
+def _strides(t, name: str, dtype, index: int):
+    """Checks a view with a contiguous last axis; returns a ctypes array of the element
+    strides of the axes before it (None: packed)."""
+    if t.get_device() != index or index < 0:
+        _device(t, name, index)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.is_contiguous() or t.numel() == 0:
-        return t.data_ptr(), None
+        return None
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have a contiguous last axis")
-    return t.data_ptr(), (ctypes.c_int64 * (t.dim() - 1))(*t.stride()[:-1])
+    return (ctypes.c_int64 * (t.dim() - 1))(*t.stride()[:-1])
 
 
-def _run(fn, device, stream, *args) -> None:
-    """Calls fn on `stream` (the device's current one when None), with `device` current."""
+def _run(fn, index: int, stream, *args) -> None:
+    """Calls fn on `stream` (GPU `index`'s current one when None), with that GPU current."""
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device.index)
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() != device.index:
-        with torch.cuda.device(device):
-            status = fn(*args, int(stream))
+        stream = torch._C._cuda_getCurrentRawStream(index)
     else:
-        status = fn(*args, int(stream))
+        stream = int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    else:
+        status = fn(*args, stream)
     if status:
         _lib.check(status)
+
+
+def _scratch(workspace, need: int, like):
+    """(pointer, bytes) of the caller's workspace, or of one allocated beside `like`."""
+    if workspace is None and need == 0:
+        return None, 0
+    return _workspace(workspace, need, like.device)
 
 
 @lru_cache(maxsize=None)
@@ -149,16 +156,16 @@ def linear_attention_fwd(q, k, v, log_decay, scale=None, *, initial_state=None, 
     _is(initial_state, "initial_state", states)
     _is(out, "out", (batch, L, H, V))
     _is(final_state, "final_state", states)
-    act, dev = q.dtype, q.device
+    act, dev = q.dtype, q.get_device()
     dt = _dt(act)
-    (qp, qs), (kp, ks), (vp, vs) = _view(q, "q", act, dev), _view(k, "k", act, dev), _view(v, "v", act, dev)
+    qs, ks, vs = _strides(q, "q", act, dev), _strides(k, "k", act, dev), _strides(v, "v", act, dev)
     if out is None:
-        out = torch.empty((batch, L, H, V), dtype=act, device=dev)
+        out = q.new_empty((batch, L, H, V))
     if final_state is None and return_final_state:
-        final_state = torch.empty(states, dtype=F32, device=dev)
-    ws_ptr, ws_bytes = _workspace(workspace, linear_attention_workspace_size(batch, L, H, K, V, act), dev)
+        final_state = q.new_empty(states, dtype=F32)
+    ws_ptr, ws_bytes = _scratch(workspace, linear_attention_workspace_size(batch, L, H, K, V, act), q)
     _run(_entry("ssm_linear_attention_fwd"), dev, stream,
-         qp, kp, vp, qs, ks, vs, _ptr(log_decay, "log_decay", F32, dev), K ** -0.5 if scale is None else float(scale),
+         q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(log_decay, "log_decay", F32, dev), K ** -0.5 if scale is None else float(scale),
          _ptr(lengths, "lengths", _I32, dev), _ptr(initial_state, "initial_state", F32, dev),
          _ptr(out, "out", act, dev), _ptr(final_state, "final_state", F32, dev), batch, L, H, Hq, Hk, Hv, K, V, dt,
          ws_ptr, ws_bytes)
@@ -184,17 +191,17 @@ def linear_attention_bwd(q, k, v, log_decay, dout, scale=None, *, initial_state=
     _is(lengths, "lengths", (batch,))
     _is(initial_state, "initial_state", states)
     _is(dfinal_state, "dfinal_state", states)
-    act, dev = q.dtype, q.device
+    act, dev = q.dtype, q.get_device()
     dt = _dt(act)
-    (qp, qs), (kp, ks), (vp, vs), (dp, ds) = (
-        _view(t, n, act, dev) for t, n in ((q, "q"), (k, "k"), (v, "v"), (dout, "dout")))
+    qs, ks, vs = _strides(q, "q", act, dev), _strides(k, "k", act, dev), _strides(v, "v", act, dev)
+    ds = _strides(dout, "dout", act, dev)
     want = initial_state is not None if want_dinitial_state is None else want_dinitial_state
-    g = _outputs(out, dev, {"dq": ((batch, L, Hq, K), act, True), "dk": ((batch, L, Hk, K), act, True),
+    g = _outputs(out, q, {"dq": ((batch, L, Hq, K), act, True), "dk": ((batch, L, Hk, K), act, True),
                             "dv": ((batch, L, Hv, V), act, True), "dinitial_state": (states, F32, want)})
-    ws_ptr, ws_bytes = _workspace(
-        workspace, linear_attention_bwd_workspace_size(batch, L, H, K, V, act, Hq=Hq, Hk=Hk, Hv=Hv), dev)
+    ws_ptr, ws_bytes = _scratch(
+        workspace, linear_attention_bwd_workspace_size(batch, L, H, K, V, act, Hq=Hq, Hk=Hk, Hv=Hv), q)
     _run(_entry("ssm_linear_attention_bwd"), dev, stream,
-         qp, kp, vp, dp, qs, ks, vs, ds, _ptr(log_decay, "log_decay", F32, dev),
+         q.data_ptr(), k.data_ptr(), v.data_ptr(), dout.data_ptr(), qs, ks, vs, ds, _ptr(log_decay, "log_decay", F32, dev),
          K ** -0.5 if scale is None else float(scale), _ptr(lengths, "lengths", _I32, dev),
          _ptr(initial_state, "initial_state", F32, dev), _ptr(dfinal_state, "dfinal_state", F32, dev),
          _ptr(g["dq"], "dq", act, dev), _ptr(g["dk"], "dk", act, dev), _ptr(g["dv"], "dv", act, dev),
@@ -221,20 +228,21 @@ def linear_attention_step(state, q_t, k_t, v_t, log_decay, scale=None, *, slots=
     _is(out, "out", (batch, H, V))
     if slots is None and states < batch:
         raise ValueError(f"{batch} rows need as many states, got {states}")
-    act, dev = q_t.dtype, state.device
+    act, dev = q_t.dtype, state.get_device()
     dt = _dt(act)
-    (qp, qs), (kp, ks), (vp, vs) = _view(q_t, "q_t", act, dev), _view(k_t, "k_t", act, dev), _view(v_t, "v_t", act, dev)
+    qs, ks, vs = _strides(q_t, "q_t", act, dev), _strides(k_t, "k_t", act, dev), _strides(v_t, "v_t", act, dev)
     state_ptr = _ptr(state, "state", F32, dev)
     if out is None:
-        out = torch.empty((batch, H, V), dtype=act, device=dev)
+        out = q_t.new_empty((batch, H, V))
     _run(_entry("ssm_linear_attention_step"), dev, stream,
-         state_ptr, state_ptr if out_state is None else _ptr(out_state, "out_state", F32, dev), qp, kp, vp, qs, ks, vs,
+         state_ptr, state_ptr if out_state is None else _ptr(out_state, "out_state", F32, dev),
+         q_t.data_ptr(), k_t.data_ptr(), v_t.data_ptr(), qs, ks, vs,
          _ptr(log_decay, "log_decay", F32, dev), K ** -0.5 if scale is None else float(scale),
          _ptr(slots, "slots", _I32, dev), _ptr(out, "out", act, dev), batch, states, H, Hq, Hk, Hv, K, V, dt)
     return out
 
 
-def _outputs(given, dev, spec) -> dict:
+def _outputs(given, like, spec) -> dict:
     """Output tensors by name: the caller's where given (checked), else new ones; None where not computed."""
     got = {}
     for name, (shape, dtype, computed) in spec.items():
@@ -245,7 +253,7 @@ def _outputs(given, dev, spec) -> dict:
                 raise TypeError(f"out[{name!r}] must be {dtype}")
             got[name] = t
         else:
-            got[name] = torch.empty(shape, dtype=dtype, device=dev) if computed else None
+            got[name] = like.new_empty(shape, dtype=dtype) if computed else None
     return got
 
 
@@ -268,7 +276,7 @@ def _rows(t, name: str, D: int):
 
 
 def _norm_inputs(x, gate, post_weight, res_scale, pre_weight, groups):
-    """Checks a block norm's inputs; returns (rows, D, device)."""
+    """Checks a block norm's inputs; returns (rows, D, the GPU's index)."""
     if not isinstance(x, _Tensor) or x.dim() < 1:
         raise ValueError("expected x [..., D]")
     D = x.shape[-1]
@@ -278,11 +286,12 @@ def _norm_inputs(x, gate, post_weight, res_scale, pre_weight, groups):
     _is(gate, "gate", x.shape)
     if int(groups) < 1 or D % int(groups):
         raise ValueError(f"groups ({groups}) must divide D ({D})")
-    dev = x.device
-    if not x.is_cuda:
+    dev = x.get_device()
+    if dev < 0:
         raise ValueError("x must live on the GPU")
     if gate is not None:
-        _device(gate, "gate", dev)
+        if gate.get_device() != dev:
+            _device(gate, "gate", dev)
         if gate.dtype != x.dtype:
             raise TypeError(f"gate must be {x.dtype}, got {gate.dtype}")
     return x.numel() // D if D else 0, D, dev
@@ -321,9 +330,9 @@ def block_norm_fwd(x, residual=None, gate=None, post_weight=None, res_scale=None
     if pre_weight is None and y is not None:
         raise ValueError("y is computed only with pre_weight")
     if h is None and (return_h or pre_weight is None):
-        h = torch.empty(shape, dtype=rdtype, device=dev)
+        h = x.new_empty(shape, dtype=rdtype)
     if y is None and pre_weight is not None:
-        y = torch.empty(shape, dtype=x.dtype, device=dev)
+        y = x.new_empty(shape)
     (xp, xs), (gp, gs) = _rows(x, "x", D), _rows(gate, "gate", D)
     act = x.dtype
     _run(_entry("ssm_block_norm_fwd"), dev, stream,
@@ -362,12 +371,12 @@ def block_norm_bwd(x, h=None, dy=None, dh=None, gate=None, post_weight=None, res
     if residual_dtype is None and (h is not None or dh is not None):
         residual_dtype = (h if h is not None else dh).dtype
     rdtype, rdt = _residual_dtype(residual_dtype, x)
-    g = _outputs(out, dev, {"dx": (x.shape, x.dtype, True), "dgate": (x.shape, x.dtype, gate is not None),
+    g = _outputs(out, x, {"dx": (x.shape, x.dtype, True), "dgate": (x.shape, x.dtype, gate is not None),
                             "dresidual": (x.shape, rdtype, has_residual),
                             "dpost_weight": ((D,), F32, post_weight is not None),
                             "dres_scale": ((D,), F32, res_scale is not None),
                             "dpre_weight": ((D,), F32, pre_weight is not None)})
-    ws_ptr, ws_bytes = _workspace(workspace, block_norm_bwd_workspace_size(rows, D), dev)
+    ws_ptr, ws_bytes = _scratch(workspace, block_norm_bwd_workspace_size(rows, D), x)
     (xp, xs), (gp, gs) = _rows(x, "x", D), _rows(gate, "gate", D)
     act = x.dtype
     _run(_entry("ssm_block_norm_bwd"), dev, stream,
