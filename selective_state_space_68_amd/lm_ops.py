@@ -362,11 +362,11 @@ def block_norm_bwd(x, h=None, dy=None, dh=None, gate=None, post_weight=None, res
     _is(h, "h", shape)
     _is(dy, "dy", shape)
     _is(dh, "dh", shape)
-    rows, D, dev = _norm_inputs(x, gate, post_weight, res_scale, pre_weight, groups)
     if (pre_weight is None) != (dy is None):
         raise ValueError("dy is given exactly when pre_weight is")
     if pre_weight is not None and h is None:
         raise ValueError("h (what the forward pass returned) is needed with pre_weight")
+    rows, D, dev = _norm_inputs(x, gate, post_weight, res_scale, pre_weight, groups)
     has_residual = residual_dtype is not None
     if residual_dtype is None and (h is not None or dh is not None):
         residual_dtype = (h if h is not None else dh).dtype

@@ -230,3 +230,23 @@ def test_runs_on_the_given_stream_and_in_a_graph():
         assert torch.equal(h, h2) and torch.equal(y, y2) and all(torch.equal(g[k], g2[k]) for k in g)
         ssm.block_norm_fwd(**d)                             # (eager work between the replays)
         torch.cuda.synchronize()
+
+
+def test_rows_past_32_bits_of_elements():
+    ssm = _ssm()
+    rows, D, far = 4, 136, 1 << 30
+    store = torch.zeros((rows - 1) * far + 2 * D, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator("cuda").manual_seed(23)
+    views = [store.as_strided((rows, D), (far, 1), i * D) for i in range(2)]
+    for x in views:
+        x.copy_(torch.randn(rows, D, device="cuda", generator=gen))
+    x, gate = (a.contiguous() for a in views)
+    w = torch.randn(D, device="cuda", generator=gen)
+    for a, b in zip(ssm.block_norm_fwd(views[0], None, views[1], w, pre_weight=w),
+                    ssm.block_norm_fwd(x, None, gate, w, pre_weight=w)):
+        assert torch.equal(a, b)
+    dh = torch.randn(rows, D, device="cuda", generator=gen).bfloat16()
+    a = ssm.block_norm_bwd(views[0], None, None, dh, views[1], w)
+    b = ssm.block_norm_bwd(x, None, None, dh, gate, w)
+    for n in ("dx", "dgate", "dpost_weight"):
+        assert torch.equal(a[n], b[n]), n

@@ -388,3 +388,46 @@ def test_step_states_past_32_bits():
     _check(out[:, None], want, torch.bfloat16, "out")
     _check(state[-1:], wfin, torch.bfloat16, "state")
     assert not state[:-1].any()
+
+
+@pytest.mark.parametrize("which", ["batch", "token"])
+def test_views_past_32_bits_of_elements(which):
+    # rows of a batch 2^31 elements apart (vector loads), tokens 2^30 apart (element by element): the same bits
+    # as packed copies, forwards and in the gradient
+    ssm = _ssm()
+    B, L, H, K = (2, 70, 2, 64) if which == "batch" else (1, 4, 2, 64)
+    far = (1 << 31) + 64 if which == "batch" else 1 << 30
+    span = (B - 1) * far if which == "batch" else (L - 1) * far
+    store = torch.zeros(span + 4 * L * H * K, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator("cuda").manual_seed(21)
+    views = {}
+    for i, n in enumerate(("q", "k", "v", "do")):
+        strides = (far, H * K, K, 1) if which == "batch" else (0, far, K, 1)
+        views[n] = store.as_strided((B, L, H, K), strides, i * L * H * K)
+        views[n].copy_(torch.randn(B, L, H, K, device="cuda", generator=gen))
+    t = {n: x.contiguous() for n, x in views.items()}
+    g = torch.tensor([-0.01, -0.2], device="cuda")
+    for a, b in zip(ssm.linear_attention_fwd(views["q"], views["k"], views["v"], g),
+                    ssm.linear_attention_fwd(t["q"], t["k"], t["v"], g)):
+        assert torch.equal(a, b)
+    a = ssm.linear_attention_bwd(views["q"], views["k"], views["v"], g, views["do"])
+    b = ssm.linear_attention_bwd(t["q"], t["k"], t["v"], g, t["do"])
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(a[n], b[n]), n
+
+
+def test_outputs_past_32_bits_of_elements():
+    # 2^31 output elements and more: the last tokens from the state before them
+    ssm = _ssm()
+    H, K, V, tail = 64, 64, 128, 100
+    L = (1 << 31) // (H * V) + tail
+    gen = torch.Generator("cuda").manual_seed(22)
+    r = lambda heads, d: torch.randn(1, L, heads, d, device="cuda", dtype=torch.bfloat16, generator=gen)
+    q, k, v = r(1, K), r(1, K), r(H, V)
+    g = torch.log(torch.linspace(0.5, 0.9, H, device="cuda"))     # what is 1000 tokens back is below 0.9^1000
+    out, fin = ssm.linear_attention_fwd(q, k, v, g)
+    n = L - tail - 1000
+    t = [x[:, n:].cpu() for x in (q, k, v)]
+    want, wfin = ref.attention(*t, g.cpu(), K ** -0.5, None)
+    _check(out[:, -tail:], want[:, -tail:], torch.bfloat16, "out")
+    _check(fin, wfin, torch.bfloat16, "state")
