@@ -121,6 +121,19 @@ struct Op<ActBF16> {
       }
     }
   }
+  // the same for 4 values, into one half of each operand
+  template <int TERMS>
+  static __device__ __forceinline__ void split4(const float (&v)[4], uint2 (&p)[TERMS]) {
+    const float x[8] = {v[0], v[1], v[2], v[3], 0.0f, 0.0f, 0.0f, 0.0f};
+    piece full[TERMS];
+    split<TERMS>(x, full);
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) p[t] = make_uint2(full[t].x, full[t].y);
+  }
+  using half = uint2;
+  static __device__ __forceinline__ void put_half(uint32_t at, const half& p) {
+    lds_write<u32x2_t>(at, __builtin_bit_cast(u32x2_t, p));
+  }
   static constexpr int kPiece = 16;                 // bytes of 8 elements
   // A lane's part of the address of columns 8g.. of row `row`, and the 8 columns at it.
   template <int RB, bool PERM>
@@ -186,6 +199,14 @@ struct Op<ActF32> {
   static __device__ __forceinline__ void split(const float (&v)[8], piece (&p)[TERMS]) {
     static_assert(TERMS == 1, "float32 operands are exact");
     p[0] = pack(v);
+  }
+  template <int TERMS>
+  static __device__ __forceinline__ void split4(const float (&v)[4], float4 (&p)[TERMS]) {
+    p[0] = make_float4(v[0], v[1], v[2], v[3]);
+  }
+  using half = float4;
+  static __device__ __forceinline__ void put_half(uint32_t at, const half& p) {
+    lds_write<f32x4_t>(at, __builtin_bit_cast(f32x4_t, p));
   }
   static constexpr int kPiece = 32;
   template <int RB, bool PERM>
@@ -308,8 +329,10 @@ struct TileLoad {
                static_cast<uint32_t>(slot_of(row, lane) * 16);
     }
   }
+  // (ALL: known to have every column)
+  template <bool ALL>
   __device__ __forceinline__ void whole(uint32_t tile, int cols, int w, int lane) {
-    if (!narrow) {
+    if (ALL || !narrow) {
 #pragma unroll
       for (int i = 0; i < kInstr; ++i) load_to_lds(tile + (w * kInstr + i) * 1024, next, off[i]);
     } else {
@@ -426,24 +449,26 @@ void la_kernel(LaArgs p) {
     if constexpr (!STATE_ONLY) q_load.start(qg, qstep, c_begin, K, w, lane0);
     v_load.start(vg, vstep, c_begin, V, w, lane0);
   }
-  auto load_k = [&](int c, int lane) __attribute__((always_inline)) {
+  auto load_k = [&](auto plain, int c, int lane) __attribute__((always_inline)) {
+    constexpr bool PLAIN = decltype(plain)::value;
     const int last = len - 1 - c * kQ;
     const int64_t r0 = static_cast<int64_t>(c) * kQ;
     if constexpr (VEC) {
       const uint32_t tile = lds_address(sKK[0]) + (c & 1) * (kQ * RK);
-      if (last >= kQ - 1) k_load.whole(tile, K, w, lane);
+      if (PLAIN || last >= kQ - 1) k_load.template whole<PLAIN>(tile, K, w, lane);
       else k_load.part(tile, kg + r0 * kstep, kstep, last, K, w, lane);
     } else {
       load_tile_scalar<elem, RK, NW, true>(sKK[c & 1], kg + r0 * kstep, kstep, last, K, tid);
     }
   };
-  auto load_qv = [&](int c, int lane) __attribute__((always_inline)) {
+  auto load_qv = [&](auto plain, int c, int lane) __attribute__((always_inline)) {
+    constexpr bool PLAIN = decltype(plain)::value;
     const int last = len - 1 - c * kQ;
     const int64_t r0 = static_cast<int64_t>(c) * kQ;
     if constexpr (VEC) {
-      if (last >= kQ - 1) {
-        if constexpr (!STATE_ONLY) q_load.whole(lds_address(sQ), K, w, lane);
-        v_load.whole(lds_address(sV), V, w, lane);
+      if (PLAIN || last >= kQ - 1) {
+        if constexpr (!STATE_ONLY) q_load.template whole<PLAIN>(lds_address(sQ), K, w, lane);
+        v_load.template whole<PLAIN>(lds_address(sV), V, w, lane);
       } else {
         if constexpr (!STATE_ONLY) q_load.part(lds_address(sQ), qg + r0 * qstep, qstep, last, K, w, lane);
         v_load.part(lds_address(sV), vg + r0 * vstep, vstep, last, V, w, lane);
@@ -475,8 +500,8 @@ void la_kernel(LaArgs p) {
     }
   }
   if (c_begin < c_live) {
-    load_k(c_begin, lane0);
-    load_qv(c_begin, lane0);
+    load_k(std::false_type{}, c_begin, lane0);
+    load_qv(std::false_type{}, c_begin, lane0);
   }
 
   const int g = lane0 >> 4, c16 = lane0 & 15;
@@ -513,20 +538,12 @@ void la_kernel(LaArgs p) {
   // every entry.  Past 2^30 the state is multiplied out, by rho as a float32 pair from
   // float64, so that no rounding of lam^64 builds up over the thousands of chunks of a head's memory.
   const double lam_q = uniform_double(decay_power(p.log_decay, h, kQ));
-  const double g2d = uniform_double(static_cast<double>(p.log_decay[h]) * 1.4426950408889634);
+  const double unlam_q = uniform_double(1.0 / lam_q);
   const float g_q = g2 * kQ;
   int a = 0;
-  // lam^(64 chunks) to float32 accuracy, |its exponent| up to 2^7
-  auto power_q = [&](int chunks) __attribute__((always_inline)) {
-    if (chunks == 0) return 1.0f;
-    const double x = g2d * (kQ * chunks), whole = __builtin_floor(x);
-    return __builtin_ldexpf(exp2_hw(static_cast<float>(x - whole)), static_cast<int>(whole));
-  };
+  double rho = 1.0, unrho = 1.0;                    // lam^(64 a) and its inverse
   auto multiply_out = [&](double by) __attribute__((always_inline)) {      // by: the decay of the chunk just done
-    double base = lam_q;
-    for (int n = a; n > 0; n >>= 1, base *= base)
-      if (n & 1) by *= base;
-    const Pair d = pair_of(by);
+    const Pair d = pair_of(by * rho);
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
@@ -536,6 +553,7 @@ void la_kernel(LaArgs p) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) E[vt][t][u][e] = __builtin_fmaf(d.hi, E[vt][t][u][e], d.lo * E[vt][t][u][e]);
     a = 0;
+    rho = unrho = 1.0;
   };
   // The last chunk of the sequence (of the segment, in the pre-pass) forwards leaves S, not lam S,
   // and may hold fewer tokens.
@@ -543,19 +561,29 @@ void la_kernel(LaArgs p) {
   const int shift = uniform_int((STATE_ONLY || !reverse) && (STATE_ONLY || c_live == live) ? 1 : 0);
   const double lam_end = uniform_double(decay_power(p.log_decay, h, n_end - shift > 0 ? n_end - shift : 0));
 
-  // Decay factors.  lam^(j-i) of P splits into a lane's lam^(j - 32t - 8g - 7) and the uniform
-  // lam^(7 - (4u + e)); the first may exceed 1 near the diagonal, so heads that decay by more
-  // than 2^16 a token (lam^7 near float32's end) take the exponent of each element instead.
-  const bool steep = !(g2 >= -16.0f);
-  constexpr int PT = NW == 8 ? 1 : 2;               // 32-token halves of it that the wave forms
-  const int t_p = NW == 8 ? w >> 2 : 0;             // the first of them
+  // Tiles of P (16 tokens j by 16 of 32 tokens i; those right of the diagonal are neither formed nor read).
+  // 4 waves: three each, (j rows w, the first 32 i) and one tile u of (j rows 2 or 3, the second
+  // 32 i).  8 waves: two each, (j rows w % 4, half w / 4 of the i).  Their weights lam^(j-i):
+  constexpr bool kThree = NW == 4;
+  const int i_half = kThree ? 0 : w >> 2, j_tile = w & 3, j_third = 2 + (w & 1), u_third = uniform_int(w < 2 ? 1 : 0);
+  const float io_scale = r.in_scale * r.out_scale;
+  const int off0 = 16 * j_tile + c16 - 32 * i_half - 8 * g, off3 = 16 * j_third + c16 - 32 - 8 * g - 4 * u_third;
+  auto decay_of = [&](int n) { return exp2_hw(g2 * static_cast<float>(n > 0 ? n : 0)); };
+  float pm[8], pm3[4];
+  if constexpr (!STATE_ONLY) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) pm[e] = decay_of(off0 - e) * io_scale;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) pm3[e] = decay_of(off3 - e) * io_scale;
+  }
   float pw[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) pw[e] = uniform_float(exp2_hw(g2 * static_cast<float>(7 - e)));
-  const float io_scale = r.in_scale * r.out_scale;
   float pj[4];
 #pragma unroll
   for (int jt = 0; jt < 4; ++jt) pj[jt] = uniform_float(exp2_hw(g2 * static_cast<float>(16 * jt)));
+  const float out_decay = exp2_hw(g2 * static_cast<float>(c16)) * r.out_scale;
+  const float in_decay = exp2_hw(g2 * static_cast<float>(kQ - 32 - 8 * g - 7)) * r.in_scale;
 
   // where the output rows of a whole chunk go: backwards, row r of the chunk is 63 - r rows up
   const bool o_f32 = kF32 || r.o_f32;
@@ -573,8 +601,12 @@ void la_kernel(LaArgs p) {
   }
 
   if (c_begin < c_live) arrived(c_begin, present(c_begin), lane0);
-  for (int c = c_begin; c < c_live; ++c) {
-    const int n = present(c);
+  // One chunk.  PLAIN: it and the next are whole and every column is there, so that nothing is
+  // decided inside: with one or two waves a SIMD each branch taken costs its fetch (@@).
+  auto chunk = [&](auto plain, int c) __attribute__((always_inline)) {
+    constexpr bool PLAIN = decltype(plain)::value;
+    const int n = PLAIN ? kQ : present(c);
+    const bool more = PLAIN || c + 1 < c_live;
     // (opaque, so that the chunk's many LDS and memory addresses are formed here from the lane's
     // number: kept in registers over the loop they crowd out the state)
     int lane = lane_id();
@@ -585,49 +617,46 @@ void la_kernel(LaArgs p) {
     constexpr int PB = O::kPiece;
     const uint32_t q_rows = O::template row_part<RK, false>(lds_address(sQ), c16, g);
     const uint32_t p_rows = O::template row_part<RP, false>(lds_address(sP[0]), c16, g);
-    if (c + 1 < c_live) load_k(c + 1, lane);
+    if (more) load_k(plain, c + 1, lane);
 
-    // ---- P row jw: tiles of k q^T, rows i = 32 t + 8 g + 4 u + e
+    // ---- P: tiles of k q^T, rows i = 32 t + 8 g + 4 u + e, column j = c16
     if constexpr (!STATE_ONLY) {
-      piece qf[KT];
+      const uint32_t k_rows = O::template row_part<RK, true>(k_tile, 8 * (c16 >> 2) + (c16 & 3), g);
+      if (kThree || i_half == 0 || j_tile >= 2) {
+        f32x4_t s[2];
 #pragma unroll
-      for (int x = 0; x < KT; ++x) qf[x] = O::row(q_rows + (w & 3) * (16 * RK), 4 * PB * x, 0);
+        for (int u = 0; u < 2; ++u) s[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int tt = 0; tt < PT; ++tt) {
-        const int t = tt + t_p;
+        for (int x = 0; x < KT; ++x) {
+          const piece qf = O::row(q_rows + j_tile * (16 * RK), 4 * PB * x, 0);
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            s[u] = O::mma(O::row(k_rows + i_half * (32 * RK), (4 * PB * x) ^ (swizzle<RK, kF32, true>(4 * u) << 4),
+                                 4 * u * RK), qf, s[u]);
+        }
         float pv[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) pv[e] = 0.0f;
-        if (t == 0 || (w & 3) >= 2) {               // the block right of the diagonal is zero
-          const uint32_t k_rows = O::template row_part<RK, true>(k_tile, 8 * (c16 >> 2) + (c16 & 3), g) + t * (32 * RK);
-          f32x4_t s[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) s[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int x = 0; x < KT; ++x)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              s[u] = O::mma(O::row(k_rows, (4 * PB * x) ^ (swizzle<RK, kF32, true>(4 * u) << 4), 4 * u * RK), qf[x], s[u]);
-          const int off0 = 16 * (w & 3) + c16 - 32 * t - 8 * g;
-          const float pl = exp2_hw(g2 * static_cast<float>(off0 - 7)) * io_scale;
-          if (__builtin_expect(steep, 0)) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int off = off0 - e;
-              pv[e] = s[e / 4][e % 4] * (exp2_hw(g2 * static_cast<float>(off > 0 ? off : 0)) * io_scale);
-              asm volatile("" : "+v"(pv[e]));       // (kept behind the branch)
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) pv[e] = s[e / 4][e % 4] * pl * pw[e];
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) pv[e] = off0 >= e ? pv[e] : 0.0f;
-        }
+        for (int e = 0; e < 8; ++e) pv[e] = off0 >= e ? s[e / 4][e % 4] * pm[e] : 0.0f;
         piece ps[ET];
         O::template split<ET>(pv, ps);
 #pragma unroll
-        for (int m = 0; m < ET; ++m) O::put((p_rows ^ (4 * PB * t)) + (w & 3) * (16 * RP), 0, m * (kQ * RP), ps[m]);
+        for (int m = 0; m < ET; ++m) O::put((p_rows ^ (4 * PB * i_half)) + j_tile * (16 * RP), 0, m * (kQ * RP), ps[m]);
+      }
+      if constexpr (kThree) {
+        f32x4_t s = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        const int flip = u_third ? swizzle<RK, kF32, true>(4) << 4 : 0, offset = 32 * RK + u_third * (4 * RK);
+#pragma unroll
+        for (int x = 0; x < KT; ++x)
+          s = O::mma(O::row(k_rows, (4 * PB * x) ^ flip, offset), O::row(q_rows + j_third * (16 * RK), 4 * PB * x, 0), s);
+        float pv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pv[e] = off3 >= e ? s[e] * pm3[e] : 0.0f;
+        typename O::half ps[ET];
+        O::template split4<ET>(pv, ps);
+        const uint32_t at = (p_rows ^ (4 * PB) ^ (u_third ? O::half_flip(1) : 0)) + (u_third ? O::half_offset(1) : 0) +
+                            j_third * (16 * RP);
+#pragma unroll
+        for (int m = 0; m < ET; ++m) O::put_half(at + m * (kQ * RP), ps[m]);
       }
     }
 
@@ -666,11 +695,11 @@ void la_kernel(LaArgs p) {
       }
     }
     barrier_lds();                                  // P complete; the tiles of q and v are free
-    if (c + 1 < c_live) load_qv(c + 1, lane);
+    if (more) load_qv(plain, c + 1, lane);
 
     // ---- P v, transposed, on top
     if constexpr (!STATE_ONLY) {
-      const float f0 = exp2_hw(g2 * static_cast<float>(c16)) * (r.out_scale * power_q(a));
+      const float f0 = out_decay * static_cast<float>(rho);
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
         const float f = f0 * pj[jt];
@@ -695,7 +724,7 @@ void la_kernel(LaArgs p) {
             for (int jt = 0; jt < 4; ++jt)
               if (t == 0 || jt >= 2) acc[vt][jt] = O::mma(vf[vt][t], pf[jt][m], acc[vt][jt]);
       }
-      if (n < kQ) {
+      if (!PLAIN && n < kQ) {
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt)
           if (16 * jt + c16 >= n) {
@@ -706,10 +735,15 @@ void la_kernel(LaArgs p) {
     }
 
     // ---- the state: lam^n E + k^T (lam^(n-i) v)
-    const bool whole = c + 1 < c_live || n - shift == kQ;
-    if (whole && fabsf(g_q * static_cast<float>(a + 1)) < 30.0f) ++a;
-    else multiply_out(whole ? lam_q : lam_end);
-    const float wc = exp2_hw(g2 * static_cast<float>(kQ - 32 - 8 * g - 7)) * (r.in_scale * power_q(-a));
+    const bool whole = more || n - shift == kQ;
+    if (__builtin_expect(whole && fabsf(g_q * static_cast<float>(a + 1)) < 30.0f, 1)) {
+      ++a;
+      rho *= lam_q;
+      unrho *= unlam_q;
+    } else {
+      multiply_out(whole ? lam_q : lam_end);
+    }
+    const float wc = in_decay * static_cast<float>(unrho);
     const uint32_t k_cols = O::template column_part<RK, true>(k_tile, 0, 8, lane);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -748,7 +782,7 @@ void la_kernel(LaArgs p) {
       }
     }
     // (without a next chunk there is nothing to clear)
-    arrived(c + 1, c + 1 < c_live ? present(c + 1) : kQ, lane);
+    arrived(c + 1, !PLAIN && more ? present(c + 1) : kQ, lane);
 
     // ---- the output rows to memory: lane (g, c) has 4 columns of row 16 jt + c.  They are issued after
     // the wait for the next chunk's rows, so that a wait covers only the stores of the chunk before.
@@ -759,7 +793,7 @@ void la_kernel(LaArgs p) {
           if constexpr (sizeof(OUT) == 4) return make_float4(a[0], a[1], a[2], a[3]);
           else return make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
         };
-        if (VEC && n == kQ && V == VD) {
+        if (PLAIN || (VEC && n == kQ && V == VD)) {
           // a uniform address that moves on by a chunk, the lane's offset in 16 rows, 16 rows' bytes
 #pragma unroll
           for (int jt = 0; jt < 4; ++jt) {
@@ -806,14 +840,20 @@ void la_kernel(LaArgs p) {
       if (o_f32) put(static_cast<float*>(r.o));
       else put(static_cast<uint16_t*>(r.o));
     }
+  };
+  int c = c_begin;
+  if (VEC && K == KD && V == VD) {
+    const int plain = (c_live < len / kQ ? c_live : len / kQ) - 1;
+    for (; c < plain; ++c) chunk(std::true_type{}, c);
   }
+  for (; c < c_live; ++c) chunk(std::false_type{}, c);
   if (a) multiply_out(1.0);
 
   // chunks with no token: zeros
   if constexpr (!STATE_ONLY) {
-    for (int64_t c = c_live > c_begin ? c_live : c_begin; c < c_end; ++c) {
+    for (int64_t z = c_live > c_begin ? c_live : c_begin; z < c_end; ++z) {
       for (int i = tid; i < kQ * V; i += 64 * NW) {
-        const int64_t token = c * kQ + i / V;
+        const int64_t token = z * kQ + i / V;
         if (token >= L) break;
         const int64_t o = ((b * L + token) * p.H + h) * V + i % V;
         if (r.o_f32 || kF32) static_cast<float*>(r.o)[o] = 0.0f;
