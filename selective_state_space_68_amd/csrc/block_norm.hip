@@ -119,14 +119,33 @@ __device__ __forceinline__ void store_row(void* base, int64_t row0, int D, int t
 
 // A weight's values of this thread's columns (fill where there is no weight or no column).
 template <int NV, bool STRIDED>
-__device__ __forceinline__ void load_weight(float (&x)[NV][8], const float* w, int D, int t, int T, float fill) {
+__device__ __forceinline__ void load_weight(float (&x)[NV][8], const float* w, int D, int t, int T, int vec, float fill) {
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
+  for (int v = 0; v < NV; ++v) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = col_of<STRIDED>(t, T, v, e);
-      x[v][e] = w && c < D ? w[c] : fill;
+    for (int e = 0; e < 8; ++e) x[v][e] = fill;
+    if (!w) continue;
+    if (!STRIDED && vec) {
+      const int c0 = (v * T + t) * 8;
+      if (c0 < D) {
+        const float4 a = *reinterpret_cast<const float4*>(w + c0), b = *reinterpret_cast<const float4*>(w + c0 + 4);
+        x[v][0] = a.x; x[v][1] = a.y; x[v][2] = a.z; x[v][3] = a.w;
+        x[v][4] = b.x; x[v][5] = b.y; x[v][6] = b.z; x[v][7] = b.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = col_of<STRIDED>(t, T, v, e);
+        if (c < D) x[v][e] = w[c];
+      }
     }
+  }
+}
+
+// A weight's address that is not known before: its loads stay in the loop that they stand in.
+__device__ __forceinline__ const float* here(const float* w) {
+  asm volatile("" : "+s"(w));
+  return w;
 }
 
 template <int VECTORS>                              // of a row, at most
@@ -214,11 +233,6 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_fwd_kern
   const int D = static_cast<int>(p.D), vec = p.vec, t = team.t, T = team.T, group = static_cast<int>(p.group);
   int turn = 0;
   float w1[NV][8], rs[NV][8], w2[NV][8];
-  if constexpr (!LEAN) {
-    load_weight<NV, STRIDED>(w1, p.w1, D, t, T, 1.0f);
-    load_weight<NV, STRIDED>(rs, p.rs, D, t, T, 1.0f);
-    load_weight<NV, STRIDED>(w2, p.w2, D, t, T, 1.0f);
-  }
   const float inv_d = 1.0f / static_cast<float>(D), inv_g = 1.0f / static_cast<float>(group);
   Row<ACT, NV> nx, nz;
   Row<RES, NV> nr;
@@ -229,6 +243,11 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_fwd_kern
   };
   int64_t row = team.row;
   if (!LEAN && row < p.rows) fetch(row);
+  if constexpr (!LEAN) {
+    load_weight<NV, STRIDED>(w1, p.w1, D, t, T, vec, 1.0f);
+    load_weight<NV, STRIDED>(rs, p.rs, D, t, T, vec, 1.0f);
+    load_weight<NV, STRIDED>(w2, p.w2, D, t, T, vec, 1.0f);
+  }
   for (; row < p.rows; row += team.step) {
     float x[NV][8], z[NV][8], r[NV][8];
     if constexpr (LEAN) fetch(row);
@@ -254,7 +273,7 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_fwd_kern
       } else {
         group_sum<NV, ONE_WAVE>(part, group, D, lds, turn, t, T);
       }
-      if constexpr (LEAN) load_weight<NV, STRIDED>(w1, p.w1, D, t, T, 1.0f);
+      if constexpr (LEAN) load_weight<NV, STRIDED>(w1, here(p.w1), D, t, T, vec, 1.0f);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const float r1 = 1.0f / sqrtf(__builtin_fmaf(part[v], inv_g, p.eps));
@@ -262,7 +281,7 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_fwd_kern
         for (int e = 0; e < 8; ++e) x[v][e] *= r1 * w1[v][e];
       }
     }
-    if constexpr (LEAN) load_weight<NV, STRIDED>(rs, p.rs, D, t, T, 1.0f);
+    if constexpr (LEAN) load_weight<NV, STRIDED>(rs, here(p.rs), D, t, T, vec, 1.0f);
     float s[1] = {0.0f};
 #pragma unroll
     for (int v = 0; v < NV; ++v)
@@ -278,7 +297,7 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_fwd_kern
     if (p.h) store_row<RES, NV, STRIDED>(p.h, row * p.D, D, t, T, vec, x);
     if (p.y) {
       team_sum<1, ONE_WAVE>(s, lds, turn, team.waves);
-      if constexpr (LEAN) load_weight<NV, STRIDED>(w2, p.w2, D, t, T, 1.0f);
+      if constexpr (LEAN) load_weight<NV, STRIDED>(w2, here(p.w2), D, t, T, vec, 1.0f);
       const float r2 = 1.0f / sqrtf(__builtin_fmaf(s[0], inv_d, p.eps));
 #pragma unroll
       for (int v = 0; v < NV; ++v)
@@ -298,16 +317,39 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_bwd_kern
   const int D = static_cast<int>(p.D), vec = p.vec, t = team.t, T = team.T, group = static_cast<int>(p.group);
   int turn = 0;
   float w1[NV][8], rs[NV][8], w2[NV][8];
-  if constexpr (!LEAN) {
-    load_weight<NV, STRIDED>(w1, p.w1, D, t, T, 1.0f);
-    load_weight<NV, STRIDED>(rs, p.rs, D, t, T, 1.0f);
-    load_weight<NV, STRIDED>(w2, p.w2, D, t, T, 1.0f);
-  }
-  float a1[NV][8], as[NV][8], a2[NV][8];            // column sums of this team's rows
+  // Column sums of this team's rows: in registers, or (the first kLds of as, a2, a1) in LDS, every
+  // thread's own, where 1024 threads leave too few registers.
+  constexpr int kLds = MAXT == 1024 ? (NV == 1 ? 3 : 2) : 0;
+  __shared__ __attribute__((aligned(16))) float sums[kLds ? kLds * NV * 8 * MAXT : 4];
+  float a1[NV][8], as[NV][8], a2[NV][8];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int e = 0; e < 8; ++e) a1[v][e] = as[v][e] = a2[v][e] = 0.0f;
+  auto sum_at = [&](int which, int v, int half) {
+    return reinterpret_cast<float4*>(sums) + ((which * NV + v) * 2 + half) * MAXT + t;
+  };
+  auto take = [&](float (&a)[NV][8], int which) __attribute__((always_inline)) {
+    if (which >= kLds) return;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 x = *sum_at(which, v, i);
+        a[v][4 * i] = x.x; a[v][4 * i + 1] = x.y; a[v][4 * i + 2] = x.z; a[v][4 * i + 3] = x.w;
+      }
+  };
+  auto give = [&](const float (&a)[NV][8], int which) __attribute__((always_inline)) {
+    if (which >= kLds) return;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *sum_at(which, v, i) = make_float4(a[v][4 * i], a[v][4 * i + 1], a[v][4 * i + 2], a[v][4 * i + 3]);
+  };
+  give(as, 0);
+  give(a2, 1);
+  give(a1, 2);
   const float inv_d = 1.0f / static_cast<float>(D), inv_g = 1.0f / static_cast<float>(group);
   const bool one_group = group == D;
   Row<ACT, NV> nx, nz, ny;
@@ -318,30 +360,47 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_bwd_kern
       load_row<ACT, NV, STRIDED>(ny, p.dy, row * p.D, D, t, T, vec);
     }
     load_row<ACT, NV, STRIDED>(nx, p.x, row * p.x_row, D, t, T, vec);
+  };
+  auto fetch_dh = [&](int64_t row) __attribute__((always_inline)) {
     if (p.dh) load_row<RES, NV, STRIDED>(ng, p.dh, row * p.D, D, t, T, vec);
+  };
+  auto fetch_gate = [&](int64_t row) __attribute__((always_inline)) {
     if (p.gate) load_row<ACT, NV, STRIDED>(nz, p.gate, row * p.gate_row, D, t, T, vec);
   };
+  auto fetch_all = [&](int64_t row) __attribute__((always_inline)) {
+    fetch(row);
+    fetch_dh(row);
+    fetch_gate(row);
+  };
   int64_t row = team.row;
-  if (!LEAN && row < p.rows) fetch(row);
+  if (!LEAN && row < p.rows) fetch_all(row);
+  if constexpr (!LEAN) {
+    load_weight<NV, STRIDED>(w1, p.w1, D, t, T, vec, 1.0f);
+    load_weight<NV, STRIDED>(rs, p.rs, D, t, T, vec, 1.0f);
+    load_weight<NV, STRIDED>(w2, p.w2, D, t, T, vec, 1.0f);
+  }
   for (; row < p.rows; row += team.step) {
     float x[NV][8], z[NV][8], dH[NV][8], h[NV][8], dy[NV][8];
     if constexpr (LEAN) fetch(row);
     unpack_row<ACT, NV>(nx, x);
-    if (p.gate) unpack_row<ACT, NV>(nz, z);
+    if (!LEAN && p.gate) unpack_row<ACT, NV>(nz, z);
     if (p.w2) {
       unpack_row<RES, NV>(nh, h);
       unpack_row<ACT, NV>(ny, dy);
     }
-    if (p.dh) {
-      unpack_row<RES, NV>(ng, dH);
-    } else {
+    auto take_dh = [&]() __attribute__((always_inline)) {
+      if (p.dh) {
+        unpack_row<RES, NV>(ng, dH);
+      } else {
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dH[v][e] = 0.0f;
-    }
-    if (!LEAN && row + team.step < p.rows) fetch(row + team.step);
-    if constexpr (LEAN) load_weight<NV, STRIDED>(w2, p.w2, D, t, T, 1.0f);
+          for (int e = 0; e < 8; ++e) dH[v][e] = 0.0f;
+      }
+    };
+    if constexpr (!LEAN) take_dh();
+    if (!LEAN && row + team.step < p.rows) fetch_all(row + team.step);
+    if constexpr (LEAN) load_weight<NV, STRIDED>(w2, here(p.w2), D, t, T, vec, 1.0f);
     // the sums over the row that need nothing but the inputs, together
     float r1[NV], s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -359,9 +418,14 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_bwd_kern
       }
     }
     if (p.w2 || one_group) team_sum<3, ONE_WAVE>(s, lds, turn, team.waves);
+    if constexpr (LEAN) {
+      fetch_dh(row);
+      take_dh();
+    }
     if (p.w2) {
       const float r2 = 1.0f / sqrtf(__builtin_fmaf(s[0], inv_d, p.eps));
       const float m = s[1] * inv_d * r2 * r2;
+      take(a2, 1);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -371,7 +435,12 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_bwd_kern
           dH[v][e] = __builtin_fmaf(r2, D > 1 ? __builtin_fmaf(-h[v][e], m, a) : a * p.eps * r2 * r2, dH[v][e]);
         }
     }
+    if (p.w2) give(a2, 1);
     if (p.dres) store_row<RES, NV, STRIDED>(p.dres, row * p.D, D, t, T, vec, dH);
+    if constexpr (LEAN) {
+      fetch_gate(row);
+      if (p.gate) unpack_row<ACT, NV>(nz, z);
+    }
     // x becomes x r1; n = x r1 post_weight
     if (p.w1) {
       if (one_group) {
@@ -387,9 +456,11 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_bwd_kern
         for (int e = 0; e < 8; ++e) x[v][e] *= r1[v];
       }
     }
-    if constexpr (LEAN) load_weight<NV, STRIDED>(w1, p.w1, D, t, T, 1.0f);
-    if constexpr (LEAN) load_weight<NV, STRIDED>(rs, p.rs, D, t, T, 1.0f);
+    if constexpr (LEAN) load_weight<NV, STRIDED>(w1, here(p.w1), D, t, T, vec, 1.0f);
+    if constexpr (LEAN) load_weight<NV, STRIDED>(rs, here(p.rs), D, t, T, vec, 1.0f);
     float m[NV];
+    take(as, 0);
+    take(a1, 2);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       m[v] = 0.0f;
@@ -411,6 +482,8 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_bwd_kern
         m[v] = __builtin_fmaf(dH[v][e], x[v][e], m[v]);
       }
     }
+    give(as, 0);
+    give(a1, 2);
     if (p.gate) store_row<ACT, NV, STRIDED>(p.dgate, row * p.D, D, t, T, vec, z);
     if (p.w1) {
       if (one_group) {
@@ -456,14 +529,17 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_bwd_kern
       store_row<ActF32, NV, STRIDED>(to, 0, D, t, T, vec, a);
     }
   };
+  take(as, 0);
+  take(a2, 1);
+  take(a1, 2);
   leave(a1, p.dw1, out);
   leave(as, p.drs, out + D);
   leave(a2, p.dw2, out + 2 * static_cast<int64_t>(D));
 }
 
 // Column sums over the workgroups' partial sums: 64 columns by 16 strands of parts a
-// workgroup, 8 parts of a strand in flight; strands are added in order.
-constexpr int kStrands = 16;
+// workgroup, 16 parts of a strand in flight; strands are added in order.
+constexpr int kStrands = 16, kFlight = 16;
 __global__ __launch_bounds__(64 * kStrands) void norm_bwd_sum_kernel(NormArgs p) {
   __shared__ float red[kStrands][64];
   const int which = blockIdx.y;
@@ -474,15 +550,15 @@ __global__ __launch_bounds__(64 * kStrands) void norm_bwd_sum_kernel(NormArgs p)
   const float* src = p.part + which * p.D + (c < p.D ? c : p.D - 1);
   const int64_t step = 3 * p.D;
   float s = 0.0f;
-  for (int i = strand; i < p.parts; i += 8 * kStrands) {
-    float v[8];
+  for (int i = strand; i < p.parts; i += kFlight * kStrands) {
+    float v[kFlight];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < kFlight; ++u) {
       const int k = i + u * kStrands;
       v[u] = src[(k < p.parts ? k : i) * step];
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) s += i + u * kStrands < p.parts ? v[u] : 0.0f;
+    for (int u = 0; u < kFlight; ++u) s += i + u * kStrands < p.parts ? v[u] : 0.0f;
   }
   red[strand][lane] = s;
   __syncthreads();
@@ -494,9 +570,11 @@ __global__ __launch_bounds__(64 * kStrands) void norm_bwd_sum_kernel(NormArgs p)
 }
 
 // How a row is laid out over threads: one wave up to 512 columns, else whole waves at one
-// vector of 8 columns a thread up to 8192, two past that.  Where a workgroup has more than 512
-// threads its registers (128 a thread) do not hold the next row and the weights besides the
-// gradient's sums: those kernels are LEAN, asking for rows and weights as they need them.
+// vector of 8 columns a thread up to 8192, two past that.  Workgroups of more than 512 threads have
+// 128 registers a thread, which hold neither the gradient's sums (they go to LDS) nor the next row and the
+// weights: those kernels are LEAN, asking for rows and weights as they need them.  Measured, gradients of
+// bfloat16 rows with gate, scale and float32 residual: 8192 x 5120 345 us with the sums in registers (spilled),
+// 282 in LDS, 330 with two vectors a thread and 512 threads; 4096 x 8192 257, 205, 215.
 struct Shape {
   int threads, rows;                  // threads and rows of a workgroup
 };
@@ -538,7 +616,10 @@ hipError_t launch_norm(const NormArgs& a, Dt dt, Dt rdt, bool bwd, int blocks, h
   return hipGetLastError();
 }
 
-// Workgroups: at most `most` threads' worth on each of the 256 CUs.
+// Workgroups: at most `most` threads' worth on each of the 256 CUs.  Rows in flight against registers of
+// column sums to add up: 1024 forwards (16384 x 2560 109 us, 185 with 512, 134 with 2048; 4096 x 1024 11.6, 14, 15.3) but 2048
+// where a row takes over 512 threads (8192 x 5120, 80 groups with gate: 58 us, 62 with 1024), 512
+// backwards (4096 x 1024 34 us, 44 with 1024, 41 with 256; 16384 x 512 43, 50, 54; 1534 x 769 23, 29, 23).
 int blocks_of(int64_t rows, int64_t D, int most) {
   const Shape sh = shape_of(D);
   const int64_t need = (rows + sh.rows - 1) / sh.rows;
@@ -548,10 +629,10 @@ int blocks_of(int64_t rows, int64_t D, int most) {
 
 }  // namespace
 
-int norm_bwd_parts(int64_t rows, int64_t D) { return blocks_of(rows, D, 1024); }
+int norm_bwd_parts(int64_t rows, int64_t D) { return blocks_of(rows, D, 512); }
 
 hipError_t launch_norm_fwd(const NormArgs& a, Dt dt, Dt rdt, hipStream_t s) {
-  return launch_norm(a, dt, rdt, false, blocks_of(a.rows, a.D, 2048), s);
+  return launch_norm(a, dt, rdt, false, blocks_of(a.rows, a.D, shape_of(a.D).threads > 512 ? 2048 : 1024), s);
 }
 
 hipError_t launch_norm_bwd(const NormArgs& a, Dt dt, Dt rdt, hipStream_t s) {

@@ -258,8 +258,14 @@ __device__ __forceinline__ Pair pair_of(double d) {
   const float lo = static_cast<float>(d - static_cast<double>(hi));
   return Pair{hi, lo == lo ? lo : 0.0f};              // (inf - inf where lam^n overflows)
 }
-__device__ __forceinline__ Pair decay_pair(const float* log_decay, int h, int n) {
-  return pair_of(decay_power(log_decay, h, n));
+// lam^n to float32 accuracy at any n: the exponent is reduced in float64.  (exp(), of which the
+// factors above take a few a workgroup, costs about a microsecond.)
+__device__ __forceinline__ float decay_float(const float* log_decay, int h, int n) {
+  double x = static_cast<double>(log_decay[h]) * 1.4426950408889634 * n;
+  if (n == 0) x = 0.0;                              // (a decay of exactly 0)
+  x = x < -1.0e4 ? -1.0e4 : x > 1.0e4 ? 1.0e4 : x;  // (NaN passes through)
+  const double whole = __builtin_floor(x);
+  return __builtin_ldexpf(exp2_hw(static_cast<float>(x - whole)), static_cast<int>(whole));
 }
 
 __device__ __forceinline__ int lane_id() { return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)); }
@@ -881,9 +887,8 @@ void la_kernel(LaArgs p) {
 }
 
 // Chains the segments' own sums T_s into the E entering each segment (written over T_s) and
-// the state after the last token.  A thread takes kChain entries 256 apart, so that the decays
-// (float64 exponentials) are a small part of its work, and reads kAhead segments' sums at a time:
-// only the arithmetic is a chain.
+// the state after the last token.  A thread takes kChain entries 256 apart and reads kAhead segments'
+// sums at a time: only the arithmetic is a chain.
 constexpr int kChain = 4, kAhead = 8;
 __global__ __launch_bounds__(256) void la_chain_kernel(LaArgs p) {
   const LaRole& r = p.role[blockIdx.z];
@@ -903,8 +908,7 @@ __global__ __launch_bounds__(256) void la_chain_kernel(LaArgs p) {
   float s[kChain], T[kAhead][kChain];
 #pragma unroll
   for (int x = 0; x < kChain; ++x) s[x] = carry && i0 + 256 * x < KV ? carry[i0 + 256 * x] : 0.0f;
-  auto times = [](const Pair& d, float x) { return __builtin_fmaf(d.hi, x, d.lo * x); };
-  Pair l1, lS;
+  float l1 = 0.0f, lS = 0.0f;
   for (int k0 = 0; k0 < p.nseg; k0 += kAhead) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -915,19 +919,19 @@ __global__ __launch_bounds__(256) void la_chain_kernel(LaArgs p) {
         T[u][x] = read && i0 + 256 * x < KV ? slot[static_cast<int64_t>(k) * KV + i0 + 256 * x] : 0.0f;
     }
     if (k0 == 0) {                                  // (while the first sums are on their way)
-      l1 = decay_pair(p.log_decay, h, 1);
-      lS = decay_pair(p.log_decay, h, seg_tokens);
+      l1 = decay_float(p.log_decay, h, 1);
+      lS = decay_float(p.log_decay, h, seg_tokens);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int k = k0 + u;
       if (k >= p.nseg) break;
       const int n = tokens(k);
-      const Pair d = n == seg_tokens ? lS : decay_pair(p.log_decay, h, n);
+      const float d = n == seg_tokens ? lS : decay_float(p.log_decay, h, n);
 #pragma unroll
       for (int x = 0; x < kChain; ++x) {
-        if (i0 + 256 * x < KV) slot[static_cast<int64_t>(k) * KV + i0 + 256 * x] = r.reverse ? s[x] : times(l1, s[x]);
-        if (n > 0) s[x] = times(d, s[x]) + (r.reverse ? times(l1, T[u][x]) : T[u][x]);
+        if (i0 + 256 * x < KV) slot[static_cast<int64_t>(k) * KV + i0 + 256 * x] = r.reverse ? s[x] : l1 * s[x];
+        if (n > 0) s[x] = __builtin_fmaf(d, s[x], r.reverse ? l1 * T[u][x] : T[u][x]);
       }
     }
   }
@@ -938,15 +942,33 @@ __global__ __launch_bounds__(256) void la_chain_kernel(LaArgs p) {
   }
 }
 
-template <typename ACT>
-__global__ __launch_bounds__(256) void la_sum_heads_kernel(const float* part, void* out, int64_t total, int64_t share,
-                                                           int64_t d) {
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += step) {   // [token][head][d]
-    const float* src = part + i / d * share * d + i % d;
-    float s = 0.0f;
-    for (int64_t x = 0; x < share; ++x) s += src[x * d];
-    store_act<ACT>(out, i, s);
+// Sums over the state heads that share a head, of one or two tensors.  W values a thread, a row of d
+// values by d / W threads, rows a grid apart (so that nothing is divided but the thread's number).
+template <typename ACT, int W>
+__global__ __launch_bounds__(256) void la_sum_heads_kernel(LaSum a, LaSum b) {
+  const LaSum& x = blockIdx.y ? b : a;
+  const int per_row = x.d / W, rows = 256 / per_row, t = threadIdx.x / per_row, c = threadIdx.x % per_row * W;
+  if (t >= rows) return;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows + t; row < x.rows; row += static_cast<int64_t>(gridDim.x) * rows) {
+    const float* src = x.part + row * x.share * x.d + c;
+    float s[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) s[e] = 0.0f;
+    for (int i = 0; i < x.share; ++i, src += x.d) {
+      if constexpr (W == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(src);
+        s[0] += y.x; s[1] += y.y; s[2] += y.z; s[3] += y.w;
+      } else {
+        s[0] += *src;
+      }
+    }
+    if constexpr (W == 4 && ACT::kBytes == 4)
+      *reinterpret_cast<float4*>(static_cast<float*>(x.out) + row * x.d + c) = make_float4(s[0], s[1], s[2], s[3]);
+    else if constexpr (W == 4)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(x.out) + row * x.d + c) =
+          make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+    else
+      store_act<ACT>(x.out, row * x.d + c, s[0]);
   }
 }
 
@@ -1037,12 +1059,28 @@ hipError_t launch_la(const LaArgs& a, Dt dt, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_la_sum_heads(const float* part, void* out, int64_t tokens, int64_t heads, int64_t share, int64_t d,
-                               Dt dt, hipStream_t s) {
-  const int64_t total = tokens * heads * d, blocks = (total + 255) / 256;
-  const dim3 grid(static_cast<unsigned>(blocks < 8192 ? blocks : 8192));
-  if (dt == Dt::BF16) hipLaunchKernelGGL(la_sum_heads_kernel<ActBF16>, grid, dim3(256), 0, s, part, out, total, share, d);
-  else hipLaunchKernelGGL(la_sum_heads_kernel<ActF32>, grid, dim3(256), 0, s, part, out, total, share, d);
+hipError_t launch_la_sum_heads(const LaSum* sums, int n, Dt dt, hipStream_t s) {
+  for (int i = 0; i < n;) {                         // two of one width go in one launch
+    const LaSum &a = sums[i], &b = i + 1 < n && sums[i + 1].d == a.d ? sums[i + 1] : a;
+    const int both = &a == &b ? 1 : 2;
+    const int64_t most = a.rows > b.rows ? a.rows : b.rows;
+    auto vector = [](const LaSum& x) { return x.d % 4 == 0 && reinterpret_cast<uintptr_t>(x.out) % 16 == 0; };
+    auto go = [&](auto act, auto width) {
+      constexpr int W = decltype(width)::value;
+      const int64_t rows = 256 / (a.d / W), blocks = (most + rows - 1) / rows;
+      const dim3 grid(static_cast<unsigned>(blocks < 4096 ? blocks : 4096), both);
+      hipLaunchKernelGGL((la_sum_heads_kernel<decltype(act), W>), grid, dim3(256), 0, s, a, b);
+    };
+    const bool vec = vector(a) && vector(b);
+    if (dt == Dt::BF16) {
+      if (vec) go(ActBF16{}, std::integral_constant<int, 4>{});
+      else go(ActBF16{}, std::integral_constant<int, 1>{});
+    } else {
+      if (vec) go(ActF32{}, std::integral_constant<int, 4>{});
+      else go(ActF32{}, std::integral_constant<int, 1>{});
+    }
+    i += both;
+  }
   return hipGetLastError();
 }
 

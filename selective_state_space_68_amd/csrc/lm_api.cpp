@@ -289,9 +289,15 @@ ssm_status ssm_linear_attention_bwd(const void* q, const void* k, const void* v,
   }
   hipError_t err = ssm::launch_la(a, dt_of(dt), s);
   const int64_t width[3] = {K, K, V};
-  for (int i = 0; i < 3 && err == hipSuccess; ++i)
-    if (part[i])
-      err = ssm::launch_la_sum_heads(part[i], outp[i], batch * L, share[i], H / share[i], width[i], dt_of(dt), s);
+  ssm::LaSum sums[3];
+  int n = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (!part[i]) continue;
+    ssm::LaSum& x = sums[n++];
+    x.part = part[i]; x.out = outp[i]; x.rows = batch * L * share[i];
+    x.share = static_cast<int>(H / share[i]); x.d = static_cast<int>(width[i]);
+  }
+  if (err == hipSuccess && n) err = ssm::launch_la_sum_heads(sums, n, dt_of(dt), s);
   return from_hip(err);
 }
 

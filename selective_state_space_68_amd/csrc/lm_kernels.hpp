@@ -48,9 +48,15 @@ constexpr int kLaMaxDim = 128;        // largest K and V
 int la_segments(int64_t batch, int64_t L, int64_t H, int roles);
 hipError_t launch_la(const LaArgs& a, Dt dt, hipStream_t s);
 
-// out[batch][L][heads][d] (act) = sum over the H / heads sharing heads of part[batch][L][H][d].
-hipError_t launch_la_sum_heads(const float* part, void* out, int64_t tokens, int64_t heads, int64_t share, int64_t d,
-                               Dt dt, hipStream_t s);
+// out[rows][d] (act) = sum over `share` of part[rows][share][d]: rows are the (batch row, token, head), d <= 128.
+// `part` is 16-byte aligned.
+struct LaSum {
+  const float* part = nullptr;
+  void* out = nullptr;
+  int64_t rows = 0;
+  int share = 1, d = 1;
+};
+hipError_t launch_la_sum_heads(const LaSum* sums, int n, Dt dt, hipStream_t s);
 
 // dst = src, or zeros when src is null (the state of an attention over no tokens).
 hipError_t launch_la_copy_state(float* dst, const float* src, int64_t n, hipStream_t s);
