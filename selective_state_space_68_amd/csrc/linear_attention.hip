@@ -304,6 +304,12 @@ __device__ __forceinline__ void load_to_lds(uint32_t tile, const char* src) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off"
                :: "s"(m0), "v"(src) : "memory");
 }
+// (4 bytes a lane, to M0 + 4 l)
+__device__ __forceinline__ void load_word_to_lds(uint32_t tile, const char* src) {
+  const int m0 = uniform_int(static_cast<int>(tile));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, off"
+               :: "s"(m0), "v"(src) : "memory");
+}
 
 // One tensor's rows into its LDS tile.  Whole chunks take the short way: a uniform address that moves
 // on by a chunk, and for each of the wave's instructions (1024 bytes, 64 lanes of 16) the lane's offset,
@@ -361,7 +367,23 @@ struct TileLoad {
   }
 };
 
-// Clears rows n.. of the slots that this wave's load_tile filled.
+// The same in 4-byte words, for rows that start at any word: four times the instructions, 256 bytes
+// each, at addresses formed where they are used.  A wave fills the same part of the tile.
+template <typename ELEM, int RB, int NW, bool PERM>
+__device__ __forceinline__ void load_tile_words(uint32_t tile, const ELEM* base, int64_t step, int last, int cols, int w,
+                                                int lane) {
+  constexpr int kWords = RB / 4, kInstr = kQ * RB / 256 / NW;
+  const int64_t bytes = step * static_cast<int64_t>(sizeof(ELEM));
+#pragma unroll 4
+  for (int i = 0; i < kInstr; ++i) {
+    const int word = (w * kInstr + i) * 64 + lane, row = word / kWords, r = row < last ? row : last;
+    const int byte = (word % kWords * 4) ^ (swizzle<RB, sizeof(ELEM) == 4, PERM>(row) << 4);
+    if (byte < cols * static_cast<int>(sizeof(ELEM)))
+      load_word_to_lds(tile + (w * kInstr + i) * 256, reinterpret_cast<const char*>(base) + r * bytes + byte);
+  }
+}
+
+// Clears rows n.. of the slots that this wave's loads filled.
 template <int RB, int NW>
 __device__ __forceinline__ void clear_tile(char* tile, int n, int w, int lane) {
   constexpr int kSlots = RB / 16, kInstr = kQ * RB / 1024 / NW;
@@ -372,7 +394,7 @@ __device__ __forceinline__ void clear_tile(char* tile, int n, int w, int lane) {
   }
 }
 
-// The same element by element, for rows that do not move as 16-byte vectors (rows past `last` as zeros).
+// The same element by element, for bfloat16 rows that do not even start at a word (rows past `last` as zeros).
 template <typename ELEM, int RB, int NW, bool PERM>
 __device__ __forceinline__ void load_tile_scalar(char* tile, const ELEM* base, int64_t step, int last, int cols, int tid) {
   constexpr int kCols = RB / sizeof(ELEM);
@@ -393,7 +415,7 @@ __device__ __forceinline__ void load_tile_scalar(char* tile, const ELEM* base, i
 template <typename ACT, int VD>
 constexpr int kColumnTiles = sizeof(typename Op<ACT>::elem) == 2 && VD == 128 ? 2 : 1;
 
-template <typename ACT, int KD, int VD, bool VEC, bool STATE_ONLY>
+template <typename ACT, int KD, int VD, int MOVE, bool STATE_ONLY>
 __global__ __launch_bounds__((4 * VD / kColumnTiles<ACT, VD>), VD == 128 || sizeof(typename Op<ACT>::elem) == 4 ? 2 : 3)
 void la_kernel(LaArgs p) {
   constexpr int VT = kColumnTiles<ACT, VD>;
@@ -450,7 +472,7 @@ void la_kernel(LaArgs p) {
   TileLoad<elem, RK, NW, true> k_load;
   TileLoad<elem, RK, NW, false> q_load;
   TileLoad<elem, RV, NW, false> v_load;
-  if constexpr (VEC) {
+  if constexpr (MOVE == 16) {
     k_load.start(kg, kstep, c_begin, K, w, lane0);
     if constexpr (!STATE_ONLY) q_load.start(qg, qstep, c_begin, K, w, lane0);
     v_load.start(vg, vstep, c_begin, V, w, lane0);
@@ -459,10 +481,12 @@ void la_kernel(LaArgs p) {
     constexpr bool PLAIN = decltype(plain)::value;
     const int last = len - 1 - c * kQ;
     const int64_t r0 = static_cast<int64_t>(c) * kQ;
-    if constexpr (VEC) {
-      const uint32_t tile = lds_address(sKK[0]) + (c & 1) * (kQ * RK);
+    const uint32_t tile = lds_address(sKK[0]) + (c & 1) * (kQ * RK);
+    if constexpr (MOVE == 16) {
       if (PLAIN || last >= kQ - 1) k_load.template whole<PLAIN>(tile, K, w, lane);
       else k_load.part(tile, kg + r0 * kstep, kstep, last, K, w, lane);
+    } else if constexpr (MOVE == 4) {
+      load_tile_words<elem, RK, NW, true>(tile, kg + r0 * kstep, kstep, last, K, w, lane);
     } else {
       load_tile_scalar<elem, RK, NW, true>(sKK[c & 1], kg + r0 * kstep, kstep, last, K, tid);
     }
@@ -471,7 +495,7 @@ void la_kernel(LaArgs p) {
     constexpr bool PLAIN = decltype(plain)::value;
     const int last = len - 1 - c * kQ;
     const int64_t r0 = static_cast<int64_t>(c) * kQ;
-    if constexpr (VEC) {
+    if constexpr (MOVE == 16) {
       if (PLAIN || last >= kQ - 1) {
         if constexpr (!STATE_ONLY) q_load.template whole<PLAIN>(lds_address(sQ), K, w, lane);
         v_load.template whole<PLAIN>(lds_address(sV), V, w, lane);
@@ -479,6 +503,9 @@ void la_kernel(LaArgs p) {
         if constexpr (!STATE_ONLY) q_load.part(lds_address(sQ), qg + r0 * qstep, qstep, last, K, w, lane);
         v_load.part(lds_address(sV), vg + r0 * vstep, vstep, last, V, w, lane);
       }
+    } else if constexpr (MOVE == 4) {
+      if constexpr (!STATE_ONLY) load_tile_words<elem, RK, NW, false>(lds_address(sQ), qg + r0 * qstep, qstep, last, K, w, lane);
+      load_tile_words<elem, RV, NW, false>(lds_address(sV), vg + r0 * vstep, vstep, last, V, w, lane);
     } else {
       if constexpr (!STATE_ONLY) load_tile_scalar<elem, RK, NW, false>(sQ, qg + r0 * qstep, qstep, last, K, tid);
       load_tile_scalar<elem, RV, NW, false>(sV, vg + r0 * vstep, vstep, last, V, tid);
@@ -486,7 +513,7 @@ void la_kernel(LaArgs p) {
   };
   // Waits for this wave's part of chunk c's rows (and for its stores of the chunk before).
   auto arrived = [&](int c, int n, int lane) __attribute__((always_inline)) {
-    if constexpr (VEC) {
+    if constexpr (MOVE > 0) {
       __builtin_amdgcn_s_waitcnt(0x0f70);           // vmcnt(0); expcnt and lgkmcnt as they are
       if (n < kQ) {
         clear_tile<RK, NW>(sKK[c & 1], n, w, lane);
@@ -496,7 +523,7 @@ void la_kernel(LaArgs p) {
     }
   };
   auto present = [&](int c) { return len - c * kQ < kQ ? len - c * kQ : kQ; };
-  if constexpr (VEC) {
+  if constexpr (MOVE > 0) {
     if (K < KD || V < VD) {                         // columns that the loads leave alone
       clear_tile<RK, NW>(sKK[0], 0, w, lane0);
       clear_tile<RK, NW>(sKK[1], 0, w, lane0);
@@ -596,7 +623,7 @@ void la_kernel(LaArgs p) {
   char* o_next = nullptr;
   int64_t o_move = 0;
   uint32_t o_off = 0, o_rows = 0;
-  if constexpr (!STATE_ONLY && VEC) {
+  if constexpr (!STATE_ONLY && MOVE == 16) {
     const int esz = o_f32 ? 4 : 2;
     const int64_t bytes = static_cast<int64_t>(p.H) * V * esz, r0 = static_cast<int64_t>(c_begin) * kQ;
     o_next = static_cast<char*>(r.o) + (b * L + (reverse ? len - kQ - r0 : r0)) * bytes + static_cast<int64_t>(h) * V * esz;
@@ -799,7 +826,7 @@ void la_kernel(LaArgs p) {
           if constexpr (sizeof(OUT) == 4) return make_float4(a[0], a[1], a[2], a[3]);
           else return make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
         };
-        if (PLAIN || (VEC && n == kQ && V == VD)) {
+        if (PLAIN || (MOVE == 16 && n == kQ && V == VD)) {
           // a uniform address that moves on by a chunk, the lane's offset in 16 rows, 16 rows' bytes
 #pragma unroll
           for (int jt = 0; jt < 4; ++jt) {
@@ -830,7 +857,7 @@ void la_kernel(LaArgs p) {
 #pragma unroll
           for (int vt = 0; vt < VT; ++vt) {
             const int v0 = 16 * (VT * w + vt) + 4 * g;
-            if constexpr (VEC) {
+            if (MOVE == 16 || r.o_vec) {
               if (v0 < V) *reinterpret_cast<decltype(four(acc[0][0]))*>(o + v0) = four(acc[vt][jt]);
             } else {
 #pragma unroll
@@ -848,7 +875,7 @@ void la_kernel(LaArgs p) {
     }
   };
   int c = c_begin;
-  if (VEC && K == KD && V == VD) {
+  if (MOVE == 16 && K == KD && V == VD) {
     const int plain = (c_live < len / kQ ? c_live : len / kQ) - 1;
     for (; c < plain; ++c) chunk(std::true_type{}, c);
   }
@@ -981,16 +1008,17 @@ template <typename ACT, int KD, int VD>
 void launch_la_t(const LaArgs& a, bool state_only, hipStream_t s) {
   const int64_t items = (a.batch * a.H * a.nseg + 7) / 8 * 8;
   const dim3 grid(static_cast<unsigned>(items * a.nroles)), block(4 * VD / kColumnTiles<ACT, VD>);
-  if (a.role[0].vec) {
-    if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VD, true, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((la_kernel<ACT, KD, VD, true, false>), grid, block, 0, s, a);
-  } else {
-    if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VD, false, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((la_kernel<ACT, KD, VD, false, false>), grid, block, 0, s, a);
-  }
+  auto go = [&](auto move) {
+    constexpr int MOVE = decltype(move)::value;
+    if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VD, MOVE, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((la_kernel<ACT, KD, VD, MOVE, false>), grid, block, 0, s, a);
+  };
+  if (a.role[0].move == 16) go(std::integral_constant<int, 16>{});
+  else if (ACT::kBytes == 4 || a.role[0].move == 4) go(std::integral_constant<int, 4>{});
+  else if constexpr (ACT::kBytes == 2) go(std::integral_constant<int, 0>{});
 }
 
-// One launch for all of `a`'s roles, which have one tile shape and one `vec`.
+// One launch for all of `a`'s roles, which have one tile shape and one `move`.
 void launch_la_roles(const LaArgs& a, Dt dt, bool state_only, hipStream_t s) {
   const bool k2 = a.role[0].K > 64, v2 = a.role[0].V > 64;
   auto go = [&](auto act) {
@@ -1029,18 +1057,20 @@ hipError_t launch_la(const LaArgs& a, Dt dt, hipStream_t s) {
   const int64_t nchunks = (a.L + kQ - 1) / kQ;
   LaArgs all = a;
   all.seg_chunks = (nchunks + a.nseg - 1) / a.nseg;
-  // launches `n` of all's roles, together where they can
+  // launches `n` of all's roles, those of one tile shape together
   auto run = [&](const int* which, int n, bool state_only) {
-    LaArgs x = all;
-    bool same = true;
+    bool done[3] = {};
     for (int i = 0; i < n; ++i) {
-      x.role[i] = all.role[which[i]];
-      same = same && (x.role[i].K > 64) == (x.role[0].K > 64) && (x.role[i].V > 64) == (x.role[0].V > 64) &&
-             x.role[i].vec == x.role[0].vec;
-    }
-    x.nroles = same ? n : 1;
-    for (int i = 0; i < n; i += x.nroles) {
-      if (!same) x.role[0] = all.role[which[i]];
+      if (done[i]) continue;
+      const LaRole& r = all.role[which[i]];
+      LaArgs x = all;
+      x.nroles = 0;
+      for (int j = i; j < n; ++j) {
+        const LaRole& o = all.role[which[j]];
+        if ((o.K > 64) != (r.K > 64) || (o.V > 64) != (r.V > 64) || o.move != r.move) continue;
+        x.role[x.nroles++] = o;
+        done[j] = true;
+      }
       launch_la_roles(x, dt, state_only, s);
     }
   };

@@ -68,14 +68,23 @@ bool make_view(const int64_t* strides, const int64_t (&n)[DIMS], int64_t width, 
   return mul_ok(last, elem, &v->extent) && v->extent <= kMaxBytes;
 }
 
-// Whether every row of the tensor starts 16-byte aligned (and the rows of a tile lie near enough).
+// Whether every row of the tensor starts at a multiple of `unit` bytes.
 template <int DIMS>
-bool rows_aligned(const void* p, const View<DIMS>& v, uint64_t elem) {
-  if (!aligned(p, 16) || (DIMS == 3 && v.stride[1] > kMaxTokenStride)) return false;
+bool rows_aligned(const void* p, const View<DIMS>& v, uint64_t elem, uint64_t unit) {
+  if (!aligned(p, unit)) return false;
   for (int i = 0; i < DIMS; ++i)
-    if (static_cast<uint64_t>(v.stride[i]) * elem % 16) return false;
+    if (static_cast<uint64_t>(v.stride[i]) * elem % unit) return false;
   return true;
 }
+
+// Bytes in which `width` elements of every row can move (16, with the rows of a tile near enough; 4; or 0: an element).
+int row_move(const void* p, const View<3>& v, int64_t width, uint64_t elem) {
+  const uint64_t bytes = static_cast<uint64_t>(width) * elem;
+  if (width % 8 == 0 && v.stride[1] <= kMaxTokenStride && rows_aligned(p, v, elem, 16)) return 16;
+  return bytes % 4 == 0 && rows_aligned(p, v, elem, 4) ? 4 : 0;
+}
+
+int least(int a, int b) { return a < b ? a : b; }
 
 bool any_overlap(const Span* outs, int n_out, const Span* ins, int n_in) {
   for (int i = 0; i < n_out; ++i) {
@@ -193,8 +202,9 @@ ssm_status ssm_linear_attention_fwd(const void* q, const void* k, const void* v,
   r.seg = static_cast<float*>(workspace);
   r.sk = static_cast<int>(V); r.sv = 1; r.K = static_cast<int>(K); r.V = static_cast<int>(V);
   r.out_scale = scale;
-  r.vec = K % 8 == 0 && V % 8 == 0 && rows_aligned(q, t.q, e) && rows_aligned(k, t.k, e) && rows_aligned(v, t.v, e) &&
-          aligned(out, 16);
+  r.move = least(least(row_move(q, t.q, K, e), row_move(k, t.k, K, e)), row_move(v, t.v, V, e));
+  r.o_vec = V % 4 == 0 && aligned(out, 4 * e);
+  if (r.move == 16 && !aligned(out, 16)) r.move = 4;
   return from_hip(ssm::launch_la(a, dt_of(dt), s));
 }
 
@@ -284,8 +294,10 @@ ssm_status ssm_linear_attention_bwd(const void* q, const void* k, const void* v,
     r.sv = i == 2 ? 1 : static_cast<int>(V);
     r.in_scale = i > 0 ? scale : 1.0f;
     r.out_scale = i > 0 ? 1.0f : scale;
-    r.vec = K % 8 == 0 && V % 8 == 0 && aligned(r.o, 16);
-    for (int x = 0; x < 3; ++x) r.vec = r.vec && rows_aligned(o[x].p, *o[x].view, e);
+    r.move = 16;
+    for (int x = 0; x < 3; ++x) r.move = least(r.move, row_move(o[x].p, *o[x].view, o[x].width, e));
+    r.o_vec = r.V % 4 == 0 && aligned(r.o, r.o_f32 ? 16 : 4 * e);
+    if (r.move == 16 && !aligned(r.o, 16)) r.move = 4;
   }
   hipError_t err = ssm::launch_la(a, dt_of(dt), s);
   const int64_t width[3] = {K, K, V};
@@ -371,7 +383,7 @@ ssm_status check_norm(const void* x, int64_t x_stride, const void* gate, int64_t
 // Whether all rows move as 8-element vectors.
 bool norm_vec(const NormSizes& sz, const void* x, const void* gate, int64_t D, uint64_t e, const void* const* packed,
               int n) {
-  bool ok = D % 8 == 0 && rows_aligned(x, sz.x, e) && (!gate || rows_aligned(gate, sz.gate, e));
+  bool ok = D % 8 == 0 && rows_aligned(x, sz.x, e, 16) && (!gate || rows_aligned(gate, sz.gate, e, 16));
   for (int i = 0; i < n; ++i) ok = ok && aligned(packed[i], 16);
   return ok;
 }

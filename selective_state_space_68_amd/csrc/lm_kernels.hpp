@@ -28,7 +28,8 @@ struct LaRole {
   int K = 0, V = 0;
   float in_scale = 1.0f, out_scale = 1.0f;
   int reverse = 0;
-  int vec = 0;                                           // rows of q, k, v, o move as 8-element vectors
+  int move = 0;                                          // bytes in which rows of q, k and v move: 16, 4, or 0 (an element)
+  int o_vec = 0;                                         // rows of o move as 4-element vectors
 };
 
 struct LaArgs {

@@ -76,6 +76,9 @@ SHAPES = [   # batch, L, H, K, V, heads of q, k, v
     (1, 129, 2, 33, 17, None),           # element by element
     (1, 70, 1, 1, 1, None),
     (3, 63, 2, 100, 128, (2, 1, 1)),
+    (2, 193, 2, 100, 100, None),         # words
+    (1, 140, 3, 34, 98, (3, 1, 1)),
+    (2, 300, 2, 128, 50, (1, 2, 2)),
     (1, 1500, 2, 64, 64, None),
 ]
 
@@ -165,9 +168,9 @@ def test_decays_from_none_to_all(log_decay):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("K,V,offset", [(64, 64, 0), (64, 64, 1), (40, 24, 0)])
+@pytest.mark.parametrize("K,V,offset", [(64, 64, 0), (64, 64, 1), (64, 64, 2), (128, 96, 2), (40, 24, 0)])
 def test_views_of_one_projection(K, V, offset, dtype):
-    # q, k, v and dout as slices of wider rows; with an odd offset rows are not 16-byte aligned
+    # q, k, v and dout as slices of wider rows; with an odd offset rows are not even 4-byte aligned in bfloat16, with 2 not 16-byte
     B, L, H, Hk = 2, 100, 4, 2
     gen = torch.Generator().manual_seed(5)
     wide = torch.randn(B, L, (H + Hk) * K + Hk * V + H * V + 8, generator=gen).to(dtype)
