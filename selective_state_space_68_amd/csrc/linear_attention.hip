@@ -323,17 +323,15 @@ struct TileLoad {
   const char* next;                   // lowest address of the chunk to load next
   int64_t move;                       // bytes from a chunk to the next
   uint32_t off[kInstr];
-  bool narrow;                        // columns past `cols` are left as they are (zeros, from the start)
 
   static __device__ __forceinline__ int slot_of(int row, int lane) {   // (the swizzle is linear in the row's bits)
     return (lane % kSlots) ^ swizzle<RB, kF32, PERM>(row);
   }
   // step: elements from a row to the next (negative: backwards)
-  __device__ __forceinline__ void start(const ELEM* base, int64_t step, int chunk, int cols, int w, int lane) {
+  __device__ __forceinline__ void start(const ELEM* base, int64_t step, int chunk, int w, int lane) {
     const int64_t bytes = step * static_cast<int64_t>(sizeof(ELEM));
     move = kQ * bytes;
     next = reinterpret_cast<const char*>(base) + chunk * move + (bytes < 0 ? (kQ - 1) * bytes : 0);
-    narrow = cols * static_cast<int>(sizeof(ELEM)) < RB;
 #pragma unroll
     for (int i = 0; i < kInstr; ++i) {
       const int row = (w * kInstr + i) * kRows + lane / kSlots;
@@ -341,18 +339,13 @@ struct TileLoad {
                static_cast<uint32_t>(slot_of(row, lane) * 16);
     }
   }
-  // (ALL: known to have every column)
+  // ALL: every column is there; else those past `cols` are left as they are (zeros, from the start).
   template <bool ALL>
   __device__ __forceinline__ void whole(uint32_t tile, int cols, int w, int lane) {
-    if (ALL || !narrow) {
 #pragma unroll
-      for (int i = 0; i < kInstr; ++i) load_to_lds(tile + (w * kInstr + i) * 1024, next, off[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kInstr; ++i)
-        if (slot_of((w * kInstr + i) * kRows + lane / kSlots, lane) * 16 < cols * static_cast<int>(sizeof(ELEM)))
-          load_to_lds(tile + (w * kInstr + i) * 1024, next, off[i]);
-    }
+    for (int i = 0; i < kInstr; ++i)
+      if (ALL || slot_of((w * kInstr + i) * kRows + lane / kSlots, lane) * 16 < cols * static_cast<int>(sizeof(ELEM)))
+        load_to_lds(tile + (w * kInstr + i) * 1024, next, off[i]);
     next += move;
   }
   // The last chunk: rows past `last` repeat it (they are cleared afterwards).
@@ -415,7 +408,8 @@ __device__ __forceinline__ void load_tile_scalar(char* tile, const ELEM* base, i
 template <typename ACT, int VD>
 constexpr int kColumnTiles = sizeof(typename Op<ACT>::elem) == 2 && VD == 128 ? 2 : 1;
 
-template <typename ACT, int KD, int VD, int MOVE, bool STATE_ONLY>
+// MOVE: the bytes that a lane of a load moves (16, 4; 0: element by element).  ALL: K = KD and V = VD.
+template <typename ACT, int KD, int VD, int MOVE, bool ALL, bool STATE_ONLY>
 __global__ __launch_bounds__((4 * VD / kColumnTiles<ACT, VD>), VD == 128 || sizeof(typename Op<ACT>::elem) == 4 ? 2 : 3)
 void la_kernel(LaArgs p) {
   constexpr int VT = kColumnTiles<ACT, VD>;
@@ -473,9 +467,9 @@ void la_kernel(LaArgs p) {
   TileLoad<elem, RK, NW, false> q_load;
   TileLoad<elem, RV, NW, false> v_load;
   if constexpr (MOVE == 16) {
-    k_load.start(kg, kstep, c_begin, K, w, lane0);
-    if constexpr (!STATE_ONLY) q_load.start(qg, qstep, c_begin, K, w, lane0);
-    v_load.start(vg, vstep, c_begin, V, w, lane0);
+    k_load.start(kg, kstep, c_begin, w, lane0);
+    if constexpr (!STATE_ONLY) q_load.start(qg, qstep, c_begin, w, lane0);
+    v_load.start(vg, vstep, c_begin, w, lane0);
   }
   auto load_k = [&](auto plain, int c, int lane) __attribute__((always_inline)) {
     constexpr bool PLAIN = decltype(plain)::value;
@@ -483,7 +477,7 @@ void la_kernel(LaArgs p) {
     const int64_t r0 = static_cast<int64_t>(c) * kQ;
     const uint32_t tile = lds_address(sKK[0]) + (c & 1) * (kQ * RK);
     if constexpr (MOVE == 16) {
-      if (PLAIN || last >= kQ - 1) k_load.template whole<PLAIN>(tile, K, w, lane);
+      if (PLAIN || last >= kQ - 1) k_load.template whole<ALL>(tile, K, w, lane);
       else k_load.part(tile, kg + r0 * kstep, kstep, last, K, w, lane);
     } else if constexpr (MOVE == 4) {
       load_tile_words<elem, RK, NW, true>(tile, kg + r0 * kstep, kstep, last, K, w, lane);
@@ -497,8 +491,8 @@ void la_kernel(LaArgs p) {
     const int64_t r0 = static_cast<int64_t>(c) * kQ;
     if constexpr (MOVE == 16) {
       if (PLAIN || last >= kQ - 1) {
-        if constexpr (!STATE_ONLY) q_load.template whole<PLAIN>(lds_address(sQ), K, w, lane);
-        v_load.template whole<PLAIN>(lds_address(sV), V, w, lane);
+        if constexpr (!STATE_ONLY) q_load.template whole<ALL>(lds_address(sQ), K, w, lane);
+        v_load.template whole<ALL>(lds_address(sV), V, w, lane);
       } else {
         if constexpr (!STATE_ONLY) q_load.part(lds_address(sQ), qg + r0 * qstep, qstep, last, K, w, lane);
         v_load.part(lds_address(sV), vg + r0 * vstep, vstep, last, V, w, lane);
@@ -524,7 +518,7 @@ void la_kernel(LaArgs p) {
   };
   auto present = [&](int c) { return len - c * kQ < kQ ? len - c * kQ : kQ; };
   if constexpr (MOVE > 0) {
-    if (K < KD || V < VD) {                         // columns that the loads leave alone
+    if (!ALL) {                                     // columns that the loads leave alone
       clear_tile<RK, NW>(sKK[0], 0, w, lane0);
       clear_tile<RK, NW>(sKK[1], 0, w, lane0);
       if constexpr (!STATE_ONLY) clear_tile<RK, NW>(sQ, 0, w, lane0);
@@ -634,8 +628,9 @@ void la_kernel(LaArgs p) {
   }
 
   if (c_begin < c_live) arrived(c_begin, present(c_begin), lane0);
-  // One chunk.  PLAIN: it and the next are whole and every column is there, so that nothing is
-  // decided inside: with one or two waves a SIMD each branch taken costs its fetch (@@).
+  // One chunk.  PLAIN: it and the next are whole, so that nothing is decided inside: with one or two
+  // waves a SIMD each branch taken costs its fetch (the gradient at 8 x 2048, 32 heads of 128: 398 us with one
+  // loop for every chunk, 358 with one of their own for these).
   auto chunk = [&](auto plain, int c) __attribute__((always_inline)) {
     constexpr bool PLAIN = decltype(plain)::value;
     const int n = PLAIN ? kQ : present(c);
@@ -826,21 +821,24 @@ void la_kernel(LaArgs p) {
           if constexpr (sizeof(OUT) == 4) return make_float4(a[0], a[1], a[2], a[3]);
           else return make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
         };
-        if (PLAIN || (MOVE == 16 && n == kQ && V == VD)) {
+        if (PLAIN || (MOVE == 16 && n == kQ)) {
           // a uniform address that moves on by a chunk, the lane's offset in 16 rows, 16 rows' bytes
+          constexpr bool kEight = VT == 2 && sizeof(OUT) == 2;   // columns of a lane, otherwise 4
 #pragma unroll
           for (int jt = 0; jt < 4; ++jt) {
             char* rows = o_next + (o_off + static_cast<uint32_t>(jt) * o_rows);
-            if constexpr (VT == 2 && sizeof(OUT) == 2) {
+            if constexpr (kEight) {
               // lane groups 2x and 2x + 1 exchange halves: 8 columns a lane, 64 bytes of a row an instruction
               const uint2 a0 = four(acc[0][jt]), a1 = four(acc[1][jt]);
               const auto lo = __builtin_amdgcn_permlane16_swap(a0.x, a1.x, false, false);
               const auto hi = __builtin_amdgcn_permlane16_swap(a0.y, a1.y, false, false);
-              *reinterpret_cast<uint4*>(rows) = make_uint4(lo[0], hi[0], lo[1], hi[1]);
+              if (ALL || 32 * w + (g & 1) * 16 + (g >> 1) * 8 < V)
+                *reinterpret_cast<uint4*>(rows) = make_uint4(lo[0], hi[0], lo[1], hi[1]);
             } else {
 #pragma unroll
               for (int vt = 0; vt < VT; ++vt)
-                *reinterpret_cast<decltype(four(acc[0][0]))*>(rows + 16 * vt * sizeof(OUT)) = four(acc[vt][jt]);
+                if (ALL || 16 * (VT * w + vt) + 4 * g < V)
+                  *reinterpret_cast<decltype(four(acc[0][0]))*>(rows + 16 * vt * sizeof(OUT)) = four(acc[vt][jt]);
             }
           }
           o_next += o_move;
@@ -875,9 +873,9 @@ void la_kernel(LaArgs p) {
     }
   };
   int c = c_begin;
-  if (MOVE == 16 && K == KD && V == VD) {
-    const int plain = (c_live < len / kQ ? c_live : len / kQ) - 1;
-    for (; c < plain; ++c) chunk(std::true_type{}, c);
+  if constexpr (MOVE == 16) {
+    const int last = (c_live < len / kQ ? c_live : len / kQ) - 1;
+    for (; c < last; ++c) chunk(std::true_type{}, c);
   }
   for (; c < c_live; ++c) chunk(std::false_type{}, c);
   if (a) multiply_out(1.0);
@@ -1008,17 +1006,20 @@ template <typename ACT, int KD, int VD>
 void launch_la_t(const LaArgs& a, bool state_only, hipStream_t s) {
   const int64_t items = (a.batch * a.H * a.nseg + 7) / 8 * 8;
   const dim3 grid(static_cast<unsigned>(items * a.nroles)), block(4 * VD / kColumnTiles<ACT, VD>);
-  auto go = [&](auto move) {
+  auto go = [&](auto move, auto all) {
     constexpr int MOVE = decltype(move)::value;
-    if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VD, MOVE, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((la_kernel<ACT, KD, VD, MOVE, false>), grid, block, 0, s, a);
+    constexpr bool ALL = decltype(all)::value;
+    if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VD, MOVE, ALL, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((la_kernel<ACT, KD, VD, MOVE, ALL, false>), grid, block, 0, s, a);
   };
-  if (a.role[0].move == 16) go(std::integral_constant<int, 16>{});
-  else if (ACT::kBytes == 4 || a.role[0].move == 4) go(std::integral_constant<int, 4>{});
-  else if constexpr (ACT::kBytes == 2) go(std::integral_constant<int, 0>{});
+  const LaRole& r = a.role[0];
+  if (r.move == 16 && r.K == KD && r.V == VD) go(std::integral_constant<int, 16>{}, std::true_type{});
+  else if (r.move == 16) go(std::integral_constant<int, 16>{}, std::false_type{});
+  else if (ACT::kBytes == 4 || r.move == 4) go(std::integral_constant<int, 4>{}, std::false_type{});
+  else if constexpr (ACT::kBytes == 2) go(std::integral_constant<int, 0>{}, std::false_type{});
 }
 
-// One launch for all of `a`'s roles, which have one tile shape and one `move`.
+// One launch for all of `a`'s roles, which are alike (below).
 void launch_la_roles(const LaArgs& a, Dt dt, bool state_only, hipStream_t s) {
   const bool k2 = a.role[0].K > 64, v2 = a.role[0].V > 64;
   auto go = [&](auto act) {
@@ -1057,7 +1058,8 @@ hipError_t launch_la(const LaArgs& a, Dt dt, hipStream_t s) {
   const int64_t nchunks = (a.L + kQ - 1) / kQ;
   LaArgs all = a;
   all.seg_chunks = (nchunks + a.nseg - 1) / a.nseg;
-  // launches `n` of all's roles, those of one tile shape together
+  // launches `n` of all's roles, those of one tile shape and form together
+  auto fits = [](const LaRole& r) { return r.K % 64 == 0 && r.V % 64 == 0; };   // no column of its tiles is empty
   auto run = [&](const int* which, int n, bool state_only) {
     bool done[3] = {};
     for (int i = 0; i < n; ++i) {
@@ -1067,7 +1069,7 @@ hipError_t launch_la(const LaArgs& a, Dt dt, hipStream_t s) {
       x.nroles = 0;
       for (int j = i; j < n; ++j) {
         const LaRole& o = all.role[which[j]];
-        if ((o.K > 64) != (r.K > 64) || (o.V > 64) != (r.V > 64) || o.move != r.move) continue;
+        if ((o.K > 64) != (r.K > 64) || (o.V > 64) != (r.V > 64) || o.move != r.move || fits(o) != fits(r)) continue;
         x.role[x.nroles++] = o;
         done[j] = true;
       }
