@@ -241,13 +241,13 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_fwd_kern
     if (p.gate) load_row<ACT, NV, STRIDED>(nz, p.gate, row * p.gate_row, D, t, T, vec);
     if (p.residual) load_row<RES, NV, STRIDED>(nr, p.residual, row * p.D, D, t, T, vec);
   };
-  int64_t row = team.row;
-  if (!LEAN && row < p.rows) fetch(row);
   if constexpr (!LEAN) {
     load_weight<NV, STRIDED>(w1, p.w1, D, t, T, vec, 1.0f);
     load_weight<NV, STRIDED>(rs, p.rs, D, t, T, vec, 1.0f);
     load_weight<NV, STRIDED>(w2, p.w2, D, t, T, vec, 1.0f);
   }
+  int64_t row = team.row;
+  if (!LEAN && row < p.rows) fetch(row);
   for (; row < p.rows; row += team.step) {
     float x[NV][8], z[NV][8], r[NV][8];
     if constexpr (LEAN) fetch(row);
