@@ -17,7 +17,12 @@
 // holds a row in registers between the sums and the results, and walks rows a grid apart:
 // its columns stay the same, so the weights stay in registers and, backwards, so do the column sums of
 // the weights' gradients, which leave once per workgroup; a second kernel adds the workgroups'
-// in a fixed order.  The next row is asked for before the current one is computed.
+// in a fixed order.  The next row is asked for before the current one is computed, past the caches
+// (streaming loads and stores: 6.1 TB/s where three tensors are read and one is written, 4.9 without).
+//
+// Measured: 8192 x 5120 bfloat16 with 80 groups and gate 54 us (4.7 TB/s); the gradient of 16384 x 4096 bfloat16 with
+// gate, scale and float32 residual, 32 groups, 328 us (4.5 TB/s; 5.4 is what a copy reaches); 256 x 2560, 6 us: a
+// launch, the rows and two sums over them.
 #include "device_common.hpp"
 #include "lm_kernels.hpp"
 #include "scan_common.hpp"

@@ -12,26 +12,38 @@
 // sequence is token n_tokens - 1 - r, and E before the first row is the gradient of the
 // final state.
 //
-// One workgroup walks the chunks of one (batch row, head, segment).  A wave owns 16 or 32
-// columns v of E and of the output, so E is used as a matrix
-// operand straight from the registers that accumulate it: a product leaves lane (g, c) of a
-// 16 x 16 tile four consecutive rows of column c, and since the order of a product's
-// summation index is free, the rows of each tile are assigned (kperm below) so that the
-// two tiles of a pair leave a lane 8 consecutive indices: what one operand needs.  q, k and
-// v go from memory straight into LDS row by row (16 bytes a lane, no registers); operands that sum over tokens
-// (k^T, v^T) come out of the same rows by transposing LDS reads.  P goes through LDS (each
-// wave forms 16 rows of it).  The next chunk's rows are asked for as early as the tiles allow: k, in
-// two buffers, at the chunk's start; q and v once P and the product with E are done, before
-// P v and the state's product.
+// One workgroup walks the chunks of one (batch row, head, segment).  A wave owns 16 or 32 columns v of E
+// and of the output, so E is used as a matrix operand straight from the registers that accumulate
+// it: a product leaves lane (g, c) of a 16 x 16 tile four consecutive rows of column c, and since the
+// order of a product's summation index is free, the rows of each tile are assigned so that the two
+// tiles of a pair leave a lane 8 consecutive indices: what one operand needs.  q, k and v go from
+// memory straight into LDS row by row (16 bytes a lane, no registers); operands that sum over
+// tokens (k^T, v^T) come out of the same rows by transposing LDS reads.  P goes through LDS.  The next
+// chunk's rows are asked for as early as the tiles allow: k, in two buffers, at the chunk's start; q
+// and v once P and the product with E are done, before P v and the state's product.
 //
-// Roundings (bfloat16 activations; float32 activations use float32 products throughout):
-// the decayed v of the state update is split into three bfloat16 terms, which carry all 24
-// bits, since the state is a float32 result; E and P as operands of the output are split
-// into two terms (16 bits), so that the output's own rounding is the one that counts.
+// Roundings (bfloat16 activations; float32 activations use float32 products throughout): the decayed v
+// of a state that is a result is split into three bfloat16 terms, which carry all 24 bits; E and P as
+// operands of the output (and the decayed v of a state that only feeds it) into two terms, 16 bits,
+// so that the output's own rounding is the one that counts.  One term of P is not enough where a
+// gradient's terms cancel.
 //
-// When the (batch row, head) pairs are too few to fill the chip the sequence is cut into
-// segments: a pre-pass forms each segment's own state sum, a small kernel chains them, and
-// the main pass runs every segment from its entering E.
+// When the (batch row, head) pairs are too few to fill the chip the sequence is cut into segments: a
+// pre-pass forms each segment's own state sum, a small kernel chains them, and the main pass runs
+// every segment from its entering E.
+//
+// What bounds it (measured, one MI355X, bfloat16):
+//   8 x 2048, 32 heads of 128, gradient: 355 us for 1.6 GB of rows read and written by the three roles (4.5 TB/s; 1.3 GB
+//     reach memory, the rest is shared in L2).  Matrix instructions take 5.2, LDS 5.1 and vector instructions
+//     3.4 of the 14 thousand cycles that the two workgroups of a CU take for a chunk each: no unit is
+//     full, the 8 waves wait for each other at two barriers a chunk.
+//   131072 tokens, 20 heads of 128: 904 us (pre-pass 285 at 4.7 TB/s, chain 26, main pass 590 at 4.5 TB/s): memory.
+//   4 x 2048, 80 heads of 64: 120 us.  320 workgroups on 256 CUs: the time of a CU with two, 6800 cycles
+//     a chunk (5400 alone); 2 or 3 segments cost more than they level (140 and 132 us).
+//   float32: the float32 matrix rate (64 x 64: 7700 cycles of products a chunk and workgroup, 2 of them a CU).
+// Tried and dropped: a second buffer for q and v (no gain); products and LDS reads interleaved by scheduling
+// groups (no gain); streaming loads (5 % faster forwards at 64 x 64, 5 % slower gradients); the output stored
+// before the state's product (127 us at 4 x 2048 against 122, 984 against 954 at 131072).
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -113,7 +125,7 @@ struct Op<ActBF16> {
       if (t + 1 < TERMS) {                          // r - p, exact: one dot product of p's pair with (-1, 0) or (0, -1)
         const uint32_t pw[4] = {p[t].x, p[t].y, p[t].z, p[t].w};
         uint32_t low = 0x0000bf80u, high = 0xbf800000u;
-        asm("" : "+s"(low), "+s"(high));            // (scalar registers: as an immediate operand -1.0 is the pair's high half alone)
+        asm("" : "+s"(low), "+s"(high));            // (scalar registers: the immediate -1.0 is the high half alone)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           r[e] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, pw[e / 2]),
@@ -313,8 +325,8 @@ __device__ __forceinline__ void load_word_to_lds(uint32_t tile, const char* src)
 
 // One tensor's rows into its LDS tile.  Whole chunks take the short way: a uniform address that moves
 // on by a chunk, and for each of the wave's instructions (1024 bytes, 64 lanes of 16) the lane's offset,
-// formed once.  Scalar work inside the loop costs a chunk dearly (at 64 x 64 the addresses of
-// its loads and stores, formed there, were 2800 of its 7300 cycles).
+// formed once.  Scalar work inside the loop costs a chunk dearly (4 x 2048, 80 heads of 64: 138 us with the
+// addresses of loads and stores formed there, 122 without).
 template <typename ELEM, int RB, int NW, bool PERM>
 struct TileLoad {
   static constexpr bool kF32 = sizeof(ELEM) == 4;
@@ -361,7 +373,8 @@ struct TileLoad {
 };
 
 // The same in 4-byte words, for rows that start at any word: four times the instructions, 256 bytes
-// each, at addresses formed where they are used.  A wave fills the same part of the tile.
+// each, at addresses formed where they are used (4 x 2048, 32 heads of 100: 183 us, 527 element by
+// element).  A wave fills the same part of the tile.
 template <typename ELEM, int RB, int NW, bool PERM>
 __device__ __forceinline__ void load_tile_words(uint32_t tile, const ELEM* base, int64_t step, int last, int cols, int w,
                                                 int lane) {
@@ -403,13 +416,18 @@ __device__ __forceinline__ void load_tile_scalar(char* tile, const ELEM* base, i
 // STATE_ONLY: the pre-pass, which leaves each segment's own sum (its state after its last
 // token, from zero) in role.seg.  Otherwise the whole of the segment's output.
 //
-// A wave owns 16 VT columns.  VT = 2 at bfloat16, V > 64: half the waves, each LDS read and
-// address used for two columns' tiles, at 256 registers and 2 waves a SIMD (@@).
+// A wave owns 16 VT columns.  VT = 2 at bfloat16, V > 64: each LDS read and address serves two columns'
+// tiles, at 256 registers and 2 waves a SIMD; 8 waves of 16 columns took as long with twice the
+// instructions (131072 tokens 1065 us, 1061 with two tiles, when both were tried), and only pairs of tiles
+// make 64-byte output pieces (1006).
 template <typename ACT, int VD>
 constexpr int kColumnTiles = sizeof(typename Op<ACT>::elem) == 2 && VD == 128 ? 2 : 1;
 
 // MOVE: the bytes that a lane of a load moves (16, 4; 0: element by element).  ALL: K = KD and V = VD.
-template <typename ACT, int KD, int VD, int MOVE, bool ALL, bool STATE_ONLY>
+// WT: operand terms of the decayed v, 3 where the state is a result, 2 where it only serves outputs,
+// whose products take E in two terms (131072 tokens: 930 us with 3, 904 with 2; gradient at 4 x 2048, 32
+// heads of 128: 195 and 181).
+template <typename ACT, int KD, int VD, int MOVE, bool ALL, bool STATE_ONLY, int WT>
 __global__ __launch_bounds__((4 * VD / kColumnTiles<ACT, VD>), VD == 128 || sizeof(typename Op<ACT>::elem) == 4 ? 2 : 3)
 void la_kernel(LaArgs p) {
   constexpr int VT = kColumnTiles<ACT, VD>;
@@ -421,7 +439,6 @@ void la_kernel(LaArgs p) {
   constexpr int RK = KD * static_cast<int>(sizeof(elem)), RV = VD * static_cast<int>(sizeof(elem));   // row bytes
   constexpr int RP = kQ * static_cast<int>(sizeof(elem));
   constexpr int KT = KD / 32;                       // pairs of state tiles along K
-  constexpr int WT = kF32 ? 1 : 3;                  // operand terms of the decayed v
   constexpr int ET = kF32 ? 1 : 2;                  // operand terms of E and of P
   __shared__ __attribute__((aligned(512))) char sQ[STATE_ONLY ? 16 : kQ * RK];
   __shared__ __attribute__((aligned(512))) char sKK[2][kQ * RK];                // k of this chunk and of the next
@@ -498,7 +515,8 @@ void la_kernel(LaArgs p) {
         v_load.part(lds_address(sV), vg + r0 * vstep, vstep, last, V, w, lane);
       }
     } else if constexpr (MOVE == 4) {
-      if constexpr (!STATE_ONLY) load_tile_words<elem, RK, NW, false>(lds_address(sQ), qg + r0 * qstep, qstep, last, K, w, lane);
+      if constexpr (!STATE_ONLY)
+        load_tile_words<elem, RK, NW, false>(lds_address(sQ), qg + r0 * qstep, qstep, last, K, w, lane);
       load_tile_words<elem, RV, NW, false>(lds_address(sV), vg + r0 * vstep, vstep, last, V, w, lane);
     } else {
       if constexpr (!STATE_ONLY) load_tile_scalar<elem, RK, NW, false>(sQ, qg + r0 * qstep, qstep, last, K, tid);
@@ -974,7 +992,8 @@ __global__ __launch_bounds__(256) void la_sum_heads_kernel(LaSum a, LaSum b) {
   const LaSum& x = blockIdx.y ? b : a;
   const int per_row = x.d / W, rows = 256 / per_row, t = threadIdx.x / per_row, c = threadIdx.x % per_row * W;
   if (t >= rows) return;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows + t; row < x.rows; row += static_cast<int64_t>(gridDim.x) * rows) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows + t; row < x.rows; row += step) {
     const float* src = x.part + row * x.share * x.d + c;
     float s[W];
 #pragma unroll
@@ -1006,11 +1025,17 @@ template <typename ACT, int KD, int VD>
 void launch_la_t(const LaArgs& a, bool state_only, hipStream_t s) {
   const int64_t items = (a.batch * a.H * a.nseg + 7) / 8 * 8;
   const dim3 grid(static_cast<unsigned>(items * a.nroles)), block(4 * VD / kColumnTiles<ACT, VD>);
+  constexpr int kTerms = ACT::kBytes == 4 ? 1 : 3;
+  bool results = false;                             // whether a state of this launch is one
+  for (int i = 0; i < a.nroles; ++i) results = results || (a.nseg == 1 && a.role[i].fin);
   auto go = [&](auto move, auto all) {
     constexpr int MOVE = decltype(move)::value;
     constexpr bool ALL = decltype(all)::value;
-    if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VD, MOVE, ALL, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((la_kernel<ACT, KD, VD, MOVE, ALL, false>), grid, block, 0, s, a);
+    if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VD, MOVE, ALL, true, kTerms>), grid, block, 0, s, a);
+    else if (MOVE < 16 || kTerms == 1 || results)
+      hipLaunchKernelGGL((la_kernel<ACT, KD, VD, MOVE, ALL, false, kTerms>), grid, block, 0, s, a);
+    else if constexpr (MOVE == 16 && kTerms == 3)
+      hipLaunchKernelGGL((la_kernel<ACT, KD, VD, MOVE, ALL, false, 2>), grid, block, 0, s, a);
   };
   const LaRole& r = a.role[0];
   if (r.move == 16 && r.K == KD && r.V == VD) go(std::integral_constant<int, 16>{}, std::true_type{});
@@ -1036,10 +1061,11 @@ void launch_la_roles(const LaArgs& a, Dt dt, bool state_only, hipStream_t s) {
 }  // namespace
 
 // Segments per sequence.  Where every CU gets a workgroup, one: the pre-pass and the chaining that
-// segments need cost more than they gain (the gradient at 8 x 2048, 32 heads of 128, 768
-// workgroups: 415 us with one, 577 with two; 4 x 2048, 80 heads of 64: 145 and 152).  With fewer, 2 workgroups a CU
-// (131072 tokens, 20 heads of 128: 1618 us with 13, 1088 with 25, 1127 with 51), each at least 4 chunks long.  The
-// count is then derived back from the segment length, so that no segment is without a chunk.
+// segments need cost more than they gain (the gradient at 8 x 2048, 32 heads of 128, 768 workgroups: 363 us
+// with one, 549 with two; 4 x 2048, 80 heads of 64: 122 with one, 140 with two, 132 with three).  With fewer, 2
+// workgroups a CU (131072 tokens, 20 heads of 128: 1332 us with 13, 944 with 25, 992 with 51), each at least 4
+// chunks long (float32, 5 x 1000, 16 heads of 64 x 128: 107 us with two, 86 with three, 88 with four, 97 with six).
+// The count is then derived back from the segment length, so that no segment is without a chunk.
 int la_segments(int64_t batch, int64_t L, int64_t H, int roles) {
   const int64_t workgroups = batch * H * roles, nch = (L + kQ - 1) / kQ;
   if (workgroups >= 256) return 1;
