@@ -112,6 +112,15 @@ def test_many_rows(dtype, rdtype):
     _run(a, dy, dh, 1, rdtype)
 
 
+@pytest.mark.parametrize("dtype,rdtype", TYPES)
+@pytest.mark.parametrize("rows,D,groups", [(1100, 769, 1), (700, 2560, 20), (600, 5120, 1), (520, 5121, 1), (300, 8192, 64),
+                                           (290, 9000, 1), (270, 12296, 1)])
+def test_many_wide_rows(rows, D, groups, dtype, rdtype):
+    # more rows than workgroups: the column sums run over several rows of one
+    a, dy, dh = _inputs(rows, D, dtype, rdtype, "all", seed=D)
+    _run(a, dy, dh, groups, rdtype)
+
+
 def test_zero_rows_and_large_values():
     # eps bounds the norm of a row of zeros; squares of 1e18 stay in float32's range
     a, dy, dh = _inputs(4, 96, F32, F32, "both_norms", seed=3)
