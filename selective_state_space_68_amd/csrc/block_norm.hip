@@ -20,8 +20,8 @@
 // in a fixed order.  The next row is asked for before the current one is computed, past the caches
 // (streaming loads and stores: 6.1 TB/s where three tensors are read and one is written, 4.9 without).
 //
-// Measured: 8192 x 5120 bfloat16 with 80 groups and gate 54 us (4.7 TB/s); the gradient of 16384 x 4096 bfloat16 with
-// gate, scale and float32 residual, 32 groups, 328 us (4.5 TB/s; 5.4 is what a copy reaches); 256 x 2560, 6 us: a
+// Measured: 8192 x 5120 bfloat16 with 80 groups and gate 50 us (5.0 TB/s); the gradient of 16384 x 4096 bfloat16 with
+// gate, scale and float32 residual, 32 groups, 314 us (4.7 TB/s; 5.4 is what a copy reaches); 256 x 2560, 6 us: a
 // launch, the rows and two sums over them.
 #include "device_common.hpp"
 #include "lm_kernels.hpp"
@@ -212,7 +212,9 @@ __device__ __forceinline__ void group_sum(float (&part)[NV], int group, int D, L
   }
 }
 
-__device__ __forceinline__ float sigmoid_f(float z) { return 1.0f / (1.0f + exp2_hw(-z * kLog2e)); }
+// (the reciprocal is good to a unit in the last place; a division's ten instructions, for every value, are
+// what a gated row would be bound by)
+__device__ __forceinline__ float sigmoid_f(float z) { return __builtin_amdgcn_rcpf(1.0f + exp2_hw(-z * kLog2e)); }
 
 // The team of a thread: rows row0, row0 + step, ... of the matrix.
 template <bool ONE_WAVE>
@@ -429,15 +431,14 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_bwd_kern
     }
     if (p.w2) {
       const float r2 = 1.0f / sqrtf(__builtin_fmaf(s[0], inv_d, p.eps));
-      const float m = s[1] * inv_d * r2 * r2;
+      const float ra = D > 1 ? r2 : r2 * p.eps * r2 * r2, rh = D > 1 ? r2 * (s[1] * inv_d * r2 * r2) : 0.0f;
       take(a2, 1);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           a2[v][e] = __builtin_fmaf(dy[v][e], h[v][e] * r2, a2[v][e]);
-          const float a = dy[v][e] * w2[v][e];
-          dH[v][e] = __builtin_fmaf(r2, D > 1 ? __builtin_fmaf(-h[v][e], m, a) : a * p.eps * r2 * r2, dH[v][e]);
+          dH[v][e] = __builtin_fmaf(-h[v][e], rh, __builtin_fmaf(dy[v][e] * w2[v][e], ra, dH[v][e]));
         }
     }
     if (p.w2) give(a2, 1);
@@ -502,10 +503,11 @@ __global__ __launch_bounds__(MAXT == 64 ? 64 * kTeams : MAXT) void norm_bwd_kern
         group_sum<NV, ONE_WAVE>(m, group, D, lds, turn, t, T);
       }
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
+      for (int v = 0; v < NV; ++v) {
+        const float rc = D > 1 ? r1[v] : r1[v] * p.eps * r1[v] * r1[v], rx = D > 1 ? r1[v] * (m[v] * inv_g) : 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          dH[v][e] = r1[v] * (D > 1 ? __builtin_fmaf(-x[v][e], m[v] * inv_g, dH[v][e]) : dH[v][e] * p.eps * r1[v] * r1[v]);
+        for (int e = 0; e < 8; ++e) dH[v][e] = __builtin_fmaf(-x[v][e], rx, dH[v][e] * rc);
+      }
     }
     store_row<ACT, NV, STRIDED>(p.dx, row * p.D, D, t, T, vec, dH);
   }
@@ -623,7 +625,7 @@ hipError_t launch_norm(const NormArgs& a, Dt dt, Dt rdt, bool bwd, int blocks, h
 
 // Workgroups: at most `most` threads' worth on each of the 256 CUs.  Rows in flight against registers of
 // column sums to add up: 1024 forwards (16384 x 2560 109 us, 185 with 512, 134 with 2048; 4096 x 1024 11.6, 14, 15.3) but 2048
-// where a row takes over 512 threads (8192 x 5120, 80 groups with gate: 58 us, 62 with 1024), 512
+// where a row takes over 512 threads (8192 x 5120, 80 groups with gate, as it was then: 58 us, 62 with 1024), 512
 // backwards (4096 x 1024 34 us, 44 with 1024, 41 with 256; 16384 x 512 43, 50, 54; 1534 x 769 23, 29, 23).
 int blocks_of(int64_t rows, int64_t D, int most) {
   const Shape sh = shape_of(D);
