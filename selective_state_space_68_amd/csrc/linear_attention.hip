@@ -951,7 +951,9 @@ __global__ __launch_bounds__(256) void la_chain_kernel(LaArgs p) {
   float s[kChain], T[kAhead][kChain];
 #pragma unroll
   for (int x = 0; x < kChain; ++x) s[x] = carry && i0 + 256 * x < KV ? carry[i0 + 256 * x] : 0.0f;
-  float l1 = 0.0f, lS = 0.0f;
+  auto times = [](const Pair& d, float x) { return __builtin_fmaf(d.hi, x, d.lo * x); };
+  float l1 = 0.0f;
+  Pair lS{0.0f, 0.0f};                              // (the factor that a state meets once a segment; the others, once)
   for (int k0 = 0; k0 < p.nseg; k0 += kAhead) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -963,18 +965,18 @@ __global__ __launch_bounds__(256) void la_chain_kernel(LaArgs p) {
     }
     if (k0 == 0) {                                  // (while the first sums are on their way)
       l1 = decay_float(p.log_decay, h, 1);
-      lS = decay_float(p.log_decay, h, seg_tokens);
+      lS = pair_of(decay_power(p.log_decay, h, seg_tokens));
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int k = k0 + u;
       if (k >= p.nseg) break;
       const int n = tokens(k);
-      const float d = n == seg_tokens ? lS : decay_float(p.log_decay, h, n);
+      const Pair d = n == seg_tokens ? lS : Pair{decay_float(p.log_decay, h, n), 0.0f};
 #pragma unroll
       for (int x = 0; x < kChain; ++x) {
         if (i0 + 256 * x < KV) slot[static_cast<int64_t>(k) * KV + i0 + 256 * x] = r.reverse ? s[x] : l1 * s[x];
-        if (n > 0) s[x] = __builtin_fmaf(d, s[x], r.reverse ? l1 * T[u][x] : T[u][x]);
+        if (n > 0) s[x] = times(d, s[x]) + (r.reverse ? l1 * T[u][x] : T[u][x]);
       }
     }
   }

@@ -6,8 +6,8 @@ difference over the root mean square 2-norm of that head's rows.  Bounds, from t
 roundings on the way:
   float32  a value is a sum of at most 64 + 128 products per chunk in float32, so at most
            192 * 2^-24 = 1.1e-5 of the terms' size, plus the chunks' decays: 5e-5.
-  bfloat16 outputs: the masked scores are rounded to 8 bits (2^-9 of each term), and so is
-           the result; a row's terms may be a few times its head's mean size: 8 * 2^-9 = 1.6e-2.
+  bfloat16 outputs: rounded to 8 bits, as the masked scores were at first (2^-9 of each term;
+           they are in two terms now); a row's terms may be a few times its head's mean size: 8 * 2^-9 = 1.6e-2.
   states   float32 from exact products (bfloat16 inputs included): 5e-5.
 """
 import pytest
@@ -80,6 +80,9 @@ SHAPES = [   # batch, L, H, K, V, heads of q, k, v
     (1, 140, 3, 34, 98, (3, 1, 1)),
     (2, 300, 2, 128, 50, (1, 2, 2)),
     (1, 1500, 2, 64, 64, None),
+    (1, 1100, 2, 100, 36, (1, 2, 2)),    # the others in segments
+    (1, 1030, 1, 33, 17, None),
+    (1, 1200, 2, 96, 128, None),
 ]
 
 
