@@ -448,24 +448,22 @@ void la_kernel(LaArgs p) {
   const int tid = threadIdx.x, lane0 = tid & 63, w = uniform_int(tid >> 6);
   // Workgroup ids go round the 8 XCDs: the roles of one (batch row, head, segment), which
   // read the same rows, are 8 ids apart, on one XCD and its L2 at about the same time.
-  const int nseg = p.nseg;
-  const int64_t per_role = static_cast<int64_t>(p.batch) * p.H * nseg;
-  const int64_t group = blockIdx.x / (8 * p.nroles) * 8;
-  const int in_group = static_cast<int>(blockIdx.x % (8 * p.nroles));
-  const int64_t item = group + in_group % 8;
+  // (32-bit numbers: each 64-bit division is 500 cycles of a short call)
+  const uint32_t nseg = static_cast<uint32_t>(p.nseg), heads = static_cast<uint32_t>(p.H);
+  const uint32_t per_role = static_cast<uint32_t>(p.batch) * heads * nseg, span = 8u * static_cast<uint32_t>(p.nroles);
+  const uint32_t group = blockIdx.x / span, in_group = blockIdx.x - group * span, item = group * 8 + in_group % 8;
   if (item >= per_role) return;
   const LaRole& r = p.role[in_group / 8];
-  const int64_t bh = item / nseg;
-  const int seg = static_cast<int>(item % nseg);
+  const uint32_t pair = nseg == 1 ? item : item / nseg, seg = item - pair * nseg, row_b = pair / heads;
   if (STATE_ONLY && seg + 1 == nseg && !r.fin) return;   // (its sum would be read by nobody)
-  const int64_t b = bh / p.H;
-  const int h = static_cast<int>(bh % p.H);
+  const int64_t bh = pair, b = row_b;
+  const int h = static_cast<int>(pair - row_b * heads);
   const int L = static_cast<int>(p.L);
   const int len = row_length(p, b);
   const int K = r.K, V = r.V, reverse = r.reverse;
   const int nchunks = (L + kQ - 1) / kQ;
   const int live = (len + kQ - 1) / kQ;             // chunks that hold a token
-  const int c_begin = seg * static_cast<int>(p.seg_chunks);
+  const int c_begin = static_cast<int>(seg) * static_cast<int>(p.seg_chunks);
   const int c_stop = c_begin + static_cast<int>(p.seg_chunks);
   const int c_end = c_stop < nchunks ? c_stop : nchunks;
   const int c_live = c_end < live ? c_end : live;
@@ -474,9 +472,9 @@ void la_kernel(LaArgs p) {
   // row r of the sequence is token r forwards, len - 1 - r backwards
   const int64_t t_first = reverse ? len - 1 : 0;
   const int t_step = reverse ? -1 : 1;
-  const elem* qg = static_cast<const elem*>(r.q) + b * r.qs[0] + (h / r.qdiv) * r.qs[2] + t_first * r.qs[1];
-  const elem* kg = static_cast<const elem*>(r.k) + b * r.ks[0] + (h / r.kdiv) * r.ks[2] + t_first * r.ks[1];
-  const elem* vg = static_cast<const elem*>(r.v) + b * r.vs[0] + (h / r.vdiv) * r.vs[2] + t_first * r.vs[1];
+  const elem* qg = static_cast<const elem*>(r.q) + b * r.qs[0] + (r.qdiv == 1 ? h : h / r.qdiv) * r.qs[2] + t_first * r.qs[1];
+  const elem* kg = static_cast<const elem*>(r.k) + b * r.ks[0] + (r.kdiv == 1 ? h : h / r.kdiv) * r.ks[2] + t_first * r.ks[1];
+  const elem* vg = static_cast<const elem*>(r.v) + b * r.vs[0] + (r.vdiv == 1 ? h : h / r.vdiv) * r.vs[2] + t_first * r.vs[1];
   const int64_t qstep = r.qs[1] * t_step, kstep = r.ks[1] * t_step, vstep = r.vs[1] * t_step;
 
   // Ask for the rows of k, or of q and v, of chunk c (in order, from c_begin).
@@ -557,26 +555,39 @@ void la_kernel(LaArgs p) {
     if (nseg > 1) src = r.seg + (bh * nseg + seg) * static_cast<int64_t>(K) * V;
     else if (r.carry) src = r.carry + bh * static_cast<int64_t>(K) * V;
   }
+  // this lane's place in a state in memory, and of its entries from there
+  auto entry = [&](int vt, int t, int u, int e) { return (32 * t + 4 * u + e) * r.sk + 16 * vt * r.sv; };
+  auto there = [&](int vt, int t, int u, int e) {
+    return ALL || (32 * t + 8 * g + 4 * u + e < K && 16 * (VT * w + vt) + c16 < V);
+  };
+  const int place = 8 * g * r.sk + (16 * VT * w + c16) * r.sv;
   // forwards the carried state decays once before the first token; the segments' states have
-  const float lam1 = exp2_hw(g2);
-  const bool decayed = nseg > 1 || reverse || len == 0;
+  const float first = nseg > 1 || reverse || len == 0 ? 1.0f : exp2_hw(g2);
 #pragma unroll
   for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u) E[vt][t][u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  if (src) {                                        // (one branch, so that all loads are under way together)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int kk = 32 * t + 8 * g + 4 * u + e, vv = 16 * (VT * w + vt) + c16;
-          float x = 0.0f;
-          if (src) {                                // (uniform; the loads themselves sit behind no branch)
-            const bool in = kk < K && vv < V;
-            x = src[static_cast<int64_t>(in ? kk : 0) * r.sk + static_cast<int64_t>(in ? vv : 0) * r.sv];
-            x = in ? (decayed ? x : x * lam1) : 0.0f;
-          }
-          E[vt][t][u][e] = x;
-        }
+    for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            E[vt][t][u][e] = src[static_cast<uint32_t>(there(vt, t, u, e) ? place + entry(vt, t, u, e) : 0)];
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) E[vt][t][u][e] = there(vt, t, u, e) ? E[vt][t][u][e] * first : 0.0f;
+  }
 
   // The registers hold the state divided by rho = lam^(64 a), a the chunks since the last time
   // it was multiplied out: a chunk then adds lam^(64 - i) v / rho' instead of decaying
@@ -922,10 +933,8 @@ void la_kernel(LaArgs p) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int kk = 32 * t + 8 * g + 4 * u + e, vv = 16 * (VT * w + vt) + c16;
-            if (kk < K && vv < V) dst[static_cast<int64_t>(kk) * r.sk + static_cast<int64_t>(vv) * r.sv] = E[vt][t][u][e];
-          }
+          for (int e = 0; e < 4; ++e)
+            if (there(vt, t, u, e)) dst[static_cast<uint32_t>(place + entry(vt, t, u, e))] = E[vt][t][u][e];
   }
 }
 
