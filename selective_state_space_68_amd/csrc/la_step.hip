@@ -4,8 +4,8 @@
 //
 // The step reads and writes each state once and does 5 flops per entry, so it is bound by
 // HBM (a state pool of a few hundred sequences is far larger than any cache).  A workgroup
-// owns all K rows of a slice of columns of one state: a lane streams 4 consecutive columns
-// of every `rows`-th row, and the workgroup adds up the rows' parts of o through LDS, in one order.
+// owns one state: a lane streams 4 consecutive columns of every `rows`-th row, and the workgroup
+// adds up the rows' parts of o through LDS, in one order.
 // q and k are read into LDS once as float32.
 //
 // Measured: 256 sequences of 40 heads, 128 x 128 (1.35 GB read and written): 258 us, 5.2 TB/s, what a copy of
@@ -21,40 +21,37 @@ constexpr int kThreads = 256;
 
 // CPT: consecutive columns per thread (4: rows of states and of v, o move as vectors).
 template <typename ACT, int CPT>
-__global__ __launch_bounds__(kThreads) void la_step_kernel(LaStepArgs p, int slice) {
+__global__ __launch_bounds__(kThreads) void la_step_kernel(LaStepArgs p) {
   __shared__ float sq[kLaMaxDim], sk[kLaMaxDim];
   __shared__ __attribute__((aligned(16))) float so[kThreads * CPT];
   const int tid = threadIdx.x;
   const int K = p.K, V = p.V;
-  const int nslices = (V + slice - 1) / slice;
-  const int64_t wg = blockIdx.x;
-  const int v_begin = static_cast<int>(wg % nslices) * slice;
-  const int64_t bh = wg / nslices, b = bh / p.H;
-  const int h = static_cast<int>(bh % p.H);
-  const int cols = V - v_begin < slice ? V - v_begin : slice;
+  const uint32_t row_b = blockIdx.x / static_cast<uint32_t>(p.H);   // (32-bit: a 64-bit division is 500 cycles)
+  const int64_t bh = blockIdx.x, b = row_b;
+  const int h = static_cast<int>(blockIdx.x - row_b * static_cast<uint32_t>(p.H));
   const int64_t slot = p.slots ? p.slots[b] : b;
   const bool live = slot >= 0 && slot < p.states;   // (an absent sequence: its output is zero, no state is touched)
-  const int64_t o0 = bh * V + v_begin;
+  const int64_t o0 = bh * V;
   if (!live) {
-    for (int i = tid; i < cols; i += kThreads) store_act<ACT>(p.o, o0 + i, 0.0f);
+    for (int i = tid; i < V; i += kThreads) store_act<ACT>(p.o, o0 + i, 0.0f);
     return;
   }
   const int64_t q0 = b * p.qs[0] + (h / p.qdiv) * p.qs[1], k0 = b * p.ks[0] + (h / p.kdiv) * p.ks[1];
   if (tid < K) sq[tid] = load_act<ACT>(p.q, q0 + tid) * p.scale;
   else if (tid >= 128 && tid - 128 < K) sk[tid - 128] = load_act<ACT>(p.k, k0 + tid - 128);
   const float lam = expf(p.log_decay[h]);
-  const int per_row = (cols + CPT - 1) / CPT;       // threads of a row
+  const int per_row = V / CPT;                      // threads of a row (CPT is 4 only where it divides V)
   const int rows = kThreads / per_row;              // rows in flight
   const int r0 = tid / per_row, c0 = tid % per_row * CPT;
-  const int64_t v0 = b * p.vs[0] + (h / p.vdiv) * p.vs[1] + v_begin;
+  const int64_t v0 = b * p.vs[0] + (h / p.vdiv) * p.vs[1];
   float vv[CPT], acc[CPT];
 #pragma unroll
   for (int e = 0; e < CPT; ++e) {
-    vv[e] = load_act<ACT>(p.v, v0 + c0 + e);        // (c0 < cols always; CPT divides cols when it is 4)
+    vv[e] = load_act<ACT>(p.v, v0 + c0 + e);        // (c0 + e < V always)
     acc[e] = 0.0f;
   }
   __syncthreads();
-  const int64_t s0 = ((slot * p.H + h) * K) * V + v_begin + c0;
+  const int64_t s0 = ((slot * p.H + h) * K) * V + c0;
   if (r0 < rows) {
 #pragma unroll 8
     for (int r = r0; r < K; r += rows) {
@@ -79,7 +76,7 @@ __global__ __launch_bounds__(kThreads) void la_step_kernel(LaStepArgs p, int sli
     for (int e = 0; e < CPT; ++e) so[(r0 * per_row) * CPT + c0 + e] = acc[e];
   }
   __syncthreads();
-  for (int i = tid; i < cols; i += kThreads) {
+  for (int i = tid; i < V; i += kThreads) {
     float s = 0.0f;
     for (int r = 0; r < rows; ++r) s += so[r * per_row * CPT + i];
     store_act<ACT>(p.o, o0 + i, s);
@@ -91,14 +88,13 @@ __global__ __launch_bounds__(kThreads) void la_step_kernel(LaStepArgs p, int sli
 hipError_t launch_la_step(const LaStepArgs& a, Dt dt, hipStream_t s) {
   const bool vec = a.V % 4 == 0 && reinterpret_cast<uintptr_t>(a.state_in) % 16 == 0 &&
                    reinterpret_cast<uintptr_t>(a.state_out) % 16 == 0;
-  int slice = 128;
-  const dim3 grid(static_cast<unsigned>(a.batch * a.H * ((a.V + slice - 1) / slice)));
+  const dim3 grid(static_cast<unsigned>(a.batch * a.H));
   if (dt == Dt::BF16) {
-    if (vec) hipLaunchKernelGGL((la_step_kernel<ActBF16, 4>), grid, dim3(kThreads), 0, s, a, slice);
-    else hipLaunchKernelGGL((la_step_kernel<ActBF16, 1>), grid, dim3(kThreads), 0, s, a, slice);
+    if (vec) hipLaunchKernelGGL((la_step_kernel<ActBF16, 4>), grid, dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((la_step_kernel<ActBF16, 1>), grid, dim3(kThreads), 0, s, a);
   } else {
-    if (vec) hipLaunchKernelGGL((la_step_kernel<ActF32, 4>), grid, dim3(kThreads), 0, s, a, slice);
-    else hipLaunchKernelGGL((la_step_kernel<ActF32, 1>), grid, dim3(kThreads), 0, s, a, slice);
+    if (vec) hipLaunchKernelGGL((la_step_kernel<ActF32, 4>), grid, dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((la_step_kernel<ActF32, 1>), grid, dim3(kThreads), 0, s, a);
   }
   return hipGetLastError();
 }

@@ -944,11 +944,12 @@ void la_kernel(LaArgs p) {
 constexpr int kChain = 4, kAhead = 8;
 __global__ __launch_bounds__(256) void la_chain_kernel(LaArgs p) {
   const LaRole& r = p.role[blockIdx.z];
+  const uint32_t row_b = blockIdx.y / static_cast<uint32_t>(p.H);
   const int64_t bh = blockIdx.y;
   const int KV = r.K * r.V;
   const int i0 = blockIdx.x * (256 * kChain) + threadIdx.x;
-  const int h = static_cast<int>(bh % p.H);
-  const int len = row_length(p, bh / p.H);
+  const int h = static_cast<int>(blockIdx.y - row_b * static_cast<uint32_t>(p.H));
+  const int len = row_length(p, row_b);
   const int seg_tokens = static_cast<int>(p.seg_chunks) * kQ;
   float* slot = r.seg + bh * p.nseg * static_cast<int64_t>(KV);
   const float* carry = r.carry ? r.carry + bh * static_cast<int64_t>(KV) : nullptr;
