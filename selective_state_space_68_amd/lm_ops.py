@@ -95,9 +95,10 @@ def _run(fn, index: int, stream, *args) -> None:
 
 
 def _scratch(workspace, need: int, like):
-    """(pointer, bytes) of the caller's workspace, or of one allocated beside `like`."""
+    """(tensor, pointer, bytes) of the caller's workspace, or of one allocated beside `like`: the
+    tensor is held until after the launches, as ops._workspace says."""
     if workspace is None and need == 0:
-        return None, 0
+        return None, None, 0
     return _workspace(workspace, need, like.device)
 
 
@@ -163,7 +164,7 @@ def linear_attention_fwd(q, k, v, log_decay, scale=None, *, initial_state=None, 
         out = q.new_empty((batch, L, H, V))
     if final_state is None and return_final_state:
         final_state = q.new_empty(states, dtype=F32)
-    ws_ptr, ws_bytes = _scratch(workspace, linear_attention_workspace_size(batch, L, H, K, V, act), q)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, linear_attention_workspace_size(batch, L, H, K, V, act), q)
     _run(_entry("ssm_linear_attention_fwd"), dev, stream,
          q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(log_decay, "log_decay", F32, dev), K ** -0.5 if scale is None else float(scale),
          _ptr(lengths, "lengths", _I32, dev), _ptr(initial_state, "initial_state", F32, dev),
@@ -198,7 +199,7 @@ def linear_attention_bwd(q, k, v, log_decay, dout, scale=None, *, initial_state=
     want = initial_state is not None if want_dinitial_state is None else want_dinitial_state
     g = _outputs(out, q, {"dq": ((batch, L, Hq, K), act, True), "dk": ((batch, L, Hk, K), act, True),
                             "dv": ((batch, L, Hv, V), act, True), "dinitial_state": (states, F32, want)})
-    ws_ptr, ws_bytes = _scratch(
+    ws, ws_ptr, ws_bytes = _scratch(
         workspace, linear_attention_bwd_workspace_size(batch, L, H, K, V, act, Hq=Hq, Hk=Hk, Hv=Hv), q)
     _run(_entry("ssm_linear_attention_bwd"), dev, stream,
          q.data_ptr(), k.data_ptr(), v.data_ptr(), dout.data_ptr(), qs, ks, vs, ds, _ptr(log_decay, "log_decay", F32, dev),
@@ -376,7 +377,7 @@ def block_norm_bwd(x, h=None, dy=None, dh=None, gate=None, post_weight=None, res
                             "dpost_weight": ((D,), F32, post_weight is not None),
                             "dres_scale": ((D,), F32, res_scale is not None),
                             "dpre_weight": ((D,), F32, pre_weight is not None)})
-    ws_ptr, ws_bytes = _scratch(workspace, block_norm_bwd_workspace_size(rows, D), x)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, block_norm_bwd_workspace_size(rows, D), x)
     (xp, xs), (gp, gs) = _rows(x, "x", D), _rows(gate, "gate", D)
     act = x.dtype
     _run(_entry("ssm_block_norm_bwd"), dev, stream,

@@ -59,17 +59,19 @@ def _stream(stream) -> int:
 
 
 def _workspace(workspace, need: int, dev):
-    """(pointer, bytes) of a caller's workspace tensor, or of one allocated here."""
+    """(tensor, pointer, bytes) of a caller's workspace tensor, or of one allocated here.  The
+    caller holds the tensor until every kernel of its call is launched: until then the
+    allocator must not give the block to another thread."""
     if workspace is None:
         if need == 0:
-            return None, 0
+            return None, None, 0
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
     nbytes = workspace.numel() * workspace.element_size()
     if nbytes < need:
         raise ValueError(f"workspace holds {nbytes} bytes, {need} needed")
-    return workspace.data_ptr(), nbytes
+    return workspace, workspace.data_ptr(), nbytes
 
 
 def _scan_shapes(u, delta, A, B, C, D, z, delta_bias, initial_state, y, final_state):
@@ -120,7 +122,7 @@ def selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, delta
     if discretization == "zoh" and ((variant & ~_lib.SSM_SCAN_AP) or tokens_per_lane or workspace is not None):
         raise ValueError("the zoh scan runs the default kernel (variant=0, tokens_per_lane=0, no workspace)")
     if discretization != "zoh":
-        ws_ptr, ws_bytes = _workspace(workspace, selective_scan_workspace_size(batch, L, Dc, N, act), dev)
+        ws, ws_ptr, ws_bytes = _workspace(workspace, selective_scan_workspace_size(batch, L, Dc, N, act), dev)
     if y is None:
         y = torch.empty((batch, Dc, L), dtype=act, device=dev)
     if final_state is None and return_final_state:
@@ -155,7 +157,7 @@ def selective_scan_fwd_save(u, delta, A, B, C, D=None, z=None, delta_bias=None, 
     act = u.dtype
     dev = u.device
     nck = (L + SAVE_CHUNK - 1) // SAVE_CHUNK
-    ws_ptr, ws_bytes = _workspace(workspace, selective_scan_workspace_size(batch, L, Dc, N, act), dev)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, selective_scan_workspace_size(batch, L, Dc, N, act), dev)
     if y is None:
         y = torch.empty((batch, Dc, L), dtype=act, device=dev)
     if final_state is None and return_final_state:
@@ -260,7 +262,7 @@ def selective_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, d
     need = selective_scan_bwd_workspace_size(batch, L, Dc, N, act, saved)
     if workspace is None:
         workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=dev)
-    ws_ptr, ws_bytes = _workspace(workspace, need, dev)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, need, dev)
     ins = (_ptr(u, "u", act, dev), _ptr(delta, "delta", act, dev), _ptr(A, "A", f32, dev),
            _ptr(B, "B", act, dev), _ptr(C, "C", act, dev), _ptr(D, "D", f32, dev),
            _ptr(z, "z", act, dev), _ptr(delta_bias, "delta_bias", f32, dev), 1 if delta_softplus else 0,
@@ -316,11 +318,11 @@ def ssd_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=True, *, init
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError(f"unknown workspace option {workspace!r}")
-        ws_ptr, ws_bytes = _workspace(None, ssd_scan_workspace_size(batch, L, H, P, N), dev)
+        ws, ws_ptr, ws_bytes = _workspace(None, ssd_scan_workspace_size(batch, L, H, P, N), dev)
     elif workspace is None:
-        ws_ptr, ws_bytes = None, 0
+        ws, ws_ptr, ws_bytes = None, None, 0
     else:
-        ws_ptr, ws_bytes = _workspace(workspace, 0, dev)
+        ws, ws_ptr, ws_bytes = _workspace(workspace, 0, dev)
     st = lib.ssm_ssd_scan_fwd(
         _ptr(x, "x", act, dev), _ptr(dt, "dt", act, dev), _ptr(A, "A", f32, dev), _ptr(B, "B", act, dev),
         _ptr(C, "C", act, dev), _ptr(D, "D", f32, dev), _ptr(dt_bias, "dt_bias", f32, dev),
