@@ -4,7 +4,8 @@ As in ops.py, torch is used for device memory and streams only, and every wrappe
 checks the shape, type and device of every tensor before it takes a pointer.
 Activations are float32 or bfloat16 tensors of one dtype; states, decays and norm
 weights are float32.  q, k, v and the output gradient may be views with a contiguous
-last axis (slices of one projection's output); other tensors are contiguous.
+last axis (slices of one projection's output); other tensors are contiguous.  `stream=`
+is as in ops.py.
 """
 from __future__ import annotations
 
@@ -15,7 +16,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
-from .ops import _shape, _workspace
+from .ops import _elsewhere, _shape, _workspace
 
 F32 = torch.float32
 BF16 = torch.bfloat16
@@ -79,12 +80,9 @@ def _strides(t, name: str, dtype, index: int):
     return (ctypes.c_int64 * (t.dim() - 1))(*t.stride()[:-1])
 
 
-def _run(fn, index: int, stream, *args) -> None:
-    """Calls fn on `stream` (GPU `index`'s current one when None), with that GPU current."""
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        stream = int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
+def _run(fn, index: int, *args) -> None:
+    """Calls fn on GPU `index`'s current stream, with that GPU current."""
+    stream = torch._C._cuda_getCurrentRawStream(index)
     if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(index):
             status = fn(*args, stream)
@@ -151,6 +149,8 @@ def linear_attention_fwd(q, k, v, log_decay, scale=None, *, initial_state=None, 
     least linear_attention_workspace_size(...) bytes, or None (allocated here).
     Returns (out [batch, L, H, V], final_state or None).
     """
+    if stream is not None:
+        return _elsewhere(linear_attention_fwd, locals())
     (batch, L), H, Hq, Hk, Hv, K, V = _attention_shapes(q, k, v, log_decay, 4)
     states = (batch, H, K, V)
     _is(lengths, "lengths", (batch,))
@@ -165,7 +165,7 @@ def linear_attention_fwd(q, k, v, log_decay, scale=None, *, initial_state=None, 
     if final_state is None and return_final_state:
         final_state = q.new_empty(states, dtype=F32)
     ws, ws_ptr, ws_bytes = _scratch(workspace, linear_attention_workspace_size(batch, L, H, K, V, act), q)
-    _run(_entry("ssm_linear_attention_fwd"), dev, stream,
+    _run(_entry("ssm_linear_attention_fwd"), dev,
          q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(log_decay, "log_decay", F32, dev), K ** -0.5 if scale is None else float(scale),
          _ptr(lengths, "lengths", _I32, dev), _ptr(initial_state, "initial_state", F32, dev),
          _ptr(out, "out", act, dev), _ptr(final_state, "final_state", F32, dev), batch, L, H, Hq, Hk, Hv, K, V, dt,
@@ -184,6 +184,8 @@ def linear_attention_bwd(q, k, v, log_decay, dout, scale=None, *, initial_state=
     `workspace`: a device tensor of at least linear_attention_bwd_workspace_size(...)
     bytes, or None (allocated here); `out` may hold preallocated outputs under the same keys.
     """
+    if stream is not None:
+        return _elsewhere(linear_attention_bwd, locals())
     (batch, L), H, Hq, Hk, Hv, K, V = _attention_shapes(q, k, v, log_decay, 4)
     states = (batch, H, K, V)
     if not isinstance(dout, _Tensor):
@@ -201,7 +203,7 @@ def linear_attention_bwd(q, k, v, log_decay, dout, scale=None, *, initial_state=
                             "dv": ((batch, L, Hv, V), act, True), "dinitial_state": (states, F32, want)})
     ws, ws_ptr, ws_bytes = _scratch(
         workspace, linear_attention_bwd_workspace_size(batch, L, H, K, V, act, Hq=Hq, Hk=Hk, Hv=Hv), q)
-    _run(_entry("ssm_linear_attention_bwd"), dev, stream,
+    _run(_entry("ssm_linear_attention_bwd"), dev,
          q.data_ptr(), k.data_ptr(), v.data_ptr(), dout.data_ptr(), qs, ks, vs, ds, _ptr(log_decay, "log_decay", F32, dev),
          K ** -0.5 if scale is None else float(scale), _ptr(lengths, "lengths", _I32, dev),
          _ptr(initial_state, "initial_state", F32, dev), _ptr(dfinal_state, "dfinal_state", F32, dev),
@@ -220,6 +222,8 @@ def linear_attention_step(state, q_t, k_t, v_t, log_decay, scale=None, *, slots=
     is outside [0, states) is idle (output 0, no state touched).  No two rows may name one
     slot.  None: row b's state is number b.
     """
+    if stream is not None:
+        return _elsewhere(linear_attention_step, locals())
     (batch,), H, Hq, Hk, Hv, K, V = _attention_shapes(q_t, k_t, v_t, log_decay, 3)
     _dims(state, "state", 4)
     states = state.shape[0]
@@ -235,7 +239,7 @@ def linear_attention_step(state, q_t, k_t, v_t, log_decay, scale=None, *, slots=
     state_ptr = _ptr(state, "state", F32, dev)
     if out is None:
         out = q_t.new_empty((batch, H, V))
-    _run(_entry("ssm_linear_attention_step"), dev, stream,
+    _run(_entry("ssm_linear_attention_step"), dev,
          state_ptr, state_ptr if out_state is None else _ptr(out_state, "out_state", F32, dev),
          q_t.data_ptr(), k_t.data_ptr(), v_t.data_ptr(), qs, ks, vs,
          _ptr(log_decay, "log_decay", F32, dev), K ** -0.5 if scale is None else float(scale),
@@ -320,6 +324,8 @@ def block_norm_fwd(x, residual=None, gate=None, post_weight=None, res_scale=None
     residual (updated in place).  Returns (h, y): h None when return_h is False and no h is
     given, y None without pre_weight.
     """
+    if stream is not None:
+        return _elsewhere(block_norm_fwd, locals())
     shape = x.shape if isinstance(x, _Tensor) else None
     _is(residual, "residual", shape)
     _is(h, "h", shape)
@@ -336,7 +342,7 @@ def block_norm_fwd(x, residual=None, gate=None, post_weight=None, res_scale=None
         y = x.new_empty(shape)
     (xp, xs), (gp, gs) = _rows(x, "x", D), _rows(gate, "gate", D)
     act = x.dtype
-    _run(_entry("ssm_block_norm_fwd"), dev, stream,
+    _run(_entry("ssm_block_norm_fwd"), dev,
          xp, xs, _ptr(residual, "residual", rdtype, dev), gp, gs, _ptr(post_weight, "post_weight", F32, dev),
          _ptr(res_scale, "res_scale", F32, dev), _ptr(pre_weight, "pre_weight", F32, dev), _ptr(h, "h", rdtype, dev),
          _ptr(y, "y", act, dev), rows, D, int(groups), float(eps), _dt(act), rdt)
@@ -359,6 +365,8 @@ def block_norm_bwd(x, h=None, dy=None, dh=None, gate=None, post_weight=None, res
     computed), else None.  Returns a dict with dx, dgate, dresidual, dpost_weight, dres_scale
     and dpre_weight (None where the input is absent).  out["dresidual"] may be dh itself.
     """
+    if stream is not None:
+        return _elsewhere(block_norm_bwd, locals())
     shape = x.shape if isinstance(x, _Tensor) else None
     _is(h, "h", shape)
     _is(dy, "dy", shape)
@@ -380,7 +388,7 @@ def block_norm_bwd(x, h=None, dy=None, dh=None, gate=None, post_weight=None, res
     ws, ws_ptr, ws_bytes = _scratch(workspace, block_norm_bwd_workspace_size(rows, D), x)
     (xp, xs), (gp, gs) = _rows(x, "x", D), _rows(gate, "gate", D)
     act = x.dtype
-    _run(_entry("ssm_block_norm_bwd"), dev, stream,
+    _run(_entry("ssm_block_norm_bwd"), dev,
          xp, xs, _ptr(h, "h", rdtype, dev), _ptr(dy, "dy", act, dev), _ptr(dh, "dh", rdtype, dev), gp, gs,
          _ptr(post_weight, "post_weight", F32, dev), _ptr(res_scale, "res_scale", F32, dev),
          _ptr(pre_weight, "pre_weight", F32, dev), _ptr(g["dx"], "dx", act, dev), _ptr(g["dgate"], "dgate", act, dev),

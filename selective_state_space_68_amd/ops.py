@@ -8,6 +8,9 @@ Layouts: u, delta, z [batch, D, L]; B, C [batch, L, N]; A [D, N]; D, bias [D].
 Every wrapper checks the shape of every tensor it is given, outputs included,
 before it takes a single pointer: the library sees only pointers and sizes, so a
 tensor smaller than its shape says would otherwise be read or written past its end.
+
+`stream=` runs a call on another stream than the current one: outputs and scratch memory
+are then that stream's, and the caller orders the two streams around the call.
 """
 from __future__ import annotations
 
@@ -52,10 +55,39 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, device=None):
     return t.data_ptr()
 
 
-def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _stream() -> int:
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _elsewhere(fn, given: dict):
+    """Makes the call fn(**given) on the stream that given["stream"] names (a torch stream or a handle).
+
+    What the call allocates then comes from that stream's memory, whose blocks are reused in the
+    order of its work; the tensors it was given are marked as in use there and its results as in
+    use on the caller's current stream, so that dropping them is safe on either side.  That the
+    inputs are ready on the stream, and the results before they are read elsewhere, is the caller's
+    to order."""
+    stream = given.pop("stream")
+    given_tensors = [t for a in given.values() for t in (a.values() if isinstance(a, dict) else (a,))
+                     if isinstance(t, torch.Tensor) and t.is_cuda]
+    if not given_tensors:
+        return fn(**given)                                  # (refused there)
+    index = given_tensors[0].get_device()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=index)
+    if stream.device_index != index:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors are on cuda:{index}")
+    here = torch.cuda.current_stream(index)
+    if stream.cuda_stream == here.cuda_stream:
+        return fn(**given)
+    for t in given_tensors:
+        t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        got = fn(**given)
+    for t in got.values() if isinstance(got, dict) else got if isinstance(got, tuple) else (got,):
+        if t is not None:
+            t.record_stream(here)
+    return got
 
 
 def _workspace(workspace, need: int, dev):
@@ -113,6 +145,8 @@ def selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, delta
     `workspace`: a device tensor of at least selective_scan_workspace_size(...)
     bytes, or None (allocated here when the size is nonzero).
     """
+    if stream is not None:
+        return _elsewhere(selective_scan_fwd, locals())
     if discretization not in ("simplified", "zoh"):
         raise ValueError(f"unknown discretization {discretization!r}")
     lib = _lib.load_library()
@@ -134,9 +168,9 @@ def selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, delta
             _ptr(y, "y", act, dev), _ptr(final_state, "final_state", torch.float32, dev),
             batch, L, Dc, N, _dt(u))
     if discretization == "zoh":
-        st = lib.ssm_selective_scan_fwd_zoh(*args, _stream(stream))
+        st = lib.ssm_selective_scan_fwd_zoh(*args, _stream())
     else:
-        st = lib.ssm_selective_scan_fwd_variant(*args, ws_ptr, ws_bytes, _stream(stream), int(variant),
+        st = lib.ssm_selective_scan_fwd_variant(*args, ws_ptr, ws_bytes, _stream(), int(variant),
                                                 int(tokens_per_lane))
     _lib.check(st)
     return y, final_state
@@ -152,6 +186,8 @@ def selective_scan_fwd_save(u, delta, A, B, C, D=None, z=None, delta_bias=None, 
     chunk, for selective_scan_bwd(..., chunk_states=...).  Returns (y, final_state or
     None, chunk_states [batch, D, ceil(L / SAVE_CHUNK), N] float32); entry 0 is the
     initial state (zeros when None).  N <= 16."""
+    if stream is not None:
+        return _elsewhere(selective_scan_fwd_save, locals())
     lib = _lib.load_library()
     batch, Dc, L, N = _scan_shapes(u, delta, A, B, C, D, z, delta_bias, initial_state, y, final_state)
     act = u.dtype
@@ -172,7 +208,7 @@ def selective_scan_fwd_save(u, delta, A, B, C, D=None, z=None, delta_bias=None, 
         _ptr(initial_state, "initial_state", torch.float32, dev), _ptr(y, "y", act, dev),
         _ptr(final_state, "final_state", torch.float32, dev),
         _ptr(chunk_states, "chunk_states", torch.float32, dev),
-        batch, L, Dc, N, _dt(u), ws_ptr, ws_bytes, _stream(stream))
+        batch, L, Dc, N, _dt(u), ws_ptr, ws_bytes, _stream())
     _lib.check(st)
     return y, final_state, chunk_states
 
@@ -224,6 +260,8 @@ def selective_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, d
     (ssm_selective_scan_bwd_saved) and the workspace is
     selective_scan_bwd_workspace_size(..., saved=True) bytes.
     """
+    if stream is not None:
+        return _elsewhere(selective_scan_bwd, locals())
     lib = _lib.load_library()
     batch, Dc, L, N = _scan_shapes(u, delta, A, B, C, D, z, delta_bias, initial_state, None, None)
     _shape(dy, "dy", (batch, Dc, L))
@@ -277,7 +315,7 @@ def selective_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, d
         _ptr(out["du"], "du"), _ptr(out["ddelta"], "ddelta"), _ptr(out["dA"], "dA"), _ptr(out["dB"], "dB"),
         _ptr(out["dC"], "dC"), _ptr(out["dD"], "dD"), _ptr(out["dz"], "dz"),
         _ptr(out["ddelta_bias"], "ddelta_bias"), _ptr(out["dinitial_state"], "dinitial_state"),
-        batch, L, Dc, N, _dt(u), ws_ptr, ws_bytes, _stream(stream))
+        batch, L, Dc, N, _dt(u), ws_ptr, ws_bytes, _stream())
     _lib.check(st)
     return out
 
@@ -295,6 +333,8 @@ def ssd_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=True, *, init
     final_state [batch, H, P, N] float32 or None).  `workspace`: a device tensor of at
     least ssd_scan_workspace_size(...) bytes, None (one segment per sequence), or
     "auto" (allocated here)."""
+    if stream is not None:
+        return _elsewhere(ssd_scan_fwd, locals())
     lib = _lib.load_library()
     if not isinstance(x, torch.Tensor) or not isinstance(B, torch.Tensor) or x.dim() != 4 or B.dim() != 3:
         raise ValueError("expected x [batch, L, H, P] and B/C [batch, L, N]")
@@ -328,7 +368,7 @@ def ssd_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=True, *, init
         _ptr(C, "C", act, dev), _ptr(D, "D", f32, dev), _ptr(dt_bias, "dt_bias", f32, dev),
         1 if dt_softplus else 0, _ptr(initial_state, "initial_state", f32, dev), _ptr(y, "y", act, dev),
         _ptr(final_state, "final_state", f32, dev), batch, L, H, P, N, _dt(x), ws_ptr, ws_bytes,
-        _stream(stream))
+        _stream())
     _lib.check(st)
     return y, final_state
 
@@ -336,6 +376,8 @@ def ssd_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=True, *, init
 def causal_conv1d(x, weight, bias=None, silu=True, *, out=None, stream=None) -> torch.Tensor:
     """Causal depthwise conv1d along L (+ SiLU).  x [batch, D, L]; weight [D, K] float32
     (K <= 4, weight[:, K-1] weighs the current token); bias [D] or None."""
+    if stream is not None:
+        return _elsewhere(causal_conv1d, locals())
     lib = _lib.load_library()
     if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor) or x.dim() != 3 \
             or weight.dim() != 2 or weight.shape[0] != x.shape[1]:
@@ -349,7 +391,7 @@ def causal_conv1d(x, weight, bias=None, silu=True, *, out=None, stream=None) -> 
     st = lib.ssm_causal_conv1d_fwd(
         _ptr(x, "x", x.dtype, dev), _ptr(weight, "weight", torch.float32, dev),
         _ptr(bias, "bias", torch.float32, dev), int(weight.shape[1]), 1 if silu else 0,
-        _ptr(out, "out", x.dtype, dev), batch, Dc, L, _dt(x), _stream(stream))
+        _ptr(out, "out", x.dtype, dev), batch, Dc, L, _dt(x), _stream())
     _lib.check(st)
     return out
 
@@ -362,6 +404,8 @@ def selective_scan_fwd_conv(x, conv_weight, conv_bias, delta, A, B, C, D=None, z
 
     Returns (y, final_state, u) where u is the convolution output when `return_u`
     (or `u_out` is given), else None."""
+    if stream is not None:
+        return _elsewhere(selective_scan_fwd_conv, locals())
     lib = _lib.load_library()
     batch, Dc, L, N = _scan_shapes(x, delta, A, B, C, D, z, delta_bias, initial_state, y, final_state)
     if not isinstance(conv_weight, torch.Tensor) or conv_weight.dim() != 2 or conv_weight.shape[0] != Dc:
@@ -385,7 +429,7 @@ def selective_scan_fwd_conv(x, conv_weight, conv_bias, delta, A, B, C, D=None, z
         1 if delta_softplus else 0, _ptr(initial_state, "initial_state", torch.float32, dev),
         _ptr(u_out, "u_out", act, dev), _ptr(y, "y", act, dev),
         _ptr(final_state, "final_state", torch.float32, dev),
-        batch, L, Dc, N, _dt(x), _stream(stream), int(tokens_per_lane))
+        batch, L, Dc, N, _dt(x), _stream(), int(tokens_per_lane))
     _lib.check(st)
     return y, final_state, u_out
 
@@ -396,6 +440,8 @@ def state_update(state, u_t, delta_t, A, B_t, C_t, D=None, z_t=None, delta_bias=
     """One decode step.  state [S, D, N] float32; u_t, delta_t, z_t [S, D]; A [D, N];
     B_t, C_t [S, N]; D, delta_bias [D].  Updates `out_state` (default: `state`, in
     place); returns y_t [S, D].  `discretization` as in selective_scan_fwd."""
+    if stream is not None:
+        return _elsewhere(state_update, locals())
     if discretization not in ("simplified", "zoh"):
         raise ValueError(f"unknown discretization {discretization!r}")
     lib = _lib.load_library()
@@ -424,6 +470,6 @@ def state_update(state, u_t, delta_t, A, B_t, C_t, D=None, z_t=None, delta_bias=
         _ptr(u_t, "u_t", act, dev), _ptr(delta_t, "delta_t", act, dev), _ptr(A, "A", torch.float32, dev),
         _ptr(B_t, "B_t", act, dev), _ptr(C_t, "C_t", act, dev), _ptr(D, "D", torch.float32, dev),
         _ptr(z_t, "z_t", act, dev), _ptr(delta_bias, "delta_bias", torch.float32, dev),
-        1 if delta_softplus else 0, _ptr(y, "y", act, dev), S, Dc, N, _dt(u_t), _stream(stream))
+        1 if delta_softplus else 0, _ptr(y, "y", act, dev), S, Dc, N, _dt(u_t), _stream())
     _lib.check(st)
     return y

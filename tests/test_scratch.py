@@ -49,9 +49,9 @@ def host(monkeypatch):
     h = Host(_lib.load_library())
     monkeypatch.setattr(torch, "empty", h.empty(torch.empty))
     monkeypatch.setattr(_lib, "load_library", lambda: h)
-    monkeypatch.setattr(ops, "_stream", lambda stream: 0)
+    monkeypatch.setattr(ops, "_stream", lambda: 0)
     monkeypatch.setattr(lm_ops, "_entry", lambda name: getattr(h, name))
-    monkeypatch.setattr(lm_ops, "_run", lambda fn, index, stream, *args: fn(*args))
+    monkeypatch.setattr(lm_ops, "_run", lambda fn, index, *args: fn(*args))
     return h
 
 
