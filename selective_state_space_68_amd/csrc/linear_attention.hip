@@ -57,6 +57,7 @@ namespace ssm {
 namespace {
 
 constexpr int kQ = 64;               // tokens per chunk
+constexpr int kRoom = 8;             // bits of decay between two scalings of the state
 constexpr float kMinLog2 = -1.0e4f;  // 2^kMinLog2 == 0 and kMinLog2 * 0 == 0: a decay of exactly 0 works like any other
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
@@ -259,6 +260,8 @@ __device__ __forceinline__ float decay_log2(const float* log_decay, int h) {
   return g < kMinLog2 ? kMinLog2 : g;
 }
 
+constexpr float kMaxFloat = 3.4028234663852886e38f;
+
 // lam^n.  A state passes through thousands of these factors, so they are formed in float64
 // and applied as a float32 pair hi + lo: the rounding of lam^n alone would grow to
 // n_chunks * 2^-24 over the head's memory.
@@ -272,6 +275,10 @@ __device__ __forceinline__ Pair pair_of(double d) {
   const float hi = static_cast<float>(d);
   const float lo = static_cast<float>(d - static_cast<double>(hi));
   return Pair{hi, lo == lo ? lo : 0.0f};              // (inf - inf where lam^n overflows)
+}
+// (an infinite x stays what it is: hi x + lo x is a NaN where lo is 0 or of the other sign)
+__device__ __forceinline__ float times(const Pair& d, float x) {
+  return __builtin_fmaf(d.hi, x, d.lo * __builtin_amdgcn_fmed3f(x, -kMaxFloat, kMaxFloat));
 }
 // lam^n to float32 accuracy at any n: the exponent is reduced in float64.  (exp(), of which the
 // factors above take a few a workgroup, costs about a microsecond.)
@@ -566,6 +573,7 @@ void la_kernel(LaArgs p) {
   const int place = 8 * g * r.sk + (16 * VT * w + c16) * r.sv;
   // forwards the carried state decays once before the first token; the segments' states have
   const float first = nseg > 1 || reverse || len == 0 ? 1.0f : exp2_hw(g2);
+  const float room = c_begin < c_live ? static_cast<float>(1 << kRoom) : 1.0f;   // (below)
 #pragma unroll
   for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
@@ -589,20 +597,23 @@ void la_kernel(LaArgs p) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) E[vt][t][u][e] = there(vt, t, u, e) ? E[vt][t][u][e] * first : 0.0f;
+          for (int e = 0; e < 4; ++e) E[vt][t][u][e] = there(vt, t, u, e) ? E[vt][t][u][e] * (first / room) : 0.0f;
   }
 
-  // The registers hold the state divided by rho = lam^(64 a), a the chunks since the last time
-  // it was multiplied out: a chunk then adds lam^(64 - i) v / rho' instead of decaying
-  // every entry.  Past 2^30 the state is multiplied out, by rho as a float32 pair from
-  // float64, so that no rounding of lam^64 builds up over the thousands of chunks of a head's memory.
+  // The registers hold the state divided by rho = 2^kRoom lam^(64 a), a the chunks since the last
+  // time they were scaled back: a chunk then adds lam^(64 - i) v / rho' instead of decaying every entry.
+  // Past 2^kRoom of decay the registers are scaled back to a = 0, by a float32 pair from float64, so that no
+  // rounding of lam^64 builds up over the thousands of chunks of a head's memory.  rho stays at 1 and more:
+  // what the registers hold is never larger than the state itself, so it overflows only where that does (and
+  // states below 2^(kRoom - 126) lose bits).
   const double lam_q = uniform_double(decay_power(p.log_decay, h, kQ));
   const double unlam_q = uniform_double(1.0 / lam_q);
   const float g_q = g2 * kQ;
+  constexpr double kUp = 1 << kRoom, kDown = 1.0 / kUp;
   int a = 0;
-  double rho = 1.0, unrho = 1.0;                    // lam^(64 a) and its inverse
-  auto multiply_out = [&](double by) __attribute__((always_inline)) {      // by: the decay of the chunk just done
-    const Pair d = pair_of(by * rho);
+  double rho = room, unrho = kDown;                 // and its inverse
+  auto scale_state = [&](double by) __attribute__((always_inline)) {
+    const Pair d = pair_of(by);
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
@@ -610,9 +621,7 @@ void la_kernel(LaArgs p) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) E[vt][t][u][e] = __builtin_fmaf(d.hi, E[vt][t][u][e], d.lo * E[vt][t][u][e]);
-    a = 0;
-    rho = unrho = 1.0;
+          for (int e = 0; e < 4; ++e) E[vt][t][u][e] = times(d, E[vt][t][u][e]);
   };
   // The last chunk of the sequence (of the segment, in the pre-pass) forwards leaves S, not lam S,
   // and may hold fewer tokens.
@@ -796,12 +805,15 @@ void la_kernel(LaArgs p) {
 
     // ---- the state: lam^n E + k^T (lam^(n-i) v)
     const bool whole = more || n - shift == kQ;
-    if (__builtin_expect(whole && fabsf(g_q * static_cast<float>(a + 1)) < 30.0f, 1)) {
+    if (__builtin_expect(whole && fabsf(g_q * static_cast<float>(a + 1)) < static_cast<float>(kRoom), 1)) {
       ++a;
       rho *= lam_q;
       unrho *= unlam_q;
     } else {
-      multiply_out(whole ? lam_q : lam_end);
+      scale_state((whole ? lam_q : lam_end) * (rho * kDown));      // (with the decay of the chunk just done)
+      a = 0;
+      rho = kUp;
+      unrho = kDown;
     }
     const float wc = in_decay * static_cast<float>(unrho);
     const uint32_t k_cols = O::template column_part<RK, true>(k_tile, 0, 8, lane);
@@ -814,7 +826,7 @@ void la_kernel(LaArgs p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int left = n - shift - (32 * t + 8 * g + e);
-          wgt[e] = exp2_hw(g2 * static_cast<float>(left > 0 ? left : 0)) * r.in_scale;
+          wgt[e] = exp2_hw(g2 * static_cast<float>(left > 0 ? left : 0)) * (r.in_scale * static_cast<float>(kDown));
           asm volatile("" : "+v"(wgt[e]));
         }
       }
@@ -910,7 +922,6 @@ void la_kernel(LaArgs p) {
     for (; c < last; ++c) chunk(std::true_type{}, c);
   }
   for (; c < c_live; ++c) chunk(std::false_type{}, c);
-  if (a) multiply_out(1.0);
 
   // chunks with no token: zeros
   if constexpr (!STATE_ONLY) {
@@ -929,6 +940,7 @@ void la_kernel(LaArgs p) {
   if (STATE_ONLY) dst = r.seg + (bh * nseg + seg) * static_cast<int64_t>(K) * V;
   else if (nseg == 1 && r.fin) dst = r.fin + bh * static_cast<int64_t>(K) * V;
   if (dst) {
+    scale_state(rho);
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
@@ -964,7 +976,6 @@ __global__ __launch_bounds__(256) void la_chain_kernel(LaArgs p) {
   float s[kChain], T[kAhead][kChain];
 #pragma unroll
   for (int x = 0; x < kChain; ++x) s[x] = carry && i0 + 256 * x < KV ? carry[i0 + 256 * x] : 0.0f;
-  auto times = [](const Pair& d, float x) { return __builtin_fmaf(d.hi, x, d.lo * x); };
   float l1 = 0.0f;
   Pair lS{0.0f, 0.0f};                              // (the factor that a state meets once a segment; the others, once)
   for (int k0 = 0; k0 < p.nseg; k0 += kAhead) {
