@@ -260,8 +260,6 @@ __device__ __forceinline__ float decay_log2(const float* log_decay, int h) {
   return g < kMinLog2 ? kMinLog2 : g;
 }
 
-constexpr float kMaxFloat = 3.4028234663852886e38f;
-
 // lam^n.  A state passes through thousands of these factors, so they are formed in float64
 // and applied as a float32 pair hi + lo: the rounding of lam^n alone would grow to
 // n_chunks * 2^-24 over the head's memory.
@@ -271,15 +269,14 @@ struct Pair {
 __device__ __forceinline__ double decay_power(const float* log_decay, int h, int n) {
   return n == 0 ? 1.0 : exp(static_cast<double>(log_decay[h]) * n);
 }
+// (hi is strictly below d and lo above 0, so that an infinite x stays what it is: hi x + lo x would be a NaN with
+// lo 0 or of the other sign.  The sum is exact to float32 in either case.)
 __device__ __forceinline__ Pair pair_of(double d) {
-  const float hi = static_cast<float>(d);
-  const float lo = static_cast<float>(d - static_cast<double>(hi));
-  return Pair{hi, lo == lo ? lo : 0.0f};              // (inf - inf where lam^n overflows)
+  float hi = static_cast<float>(d);
+  if (d > 0.0 && static_cast<double>(hi) >= d) hi = __builtin_bit_cast(float, __builtin_bit_cast(int, hi) - 1);
+  return Pair{hi, static_cast<float>(d - static_cast<double>(hi))};
 }
-// (an infinite x stays what it is: hi x + lo x is a NaN where lo is 0 or of the other sign)
-__device__ __forceinline__ float times(const Pair& d, float x) {
-  return __builtin_fmaf(d.hi, x, d.lo * __builtin_amdgcn_fmed3f(x, -kMaxFloat, kMaxFloat));
-}
+__device__ __forceinline__ float times(const Pair& d, float x) { return __builtin_fmaf(d.hi, x, d.lo * x); }
 // lam^n to float32 accuracy at any n: the exponent is reduced in float64.  (exp(), of which the
 // factors above take a few a workgroup, costs about a microsecond.)
 __device__ __forceinline__ float decay_float(const float* log_decay, int h, int n) {
@@ -573,13 +570,14 @@ void la_kernel(LaArgs p) {
   const int place = 8 * g * r.sk + (16 * VT * w + c16) * r.sv;
   // forwards the carried state decays once before the first token; the segments' states have
   const float first = nseg > 1 || reverse || len == 0 ? 1.0f : exp2_hw(g2);
-  const float room = c_begin < c_live ? static_cast<float>(1 << kRoom) : 1.0f;   // (below)
+  const bool scaled = c_begin < c_live;             // (below)
 #pragma unroll
   for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int u = 0; u < 2; ++u) E[vt][t][u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const float entering = scaled ? first * (1.0f / (1 << kRoom)) : first;
   if (src) {                                        // (one branch, so that all loads are under way together)
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
@@ -597,7 +595,7 @@ void la_kernel(LaArgs p) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) E[vt][t][u][e] = there(vt, t, u, e) ? E[vt][t][u][e] * (first / room) : 0.0f;
+          for (int e = 0; e < 4; ++e) E[vt][t][u][e] = there(vt, t, u, e) ? E[vt][t][u][e] * entering : 0.0f;
   }
 
   // The registers hold the state divided by rho = 2^kRoom lam^(64 a), a the chunks since the last
@@ -611,7 +609,7 @@ void la_kernel(LaArgs p) {
   const float g_q = g2 * kQ;
   constexpr double kUp = 1 << kRoom, kDown = 1.0 / kUp;
   int a = 0;
-  double rho = room, unrho = kDown;                 // and its inverse
+  double rho = scaled ? kUp : 1.0, unrho = kDown;                 // and its inverse
   auto scale_state = [&](double by) __attribute__((always_inline)) {
     const Pair d = pair_of(by);
 #pragma unroll
@@ -996,7 +994,7 @@ __global__ __launch_bounds__(256) void la_chain_kernel(LaArgs p) {
       const int k = k0 + u;
       if (k >= p.nseg) break;
       const int n = tokens(k);
-      const Pair d = n == seg_tokens ? lS : Pair{decay_float(p.log_decay, h, n), 0.0f};
+      const Pair d = n == seg_tokens ? lS : pair_of(static_cast<double>(decay_float(p.log_decay, h, n)));
 #pragma unroll
       for (int x = 0; x < kChain; ++x) {
         if (i0 + 256 * x < KV) slot[static_cast<int64_t>(k) * KV + i0 + 256 * x] = r.reverse ? s[x] : l1 * s[x];
