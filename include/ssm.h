@@ -482,9 +482,11 @@ ssm_status ssm_ssd_scan_fwd_noalloc(
  * With float32 activations every product is in float32.  With bfloat16 the products are
  * bfloat16 with float32 accumulation: q, k and v enter as they are, the masked scores and
  * the state as two bfloat16 terms (16 bits), the decayed values that enter the state as three (24
- * bits; two where the state is not returned); the state is float32 throughout.  16-byte aligned rows
+ * bits; two for the outputs, not for the final state, of a sequence that runs in segments, which it
+ * does where a workspace is needed for it); the state is float32 throughout.  16-byte aligned rows
  * (K and V multiples of 8, strides multiples of 16 bytes) move as vectors; rows of whole 4-byte words
- * run slower, others slower still, with the same results.  A NaN or infinity in a token that is there reaches every later
+ * run slower, others slower still, with the same results.  Which states are asked for changes no other
+ * result either.  A NaN or infinity in a token that is there reaches every later
  * output of its row and head, and may reach earlier outputs within 63 tokens of it.
  *
  * ssm_linear_attention_bwd: the gradients of sum(dout * out) + sum(dfinal_state * final_state).

@@ -23,9 +23,9 @@
 // and v once P and the product with E are done, before P v and the state's product.
 //
 // Roundings (bfloat16 activations; float32 activations use float32 products throughout): the decayed v
-// of a state that is a result is split into three bfloat16 terms, which carry all 24 bits; E and P as
-// operands of the output (and the decayed v of a state that only feeds it) into two terms, 16 bits,
-// so that the output's own rounding is the one that counts.  One term of P is not enough where a
+// is split into three bfloat16 terms, which carry all 24 bits; E and P as operands of the output (and in
+// segments the decayed v of the pass that only feeds it, WT below) into two terms, 16 bits, so that the
+// output's own rounding is the one that counts.  One term of P is not enough where a
 // gradient's terms cancel.
 //
 // When the (batch row, head) pairs are too few to fill the chip the sequence is cut into segments: a
@@ -431,9 +431,11 @@ template <typename ACT, int VD>
 constexpr int kColumnTiles = sizeof(typename Op<ACT>::elem) == 2 && VD == 128 ? 2 : 1;
 
 // MOVE: the bytes that a lane of a load moves (16, 4; 0: element by element).  ALL: K = KD and V = VD.
-// WT: operand terms of the decayed v, 3 where the state is a result, 2 where it only serves outputs,
-// whose products take E in two terms (131072 tokens: 930 us with 3, 904 with 2; gradient at 4 x 2048, 32
-// heads of 128: 195 and 181).
+// WT: operand terms of the decayed v: 3, or 2 in the main pass of a sequence in segments, where the state that
+// is returned comes from the pre-pass and this one only serves outputs, whose products take E in two terms
+// (131072 tokens: 916 us with 3, 877 with 2).  It goes by the number of segments alone, so that neither the
+// rows' alignment nor whether a state is asked for changes a bit of the outputs.  (With 2 wherever no state is
+// returned the gradient at 8 x 2048, 32 heads of 128, took 323 us without dinitial_state, 349 so.)
 template <typename ACT, int KD, int VD, int MOVE, bool ALL, bool STATE_ONLY, int WT>
 __global__ __launch_bounds__((4 * VD / kColumnTiles<ACT, VD>), VD == 128 || sizeof(typename Op<ACT>::elem) == 4 ? 2 : 3)
 void la_kernel(LaArgs p) {
@@ -1050,15 +1052,13 @@ void launch_la_t(const LaArgs& a, bool state_only, hipStream_t s) {
   const int64_t items = (a.batch * a.H * a.nseg + 7) / 8 * 8;
   const dim3 grid(static_cast<unsigned>(items * a.nroles)), block(4 * VD / kColumnTiles<ACT, VD>);
   constexpr int kTerms = ACT::kBytes == 4 ? 1 : 3;
-  bool results = false;                             // whether a state of this launch is one
-  for (int i = 0; i < a.nroles; ++i) results = results || (a.nseg == 1 && a.role[i].fin);
   auto go = [&](auto move, auto all) {
     constexpr int MOVE = decltype(move)::value;
     constexpr bool ALL = decltype(all)::value;
     if (state_only) hipLaunchKernelGGL((la_kernel<ACT, KD, VD, MOVE, ALL, true, kTerms>), grid, block, 0, s, a);
-    else if (MOVE < 16 || kTerms == 1 || results)
+    else if (kTerms == 1 || a.nseg == 1)
       hipLaunchKernelGGL((la_kernel<ACT, KD, VD, MOVE, ALL, false, kTerms>), grid, block, 0, s, a);
-    else if constexpr (MOVE == 16 && kTerms == 3)
+    else if constexpr (kTerms == 3)
       hipLaunchKernelGGL((la_kernel<ACT, KD, VD, MOVE, ALL, false, 2>), grid, block, 0, s, a);
   };
   const LaRole& r = a.role[0];
