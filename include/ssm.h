@@ -486,8 +486,9 @@ ssm_status ssm_ssd_scan_fwd_noalloc(
  * does where a workspace is needed for it); the state is float32 throughout.  16-byte aligned rows
  * (K and V multiples of 8, strides multiples of 16 bytes) move as vectors; rows of whole 4-byte words
  * run slower, others slower still, with the same results.  Which states are asked for changes no other
- * result either.  A NaN or infinity in a token that is there reaches every later
- * output of its row and head, and may reach earlier outputs within 63 tokens of it.
+ * result either.  A NaN or infinity in a token that is there reaches the
+ * later outputs that the recurrence takes it to (as a NaN, maybe, where that has an infinity) and no
+ * earlier one; a row and head with one takes twice the time.
  *
  * ssm_linear_attention_bwd: the gradients of sum(dout * out) + sum(dfinal_state * final_state).
  *   dout          : [batch][L][H][V] act, a view as q is (dout_strides)

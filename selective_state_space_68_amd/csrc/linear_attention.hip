@@ -287,6 +287,7 @@ __device__ __forceinline__ float decay_float(const float* log_decay, int h, int 
   return __builtin_ldexpf(exp2_hw(static_cast<float>(x - whole)), static_cast<int>(whole));
 }
 
+__device__ __forceinline__ int least(int a, int b) { return a < b ? a : b; }
 __device__ __forceinline__ int lane_id() { return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)); }
 
 // A value that is the same in every lane, kept in a scalar register.
@@ -490,11 +491,6 @@ void la_kernel(LaArgs p) {
   TileLoad<elem, RK, NW, true> k_load;
   TileLoad<elem, RK, NW, false> q_load;
   TileLoad<elem, RV, NW, false> v_load;
-  if constexpr (MOVE == 16) {
-    k_load.start(kg, kstep, c_begin, w, lane0);
-    if constexpr (!STATE_ONLY) q_load.start(qg, qstep, c_begin, w, lane0);
-    v_load.start(vg, vstep, c_begin, w, lane0);
-  }
   auto load_k = [&](auto plain, int c, int lane) __attribute__((always_inline)) {
     constexpr bool PLAIN = decltype(plain)::value;
     const int last = len - 1 - c * kQ;
@@ -542,19 +538,28 @@ void la_kernel(LaArgs p) {
     }
   };
   auto present = [&](int c) { return len - c * kQ < kQ ? len - c * kQ : kQ; };
-  if constexpr (MOVE > 0) {
-    if (!ALL) {                                     // columns that the loads leave alone
-      clear_tile<RK, NW>(sKK[0], 0, w, lane0);
-      clear_tile<RK, NW>(sKK[1], 0, w, lane0);
-      if constexpr (!STATE_ONLY) clear_tile<RK, NW>(sQ, 0, w, lane0);
-      clear_tile<RV, NW>(sV, 0, w, lane0);
-      __builtin_amdgcn_s_waitcnt(0xc07f);           // lgkmcnt(0): before the loads into the same slots
+  // The walk begins: the first chunk's rows are asked for.
+  auto ask = [&]() __attribute__((always_inline)) {
+    if constexpr (MOVE == 16) {
+      k_load.start(kg, kstep, c_begin, w, lane0);
+      if constexpr (!STATE_ONLY) q_load.start(qg, qstep, c_begin, w, lane0);
+      v_load.start(vg, vstep, c_begin, w, lane0);
     }
-  }
-  if (c_begin < c_live) {
-    load_k(std::false_type{}, c_begin, lane0);
-    load_qv(std::false_type{}, c_begin, lane0);
-  }
+    if constexpr (MOVE > 0) {
+      if (!ALL) {                                   // columns that the loads leave alone
+        clear_tile<RK, NW>(sKK[0], 0, w, lane0);
+        clear_tile<RK, NW>(sKK[1], 0, w, lane0);
+        if constexpr (!STATE_ONLY) clear_tile<RK, NW>(sQ, 0, w, lane0);
+        clear_tile<RV, NW>(sV, 0, w, lane0);
+        __builtin_amdgcn_s_waitcnt(0xc07f);         // lgkmcnt(0): before the loads into the same slots
+      }
+    }
+    if (c_begin < c_live) {
+      load_k(std::false_type{}, c_begin, lane0);
+      load_qv(std::false_type{}, c_begin, lane0);
+    }
+  };
+  ask();
 
   const int g = lane0 >> 4, c16 = lane0 & 15;
   // E[vt][t][u][e] is the entry k = 32 t + 8 g + 4 u + e, v = 16 (VT w + vt) + c16
@@ -573,32 +578,35 @@ void la_kernel(LaArgs p) {
   // forwards the carried state decays once before the first token; the segments' states have
   const float first = nseg > 1 || reverse || len == 0 ? 1.0f : exp2_hw(g2);
   const bool scaled = c_begin < c_live;             // (below)
-#pragma unroll
-  for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) E[vt][t][u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const float entering = scaled ? first * (1.0f / (1 << kRoom)) : first;
-  if (src) {                                        // (one branch, so that all loads are under way together)
+  auto enter = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
       for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) E[vt][t][u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    if (src) {                                      // (one branch, so that all loads are under way together)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            E[vt][t][u][e] = src[static_cast<uint32_t>(there(vt, t, u, e) ? place + entry(vt, t, u, e) : 0)];
+      for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
-    for (int vt = 0; vt < VT; ++vt)
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int t = 0; t < KT; ++t)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+            for (int e = 0; e < 4; ++e)
+              E[vt][t][u][e] = src[static_cast<uint32_t>(there(vt, t, u, e) ? place + entry(vt, t, u, e) : 0)];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) E[vt][t][u][e] = there(vt, t, u, e) ? E[vt][t][u][e] * entering : 0.0f;
-  }
+      for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) E[vt][t][u][e] = there(vt, t, u, e) ? E[vt][t][u][e] * entering : 0.0f;
+    }
+  };
+  enter();
 
   // The registers hold the state divided by rho = 2^kRoom lam^(64 a), a the chunks since the last
   // time they were scaled back: a chunk then adds lam^(64 - i) v / rho' instead of decaying every entry.
@@ -655,13 +663,14 @@ void la_kernel(LaArgs p) {
 
   // where the output rows of a whole chunk go: backwards, row r of the chunk is 63 - r rows up
   const bool o_f32 = kF32 || r.o_f32;
-  char* o_next = nullptr;
+  char *o_first = nullptr, *o_next = nullptr;
   int64_t o_move = 0;
   uint32_t o_off = 0, o_rows = 0;
   if constexpr (!STATE_ONLY && MOVE == 16) {
     const int esz = o_f32 ? 4 : 2;
     const int64_t bytes = static_cast<int64_t>(p.H) * V * esz, r0 = static_cast<int64_t>(c_begin) * kQ;
-    o_next = static_cast<char*>(r.o) + (b * L + (reverse ? len - kQ - r0 : r0)) * bytes + static_cast<int64_t>(h) * V * esz;
+    o_first = static_cast<char*>(r.o) + (b * L + (reverse ? len - kQ - r0 : r0)) * bytes + static_cast<int64_t>(h) * V * esz;
+    o_next = o_first;
     o_move = (reverse ? -kQ : kQ) * bytes;
     const int col = VT == 2 && esz == 2 ? 16 * VT * w + (g & 1) * 16 + (g >> 1) * 8 : 16 * VT * w + 4 * g;
     o_rows = static_cast<uint32_t>(reverse ? -16 * bytes : 16 * bytes);
@@ -672,8 +681,8 @@ void la_kernel(LaArgs p) {
   // One chunk.  PLAIN: it and the next are whole, so that nothing is decided inside: with one or two
   // waves a SIMD each branch taken costs its fetch (the gradient at 8 x 2048, 32 heads of 128: 398 us with one
   // loop for every chunk, 358 with one of their own for these).
-  auto chunk = [&](auto plain, int c) __attribute__((always_inline)) {
-    constexpr bool PLAIN = decltype(plain)::value;
+  auto chunk = [&](auto plain, auto careful, int c) __attribute__((always_inline)) {
+    constexpr bool PLAIN = decltype(plain)::value, CAREFUL = decltype(careful)::value;
     const int n = PLAIN ? kQ : present(c);
     const bool more = PLAIN || c + 1 < c_live;
     // (opaque, so that the chunk's many LDS and memory addresses are formed here from the lane's
@@ -777,21 +786,58 @@ void la_kernel(LaArgs p) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[vt][jt][e] *= f;
       }
+      if constexpr (!CAREFUL) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        piece pf[4][ET];
+        for (int t = 0; t < 2; ++t) {
+          piece pf[4][ET];
 #pragma unroll
-        for (int jt = 0; jt < 4; ++jt)
+          for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+            for (int m = 0; m < ET; ++m)
+              if (t == 0 || jt >= 2) pf[jt][m] = O::row(p_rows, 4 * PB * t, 16 * jt * RP + m * (kQ * RP));
 #pragma unroll
           for (int m = 0; m < ET; ++m)
-            if (t == 0 || jt >= 2) pf[jt][m] = O::row(p_rows, 4 * PB * t, 16 * jt * RP + m * (kQ * RP));
 #pragma unroll
-        for (int m = 0; m < ET; ++m)
+            for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
-          for (int vt = 0; vt < VT; ++vt)
+              for (int jt = 0; jt < 4; ++jt)
+                if (t == 0 || jt >= 2) acc[vt][jt] = O::mma(vf[vt][t], pf[jt][m], acc[vt][jt]);
+        }
+      } else {
+        // without the values that are not finite: a zero of P times one is NaN.  The rows from its token on are.
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) {
+          int gone = kQ;                            // first such token of column c16
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            float x[8];
+            O::unpack(vf[vt][t], x);
+#pragma unroll
+            for (int e = 7; e >= 0; --e)
+              if (!(fabsf(x[e]) < __builtin_huge_valf())) {
+                x[e] = 0.0f;
+                gone = least(gone, 32 * t + 8 * g + e);
+              }
+            const piece clean = O::pack(x);
+#pragma unroll
+            for (int m = 0; m < ET; ++m) {
+              __builtin_amdgcn_sched_barrier(0);    // (few registers before speed here)
+#pragma unroll
+              for (int jt = 2 * t; jt < 4; ++jt)
+                acc[vt][jt] = O::mma(clean, O::row(p_rows, 4 * PB * t, 16 * jt * RP + m * (kQ * RP)), acc[vt][jt]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          gone = least(gone, __shfl_xor(gone, 16));
+          gone = least(gone, __shfl_xor(gone, 32));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {             // (the output's columns are the lanes' columns of v)
+            const int from = __shfl(gone, 4 * g + e);
 #pragma unroll
             for (int jt = 0; jt < 4; ++jt)
-              if (t == 0 || jt >= 2) acc[vt][jt] = O::mma(vf[vt][t], pf[jt][m], acc[vt][jt]);
+              if (16 * jt + c16 >= from) acc[vt][jt][e] = __builtin_nanf("");
+          }
+        }
       }
       if (!PLAIN && n < kQ) {
 #pragma unroll
@@ -919,9 +965,41 @@ void la_kernel(LaArgs p) {
   int c = c_begin;
   if constexpr (MOVE == 16) {
     const int last = (c_live < len / kQ ? c_live : len / kQ) - 1;
-    for (; c < last; ++c) chunk(std::true_type{}, c);
+    for (; c < last; ++c) chunk(std::true_type{}, std::false_type{}, c);
   }
-  for (; c < c_live; ++c) chunk(std::false_type{}, c);
+  for (; c < c_live; ++c) chunk(std::false_type{}, std::false_type{}, c);
+
+  // A value of v that is not finite must not reach the outputs before it, but in its own chunk P's zeros times it
+  // did.  It stays in every entry of its column of E, so one entry a column tells, here at the end and
+  // without a word in the loop; the walk is then made once more with care.  (q's tile is free: it holds
+  // the waves' findings.)
+  if constexpr (!STATE_ONLY) {
+    if (scaled) {
+      float z = E[0][0][0][0] * 0.0f;
+      if constexpr (VT == 2) z += E[1][0][0][0] * 0.0f;
+      const bool found = __builtin_amdgcn_ballot_w64(z != z) != 0;
+      const uint32_t at = lds_address(sQ);
+      if (lane0 == 0) lds_write<int>(at + 4 * w, found);
+      barrier_lds();
+      int any = 0;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) any |= lds_read<int>(at + 4 * i);
+      if (__builtin_expect(uniform_int(any), 0)) {
+        barrier_lds();                              // (everyone has read them)
+        if (lane0 == 0) lds_write<int>(at + 4 * w, 0);
+        barrier_lds();
+        ask();
+        enter();
+        a = 0;
+        rho = kUp;
+        unrho = kDown;
+        o_next = o_first;
+        arrived(c_begin, present(c_begin), lane0);
+#pragma unroll 1
+        for (c = c_begin; c < c_live; ++c) chunk(std::false_type{}, std::true_type{}, c);
+      }
+    }
+  }
 
   // chunks with no token: zeros
   if constexpr (!STATE_ONLY) {
