@@ -59,7 +59,8 @@ struct LaSum {
 };
 hipError_t launch_la_sum_heads(const LaSum* sums, int n, Dt dt, hipStream_t s);
 
-// dst = src, or zeros when src is null (the state of an attention over no tokens).
+// dst = src, or zeros when src is null (the state of an attention over no tokens; up to 2^34 entries, of which
+// launch_copy_state's thread for each takes fewer than 2^32).
 hipError_t launch_la_copy_state(float* dst, const float* src, int64_t n, hipStream_t s);
 
 struct LaStepArgs {
@@ -92,7 +93,6 @@ struct NormArgs {
   float* part = nullptr;                                      // [parts][3][D] column sums of row blocks
   int parts = 0;
 };
-constexpr int64_t kNormMaxD = 16384;
 hipError_t launch_norm_fwd(const NormArgs& a, Dt dt, Dt rdt, hipStream_t s);
 // Row blocks of the backward pass: each forms its own column sums.
 int norm_bwd_parts(int64_t rows, int64_t D);
