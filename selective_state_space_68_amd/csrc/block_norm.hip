@@ -183,7 +183,9 @@ __device__ __forceinline__ void team_sum(float (&s)[N], LDS& lds, int& turn, int
 }
 
 // part[v] (the sum over vector v's 8 columns) -> its group's sum, for more than one group.  Groups of
-// 8 * 2^k columns up to 512 are summed across lanes; others through LDS, in column order.
+// 8 * 2^k columns up to 512 are summed across lanes; others through LDS, in column order, where every thread adds
+// its group's group / 8 sums: wide groups are bound by that (8192 x 5120 bfloat16 with gate: 80 groups 49 us, 8
+// groups 64, 2 groups 129; gradient 125, 181, 309).
 template <int NV, bool ONE_WAVE, typename LDS>
 __device__ __forceinline__ void group_sum(float (&part)[NV], int group, int D, LDS& lds, int& turn, int t, int T) {
   const int span = group / 8;                       // vectors per group
@@ -624,8 +626,8 @@ hipError_t launch_norm(const NormArgs& a, Dt dt, Dt rdt, bool bwd, int blocks, h
 }
 
 // Workgroups: at most `most` threads' worth on each of the 256 CUs.  Rows in flight against registers of
-// column sums to add up: 1024 forwards (16384 x 2560 109 us, 185 with 512, 134 with 2048; 4096 x 1024 11.6, 14, 15.3) but 2048
-// where a row takes over 512 threads (8192 x 5120, 80 groups with gate, as it was then: 58 us, 62 with 1024), 512
+// column sums to add up: 1024 forwards (16384 x 2560 109 us, 185 with 512, 134 with 2048; 4096 x 1024 11.6, 14, 15.3;
+// where a row takes over 512 threads, 8192 x 5120, 80 groups with gate: 49 us, 51 with 2048; 8192 x 6144 73, 74), 512
 // backwards (4096 x 1024 34 us, 44 with 1024, 41 with 256; 16384 x 512 43, 50, 54; 1534 x 769 23, 29, 23).
 int blocks_of(int64_t rows, int64_t D, int most) {
   const Shape sh = shape_of(D);
@@ -639,7 +641,7 @@ int blocks_of(int64_t rows, int64_t D, int most) {
 int norm_bwd_parts(int64_t rows, int64_t D) { return blocks_of(rows, D, 512); }
 
 hipError_t launch_norm_fwd(const NormArgs& a, Dt dt, Dt rdt, hipStream_t s) {
-  return launch_norm(a, dt, rdt, false, blocks_of(a.rows, a.D, shape_of(a.D).threads > 512 ? 2048 : 1024), s);
+  return launch_norm(a, dt, rdt, false, blocks_of(a.rows, a.D, 1024), s);
 }
 
 hipError_t launch_norm_bwd(const NormArgs& a, Dt dt, Dt rdt, hipStream_t s) {
