@@ -20,7 +20,7 @@
 // in a fixed order.  The next row is asked for before the current one is computed, past the caches
 // (streaming loads and stores: 6.1 TB/s where three tensors are read and one is written, 4.9 without).
 //
-// Measured: 8192 x 5120 bfloat16 with 80 groups and gate 50 us (5.0 TB/s); the gradient of 16384 x 4096 bfloat16 with
+// Measured: 8192 x 5120 bfloat16 with 80 groups and gate 49 us (5.1 TB/s); the gradient of 16384 x 4096 bfloat16 with
 // gate, scale and float32 residual, 32 groups, 314 us (4.7 TB/s; 5.4 is what a copy reaches); 256 x 2560, 6 us: a
 // launch, the rows and two sums over them.
 #include "device_common.hpp"

@@ -33,15 +33,15 @@
 // every segment from its entering E.
 //
 // What bounds it (measured, one MI355X, bfloat16):
-//   8 x 2048, 32 heads of 128, gradient: 350 us for 1.6 GB of rows read and written by the three roles
+//   8 x 2048, 32 heads of 128, gradient: 350 to 360 us for 1.6 GB of rows read and written by the three roles
 //     (4.6 TB/s; 1.3 GB reach memory, the rest is shared in L2).  Matrix instructions take about 6, LDS 5 and
 //     vector instructions 5 of the 14 thousand cycles that the two workgroups of a CU take for a chunk
 //     each: no unit is full, the 8 waves wait for each other at two barriers a chunk.
-//   131072 tokens, 20 heads of 128: 883 us, 4.6 TB/s (under a trace pre-pass 314, chain 26, main pass 664): memory.
+//   131072 tokens, 20 heads of 128: 880 to 905 us, 4.6 TB/s (under a trace pre-pass 327, chain 27, main pass 680): memory.
 //   4 x 2048, 80 heads of 64: 119 us.  320 workgroups on 256 CUs: the time of a CU with two, 6800 cycles
 //     a chunk (5400 alone); 2 or 3 segments cost more than they level (140 and 132 us).
 //   float32: the float32 matrix rate (64 x 64: 7200 cycles of products a chunk and workgroup, 2 of them a CU).
-//   1 x 77, 24 heads of 64: a kernel of 10 us, of which 3 before the first chunk's products, 7 for its two chunks.
+//   1 x 77, 24 heads of 64: a kernel of 10.8 us, of which 3 before the first chunk's products, 7 for its two chunks.
 // Tried and dropped: a second buffer for q and v (no gain); products and LDS reads interleaved by scheduling
 // groups (no gain); streaming loads (5 % faster forwards at 64 x 64, 5 % slower gradients); the output stored
 // before the state's product (127 us at 4 x 2048 against 122, 984 against 954 at 131072); neighbouring heads on one

@@ -5,7 +5,8 @@ checks the shape, type and device of every tensor before it takes a pointer.
 Activations are float32 or bfloat16 tensors of one dtype; states, decays and norm
 weights are float32.  q, k, v and the output gradient may be views with a contiguous
 last axis (slices of one projection's output); other tensors are contiguous.  `stream=`
-is as in ops.py.
+is as in ops.py.  Automatic differentiation does not see these calls: a gradient comes from
+the _bwd functions, as in the torch.autograd.Functions of examples/linear_attention_lm.py.
 """
 from __future__ import annotations
 
