@@ -100,6 +100,8 @@ def _workspace(workspace, need: int, dev):
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
+    if workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
     nbytes = workspace.numel() * workspace.element_size()
     if nbytes < need:
         raise ValueError(f"workspace holds {nbytes} bytes, {need} needed")

@@ -84,3 +84,16 @@ CALLS = {
 def test_scratch_lives_until_the_launch(host, name):
     CALLS[name]()
     assert host.launches == 1
+
+
+def test_workspace_of_another_gpu_is_refused(host):
+    class Elsewhere(OnGpu):
+        device = property(lambda self: torch.device("cuda", 1))
+
+    workspace = torch.zeros(1 << 20, dtype=torch.uint8).as_subclass(Elsewhere)
+    with pytest.raises(ValueError, match="workspace is on cuda:1"):
+        ssm.linear_attention_fwd(*attention(), workspace=workspace)
+    with pytest.raises(ValueError, match="workspace is on cuda:1"):
+        ssm.ssd_scan_fwd(t(1, 4096, 2, 64, dtype=BF16), t(1, 4096, 2, dtype=BF16), t(2), t(1, 4096, 64, dtype=BF16),
+                         t(1, 4096, 64, dtype=BF16), workspace=workspace)
+    assert host.launches == 0
