@@ -547,6 +547,48 @@ ssm_status ssm_linear_attention_step(
     ssm_dtype dt, void *stream);
 
 /*
+ * The gated delta rule, prompt form.  For batch row b, token t and head h, with a_t = exp(g[b][t][h]),
+ * beta_t = beta[b][t][h] and the K x V state S:
+ *
+ *   u_t = beta_t (v_t - a_t S_{t-1}^T k_t)      S_t = a_t S_{t-1} + k_t u_t^T      o_t = scale * S_t^T q_t
+ *
+ * computed chunk by chunk on the matrix cores.  Arguments that linear attention has are as there; in their place of
+ * log_decay:
+ *
+ *   g, beta      : [batch][L][H] float32, packed: the logarithm of a token's decay, <= 0 in the models (-inf is a
+ *                  decay of 0), and how much of the value under a key is replaced, 0..1 in the models.  Keys of
+ *                  length 1 (ssm_qk_norm_fwd with SSM_NORM_L2 makes them) keep the state bounded; the call does not
+ *                  scale them.
+ *   lengths      : what g and beta hold for an absent token does not matter either
+ *   workspace    : >= ssm_gated_delta_workspace_size(...) bytes, for every call with tokens
+ *   batch * H * ceil(L / 64) < 2^31
+ *
+ * With float32 activations every product is in float32.  With bfloat16, q, k and v enter the products as they are;
+ * what the state depends on enters them as three bfloat16 terms (24 bits) and what only outputs depend on as two (16
+ * bits); sums and the state are float32.  A NaN or infinity in a token that is there reaches its own and later
+ * outputs (as a NaN) and no earlier one.  Errors as there.  Deterministic; which states are asked for and how rows
+ * are aligned change no result.
+ */
+size_t ssm_gated_delta_workspace_size(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V, ssm_dtype dt);
+
+ssm_status ssm_gated_delta_fwd(
+    const void *q, const void *k, const void *v, const int64_t *q_strides, const int64_t *k_strides,
+    const int64_t *v_strides, const float *g, const float *beta, float scale, const int32_t *lengths,
+    const float *initial_state, void *out, float *final_state,
+    int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv, int64_t K, int64_t V, ssm_dtype dt,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of the gated delta rule.  g, beta: [batch][H] float32; everything else, the pool of states and its slots
+ * among it, as in ssm_linear_attention_step.  float32 arithmetic.
+ */
+ssm_status ssm_gated_delta_step(
+    const float *state_in, float *state_out, const void *q, const void *k, const void *v, const int64_t *q_strides,
+    const int64_t *k_strides, const int64_t *v_strides, const float *g, const float *beta, float scale,
+    const int32_t *slots, void *out, int64_t batch, int64_t states, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv,
+    int64_t K, int64_t V, ssm_dtype dt, void *stream);
+
+/*
  * The norms around a block, fused with its gate, residual and residual scale.  For each
  * row of D columns:
  *

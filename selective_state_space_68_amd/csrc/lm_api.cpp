@@ -1,4 +1,4 @@
-// C-ABI host layer of the linear attention and block norm entry points: argument
+// C-ABI host layer of the linear attention, gated delta rule and block norm entry points: argument
 // validation, aliasing checks and dispatch to the gfx950 kernels on the caller's stream.
 #include <hip/hip_runtime.h>
 
@@ -350,6 +350,127 @@ ssm_status ssm_linear_attention_step(const float* state_in, float* state_out, co
   a.log_decay = log_decay; a.slots = slots; a.o = out; a.batch = batch; a.states = states;
   a.H = static_cast<int>(H); a.K = static_cast<int>(K); a.V = static_cast<int>(V); a.scale = scale;
   return from_hip(ssm::launch_la_step(a, dt_of(dt), static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Workspace of a gated delta call: the chunks' records.
+struct GdPlan {
+  uint64_t rec_bytes = 0;
+  uint64_t total = 0;
+};
+
+bool gd_plan(int64_t batch, int64_t L, int64_t H, ssm_dtype dt, GdPlan* p) {
+  if (batch == 0 || L == 0 || H == 0) return true;
+  const int64_t nch = (L + 63) / 64;
+  if (!bytes_of(static_cast<uint64_t>(ssm::gd_record_bytes(dt_of(dt))), &p->rec_bytes, batch, H, nch)) return false;
+  p->total = up256(p->rec_bytes);
+  return p->total <= kMaxBytes;
+}
+
+// As check_la_sizes, with the limit of 2^31 chunks in all.
+ssm_status check_gd_sizes(int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv, int64_t K, int64_t V,
+                          ssm_dtype dt) {
+  const ssm_status st = check_la_sizes(batch, L, H, Hq, Hk, Hv, K, V, kMaxPairs, dt);
+  if (st != SSM_OK) return st;
+  return batch * H * ((L + 63) / 64) < (int64_t(1) << 31) ? SSM_OK : SSM_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssm_gated_delta_workspace_size(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V, ssm_dtype dt) {
+  GdPlan p;
+  if (check_gd_sizes(batch, L, H, H, H, H, K, V, dt) != SSM_OK) return 0;
+  return gd_plan(batch, L, H, dt, &p) ? p.total : 0;
+}
+
+ssm_status ssm_gated_delta_fwd(const void* q, const void* k, const void* v, const int64_t* q_strides,
+                               const int64_t* k_strides, const int64_t* v_strides, const float* g, const float* beta,
+                               float scale, const int32_t* lengths, const float* initial_state, void* out,
+                               float* final_state, int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk,
+                               int64_t Hv, int64_t K, int64_t V, ssm_dtype dt, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  ssm_status st = check_gd_sizes(batch, L, H, Hq, Hk, Hv, K, V, dt);
+  if (st != SSM_OK) return st;
+  const uint64_t e = dt == SSM_BF16 ? 2 : 4;
+  LaTensors t;
+  uint64_t out_bytes, state_bytes, gate_bytes;
+  GdPlan plan;
+  if (!make_view<3>(q_strides, {batch, L, Hq}, K, e, &t.q) || !make_view<3>(k_strides, {batch, L, Hk}, K, e, &t.k) ||
+      !make_view<3>(v_strides, {batch, L, Hv}, V, e, &t.v) || !bytes_of(e, &out_bytes, batch, L, H, V) ||
+      !bytes_of(4, &state_bytes, batch, H, K, V) || !bytes_of(4, &gate_bytes, batch, L, H) ||
+      !gd_plan(batch, L, H, dt, &plan))
+    return SSM_ERR_INVALID_ARG;
+  if (out_bytes && (!q || !k || !v || !g || !beta || !out)) return SSM_ERR_INVALID_ARG;
+  if (!aligned(q, e) || !aligned(k, e) || !aligned(v, e) || !aligned(out, e) || !aligned(g, 4) || !aligned(beta, 4) ||
+      !aligned(lengths, 4) || !aligned(initial_state, 4) || !aligned(final_state, 4) || !aligned(workspace, 16))
+    return SSM_ERR_INVALID_ARG;
+  if ((workspace_bytes && !workspace) || workspace_bytes < plan.total) return SSM_ERR_INVALID_ARG;
+  const Span ins[] = {span(q, t.q.extent),   span(k, t.k.extent),    span(v, t.v.extent),
+                      span(g, gate_bytes),   span(beta, gate_bytes), span(lengths, 4 * static_cast<uint64_t>(batch))};
+  const Span outs[] = {span(out, out_bytes), span(final_state, state_bytes), span(workspace, workspace_bytes)};
+  const Span init = span(initial_state, state_bytes);
+  if (any_overlap(outs, 3, ins, 6) || overlaps(outs[0], init) || overlaps(outs[2], init)) return SSM_ERR_INVALID_ARG;
+  if (overlaps(outs[1], init) && final_state != initial_state) return SSM_ERR_INVALID_ARG;
+  if (batch == 0 || H == 0) return SSM_OK;
+  st = probe_device();
+  if (st != SSM_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (L == 0)
+    return final_state ? from_hip(ssm::launch_la_copy_state(final_state, initial_state, batch * H * K * V, s)) : SSM_OK;
+  ssm::GdArgs a;
+  a.q = q; a.k = k; a.v = v;
+  for (int i = 0; i < 3; ++i) { a.qs[i] = t.q.stride[i]; a.ks[i] = t.k.stride[i]; a.vs[i] = t.v.stride[i]; }
+  a.qdiv = static_cast<int>(H / Hq); a.kdiv = static_cast<int>(H / Hk); a.vdiv = static_cast<int>(H / Hv);
+  a.g = g; a.beta = beta; a.lengths = lengths; a.carry = initial_state; a.fin = final_state; a.o = out;
+  a.rec = static_cast<char*>(workspace);
+  a.batch = batch; a.L = L; a.H = static_cast<int>(H); a.K = static_cast<int>(K); a.V = static_cast<int>(V);
+  a.scale = scale;
+  a.move = least(least(row_move(q, t.q, K, e), row_move(k, t.k, K, e)), row_move(v, t.v, V, e));
+  a.o_vec = V % 4 == 0 && aligned(out, 4 * e);
+  return from_hip(ssm::launch_gd(a, dt_of(dt), s));
+}
+
+ssm_status ssm_gated_delta_step(const float* state_in, float* state_out, const void* q, const void* k, const void* v,
+                                const int64_t* q_strides, const int64_t* k_strides, const int64_t* v_strides,
+                                const float* g, const float* beta, float scale, const int32_t* slots, void* out,
+                                int64_t batch, int64_t states, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv, int64_t K,
+                                int64_t V, ssm_dtype dt, void* stream) {
+  ssm_status st = check_la_sizes(batch, 1, H, Hq, Hk, Hv, K, V, kMaxStepPairs, dt);
+  if (st != SSM_OK) return st;
+  if (states < 0 || (!slots && states < batch)) return SSM_ERR_INVALID_ARG;
+  const uint64_t e = dt == SSM_BF16 ? 2 : 4;
+  View<2> vq, vk, vv;
+  uint64_t out_bytes, state_bytes, gate_bytes;
+  if (!make_view<2>(q_strides, {batch, Hq}, K, e, &vq) || !make_view<2>(k_strides, {batch, Hk}, K, e, &vk) ||
+      !make_view<2>(v_strides, {batch, Hv}, V, e, &vv) || !bytes_of(e, &out_bytes, batch, H, V) ||
+      !bytes_of(4, &state_bytes, states, H, K, V) || !bytes_of(4, &gate_bytes, batch, H))
+    return SSM_ERR_INVALID_ARG;
+  if (out_bytes && (!q || !k || !v || !out || !g || !beta)) return SSM_ERR_INVALID_ARG;
+  if (out_bytes && state_bytes && (!state_in || !state_out)) return SSM_ERR_INVALID_ARG;
+  if (!aligned(q, e) || !aligned(k, e) || !aligned(v, e) || !aligned(out, e) || !aligned(state_in, 4) ||
+      !aligned(state_out, 4) || !aligned(g, 4) || !aligned(beta, 4) || !aligned(slots, 4))
+    return SSM_ERR_INVALID_ARG;
+  const Span ins[] = {span(q, vq.extent),  span(k, vk.extent),     span(v, vv.extent),
+                      span(g, gate_bytes), span(beta, gate_bytes), span(slots, 4 * static_cast<uint64_t>(batch))};
+  const Span outs[] = {span(out, out_bytes), span(state_out, state_bytes)};
+  const Span sin = span(state_in, state_bytes);
+  if (any_overlap(outs, 2, ins, 6) || overlaps(outs[0], sin)) return SSM_ERR_INVALID_ARG;
+  if (overlaps(outs[1], sin) && state_out != state_in) return SSM_ERR_INVALID_ARG;
+  if (batch == 0 || H == 0) return SSM_OK;
+  st = probe_device();
+  if (st != SSM_OK) return st;
+  ssm::GdStepArgs a;
+  a.state_in = state_in; a.state_out = state_out; a.q = q; a.k = k; a.v = v;
+  for (int i = 0; i < 2; ++i) { a.qs[i] = vq.stride[i]; a.ks[i] = vk.stride[i]; a.vs[i] = vv.stride[i]; }
+  a.qdiv = static_cast<int>(H / Hq); a.kdiv = static_cast<int>(H / Hk); a.vdiv = static_cast<int>(H / Hv);
+  a.g = g; a.beta = beta; a.slots = slots; a.o = out; a.batch = batch; a.states = states;
+  a.H = static_cast<int>(H); a.K = static_cast<int>(K); a.V = static_cast<int>(V); a.scale = scale;
+  return from_hip(ssm::launch_gd_step(a, dt_of(dt), static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -78,6 +78,41 @@ struct LaStepArgs {
 };
 hipError_t launch_la_step(const LaStepArgs& a, Dt dt, hipStream_t s);
 
+// The gated delta rule over the tokens of every (batch row, head).
+struct GdArgs {
+  const void *q = nullptr, *k = nullptr, *v = nullptr;
+  int64_t qs[3] = {}, ks[3] = {}, vs[3] = {};            // element strides: batch, token, head
+  int qdiv = 1, kdiv = 1, vdiv = 1;                      // head h of the state uses head h / div
+  const float *g = nullptr, *beta = nullptr;             // [batch][L][H]
+  const int32_t* lengths = nullptr;                      // [batch] or null
+  const float* carry = nullptr;                          // state before the first token, or null (zero)
+  float* fin = nullptr;                                  // state after the last token, or null
+  void* o = nullptr;                                     // [batch][L][H][V]
+  char* rec = nullptr;                                   // a record for each chunk of each (batch row, head)
+  int64_t batch = 0, L = 0;
+  int H = 0, K = 0, V = 0;
+  float scale = 1.0f;
+  int move = 0;                                          // bytes in which rows of q, k and v move: 16, 4, or 0 (an element)
+  int o_vec = 0;                                         // rows of o move as 4-element vectors
+};
+struct GdStepArgs {
+  const float* state_in = nullptr;    // [states][H][K][V]
+  float* state_out = nullptr;
+  const void *q = nullptr, *k = nullptr, *v = nullptr;
+  int64_t qs[2] = {}, ks[2] = {}, vs[2] = {};            // element strides: batch, head
+  int qdiv = 1, kdiv = 1, vdiv = 1;
+  const float *g = nullptr, *beta = nullptr;             // [batch][H]
+  const int32_t* slots = nullptr;     // [batch] or null
+  void* o = nullptr;                  // [batch][H][V]
+  int64_t batch = 0, states = 0;
+  int H = 0, K = 0, V = 0;
+  float scale = 1.0f;
+};
+hipError_t launch_gd_step(const GdStepArgs& a, Dt dt, hipStream_t s);
+
+int64_t gd_record_bytes(Dt dt);
+hipError_t launch_gd(const GdArgs& a, Dt dt, hipStream_t s);
+
 struct NormArgs {
   const void *x = nullptr, *gate = nullptr, *residual = nullptr;
   const float *w1 = nullptr, *rs = nullptr, *w2 = nullptr;   // post weight, residual scale, pre weight: [D] or null

@@ -248,6 +248,105 @@ def linear_attention_step(state, q_t, k_t, v_t, log_decay, scale=None, *, slots=
     return out
 
 
+def _gates(g, beta, lead):
+    """Checks g and beta [*lead, H]; returns H."""
+    _dims(g, "g", len(lead) + 1)
+    _is(g, "g", (*lead, g.shape[-1]))
+    _is(beta, "beta", g.shape)
+    if beta is None:
+        raise ValueError("beta must be a tensor")
+    return g.shape[-1]
+
+
+def _delta_shapes(q, k, v, g, beta, n: int):
+    """Checks q, k, v [..., heads, width] of n dimensions and g, beta [..., H]; as _attention_shapes."""
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _dims(t, name, n)
+    *lead, Hq, K = q.shape
+    Hk, (Hv, V), H = k.shape[-2], v.shape[-2:], _gates(g, beta, lead)
+    _is(k, "k", (*lead, Hk, K))
+    _is(v, "v", (*lead, Hv, V))
+    for heads, name in ((Hq, "q"), (Hk, "k"), (Hv, "v")):
+        if heads < 1 or H % heads:
+            raise ValueError(f"{name} has {heads} heads, which does not divide g's {H}")
+    return lead, H, Hq, Hk, Hv, K, V
+
+
+@lru_cache(maxsize=4096)
+def gated_delta_workspace_size(batch, L, H, K, V, dtype=BF16) -> int:
+    """Bytes of device workspace gated_delta_fwd needs for this shape."""
+    return int(_entry("ssm_gated_delta_workspace_size")(int(batch), int(L), int(H), int(K), int(V), _dt(dtype)))
+
+
+def gated_delta_fwd(q, k, v, g, beta, scale=None, *, initial_state=None, lengths=None, out=None, final_state=None,
+                    return_final_state=True, workspace=None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The gated delta rule: u_t = beta_t (v_t - a_t S_{t-1}^T k_t), S_t = a_t S_{t-1} + k_t u_t^T,
+    o_t = scale S_t^T q_t with a_t = exp(g_t).
+
+    q [batch, L, Hq, K], k [batch, L, Hk, K], v [batch, L, Hv, V] (each head count divides H; views with a
+    contiguous last axis are fine); g, beta [batch, L, H] float32: the logarithm of each token's decay and its
+    writing strength.  The keys are meant to have length 1 (qk_norm_fwd with norm="l2").  scale defaults to
+    K ** -0.5.  `initial_state` [batch, H, K, V] float32 (zero when None); `final_state` may be the same tensor
+    (updated in place).  `lengths` [batch] int32: tokens at or past a row's length are absent (their outputs are 0).
+    `workspace`: a device tensor of at least gated_delta_workspace_size(...) bytes, or None (allocated here).
+    Returns (out [batch, L, H, V], final_state or None).
+    """
+    if stream is not None:
+        return _elsewhere(gated_delta_fwd, locals())
+    (batch, L), H, Hq, Hk, Hv, K, V = _delta_shapes(q, k, v, g, beta, 4)
+    states = (batch, H, K, V)
+    _is(lengths, "lengths", (batch,))
+    _is(initial_state, "initial_state", states)
+    _is(out, "out", (batch, L, H, V))
+    _is(final_state, "final_state", states)
+    act, dev = q.dtype, q.get_device()
+    dt = _dt(act)
+    qs, ks, vs = _strides(q, "q", act, dev), _strides(k, "k", act, dev), _strides(v, "v", act, dev)
+    if out is None:
+        out = q.new_empty((batch, L, H, V))
+    if final_state is None and return_final_state:
+        final_state = q.new_empty(states, dtype=F32)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, gated_delta_workspace_size(batch, L, H, K, V, act), q)
+    _run(_entry("ssm_gated_delta_fwd"), dev,
+         q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(g, "g", F32, dev), _ptr(beta, "beta", F32, dev),
+         K ** -0.5 if scale is None else float(scale),
+         _ptr(lengths, "lengths", _I32, dev), _ptr(initial_state, "initial_state", F32, dev),
+         _ptr(out, "out", act, dev), _ptr(final_state, "final_state", F32, dev), batch, L, H, Hq, Hk, Hv, K, V, dt,
+         ws_ptr, ws_bytes)
+    return out, final_state
+
+
+def gated_delta_step(state, q_t, k_t, v_t, g_t, beta_t, scale=None, *, slots=None, out_state=None, out=None,
+                     stream=None) -> torch.Tensor:
+    """One token of gated_delta_fwd.  state [states, H, K, V] float32; q_t [batch, Hq, K], k_t [batch, Hk, K],
+    v_t [batch, Hv, V]; g_t, beta_t [batch, H] float32.  Updates `out_state` (default: `state`, in place) and
+    returns out [batch, H, V].  `slots` is as in linear_attention_step.
+    """
+    if stream is not None:
+        return _elsewhere(gated_delta_step, locals())
+    (batch,), H, Hq, Hk, Hv, K, V = _delta_shapes(q_t, k_t, v_t, g_t, beta_t, 3)
+    _dims(state, "state", 4)
+    states = state.shape[0]
+    _is(state, "state", (states, H, K, V))
+    _is(slots, "slots", (batch,))
+    _is(out_state, "out_state", state.shape)
+    _is(out, "out", (batch, H, V))
+    if slots is None and states < batch:
+        raise ValueError(f"{batch} rows need as many states, got {states}")
+    act, dev = q_t.dtype, state.get_device()
+    dt = _dt(act)
+    qs, ks, vs = _strides(q_t, "q_t", act, dev), _strides(k_t, "k_t", act, dev), _strides(v_t, "v_t", act, dev)
+    state_ptr = _ptr(state, "state", F32, dev)
+    if out is None:
+        out = q_t.new_empty((batch, H, V))
+    _run(_entry("ssm_gated_delta_step"), dev,
+         state_ptr, state_ptr if out_state is None else _ptr(out_state, "out_state", F32, dev),
+         q_t.data_ptr(), k_t.data_ptr(), v_t.data_ptr(), qs, ks, vs, _ptr(g_t, "g_t", F32, dev),
+         _ptr(beta_t, "beta_t", F32, dev), K ** -0.5 if scale is None else float(scale),
+         _ptr(slots, "slots", _I32, dev), _ptr(out, "out", act, dev), batch, states, H, Hq, Hk, Hv, K, V, dt)
+    return out
+
+
 def _outputs(given, like, spec) -> dict:
     """Output tensors by name: the caller's where given (checked), else new ones; None where not computed."""
     got = {}
