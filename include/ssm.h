@@ -579,6 +579,26 @@ ssm_status ssm_gated_delta_fwd(
     void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * The gradients of sum(dout * out) + sum(dfinal_state * final_state) of ssm_gated_delta_fwd.  dout, dfinal_state,
+ * dq, dk, dv and dinitial_state are as in ssm_linear_attention_bwd;
+ *   dg, dbeta     : out, [batch][L][H] float32 (0 for absent tokens)
+ *   workspace     : >= ssm_gated_delta_bwd_workspace_size(...) bytes, for every call with tokens
+ *   batch * H * ceil(L / 64) <= 2^26
+ * A NaN or infinity makes gradients of its (batch row, head) NaN, of earlier tokens and of other columns too.
+ * Deterministic.
+ */
+size_t ssm_gated_delta_bwd_workspace_size(int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv,
+                                          int64_t K, int64_t V, ssm_dtype dt);
+
+ssm_status ssm_gated_delta_bwd(
+    const void *q, const void *k, const void *v, const void *dout, const int64_t *q_strides, const int64_t *k_strides,
+    const int64_t *v_strides, const int64_t *dout_strides, const float *g, const float *beta, float scale,
+    const int32_t *lengths, const float *initial_state, const float *dfinal_state, void *dq, void *dk, void *dv,
+    float *dg, float *dbeta, float *dinitial_state,
+    int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv, int64_t K, int64_t V, ssm_dtype dt,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * One token of the gated delta rule.  g, beta: [batch][H] float32; everything else, the pool of states and its slots
  * among it, as in ssm_linear_attention_step.  float32 arithmetic.
  */

@@ -13,7 +13,8 @@ from .ops import (selective_scan_fwd, selective_scan_fwd_save, SAVE_CHUNK,  # no
                   ssd_scan_fwd, ssd_scan_workspace_size)
 from .lm_ops import (linear_attention_fwd, linear_attention_bwd, linear_attention_step,  # noqa: F401
                      linear_attention_workspace_size, linear_attention_bwd_workspace_size,
-                     gated_delta_fwd, gated_delta_step, gated_delta_workspace_size,
+                     gated_delta_fwd, gated_delta_bwd, gated_delta_step, gated_delta_workspace_size,
+                     gated_delta_bwd_workspace_size,
                      block_norm_fwd, block_norm_bwd, block_norm_bwd_workspace_size)
 
 __all__ = ["selective_scan_fwd", "selective_scan_fwd_save", "SAVE_CHUNK", "selective_scan_fwd_conv", "selective_scan_fwd_kernel", "selective_scan_bwd",
@@ -21,6 +22,7 @@ __all__ = ["selective_scan_fwd", "selective_scan_fwd_save", "SAVE_CHUNK", "selec
            "ssd_scan_fwd", "ssd_scan_workspace_size",
            "linear_attention_fwd", "linear_attention_bwd", "linear_attention_step", "linear_attention_workspace_size",
            "linear_attention_bwd_workspace_size",
-           "gated_delta_fwd", "gated_delta_step", "gated_delta_workspace_size", "block_norm_fwd", "block_norm_bwd", "block_norm_bwd_workspace_size",
+           "gated_delta_fwd", "gated_delta_bwd", "gated_delta_step", "gated_delta_workspace_size",
+           "gated_delta_bwd_workspace_size", "block_norm_fwd", "block_norm_bwd", "block_norm_bwd_workspace_size",
            "SsmError", "load_library", "LIB_PATH",
            "SSM_SCAN_AUTO", "SSM_SCAN_SEQUENTIAL", "SSM_SCAN_CHUNKED", "SSM_SCAN_TOKSEQ", "SSM_SCAN_AP"]

@@ -74,6 +74,8 @@ SIGNATURES = {
     "ssm_linear_attention_step": (_int, [_vp] * 9 + [_f32, _vp, _vp] + [_i64] * 8 + [_int, _vp]),
     "ssm_gated_delta_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i64, _int]),
     "ssm_gated_delta_fwd": (_int, [_vp] * 8 + [_f32, _vp, _vp, _vp, _vp] + [_i64] * 8 + [_int, _vp, _sz, _vp]),
+    "ssm_gated_delta_bwd_workspace_size": (_sz, [_i64] * 8 + [_int]),
+    "ssm_gated_delta_bwd": (_int, [_vp] * 10 + [_f32] + [_vp] * 9 + [_i64] * 8 + [_int, _vp, _sz, _vp]),
     "ssm_gated_delta_step": (_int, [_vp] * 10 + [_f32, _vp, _vp] + [_i64] * 8 + [_int, _vp]),
     "ssm_block_norm_fwd": (_int, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _f32, _int,
                                   _int, _vp]),

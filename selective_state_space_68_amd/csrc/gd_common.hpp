@@ -1,0 +1,68 @@
+// What the gated delta rule's kernels share: a chunk's record (T in operand order and the chunk's vectors), sums of
+// logarithms as pairs, and products of values in several terms.
+#pragma once
+
+#include "device_common.hpp"
+#include "la_tiles.hpp"
+
+namespace ssm {
+namespace {
+
+constexpr int kT = 6;                     // operands of T (and of the scores): 16 rows by 32 tokens, where it is not zero
+constexpr int kVecs = 8;                  // vectors of 64 floats in a chunk's record
+enum { kInto = 0, kLast, kBeta, kSumHi, kSumLo, kWhole };   // exp(G), exp(G_Q - G), beta, G in two parts, exp(G_Q)
+constexpr double kMinGate = -4096.0;      // 2^kMinGate == 0; sums of 64 of these and their differences stay finite
+
+template <typename ACT>
+constexpr int kTerms = ACT::kBytes == 2 ? 3 : 1;       // operand terms of what the state depends on
+template <typename ACT>
+constexpr int kOutTerms = ACT::kBytes == 2 ? 2 : 1;    // ... and of what outputs alone do
+template <typename ACT>
+constexpr int kPieceBytes = ACT::kBytes == 2 ? 1024 : 2048;   // an operand of 64 lanes
+template <typename ACT>
+constexpr int kTBytes = kT * kTerms<ACT> * kPieceBytes<ACT>;
+template <typename ACT>
+constexpr int kRecord = kTBytes<ACT> + kVecs * 256;    // a chunk's T and vectors
+
+// 2^(hi + lo) for |lo| far below 1: the sum of logarithms is kept as a float32 pair, so that a factor
+// exp(G_i - G_j) is as good as float32 where the sums themselves are in the hundreds.
+__device__ __forceinline__ float exp2_pair(float hi, float lo) {
+  const float e = exp2_hw(hi);
+  return __builtin_fmaf(e, lo * kLn2, e);
+}
+
+__device__ __forceinline__ int gd_length(const int32_t* lengths, int L, int64_t b) {
+  if (!lengths) return L;
+  const int n = uniform_int(lengths[b]);
+  return n < 0 ? 0 : (n > L ? L : n);
+}
+
+__device__ __forceinline__ void store_piece(char* at, const uint4& p) { *reinterpret_cast<uint4*>(at) = p; }
+__device__ __forceinline__ void store_piece(char* at, const F8& p) {
+  reinterpret_cast<float4*>(at)[0] = p.a;
+  reinterpret_cast<float4*>(at)[1] = p.b;
+}
+__device__ __forceinline__ void load_piece(const char* at, uint4& p) { p = *reinterpret_cast<const uint4*>(at); }
+__device__ __forceinline__ void load_piece(const char* at, F8& p) {
+  p.a = reinterpret_cast<const float4*>(at)[0];
+  p.b = reinterpret_cast<const float4*>(at)[1];
+}
+
+// The sum of products of two values in N terms each, of those terms that count at N terms (largest last).
+template <typename O, int NA, int NB>
+__device__ __forceinline__ f32x4_t mma_terms(const typename O::piece (&a)[NA], const typename O::piece (&b)[NB], f32x4_t c) {
+  constexpr int most = NA > NB ? NA : NB;
+#pragma unroll
+  for (int sum = most - 1; sum >= 0; --sum)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (sum - i >= 0 && sum - i < NB) c = O::mma(a[i], b[sum - i], c);
+  return c;
+}
+
+// A wave owns 16 VT columns.  VT = 2 at bfloat16, V > 64: each LDS read serves two columns' tiles.
+template <typename ACT, int VD>
+constexpr int kGdColumnTiles = ACT::kBytes == 2 && VD == 128 ? 2 : 1;
+
+}  // namespace
+}  // namespace ssm

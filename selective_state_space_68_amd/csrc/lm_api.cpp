@@ -370,6 +370,35 @@ bool gd_plan(int64_t batch, int64_t L, int64_t H, ssm_dtype dt, GdPlan* p) {
   return p->total <= kMaxBytes;
 }
 
+// ... of its gradient: the records of both walks, their rows of w and y, their states, and float32 parts.
+struct GdBwdPlan {
+  GdPlan fwd;
+  uint64_t rows = 0, kept = 0;        // of one walk
+  uint64_t dk = 0, dq = 0, dv = 0;    // dk's parts always, the others' of shared heads
+  uint64_t total = 0;
+};
+
+bool gd_bwd_plan(int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hv, int64_t K, int64_t V, ssm_dtype dt,
+                 GdBwdPlan* p) {
+  if (!gd_plan(batch, L, H, dt, &p->fwd)) return false;
+  if (batch == 0 || L == 0 || H == 0) return true;
+  const int64_t nch = (L + 63) / 64, every = ssm::gd_every(batch, L, H);
+  if (!bytes_of(4, &p->rows, batch, H, nch, 64, V > 64 ? 128 : 64) ||
+      !bytes_of(4, &p->kept, batch, H, (nch + every - 1) / every, K, V) || !bytes_of(4, &p->dk, batch, L, H, K) ||
+      (Hq != H && !bytes_of(4, &p->dq, batch, L, H, K)) || (Hv != H && !bytes_of(4, &p->dv, batch, L, H, V)))
+    return false;
+  p->total = 2 * (p->fwd.total + up256(p->rows) + up256(p->kept)) + up256(p->dk) + up256(p->dq) + up256(p->dv);
+  return p->total <= kMaxBytes;
+}
+
+// ... and of 2^26 for the gradient.
+ssm_status check_gd_bwd_sizes(int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv, int64_t K,
+                              int64_t V, ssm_dtype dt) {
+  const ssm_status st = check_la_sizes(batch, L, H, Hq, Hk, Hv, K, V, kMaxPairs, dt);
+  if (st != SSM_OK) return st;
+  return batch * H * ((L + 63) / 64) <= (int64_t(1) << 26) ? SSM_OK : SSM_ERR_UNSUPPORTED;
+}
+
 // As check_la_sizes, with the limit of 2^31 chunks in all.
 ssm_status check_gd_sizes(int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv, int64_t K, int64_t V,
                           ssm_dtype dt) {
@@ -433,6 +462,121 @@ ssm_status ssm_gated_delta_fwd(const void* q, const void* k, const void* v, cons
   a.move = least(least(row_move(q, t.q, K, e), row_move(k, t.k, K, e)), row_move(v, t.v, V, e));
   a.o_vec = V % 4 == 0 && aligned(out, 4 * e);
   return from_hip(ssm::launch_gd(a, dt_of(dt), s));
+}
+
+size_t ssm_gated_delta_bwd_workspace_size(int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv,
+                                          int64_t K, int64_t V, ssm_dtype dt) {
+  GdBwdPlan p;
+  if (check_gd_bwd_sizes(batch, L, H, Hq, Hk, Hv, K, V, dt) != SSM_OK) return 0;
+  return gd_bwd_plan(batch, L, H, Hq, Hv, K, V, dt, &p) ? p.total : 0;
+}
+
+ssm_status ssm_gated_delta_bwd(const void* q, const void* k, const void* v, const void* dout, const int64_t* q_strides,
+                               const int64_t* k_strides, const int64_t* v_strides, const int64_t* dout_strides,
+                               const float* g, const float* beta, float scale, const int32_t* lengths,
+                               const float* initial_state, const float* dfinal_state, void* dq, void* dk, void* dv,
+                               float* dg, float* dbeta, float* dinitial_state, int64_t batch, int64_t L, int64_t H,
+                               int64_t Hq, int64_t Hk, int64_t Hv, int64_t K, int64_t V, ssm_dtype dt, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  ssm_status st = check_gd_bwd_sizes(batch, L, H, Hq, Hk, Hv, K, V, dt);
+  if (st != SSM_OK) return st;
+  const uint64_t e = dt == SSM_BF16 ? 2 : 4;
+  LaTensors t;
+  uint64_t qb, kb, vb, state_bytes, gate_bytes;
+  GdBwdPlan plan;
+  if (!make_view<3>(q_strides, {batch, L, Hq}, K, e, &t.q) || !make_view<3>(k_strides, {batch, L, Hk}, K, e, &t.k) ||
+      !make_view<3>(v_strides, {batch, L, Hv}, V, e, &t.v) || !make_view<3>(dout_strides, {batch, L, H}, V, e, &t.d) ||
+      !bytes_of(e, &qb, batch, L, Hq, K) || !bytes_of(e, &kb, batch, L, Hk, K) || !bytes_of(e, &vb, batch, L, Hv, V) ||
+      !bytes_of(4, &state_bytes, batch, H, K, V) || !bytes_of(4, &gate_bytes, batch, L, H) ||
+      !gd_bwd_plan(batch, L, H, Hq, Hv, K, V, dt, &plan))
+    return SSM_ERR_INVALID_ARG;
+  if (qb && (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta)) return SSM_ERR_INVALID_ARG;
+  if (!aligned(q, e) || !aligned(k, e) || !aligned(v, e) || !aligned(dout, e) || !aligned(dq, e) || !aligned(dk, e) ||
+      !aligned(dv, e) || !aligned(g, 4) || !aligned(beta, 4) || !aligned(dg, 4) || !aligned(dbeta, 4) ||
+      !aligned(lengths, 4) || !aligned(initial_state, 4) || !aligned(dfinal_state, 4) || !aligned(dinitial_state, 4) ||
+      !aligned(workspace, 16))
+    return SSM_ERR_INVALID_ARG;
+  if ((workspace_bytes && !workspace) || workspace_bytes < plan.total) return SSM_ERR_INVALID_ARG;
+  const Span ins[] = {span(q, t.q.extent),
+                      span(k, t.k.extent),
+                      span(v, t.v.extent),
+                      span(dout, t.d.extent),
+                      span(g, gate_bytes),
+                      span(beta, gate_bytes),
+                      span(lengths, 4 * static_cast<uint64_t>(batch)),
+                      span(initial_state, state_bytes),
+                      span(dfinal_state, state_bytes)};
+  const Span outs[] = {span(dq, qb),         span(dk, kb),
+                       span(dv, vb),         span(dg, gate_bytes),
+                       span(dbeta, gate_bytes), span(dinitial_state, state_bytes),
+                       span(workspace, workspace_bytes)};
+  if (any_overlap(outs, 7, ins, 9)) return SSM_ERR_INVALID_ARG;
+  if (batch == 0 || H == 0) return SSM_OK;
+  st = probe_device();
+  if (st != SSM_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (L == 0)
+    return dinitial_state ? from_hip(ssm::launch_la_copy_state(dinitial_state, dfinal_state, batch * H * K * V, s))
+                          : SSM_OK;
+  char* at = static_cast<char*>(workspace);
+  auto take = [&](uint64_t bytes) {
+    char* p = at;
+    at += up256(bytes);
+    return bytes ? p : nullptr;
+  };
+  ssm::GdArgs a;
+  a.q = q; a.k = k; a.v = v;
+  for (int i = 0; i < 3; ++i) { a.qs[i] = t.q.stride[i]; a.ks[i] = t.k.stride[i]; a.vs[i] = t.v.stride[i]; }
+  a.qdiv = static_cast<int>(H / Hq); a.kdiv = static_cast<int>(H / Hk); a.vdiv = static_cast<int>(H / Hv);
+  a.g = g; a.beta = beta; a.lengths = lengths; a.carry = initial_state;
+  a.batch = batch; a.L = L; a.H = static_cast<int>(H); a.K = static_cast<int>(K); a.V = static_cast<int>(V);
+  a.scale = scale;
+  a.every = ssm::gd_every(batch, L, H);
+  a.rec = take(plan.fwd.rec_bytes);
+  a.rec_back = take(plan.fwd.rec_bytes);
+  a.w_out = reinterpret_cast<float*>(take(plan.rows));
+  a.kept = reinterpret_cast<float*>(take(plan.kept));
+  a.move = least(row_move(k, t.k, K, e), row_move(v, t.v, V, e));
+  ssm::GdArgs r = a;
+  r.v = dout;
+  for (int i = 0; i < 3; ++i) r.vs[i] = t.d.stride[i];
+  r.vdiv = 1;
+  r.carry = dfinal_state; r.fin = dinitial_state;
+  r.w_out = reinterpret_cast<float*>(take(plan.rows));
+  r.kept = reinterpret_cast<float*>(take(plan.kept));
+  r.move = least(least(row_move(q, t.q, K, e), row_move(k, t.k, K, e)), row_move(dout, t.d, V, e));
+  float* dk_part = reinterpret_cast<float*>(take(plan.dk));
+  float* dq_part = reinterpret_cast<float*>(take(plan.dq));
+  float* dv_part = reinterpret_cast<float*>(take(plan.dv));
+  r.o = dv_part ? static_cast<void*>(dv_part) : dv;
+  r.o_f32 = dv_part != nullptr;
+  hipError_t err = ssm::launch_gd_walks(a, r, dt_of(dt), s);
+  if (err != hipSuccess) return from_hip(err);
+  ssm::GdGradArgs x;
+  x.q = q; x.k = k; x.d = dout;
+  for (int i = 0; i < 3; ++i) { x.qs[i] = t.q.stride[i]; x.ks[i] = t.k.stride[i]; x.ds[i] = t.d.stride[i]; }
+  x.qdiv = a.qdiv; x.kdiv = a.kdiv;
+  x.rec = a.rec; x.w = a.w_out; x.y = r.w_out; x.kept_e = a.kept; x.kept_f = r.kept; x.lengths = lengths;
+  x.dq = dq_part ? static_cast<void*>(dq_part) : dq; x.dq_f32 = dq_part != nullptr;
+  x.dk_part = dk_part; x.dk = dk; x.dk_f32 = Hk != H;
+  x.dg = dg; x.dbeta = dbeta; x.batch = batch; x.L = L; x.H = a.H; x.K = a.K; x.V = a.V; x.every = a.every; x.scale = scale;
+  x.carried = initial_state != nullptr;
+  x.d_vec = V % 8 == 0 && rows_aligned(dout, t.d, e, 16);
+  x.part_vec = K % 4 == 0 && aligned(x.dq, dq_part ? 16 : 4 * e) && (x.dk_f32 || aligned(dk, 4 * e));
+  err = ssm::launch_gd_qk(x, dt_of(dt), s);
+  ssm::LaSum sums[3];
+  int n = 0;
+  auto sum = [&](const float* part, void* out, int64_t heads, int64_t width) {
+    if (!part || heads == H) return;
+    ssm::LaSum& y = sums[n++];
+    y.part = part; y.out = out; y.rows = batch * L * heads;
+    y.share = static_cast<int>(H / heads); y.d = static_cast<int>(width);
+  };
+  sum(dq_part, dq, Hq, K);
+  sum(dk_part, dk, Hk, K);
+  sum(dv_part, dv, Hv, V);
+  if (err == hipSuccess && n) err = ssm::launch_la_sum_heads(sums, n, dt_of(dt), s);
+  return from_hip(err);
 }
 
 ssm_status ssm_gated_delta_step(const float* state_in, float* state_out, const void* q, const void* k, const void* v,

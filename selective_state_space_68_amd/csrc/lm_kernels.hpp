@@ -88,13 +88,41 @@ struct GdArgs {
   const float* carry = nullptr;                          // state before the first token, or null (zero)
   float* fin = nullptr;                                  // state after the last token, or null
   void* o = nullptr;                                     // [batch][L][H][V]
-  char* rec = nullptr;                                   // a record for each chunk of each (batch row, head)
+  int o_f32 = 0;                                         // (the gradient of a shared head of v) o is float32
+  char *rec = nullptr, *rec_back = nullptr;              // a record for each chunk of each (batch row, head)
+  float* w_out = nullptr;                                // gradient walks: [batch * H][chunks][64][V as a tile has it]
+  float* kept = nullptr;                                 // ... the state before every `every` chunks, [batch * H][..][K * V]
+  int every = 1;
   int64_t batch = 0, L = 0;
   int H = 0, K = 0, V = 0;
   float scale = 1.0f;
   int move = 0;                                          // bytes in which rows of q, k and v move: 16, 4, or 0 (an element)
   int o_vec = 0;                                         // rows of o move as 4-element vectors
 };
+// The gradients of q, k, g and beta from what the walks left.
+struct GdGradArgs {
+  const void *q = nullptr, *k = nullptr, *d = nullptr;   // d: the outputs' gradient, [batch][L][H][V]
+  int64_t qs[3] = {}, ks[3] = {}, ds[3] = {};
+  int qdiv = 1, kdiv = 1;
+  const char* rec = nullptr;
+  const float *w = nullptr, *y = nullptr;                // w_out of the two walks
+  const float *kept_e = nullptr, *kept_f = nullptr;      // kept of the two walks
+  const int32_t* lengths = nullptr;
+  void* dq = nullptr;                                    // [batch][L][H][K]; dq_f32: float32 (partial sums of a shared head)
+  float* dk_part = nullptr;                              // [batch][L][H][K] float32
+  void* dk = nullptr;                                    // [batch][L][H][K]; dk_f32: the sum stays in dk_part
+  float *dg = nullptr, *dbeta = nullptr;                 // [batch][L][H]
+  int64_t batch = 0, L = 0;
+  int H = 0, K = 0, V = 0, every = 1;
+  float scale = 1.0f;
+  int dq_f32 = 0, dk_f32 = 0;
+  int carried = 0;                                       // there is an initial state
+  int d_vec = 0;                                         // rows of d move as 16 bytes
+  int part_vec = 0;                                      // rows of dq, dk and dk_part move as 4 elements
+};
+int gd_every(int64_t batch, int64_t L, int64_t H);
+hipError_t launch_gd_qk(const GdGradArgs& a, Dt dt, hipStream_t s);
+
 struct GdStepArgs {
   const float* state_in = nullptr;    // [states][H][K][V]
   float* state_out = nullptr;
@@ -112,6 +140,9 @@ hipError_t launch_gd_step(const GdStepArgs& a, Dt dt, hipStream_t s);
 
 int64_t gd_record_bytes(Dt dt);
 hipError_t launch_gd(const GdArgs& a, Dt dt, hipStream_t s);
+// The two walks of the gradient: forwards (v, carry: the inputs'), then backwards (v: the outputs' gradient, carry: the
+// final state's, o: dv, fin: the initial state's).
+hipError_t launch_gd_walks(const GdArgs& forwards, const GdArgs& backwards, Dt dt, hipStream_t s);
 
 struct NormArgs {
   const void *x = nullptr, *gate = nullptr, *residual = nullptr;

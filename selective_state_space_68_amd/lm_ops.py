@@ -316,6 +316,53 @@ def gated_delta_fwd(q, k, v, g, beta, scale=None, *, initial_state=None, lengths
     return out, final_state
 
 
+@lru_cache(maxsize=4096)
+def gated_delta_bwd_workspace_size(batch, L, H, K, V, dtype=BF16, *, Hq=None, Hk=None, Hv=None) -> int:
+    """Bytes of device workspace gated_delta_bwd needs (Hq, Hk, Hv: heads of q, k and v, H when None)."""
+    return int(_entry("ssm_gated_delta_bwd_workspace_size")(
+        int(batch), int(L), int(H), int(Hq or H), int(Hk or H), int(Hv or H), int(K), int(V), _dt(dtype)))
+
+
+def gated_delta_bwd(q, k, v, g, beta, dout, scale=None, *, initial_state=None, dfinal_state=None, lengths=None,
+                    want_dinitial_state=None, workspace=None, out=None, stream=None) -> dict:
+    """Gradients of gated_delta_fwd (same inputs) for the output gradient dout [batch, L, H, V] and optionally the final
+    state's, dfinal_state [batch, H, K, V].
+
+    Returns a dict with dq, dk, dv (packed, in the shapes of q, k and v: summed over the state heads that share a
+    head), dg, dbeta [batch, L, H] float32 and dinitial_state (None unless an initial state is given or
+    want_dinitial_state says so).  `workspace`: a device tensor of at least gated_delta_bwd_workspace_size(...) bytes,
+    or None (allocated here); `out` may hold preallocated outputs under the same keys.
+    """
+    if stream is not None:
+        return _elsewhere(gated_delta_bwd, locals())
+    (batch, L), H, Hq, Hk, Hv, K, V = _delta_shapes(q, k, v, g, beta, 4)
+    states = (batch, H, K, V)
+    if not isinstance(dout, _Tensor):
+        raise TypeError("dout must be a torch.Tensor")
+    _is(dout, "dout", (batch, L, H, V))
+    _is(lengths, "lengths", (batch,))
+    _is(initial_state, "initial_state", states)
+    _is(dfinal_state, "dfinal_state", states)
+    act, dev = q.dtype, q.get_device()
+    dt = _dt(act)
+    qs, ks, vs = _strides(q, "q", act, dev), _strides(k, "k", act, dev), _strides(v, "v", act, dev)
+    ds = _strides(dout, "dout", act, dev)
+    want = initial_state is not None if want_dinitial_state is None else want_dinitial_state
+    grads = _outputs(out, q, {"dq": ((batch, L, Hq, K), act, True), "dk": ((batch, L, Hk, K), act, True),
+                              "dv": ((batch, L, Hv, V), act, True), "dg": ((batch, L, H), F32, True),
+                              "dbeta": ((batch, L, H), F32, True), "dinitial_state": (states, F32, want)})
+    ws, ws_ptr, ws_bytes = _scratch(
+        workspace, gated_delta_bwd_workspace_size(batch, L, H, K, V, act, Hq=Hq, Hk=Hk, Hv=Hv), q)
+    _run(_entry("ssm_gated_delta_bwd"), dev,
+         q.data_ptr(), k.data_ptr(), v.data_ptr(), dout.data_ptr(), qs, ks, vs, ds, _ptr(g, "g", F32, dev),
+         _ptr(beta, "beta", F32, dev), K ** -0.5 if scale is None else float(scale), _ptr(lengths, "lengths", _I32, dev),
+         _ptr(initial_state, "initial_state", F32, dev), _ptr(dfinal_state, "dfinal_state", F32, dev),
+         _ptr(grads["dq"], "dq", act, dev), _ptr(grads["dk"], "dk", act, dev), _ptr(grads["dv"], "dv", act, dev),
+         _ptr(grads["dg"], "dg", F32, dev), _ptr(grads["dbeta"], "dbeta", F32, dev),
+         _ptr(grads["dinitial_state"], "dinitial_state", F32, dev), batch, L, H, Hq, Hk, Hv, K, V, dt, ws_ptr, ws_bytes)
+    return grads
+
+
 def gated_delta_step(state, q_t, k_t, v_t, g_t, beta_t, scale=None, *, slots=None, out_state=None, out=None,
                      stream=None) -> torch.Tensor:
     """One token of gated_delta_fwd.  state [states, H, K, V] float32; q_t [batch, Hq, K], k_t [batch, Hk, K],

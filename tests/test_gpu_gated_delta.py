@@ -7,6 +7,10 @@ Error of a row (one token's V values of one head; one row of a state): the 2-nor
            root of their number, 4 * sqrt(192) * 2^-24 = 3.3e-6, times the few sizes that a term may exceed its head's
            mean by, as they fall: 2e-5.
   states   float32 from operands of 24 bits (bfloat16 inputs included): the same 2e-5.
+  the initial state's gradient is what its first chunk leaves of the gradient that enters it, exp(G_Q) F - K^T (beta
+           exp(G) Y) + scale (exp(G) Q)^T D: where the keys are alike the terms cancel (with K = 1 a chunk takes the
+           product of 64 factors 1 - beta off F), and float32 sums are good to 2^-24 of their terms, not of what is
+           left.  The terms' 2-norms are added to that row's size.
   bfloat16 outputs: rounded by up to 2^-8 of each value, operands of 16 bits before that (2^-16 a product, far below):
            2^-8 * 1.02 + 2e-5.
 """
@@ -33,7 +37,20 @@ def _ssm():
     return ssm
 
 
-def _check(got, want, tol, what):
+def _first_chunk_terms(t, s0, df, scale):
+    """[B, H, K]: the 2-norms of the terms whose sum is the initial state's gradient, row by row."""
+    H = t["g"].shape[-1]
+    x = {n: ref.heads(t[n], H) if n in "qkv" else t[n].double() for n in t}
+    first, rest = ({n: y[:, i] for n, y in x.items()} for i in (slice(0, 64), slice(64, None)))
+    state = ref.delta(*(first[n] for n in ("q", "k", "v", "g", "beta")), scale, s0)[1]
+    F = ref.delta_grad(*rest.values(), scale, state, df)["dinitial_state"]
+    dv = ref.delta_grad(*first.values(), scale, s0, F)["dv"]
+    decay = first["g"].cumsum(1).exp()                          # [B, L, H]
+    both = first["k"].abs() * dv.norm(dim=-1, keepdim=True) + scale * first["q"].abs() * first["do"].norm(dim=-1, keepdim=True)
+    return decay[:, -1, :, None] * F.norm(dim=-1) + (decay[..., None] * both).sum(1)
+
+
+def _check(got, want, tol, what, more=0.0):
     got, want = got.detach().double().cpu(), want.double()
     assert got.shape == want.shape
     assert torch.isfinite(got).all(), what
@@ -41,7 +58,7 @@ def _check(got, want, tol, what):
     if d.numel() == 0:
         return
     axes = (0, 1) if d.dim() == 3 and "state" not in what else (0, 2)
-    size = r + r.square().mean(axes, keepdim=True).sqrt()
+    size = r + r.square().mean(axes, keepdim=True).sqrt() + more
     e = float((d / size.clamp(min=1e-30)).max()) if float(d.max()) > 0 else 0.0
     print(f"{what} {tuple(got.shape)}: {e:.2e}", flush=True)
     assert e <= tol, (what, e)
@@ -96,6 +113,39 @@ def test_forward(B, L, H, K, V, heads, dtype):
     _check(out2, _want(t, 0.3)[0], OUT[dtype], "out")
 
 
+def _gradient(t, s0=None, df=None, lengths=None, scale=None, **named):
+    d = _cuda(t)
+    return _ssm().gated_delta_bwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d["do"], scale,
+                                  initial_state=None if s0 is None else s0.cuda(),
+                                  dfinal_state=None if df is None else df.cuda(),
+                                  lengths=None if lengths is None else torch.tensor(lengths, dtype=torch.int32).cuda(),
+                                  **named)
+
+
+def _check_grads(got, want, dtype, terms=0.0):
+    """g's and beta's gradients are float32 and a row of theirs is a head's tokens."""
+    for n, w in want.items():
+        if got[n] is None:
+            continue
+        if n in ("dg", "dbeta"):
+            _check(got[n].transpose(1, 2)[:, :, None], w.transpose(1, 2)[:, :, None], OUT[F32], n)
+        else:
+            _check(got[n], w, STATE if "state" in n else OUT[dtype], n, terms if "state" in n else 0.0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,L,H,K,V,heads", SHAPES)
+def test_gradient(B, L, H, K, V, heads, dtype):
+    t, s0, df = ref.inputs(B, L, H, K, V, dtype, heads, seed=L + V)
+    got = _gradient(t, s0, df)
+    want = ref.delta_grad(*t.values(), K ** -0.5, s0, df)
+    assert got.keys() == want.keys()
+    _check_grads(got, want, dtype, _first_chunk_terms(t, s0, df, K ** -0.5))
+    got = _gradient(t, scale=0.3)
+    assert got["dinitial_state"] is None
+    _check_grads(got, ref.delta_grad(*t.values(), 0.3), dtype)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_absent_tokens_hold_anything(dtype):
     B, L, H, K, V = 6, 150, 3, 64, 72
@@ -113,6 +163,12 @@ def test_absent_tokens_hold_anything(dtype):
     assert torch.equal(fin[1].cpu(), s0[1])                 # no token: the state as it was
     out2, fin2 = _forward(t, s0, [1000, -5, 1, 64, 65, 149])    # clamped to [0, L]
     assert torch.equal(out2, out) and torch.equal(fin2, fin)
+    df = torch.randn(B, H, K, V, generator=torch.Generator().manual_seed(2))
+    got = _gradient(bad, s0, df, lengths)
+    _check_grads(got, ref.delta_grad(*t.values(), K ** -0.5, s0, df, lengths), dtype)
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert not got[n].cpu()[absent].any(), n
+    assert torch.equal(got["dinitial_state"][1].cpu(), df[1])
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
