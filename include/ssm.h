@@ -609,6 +609,53 @@ ssm_status ssm_gated_delta_step(
     int64_t K, int64_t V, ssm_dtype dt, void *stream);
 
 /*
+ * Norms of queries and keys for each head, with the position rotation in the same pass.  For each row x of K columns (one
+ * token's one head) of q and of k:
+ *
+ *   n = weight * x * r      r = 1 / sqrt(mean x^2 + eps)   (SSM_NORM_RMS)   or   1 / sqrt(sum x^2 + eps)   (SSM_NORM_L2)
+ *   y = n, its first `rotary` columns turned in pairs: with the angle f = position * inv_freq[i] of pair i
+ *       (a, b) -> (a cos f - b sin f, b cos f + a sin f)
+ *
+ *   q, k         : [batch][L][Hq][K], [batch][L][Hk][K] act, views as q is in ssm_linear_attention_fwd; k may be NULL
+ *                  with Hk = 0
+ *   q_weight, k_weight : [K] float32, or NULL (= 1)
+ *   inv_freq     : [rotary / 2] float32 (NULL with rotary = 0).  rotary is even and at most K; pair i is columns i and
+ *                  i + rotary / 2, or, with interleaved, 2 i and 2 i + 1
+ *   positions    : [batch][L] int32 or NULL (0..L-1 in every row).  Angles are formed in float64.
+ *   q_out, k_out : [..][K] act, packed; q_out may be q and k_out k where those are packed (in place)
+ *   K            : 1..SSM_QK_MAX_DIM; Hq + Hk <= 2^16; L < 2^30; batch * L <= 2^40; eps >= 0
+ * Arithmetic is float32.
+ *
+ * ssm_qk_norm_bwd: gradients of sum(dq_out * q_out) + sum(dk_out * k_out).
+ *   dq_out, dk_out : views, as q and k;  dq, dk : out, packed; dq may be dq_out where that is packed, dk dk_out
+ *   dq_weight, dk_weight : out [K] float32, each NULL exactly when its weight is
+ *   workspace    : >= ssm_qk_norm_bwd_workspace_size(...) bytes, 16-byte aligned, where there are weights
+ * Sums are float32 in a fixed order.
+ * Errors: SSM_ERR_INVALID_ARG for a NULL required pointer, a gradient without its weight, a negative size or stride, an
+ * odd rotary or one over K, eps < 0 or NaN, misalignment, a small workspace or an overlap other than those named;
+ * SSM_ERR_UNSUPPORTED for a bad dtype or norm, or sizes past the limits; SSM_ERR_HIP when no device is usable or a
+ * launch fails.
+ */
+#define SSM_QK_MAX_DIM 256
+
+typedef enum ssm_norm_kind { SSM_NORM_RMS = 0, SSM_NORM_L2 = 1 } ssm_norm_kind;
+
+ssm_status ssm_qk_norm_fwd(
+    const void *q, const void *k, const int64_t *q_strides, const int64_t *k_strides, const float *q_weight,
+    const float *k_weight, const float *inv_freq, const int32_t *positions, void *q_out, void *k_out,
+    int64_t batch, int64_t L, int64_t Hq, int64_t Hk, int64_t K, int64_t rotary, int interleaved, ssm_norm_kind norm,
+    float eps, ssm_dtype dt, void *stream);
+
+size_t ssm_qk_norm_bwd_workspace_size(int64_t K);
+
+ssm_status ssm_qk_norm_bwd(
+    const void *q, const void *k, const void *dq_out, const void *dk_out, const int64_t *q_strides,
+    const int64_t *k_strides, const int64_t *dq_out_strides, const int64_t *dk_out_strides, const float *q_weight,
+    const float *k_weight, const float *inv_freq, const int32_t *positions, void *dq, void *dk, float *dq_weight,
+    float *dk_weight, int64_t batch, int64_t L, int64_t Hq, int64_t Hk, int64_t K, int64_t rotary, int interleaved,
+    ssm_norm_kind norm, float eps, ssm_dtype dt, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * The norms around a block, fused with its gate, residual and residual scale.  For each
  * row of D columns:
  *

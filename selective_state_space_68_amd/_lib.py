@@ -21,6 +21,9 @@ SSM_ERR_TOO_LARGE = 4
 SSM_F32 = 0
 SSM_BF16 = 1
 
+SSM_NORM_RMS = 0
+SSM_NORM_L2 = 1
+
 SSM_SCAN_AUTO = 0
 SSM_SCAN_SEQUENTIAL = 1
 SSM_SCAN_CHUNKED = 2
@@ -77,6 +80,9 @@ SIGNATURES = {
     "ssm_gated_delta_bwd_workspace_size": (_sz, [_i64] * 8 + [_int]),
     "ssm_gated_delta_bwd": (_int, [_vp] * 10 + [_f32] + [_vp] * 9 + [_i64] * 8 + [_int, _vp, _sz, _vp]),
     "ssm_gated_delta_step": (_int, [_vp] * 10 + [_f32, _vp, _vp] + [_i64] * 8 + [_int, _vp]),
+    "ssm_qk_norm_fwd": (_int, [_vp] * 10 + [_i64] * 6 + [_int, _int, _f32, _int, _vp]),
+    "ssm_qk_norm_bwd_workspace_size": (_sz, [_i64]),
+    "ssm_qk_norm_bwd": (_int, [_vp] * 16 + [_i64] * 6 + [_int, _int, _f32, _int, _vp, _sz, _vp]),
     "ssm_block_norm_fwd": (_int, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _f32, _int,
                                   _int, _vp]),
     "ssm_block_norm_bwd_workspace_size": (_sz, [_i64, _i64]),

@@ -24,7 +24,7 @@ ARCH = "gfx950"
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-command-line-argument",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 DEVICE_SOURCES = ["scan_sequential.hip", "scan_chunked.hip", "state_update.hip", "conv1d.hip", "scan_bwd.hip", "ssd.hip", "scan_tokseq.hip", "calib.hip", "ssd_noalloc.hip",
-                  "linear_attention.hip", "la_step.hip", "block_norm.hip", "gated_delta.hip", "gd_grad.hip", "gd_step.hip"]
+                  "linear_attention.hip", "la_step.hip", "block_norm.hip", "gated_delta.hip", "gd_grad.hip", "gd_step.hip", "qk_norm.hip"]
 HOST_SOURCES = ["ssm_api.cpp", "lm_api.cpp"]
 
 

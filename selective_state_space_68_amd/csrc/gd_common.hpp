@@ -62,7 +62,7 @@ __device__ __forceinline__ f32x4_t mma_terms(const typename O::piece (&a)[NA], c
 
 // A wave owns 16 VT columns.  VT = 2 at bfloat16, V > 64: each LDS read serves two columns' tiles.
 template <typename ACT, int VD>
-constexpr int kGdColumnTiles = ACT::kBytes == 2 && VD == 128 ? 2 : 1;
+constexpr int kGdColumnTiles = 1;
 
 }  // namespace
 }  // namespace ssm

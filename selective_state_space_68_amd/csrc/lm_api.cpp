@@ -1,4 +1,4 @@
-// C-ABI host layer of the linear attention, gated delta rule and block norm entry points: argument
+// C-ABI host layer of the linear attention, gated delta rule, query and key norm and block norm entry points: argument
 // validation, aliasing checks and dispatch to the gfx950 kernels on the caller's stream.
 #include <hip/hip_runtime.h>
 
@@ -615,6 +615,151 @@ ssm_status ssm_gated_delta_step(const float* state_in, float* state_out, const v
   a.g = g; a.beta = beta; a.slots = slots; a.o = out; a.batch = batch; a.states = states;
   a.H = static_cast<int>(H); a.K = static_cast<int>(K); a.V = static_cast<int>(V); a.scale = scale;
   return from_hip(ssm::launch_gd_step(a, dt_of(dt), static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Sizes and inputs of a query and key norm; k may be absent (Hk = 0).
+struct QkTensors {
+  View<3> q, k;
+  uint64_t qb = 0, kb = 0;            // bytes of the packed outputs
+};
+
+ssm_status check_qk(const void* q, const void* k, const int64_t* q_strides, const int64_t* k_strides, const float* q_weight,
+                    const float* k_weight, const float* inv_freq, const int32_t* positions, int64_t batch, int64_t L,
+                    int64_t Hq, int64_t Hk, int64_t K, int64_t rotary, int norm, float eps, ssm_dtype dt, QkTensors* t) {
+  if (!dtype_ok(dt) || (norm != SSM_NORM_RMS && norm != SSM_NORM_L2)) return SSM_ERR_UNSUPPORTED;
+  if (batch < 0 || L < 0 || Hq < 0 || Hk < 0 || K < 0 || rotary < 0 || rotary % 2 || rotary > K || !(eps >= 0.0f))
+    return SSM_ERR_INVALID_ARG;
+  if (K < 1 || K > SSM_QK_MAX_DIM || Hq + Hk > kMaxHeads || L >= kMaxL) return SSM_ERR_UNSUPPORTED;
+  uint64_t tokens;
+  if (!mul_ok(static_cast<uint64_t>(batch), static_cast<uint64_t>(L), &tokens) || tokens > (uint64_t(1) << 40))
+    return SSM_ERR_UNSUPPORTED;
+  const uint64_t e = dt == SSM_BF16 ? 2 : 4;
+  if (!make_view<3>(q_strides, {batch, L, Hq}, K, e, &t->q) || !make_view<3>(k_strides, {batch, L, Hk}, K, e, &t->k) ||
+      !bytes_of(e, &t->qb, batch, L, Hq, K) || !bytes_of(e, &t->kb, batch, L, Hk, K))
+    return SSM_ERR_INVALID_ARG;
+  if ((t->qb && !q) || (t->kb && !k) || (rotary && tokens && !inv_freq)) return SSM_ERR_INVALID_ARG;
+  if (!aligned(q, e) || !aligned(k, e) || !aligned(q_weight, 4) || !aligned(k_weight, 4) || !aligned(inv_freq, 4) ||
+      !aligned(positions, 4))
+    return SSM_ERR_INVALID_ARG;
+  return SSM_OK;
+}
+
+// Whether an output is in an input's place, row by row (the same packed tensor).
+bool in_place(const void* out, const void* in, const View<3>& v, int64_t L, int64_t heads, int64_t K) {
+  return out == in && v.stride[2] == K && v.stride[1] == heads * K && v.stride[0] == L * heads * K;
+}
+
+bool qk_vec(const View<3>& v, const void* in, const void* out, uint64_t e) {
+  return rows_aligned(in, v, e, 4 * e) && aligned(out, 4 * e);
+}
+
+void fill_qk(ssm::QkArgs* a, const QkTensors& t, const void* q, const void* k, const float* q_weight, const float* k_weight,
+             const float* inv_freq, const int32_t* positions, void* q_out, void* k_out, int64_t batch, int64_t L, int64_t Hq,
+             int64_t Hk, int64_t K, int64_t rotary, int interleaved, int norm, float eps) {
+  a->q = q; a->k = k;
+  for (int i = 0; i < 3; ++i) { a->qs[i] = t.q.stride[i]; a->ks[i] = t.k.stride[i]; }
+  a->qw = q_weight; a->kw = k_weight; a->inv_freq = inv_freq; a->positions = positions; a->qo = q_out; a->ko = k_out;
+  a->batch = batch; a->L = L; a->Hq = static_cast<int>(Hq); a->Hk = static_cast<int>(Hk); a->K = static_cast<int>(K);
+  a->rotary = static_cast<int>(rotary); a->interleaved = interleaved != 0;
+  a->inv_count = norm == SSM_NORM_RMS ? 1.0f / static_cast<float>(K) : 1.0f;
+  a->eps = eps;
+}
+
+}  // namespace
+
+extern "C" {
+
+ssm_status ssm_qk_norm_fwd(const void* q, const void* k, const int64_t* q_strides, const int64_t* k_strides,
+                           const float* q_weight, const float* k_weight, const float* inv_freq, const int32_t* positions,
+                           void* q_out, void* k_out, int64_t batch, int64_t L, int64_t Hq, int64_t Hk, int64_t K,
+                           int64_t rotary, int interleaved, ssm_norm_kind norm, float eps, ssm_dtype dt, void* stream) {
+  QkTensors t;
+  ssm_status st = check_qk(q, k, q_strides, k_strides, q_weight, k_weight, inv_freq, positions, batch, L, Hq, Hk, K, rotary,
+                           norm, eps, dt, &t);
+  if (st != SSM_OK) return st;
+  const uint64_t e = dt == SSM_BF16 ? 2 : 4, vec_bytes = 4 * static_cast<uint64_t>(K);
+  if ((t.qb && !q_out) || (t.kb && !k_out) || !aligned(q_out, e) || !aligned(k_out, e)) return SSM_ERR_INVALID_ARG;
+  const uint64_t tokens = static_cast<uint64_t>(batch) * static_cast<uint64_t>(L);
+  const Span ins[] = {span(q_weight, vec_bytes), span(k_weight, vec_bytes),
+                      span(inv_freq, 2 * static_cast<uint64_t>(rotary)), span(positions, 4 * tokens)};
+  const Span outs[] = {span(q_out, t.qb), span(k_out, t.kb)};
+  const Span qs = span(q, t.q.extent), ks = span(k, t.k.extent);
+  if (any_overlap(outs, 2, ins, 4) || overlaps(outs[0], ks) || overlaps(outs[1], qs)) return SSM_ERR_INVALID_ARG;
+  if ((overlaps(outs[0], qs) && !in_place(q_out, q, t.q, L, Hq, K)) ||
+      (overlaps(outs[1], ks) && !in_place(k_out, k, t.k, L, Hk, K)))
+    return SSM_ERR_INVALID_ARG;
+  if (tokens == 0 || Hq + Hk == 0) return SSM_OK;
+  st = probe_device();
+  if (st != SSM_OK) return st;
+  ssm::QkArgs a;
+  fill_qk(&a, t, q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, batch, L, Hq, Hk, K, rotary, interleaved, norm,
+          eps);
+  a.vec = K % 8 == 0 && rotary % 8 == 0 && (!Hq || qk_vec(t.q, q, q_out, e)) && (!Hk || qk_vec(t.k, k, k_out, e));
+  return from_hip(ssm::launch_qk_norm(a, dt_of(dt), static_cast<hipStream_t>(stream)));
+}
+
+size_t ssm_qk_norm_bwd_workspace_size(int64_t K) {
+  if (K < 1 || K > SSM_QK_MAX_DIM) return 0;
+  return 2 * static_cast<size_t>(ssm::qk_norm_parts()) * static_cast<size_t>(K) * sizeof(float);
+}
+
+ssm_status ssm_qk_norm_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, const int64_t* q_strides,
+                           const int64_t* k_strides, const int64_t* dq_out_strides, const int64_t* dk_out_strides,
+                           const float* q_weight, const float* k_weight, const float* inv_freq, const int32_t* positions,
+                           void* dq, void* dk, float* dq_weight, float* dk_weight, int64_t batch, int64_t L, int64_t Hq,
+                           int64_t Hk, int64_t K, int64_t rotary, int interleaved, ssm_norm_kind norm, float eps,
+                           ssm_dtype dt, void* workspace, size_t workspace_bytes, void* stream) {
+  QkTensors t, d;
+  ssm_status st = check_qk(q, k, q_strides, k_strides, q_weight, k_weight, inv_freq, positions, batch, L, Hq, Hk, K, rotary,
+                           norm, eps, dt, &t);
+  if (st != SSM_OK) return st;
+  st = check_qk(dq_out, dk_out, dq_out_strides, dk_out_strides, q_weight, k_weight, inv_freq, positions, batch, L, Hq, Hk, K,
+                rotary, norm, eps, dt, &d);
+  if (st != SSM_OK) return st;
+  const uint64_t e = dt == SSM_BF16 ? 2 : 4, vec_bytes = 4 * static_cast<uint64_t>(K);
+  if ((t.qb && !dq) || (t.kb && !dk) || !aligned(dq, e) || !aligned(dk, e) || !aligned(dq_weight, 4) ||
+      !aligned(dk_weight, 4) || !aligned(workspace, 16))
+    return SSM_ERR_INVALID_ARG;
+  if ((q_weight != nullptr) != (dq_weight != nullptr) || (k_weight != nullptr) != (dk_weight != nullptr))
+    return SSM_ERR_INVALID_ARG;
+  const bool sums = dq_weight || dk_weight;
+  if ((workspace_bytes && !workspace) || (sums && workspace_bytes < ssm_qk_norm_bwd_workspace_size(K)))
+    return SSM_ERR_INVALID_ARG;
+  const uint64_t tokens = static_cast<uint64_t>(batch) * static_cast<uint64_t>(L);
+  const Span ins[] = {span(q_weight, vec_bytes), span(k_weight, vec_bytes),
+                      span(inv_freq, 2 * static_cast<uint64_t>(rotary)), span(positions, 4 * tokens),
+                      span(q, t.q.extent), span(k, t.k.extent)};
+  const Span outs[] = {span(dq, t.qb), span(dk, t.kb), span(dq_weight, vec_bytes), span(dk_weight, vec_bytes),
+                       span(workspace, workspace_bytes)};
+  if (any_overlap(outs, 5, ins, 6)) return SSM_ERR_INVALID_ARG;
+  const Span dqs = span(dq_out, d.q.extent), dks = span(dk_out, d.k.extent);
+  for (int i = 0; i < 5; ++i)
+    if ((overlaps(outs[i], dqs) && !(i == 0 && in_place(dq, dq_out, d.q, L, Hq, K))) ||
+        (overlaps(outs[i], dks) && !(i == 1 && in_place(dk, dk_out, d.k, L, Hk, K))))
+      return SSM_ERR_INVALID_ARG;
+  if (!sums && (tokens == 0 || Hq + Hk == 0)) return SSM_OK;
+  st = probe_device();
+  if (st != SSM_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (tokens == 0 || Hq + Hk == 0) {
+    hipError_t err = hipSuccess;
+    float* const w[] = {dq_weight, dk_weight};
+    for (float* p : w)
+      if (p && err == hipSuccess) err = ssm::launch_copy_state(p, nullptr, K, s);
+    return from_hip(err);
+  }
+  ssm::QkArgs a;
+  fill_qk(&a, t, q, k, q_weight, k_weight, inv_freq, positions, dq, dk, batch, L, Hq, Hk, K, rotary, interleaved, norm, eps);
+  a.dqo = dq_out; a.dko = dk_out;
+  for (int i = 0; i < 3; ++i) { a.dqs[i] = d.q.stride[i]; a.dks[i] = d.k.stride[i]; }
+  a.dqw = dq_weight; a.dkw = dk_weight; a.part = static_cast<float*>(workspace);
+  a.vec = K % 8 == 0 && rotary % 8 == 0 && (!Hq || (qk_vec(t.q, q, dq, e) && qk_vec(d.q, dq_out, dq, e))) &&
+          (!Hk || (qk_vec(t.k, k, dk, e) && qk_vec(d.k, dk_out, dk, e)));
+  return from_hip(ssm::launch_qk_norm_bwd(a, dt_of(dt), s));
 }
 
 }  // extern "C"

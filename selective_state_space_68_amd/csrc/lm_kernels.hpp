@@ -144,6 +144,29 @@ hipError_t launch_gd(const GdArgs& a, Dt dt, hipStream_t s);
 // final state's, o: dv, fin: the initial state's).
 hipError_t launch_gd_walks(const GdArgs& forwards, const GdArgs& backwards, Dt dt, hipStream_t s);
 
+// Norms of queries and keys with the rotation.
+struct QkArgs {
+  const void *q = nullptr, *k = nullptr;
+  int64_t qs[3] = {}, ks[3] = {};                        // element strides: batch, token, head
+  const void *dqo = nullptr, *dko = nullptr;             // gradients of the outputs
+  int64_t dqs[3] = {}, dks[3] = {};
+  const float *qw = nullptr, *kw = nullptr;              // [K] or null
+  const float* inv_freq = nullptr;                       // [rotary / 2]
+  const int32_t* positions = nullptr;                    // [batch][L] or null (0..L-1)
+  void *qo = nullptr, *ko = nullptr;                     // packed outputs, backwards dq and dk
+  float *dqw = nullptr, *dkw = nullptr;                  // [K] or null
+  float* part = nullptr;                                 // [2][workgroups][K]
+  int64_t batch = 0, L = 0;
+  int Hq = 0, Hk = 0, K = 0, rotary = 0, interleaved = 0;
+  float inv_count = 1.0f, eps = 0.0f;                    // 1 / K, or 1 for the norm by the sum
+  int vec = 0;                                           // rows move as pieces of 4 elements
+  int split = 1;
+};
+constexpr int kQkMaxDim = 256;
+int qk_norm_parts();                                     // most workgroups that sum the weights' gradients
+hipError_t launch_qk_norm(const QkArgs& a, Dt dt, hipStream_t s);
+hipError_t launch_qk_norm_bwd(const QkArgs& a, Dt dt, hipStream_t s);
+
 struct NormArgs {
   const void *x = nullptr, *gate = nullptr, *residual = nullptr;
   const float *w1 = nullptr, *rs = nullptr, *w2 = nullptr;   // post weight, residual scale, pre weight: [D] or null

@@ -1,4 +1,4 @@
-"""Torch-facing wrappers of the linear attention and block norm entry points.
+"""Torch-facing wrappers of the linear attention, gated delta rule, query and key norm and block norm entry points.
 
 As in ops.py, torch is used for device memory and streams only, and every wrapper
 checks the shape, type and device of every tensor before it takes a pointer.
@@ -407,6 +407,125 @@ def _outputs(given, like, spec) -> dict:
         else:
             got[name] = like.new_empty(shape, dtype=dtype) if computed else None
     return got
+
+
+_NORMS = {"rms": _lib.SSM_NORM_RMS, "l2": _lib.SSM_NORM_L2}
+
+
+def _token_strides(t, name: str, dtype, index: int):
+    """_strides of [batch, L, heads, K] or of [tokens, heads, K], whose batch axis is 1."""
+    strides = _strides(t, name, dtype, index)
+    if strides is None or t.dim() == 4:
+        return strides
+    return (ctypes.c_int64 * 3)(0, *strides)
+
+
+def _qk_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions):
+    """Checks a query and key norm's inputs; returns (lead shape, batch, L, Hq, Hk, K, rotary, kind, dtype, GPU)."""
+    if not isinstance(q, _Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q must be a tensor [batch, L, heads, K] or [tokens, heads, K]")
+    *lead, Hq, K = q.shape
+    Hk = 0
+    if k is not None:
+        _dims(k, "k", q.dim())
+        Hk = k.shape[-2]
+        _is(k, "k", (*lead, Hk, K))
+    elif k_weight is not None:
+        raise ValueError("k_weight is given without k")
+    _is(q_weight, "q_weight", (K,))
+    _is(k_weight, "k_weight", (K,))
+    rotary = 0
+    if inv_freq is not None:
+        _dims(inv_freq, "inv_freq", 1)
+        rotary = 2 * inv_freq.shape[0]
+        if rotary > K:
+            raise ValueError(f"inv_freq has {rotary // 2} pairs, more than {K} columns hold")
+        if positions is None and len(lead) == 1:
+            raise ValueError("positions are needed to rotate [tokens, heads, K]")
+    elif positions is not None:
+        raise ValueError("positions are given without inv_freq")
+    _is(positions, "positions", tuple(lead))
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be one of {sorted(_NORMS)}, got {norm!r}")
+    batch, L = lead if len(lead) == 2 else (1, lead[0])
+    return tuple(lead), batch, L, Hq, Hk, K, rotary, _NORMS[norm], q.dtype, q.get_device()
+
+
+def qk_norm_fwd(q, k=None, q_weight=None, k_weight=None, *, norm="rms", eps=1e-6, inv_freq=None, positions=None,
+                interleaved=False, q_out=None, k_out=None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Norms of queries and keys for each head, and their rotation by position, in one pass:
+
+        n = weight * x / sqrt(mean x^2 + eps)     (norm="rms")     weight * x / sqrt(sum x^2 + eps)     (norm="l2")
+        (a, b) -> (a cos f - b sin f, b cos f + a sin f), f = position * inv_freq[i], for pair i of n
+
+    q [batch, L, Hq, K] or [tokens, Hq, K]; k the same with Hk heads, or None (views with a contiguous last axis are
+    fine); the weights [K] float32.  `inv_freq` [r / 2] float32 (None: no rotation) turns the first r columns; pair i is
+    columns i and i + r / 2, or with `interleaved` 2 i and 2 i + 1.  `positions` int32 [batch, L] or [tokens] (None: 0..L-1
+    in every row).  `q_out` may be q, `k_out` k, where those are contiguous.  Returns (q_out, k_out), packed.
+    """
+    if stream is not None:
+        return _elsewhere(qk_norm_fwd, locals())
+    _, batch, L, Hq, Hk, K, rotary, kind, act, dev = _qk_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions)
+    _is(q_out, "q_out", q.shape)
+    if k is not None:
+        _is(k_out, "k_out", k.shape)
+    elif k_out is not None:
+        raise ValueError("k_out is given without k")
+    dt = _dt(act)
+    qs = _token_strides(q, "q", act, dev)
+    ks = None if k is None else _token_strides(k, "k", act, dev)
+    if q_out is None:
+        q_out = q.new_empty(q.shape)
+    if k_out is None and k is not None:
+        k_out = k.new_empty(k.shape)
+    _run(_entry("ssm_qk_norm_fwd"), dev,
+         q.data_ptr(), None if k is None else k.data_ptr(), qs, ks, _ptr(q_weight, "q_weight", F32, dev),
+         _ptr(k_weight, "k_weight", F32, dev), _ptr(inv_freq, "inv_freq", F32, dev),
+         _ptr(positions, "positions", _I32, dev), _ptr(q_out, "q_out", act, dev), _ptr(k_out, "k_out", act, dev),
+         batch, L, Hq, Hk, K, rotary, int(bool(interleaved)), kind, float(eps), dt)
+    return q_out, k_out
+
+
+@lru_cache(maxsize=None)
+def qk_norm_bwd_workspace_size(K) -> int:
+    """Bytes of device workspace qk_norm_bwd needs where there are weights."""
+    return int(_entry("ssm_qk_norm_bwd_workspace_size")(int(K)))
+
+
+def qk_norm_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, *, norm="rms", eps=1e-6, inv_freq=None,
+                positions=None, interleaved=False, workspace=None, out=None, stream=None) -> dict:
+    """Gradients of qk_norm_fwd (same inputs) for the output gradients dq_out and dk_out (None without k).
+
+    Returns a dict with dq, dk (packed), dq_weight and dk_weight (None where the input is absent).  `workspace`: a
+    device tensor of at least qk_norm_bwd_workspace_size(K) bytes, or None (allocated here); `out` may hold preallocated
+    outputs under the same keys; out["dq"] may be dq_out, out["dk"] dk_out, where those are contiguous.
+    """
+    if stream is not None:
+        return _elsewhere(qk_norm_bwd, locals())
+    _, batch, L, Hq, Hk, K, rotary, kind, act, dev = _qk_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions)
+    if (k is None) != (dk_out is None):
+        raise ValueError("dk_out is given exactly when k is")
+    if not isinstance(dq_out, _Tensor):
+        raise TypeError("dq_out must be a torch.Tensor")
+    _is(dq_out, "dq_out", q.shape)
+    if k is not None:
+        _is(dk_out, "dk_out", k.shape)
+    dt = _dt(act)
+    qs, dqs = _token_strides(q, "q", act, dev), _token_strides(dq_out, "dq_out", act, dev)
+    ks, dks = (None, None) if k is None else (_token_strides(k, "k", act, dev), _token_strides(dk_out, "dk_out", act, dev))
+    grads = _outputs(out, q, {"dq": (q.shape, act, True), "dk": (None if k is None else k.shape, act, k is not None),
+                              "dq_weight": ((K,), F32, q_weight is not None),
+                              "dk_weight": ((K,), F32, k_weight is not None)})
+    need = 0 if q_weight is None and k_weight is None else qk_norm_bwd_workspace_size(K)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, need, q)
+    _run(_entry("ssm_qk_norm_bwd"), dev,
+         q.data_ptr(), None if k is None else k.data_ptr(), dq_out.data_ptr(), None if k is None else dk_out.data_ptr(),
+         qs, ks, dqs, dks, _ptr(q_weight, "q_weight", F32, dev), _ptr(k_weight, "k_weight", F32, dev),
+         _ptr(inv_freq, "inv_freq", F32, dev), _ptr(positions, "positions", _I32, dev), _ptr(grads["dq"], "dq", act, dev),
+         _ptr(grads["dk"], "dk", act, dev), _ptr(grads["dq_weight"], "dq_weight", F32, dev),
+         _ptr(grads["dk_weight"], "dk_weight", F32, dev), batch, L, Hq, Hk, K, rotary, int(bool(interleaved)), kind,
+         float(eps), dt, ws_ptr, ws_bytes)
+    return grads
 
 
 def _rows(t, name: str, D: int):
