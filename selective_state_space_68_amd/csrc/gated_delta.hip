@@ -8,15 +8,15 @@
 //     X = V - exp(G) K E                            W = T X,   U = beta W
 //     O = scale (exp(G) Q E + lower(M_ij q_i.k_j) U)
 //     E' = exp(G_Q) E + K^T (exp(G_Q - G) U)
-// T depends on no state, so a kernel of its own (gd_prepare_kernel, a workgroup a chunk) forms it for all chunks
+// T and the scores depend on no state, so a kernel of its own (gd_prepare_kernel, a wave a chunk) forms them for all chunks
 // at once.  The walk (gd_walk_kernel) takes a (batch row, head)'s chunks one after the other; only E crosses
 // chunks, in float32 registers.
 //
-// The walk's layout is linear attention's: a wave owns 16 or 32 columns of E, and the columns of a state are
+// The walk's layout is linear attention's: a wave owns 16 columns of E, and the columns of a state are
 // independent, so X, U and E go from product to product in registers.  A product leaves lane (g, c) of a 16 x 16
 // tile four consecutive rows of column c; the rows of each pair of tiles are assigned so that the pair leaves a
 // lane 8 consecutive indices, which is what an operand needs.  q, k and v go from memory into LDS row by row;
-// T comes in operand order straight into registers.
+// T and the scores come in operand order, T straight into registers.
 //
 // Roundings (bfloat16 activations; float32 activations use float32 products throughout): every value that the
 // state depends on enters a product as three bfloat16 terms, which carry 24 bits (E, T, X and the decayed U; a
@@ -34,81 +34,93 @@
 namespace ssm {
 namespace {
 
-// ---- T of every chunk
+// ---- T, the scores and the vectors of every chunk
 
-// The 16 x 16 block at (r0, c0) of a float32 matrix in LDS with rows of kRow floats, as a left operand whose
-// summation index is 4 g + s in step s: a lane's four values are a row's neighbours.
-constexpr int kRow = 68;
-__device__ __forceinline__ f32x4_t block_mma(const float* a, int ar, int ac, const f32x4_t& b, f32x4_t c, int g, int c16) {
-  const float4 x = *reinterpret_cast<const float4*>(a + (ar + c16) * kRow + ac + 4 * g);
+// A chunk's matrix is worked on by one wave, in LDS by blocks of 16 x 16 on and below the diagonal, rows kRow floats apart.
+constexpr int kRow = 20, kBlock = 16 * kRow;
+__device__ __forceinline__ constexpr int block_at(int i, int j) { return (i * (i + 1) / 2 + j) * kBlock; }
+
+// c + a b of two blocks, the summation index 4 g + s in step s, so that a lane's four values of a are a row's neighbours and
+// those of b are what a product left it.
+__device__ __forceinline__ f32x4_t block_mma(const float* a, const f32x4_t& b, f32x4_t c, int g, int c16) {
+  const float4 x = *reinterpret_cast<const float4*>(a + c16 * kRow + 4 * g);
   c = __builtin_amdgcn_mfma_f32_16x16x4f32(x.x, b[0], c, 0, 0, 0);
   c = __builtin_amdgcn_mfma_f32_16x16x4f32(x.y, b[1], c, 0, 0, 0);
   c = __builtin_amdgcn_mfma_f32_16x16x4f32(x.z, b[2], c, 0, 0, 0);
   return __builtin_amdgcn_mfma_f32_16x16x4f32(x.w, b[3], c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4_t block_rows(const float* b, int br, int bc, int g, int c16) {
+__device__ __forceinline__ f32x4_t block_rows(const float* b, int g, int c16) {
   f32x4_t v;
 #pragma unroll
-  for (int s = 0; s < 4; ++s) v[s] = b[(br + 4 * g + s) * kRow + bc + c16];
+  for (int s = 0; s < 4; ++s) v[s] = b[(4 * g + s) * kRow + c16];
   return v;
 }
 
+// LDS that a wave wrote is read by its other lanes (a wave's LDS accesses are carried out in order).
+__device__ __forceinline__ void wave_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+// One wave a chunk: 12 waves a CU that never wait for each other (4 waves on a chunk met at 7 barriers: 4 x 2048, 40 heads of 128,
+// 69 us without the scores).  Rows come straight from memory in operand order.
 // BACK: the rows are the chunk's tokens from its last place to its first, as the backward walk takes them; its matrix is
-// the same with the lower triangle of M_ji k_i.k_j for M_ij k_i.k_j.
-template <typename ACT, int KD, int MOVE, bool BACK>
-__global__ __launch_bounds__(256) void gd_prepare_kernel(GdArgs p) {
+// the same with M_ji k_i.k_j for M_ij k_i.k_j.  PT: the scores' terms (0: not wanted).
+template <typename ACT, int KD, int MOVE, bool BACK, int PT>
+__global__ __launch_bounds__(256, 2) void gd_prepare_kernel(GdArgs p) {
   using O = Op<ACT>;
   using elem = typename O::elem;
   using piece = typename O::piece;
-  constexpr bool kF32 = ACT::kBytes == 4;
-  constexpr int RK = KD * static_cast<int>(sizeof(elem)), PB = O::kPiece, KT = KD / 32;
-  __shared__ __attribute__((aligned(512))) char sK[kQ * RK];
-  __shared__ __attribute__((aligned(16))) float sA[kQ * kRow], sT[kQ * kRow];
-  __shared__ float sHi[kQ], sLo[kQ], sB[kQ];
+  constexpr int KT = KD / 32, NT = kTerms<ACT>, kOne = kPieceBytes<ACT>;
+  __shared__ __attribute__((aligned(16))) float blocks[4][10 * kBlock];
+  __shared__ __attribute__((aligned(16))) float vectors[4][3][kQ];              // G in two parts, beta
 
-  const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6), g = lane >> 4, c16 = lane & 15;
+  const int lane = threadIdx.x & 63, w = uniform_int(threadIdx.x >> 6), g = lane >> 4, c16 = lane & 15;
+  float *A = blocks[w], *sHi = vectors[w][0], *sLo = vectors[w][1], *sB = vectors[w][2];
   const uint32_t nch = static_cast<uint32_t>((p.L + kQ - 1) / kQ), all = static_cast<uint32_t>(p.batch) * p.H * nch;
-  for (uint32_t item = blockIdx.x; item < all; item += gridDim.x) {
+  auto token = [](int row) { return BACK ? kQ - 1 - row : row; };               // (its own inverse)
+  for (uint32_t item = blockIdx.x * 4 + w; item < all; item += gridDim.x * 4) {
     const uint32_t pair = item / nch, c = item - pair * nch;
     const uint32_t row_b = pair / static_cast<uint32_t>(p.H);
     const int h = static_cast<int>(pair - row_b * static_cast<uint32_t>(p.H));
     const int64_t b = row_b, t0 = static_cast<int64_t>(c) * kQ;
     const int left = gd_length(p.lengths, static_cast<int>(p.L), b) - static_cast<int>(t0), n = left < kQ ? left : kQ;
-    if (n <= 0) continue;                             // (nobody reads the record of a chunk without tokens)
-    char* rec = (BACK ? p.rec_back : p.rec) + (static_cast<int64_t>(pair) * nch + c) * kRecord<ACT>;
+    if (n <= 0) continue;                           // (nobody reads the record of a chunk without tokens)
+    char* rec = (BACK ? p.rec_back : p.rec) + static_cast<int64_t>(item) * kRecord<ACT, PT>;
+    const int64_t gate = (b * p.L + t0 + lane) * p.H + h;
+    const bool on = lane < n;
+    const float g_in = on ? p.g[gate] : 0.0f, beta = on ? p.beta[gate] : 0.0f;
 
+    // columns 32 y + 8 g .. of a row as an operand's
     const elem* kg = static_cast<const elem*>(p.k) + b * p.ks[0] + (h / p.kdiv) * p.ks[2] + t0 * p.ks[1];
-    auto token = [](int row) { return BACK ? kQ - 1 - row : row; };
-    if constexpr (MOVE == 16) {
-      constexpr int kSlots = RK / 16;
-  #pragma unroll
-      for (int i = tid; i < kQ * kSlots; i += 256) {
-        const int row = i / kSlots, slot = i % kSlots;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (token(row) < n && slot * 16 < p.K * static_cast<int>(sizeof(elem)))
-          x = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(kg + token(row) * p.ks[1]) + slot * 16);
-        *reinterpret_cast<uint4*>(sK + row * RK + ((slot ^ swizzle<RK, kF32, false>(row)) << 4)) = x;
+    const elem* qg = static_cast<const elem*>(p.q) + b * p.qs[0] + (h / p.qdiv) * p.qs[2] + t0 * p.qs[1];
+    auto load_row = [&](const elem* base, int64_t stride, int row, piece (&out)[KT]) __attribute__((always_inline)) {
+      const int at = token(row);
+      const elem* from = base + at * stride + 8 * g;
+#pragma unroll
+      for (int y = 0; y < KT; ++y) {
+        out[y] = O::zero();
+        if constexpr (MOVE == 16) {
+          if (at < n && 32 * y + 8 * g < p.K) load_piece(reinterpret_cast<const char*>(from + 32 * y), out[y]);
+        } else {
+          elem v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = at < n && 32 * y + 8 * g + e < p.K ? from[32 * y + e] : elem(0);
+          out[y] = __builtin_bit_cast(piece, v);
+        }
       }
-    } else {
-      for (int i = tid; i < kQ * KD; i += 256) {
-        const int row = i / KD, col = i % KD;
-        elem x = elem(0);
-        if (token(row) < n && col < p.K) x = kg[token(row) * p.ks[1] + col];
-        const int byte = col * static_cast<int>(sizeof(elem));
-        *reinterpret_cast<elem*>(sK + row * RK + (byte ^ (swizzle<RK, kF32, false>(row) << 4))) = x;
-      }
-    }
-    if (w == 0) {
-      // the running sum of g, in units of log 2, from float64 as a pair of float32
-      const int64_t at = (b * p.L + t0 + lane) * p.H + h;
-      double G = 0.0;
-      float beta = 0.0f;
-      if (lane < n) {
-        G = static_cast<double>(p.g[at]) * 1.4426950408889634;
-        G = G < kMinGate ? kMinGate : G;              // (NaN passes through)
-        beta = p.beta[at];
-      }
-  #pragma unroll
+    };
+    const int perm_row = 8 * (c16 >> 2) + (c16 & 3);
+    piece kp[2][2][KT];                             // rows 32 t + 8 (c / 4) + 4 u + c % 4
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_row(kg, p.ks[1], 32 * (i / 2) + 4 * (i % 2) + perm_row, kp[i / 2][i % 2]);
+
+    // the running sum of g, in units of log 2, from float64 as a pair of float32
+    {
+      double G = static_cast<double>(g_in) * 1.4426950408889634;
+      G = G < kMinGate ? kMinGate : G;              // (NaN passes through)
+#pragma unroll
       for (int d = 1; d < 64; d *= 2) {
         const double before = __shfl_up(G, d);
         if (lane >= d) G += before;
@@ -118,7 +130,7 @@ __global__ __launch_bounds__(256) void gd_prepare_kernel(GdArgs p) {
       const float ehi = static_cast<float>(left_over), elo = static_cast<float>(left_over - ehi);
       float* vec = reinterpret_cast<float*>(rec + kTBytes<ACT>);
       const float into = exp2_pair(hi, lo);
-      const int row = token(lane);                  // (its own inverse)
+      const int row = token(lane);
       vec[kInto * 64 + row] = into;
       vec[kLast * 64 + row] = exp2_pair(ehi, elo);
       vec[kBeta * 64 + row] = beta;
@@ -127,37 +139,95 @@ __global__ __launch_bounds__(256) void gd_prepare_kernel(GdArgs p) {
       vec[kWhole * 64 + row] = __shfl(into, 63);
       sHi[row] = hi; sLo[row] = lo; sB[row] = beta;
     }
-    __syncthreads();
+    wave_lds();
 
-    // A, the 10 blocks on and below the diagonal.  An entry that is not finite belongs to a token whose state and
-    // whose successors' are not either (the walk sees to those); as a zero it leaves the rows before alone.
-    const uint32_t rows = O::template row_part<RK, false>(lds_address(sK), c16, g);
-    for (int t = w; t < 10; t += 4) {
-      const int ib = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jb = t - ib * (ib + 1) / 2;
-      f32x4_t s = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  #pragma unroll
-      for (int x = 0; x < KT; ++x)
-        s = O::mma(O::row(rows + ib * (16 * RK), 4 * PB * x, 0), O::row(rows + jb * (16 * RK), 4 * PB * x, 0), s);
-      const int j = 16 * jb + c16;
-      const float jhi = sHi[j], jlo = sLo[j], jbeta = sB[j];
-  #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 16 * ib + 4 * g + e;
-        float x = jbeta * (exp2_pair(BACK ? jhi - sHi[i] : sHi[i] - jhi, BACK ? jlo - sLo[i] : sLo[i] - jlo) * s[e]);
-        if (i <= j || !(fabsf(x) < __builtin_huge_valf())) x = 0.0f;
-        sA[i * kRow + j] = x;
+    // A's and the scores' tiles: rows i = 32 t + 8 g + 4 u + e, column j, for i <= j.  Forwards column j = 16 jt + c16 of k and
+    // q; backwards j = 32 two + 8 (c / 4) + 4 one + c % 4 of k, with the rows of k and of q.  An entry of A that is not finite
+    // belongs to a token whose state and whose successors' are not either (the walk sees to those); as a zero it leaves
+    // the rows before alone.
+    auto tile = [&](int t, int j, const f32x4_t (&s1)[2], const f32x4_t (&s2)[2], int x) __attribute__((always_inline)) {
+      const float jhi = sHi[j], jlo = sLo[j];
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i0 = 32 * t + 8 * g + 4 * u;
+        const float4 hi = *reinterpret_cast<const float4*>(sHi + i0), lo = *reinterpret_cast<const float4*>(sLo + i0);
+        const float4 be = *reinterpret_cast<const float4*>(sB + i0);
+        const float ihi[4] = {hi.x, hi.y, hi.z, hi.w}, ilo[4] = {lo.x, lo.y, lo.z, lo.w}, ib[4] = {be.x, be.y, be.z, be.w};
+        float a[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float m = BACK ? exp2_pair(ihi[e] - jhi, ilo[e] - jlo) : exp2_pair(jhi - ihi[e], jlo - ilo[e]);
+          a[e] = ib[e] * (m * s1[u][e]);
+          if (i0 + e >= j || !(fabsf(a[e]) < __builtin_huge_valf())) a[e] = 0.0f;
+          if constexpr (PT > 0) v[4 * u + e] = i0 + e <= j ? s2[u][e] * (p.scale * m) : 0.0f;
+        }
+        if (i0 / 16 <= j / 16)
+          *reinterpret_cast<float4*>(A + block_at(j / 16, i0 / 16) + j % 16 * kRow + i0 % 16) = make_float4(a[0], a[1], a[2], a[3]);
+      }
+      if constexpr (PT > 0) {
+        piece ps[PT];
+        O::template split<PT>(v, ps);
+#pragma unroll
+        for (int m = 0; m < PT; ++m)
+          store_piece(rec + kTBytes<ACT> + kVecs * 256 + (x * PT + m) * kOne + lane * (kOne / 64), ps[m]);
+      }
+    };
+    if constexpr (!BACK) {
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt) {
+        piece kn[KT], qn[KT];
+        load_row(kg, p.ks[1], 16 * jt + c16, kn);
+        if constexpr (PT > 0) load_row(qg, p.qs[1], 16 * jt + c16, qn);
+#pragma unroll
+        for (int t = 0; t <= jt / 2; ++t) {
+          f32x4_t s1[2], s2[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) s1[u] = s2[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int y = 0; y < KT; ++y)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              s1[u] = O::mma(kp[t][u][y], kn[y], s1[u]);
+              if constexpr (PT > 0) s2[u] = O::mma(kp[t][u][y], qn[y], s2[u]);
+            }
+          tile(t, 16 * jt + c16, s1, s2, jt + 2 * t);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        piece qp[2][KT];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) load_row(qg, p.qs[1], 32 * t + 4 * u + perm_row, qp[u]);
+#pragma unroll
+        for (int two = t; two < 2; ++two)
+#pragma unroll
+          for (int one = 0; one < 2; ++one) {
+            f32x4_t s1[2], s2[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) s1[u] = s2[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int y = 0; y < KT; ++y)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                s1[u] = O::mma(kp[t][u][y], kp[two][one][y], s1[u]);
+                s2[u] = O::mma(qp[u][y], kp[two][one][y], s2[u]);
+              }
+            tile(t, 32 * two + 4 * one + perm_row, s1, s2, 2 * two + 2 * t + one);
+          }
       }
     }
-    __syncthreads();
+    wave_lds();
 
-    // the inverses of the diagonal blocks of I + A, one a wave: lane c16 solves for column c16
+    // the inverses of the diagonal blocks of I + A, in place: 16 lanes a block, lane c16 solves for its column
     {
-      const float* a = sA + 16 * w * kRow + 16 * w;
+      float* a = A + (g * (g + 1) / 2 + g) * kBlock;
       float x[16];
-  #pragma unroll
+#pragma unroll
       for (int i = 0; i < 16; ++i) {
         float s = i == c16 ? 1.0f : 0.0f;
-  #pragma unroll
+#pragma unroll
         for (int j4 = 0; j4 < i; j4 += 4) {
           const float4 y = *reinterpret_cast<const float4*>(a + i * kRow + j4);
           s = __builtin_fmaf(-y.x, x[j4], s);
@@ -167,42 +237,48 @@ __global__ __launch_bounds__(256) void gd_prepare_kernel(GdArgs p) {
         }
         x[i] = s;
       }
-      if (g == 0) {
-  #pragma unroll
-        for (int i = 0; i < 16; ++i) sT[(16 * w + i) * kRow + 16 * w + c16] = x[i];
-      } else if (g == 1 && (w & 1) == 0) {            // the zero blocks right of it
-  #pragma unroll
-        for (int i = 0; i < 16; ++i) sT[(16 * w + i) * kRow + 16 * w + 16 + c16] = 0.0f;
-      }
+      wave_lds();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) a[i * kRow + c16] = x[i];
     }
-    __syncthreads();
-    // the blocks below, diagonal by diagonal: T_ij = -T_ii sum over m = j .. i-1 of A_im T_mj
-    for (int d = 1; d < 4; ++d) {
-      if (w < 4 - d) {
-        const int i = w + d, j = w;
-        f32x4_t s = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int m = j; m < i; ++m) s = block_mma(sA, 16 * i, 16 * m, block_rows(sT, 16 * m, 16 * j, g, c16), s, g, c16);
-        const f32x4_t t = block_mma(sT, 16 * i, 16 * i, s, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, g, c16);
-  #pragma unroll
-        for (int e = 0; e < 4; ++e) sT[(16 * i + 4 * g + e) * kRow + 16 * j + c16] = -t[e];
+    wave_lds();
+    // the blocks below, row by row in place: T_ij = -T_ii sum over m = j .. i-1 of A_im T_mj
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      f32x4_t s[3];
+#pragma unroll
+      for (int j = 0; j < i; ++j) {
+        s[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int m = j; m < i; ++m) s[j] = block_mma(A + block_at(i, m), block_rows(A + block_at(m, j), g, c16), s[j], g, c16);
       }
-      __syncthreads();
+      wave_lds();
+#pragma unroll
+      for (int j = 0; j < i; ++j) {
+        const f32x4_t t = block_mma(A + block_at(i, i), s[j], f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, g, c16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) A[block_at(i, j) + (4 * g + e) * kRow + c16] = -t[e];
+      }
+      wave_lds();
     }
 
     // T in operand order: operands 0, 1 are rows 32 t + 8 (c / 4) + 4 u + c % 4 with t = 0, of tokens 0..31; 2, 3
     // those with t = 1 of tokens 0..31; 4, 5 of tokens 32..63
-    for (int x = w; x < kT; x += 4) {
-      const int row = (x < 2 ? 0 : 32) + 8 * (c16 >> 2) + 4 * (x & 1) + (c16 & 3), col = (x < 4 ? 0 : 32) + 8 * g;
-      float v[8];
-  #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = sT[row * kRow + col + e];
-      piece t[kTerms<ACT>];
-      O::template split<kTerms<ACT>>(v, t);
-  #pragma unroll
-      for (int m = 0; m < kTerms<ACT>; ++m)
-        store_piece(rec + (x * kTerms<ACT> + m) * kPieceBytes<ACT> + lane * (kPieceBytes<ACT> / 64), t[m]);
+#pragma unroll
+    for (int x = 0; x < kT; ++x) {
+      const int row = (x < 2 ? 0 : 32) + 4 * (x & 1) + perm_row, ib = row / 16, jb = (x < 4 ? 0 : 2) + (g >> 1);
+      float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      if (jb <= ib) {
+        const float* from = A + (ib * (ib + 1) / 2 + jb) * kBlock + row % 16 * kRow + 8 * (g & 1);
+        const float4 y = reinterpret_cast<const float4*>(from)[0], z = reinterpret_cast<const float4*>(from)[1];
+        v[0] = y.x; v[1] = y.y; v[2] = y.z; v[3] = y.w; v[4] = z.x; v[5] = z.y; v[6] = z.z; v[7] = z.w;
+      }
+      piece t[NT];
+      O::template split<NT>(v, t);
+#pragma unroll
+      for (int m = 0; m < NT; ++m) store_piece(rec + (x * NT + m) * kOne + lane * (kOne / 64), t[m]);
     }
-    __syncthreads();                                  // (the next chunk's K comes where this one's T was read)
+    wave_lds();                                     // (the next chunk's A comes where T was read)
   }
 }
 
@@ -293,59 +369,96 @@ struct ChunkRows {
 //     X = scale P^T D + exp(G_Q - G) K E      Y = T^T X      dV = beta Y
 //     E' = exp(G_Q) E + scale (exp(G) Q)^T D - K^T (beta exp(G) Y)
 // with rows from the chunk's last token to its first, so that T^T and P^T are lower triangular here too.
-enum { kOut, kSave, kBack };
+// kState and kBackState: the pre-pass of a walk in segments, which leaves the state that a segment makes of none (N);
+// kState's further column blocks carry the identity with no values, which makes M, and E' = M E + N.
+enum { kOut, kSave, kBack, kState, kBackState };
 
-template <typename ACT, int KD, int VD, int MOVE, bool ALL, int MODE>
-__global__ __launch_bounds__((4 * VD / kGdColumnTiles<ACT, VD>), 1)
+// A workgroup takes COLUMNS (64 or 128) columns of one (batch row, head, segment), a wave 16 of them.  A chunk's record comes
+// into LDS whole, once a workgroup: T read by every wave for itself kept the loads' unit busy for a quarter of the time.
+
+// Terms of a walk's scores in its chunks' records.
+template <typename ACT, int MODE>
+constexpr int score_terms() {
+  return MODE == kOut ? kOutTerms<ACT> : MODE == kBack || MODE == kBackState ? kTerms<ACT> : 0;
+}
+
+// PR: terms of the scores in the records.
+template <typename ACT, int KD, int COLUMNS, int MOVE, bool ALL, int MODE, int PR>
+__global__ __launch_bounds__(4 * COLUMNS, 2)
 void gd_walk_kernel(GdArgs p) {
-  constexpr bool BACK = MODE == kBack;
-  constexpr int VT = kGdColumnTiles<ACT, VD>;
+  constexpr int kColumns = COLUMNS;
+  constexpr bool BACK = MODE == kBack || MODE == kBackState, STATE = MODE == kState || MODE == kBackState;
+  constexpr bool SCORES = MODE == kOut || BACK;     // q and the scores are needed
+  constexpr int PT = score_terms<ACT, MODE>();
   using O = Op<ACT>;
   using elem = typename O::elem;
   using piece = typename O::piece;
   constexpr bool kF32 = sizeof(elem) == 4;
-  constexpr int NW = VD / 16 / VT, NT = kTerms<ACT>, OT = kOutTerms<ACT>;
-  constexpr int PT = MODE == kSave ? 0 : BACK ? NT : OT;                        // terms of the scores
-  constexpr int RK = KD * static_cast<int>(sizeof(elem)), RV = VD * static_cast<int>(sizeof(elem));   // row bytes
+  constexpr int NW = COLUMNS / 16, NT = kTerms<ACT>, OT = kOutTerms<ACT>;
+  constexpr int RK = KD * static_cast<int>(sizeof(elem)), RV = kColumns * static_cast<int>(sizeof(elem));   // row bytes
   constexpr int KT = KD / 32;                       // pairs of state tiles along K
   constexpr int PB = O::kPiece, kOne = kPieceBytes<ACT>;
-  __shared__ __attribute__((aligned(512))) char sQ[MODE == kSave ? 16 : kQ * RK];
+  __shared__ __attribute__((aligned(512))) char sQ[SCORES ? kQ * RK : 16];
   __shared__ __attribute__((aligned(512))) char sKK[2][kQ * RK];                // k of this chunk and of the next
   __shared__ __attribute__((aligned(512))) char sV[kQ * RV];                    // v, backwards the outputs' gradient
-  __shared__ __attribute__((aligned(512))) char sP[PT ? kT * PT * kOne : 16];   // the scores in operand order
-  __shared__ __attribute__((aligned(512))) float sVec[2][kVecs * 64];
+  // the record (T, vectors, scores), of this chunk and, where there is room, of the next
+  constexpr int kRec = kTBytes<ACT> + kVecs * 256 + (SCORES ? kT * PT * kOne : 0);
+  constexpr bool AHEAD = (SCORES ? 3 : 2) * kQ * RK + kQ * RV + 2 * kRec <= 160 * 1024;
+  __shared__ __attribute__((aligned(512))) char sRec[AHEAD ? 2 : 1][kRec];
 
   const int tid = threadIdx.x, lane0 = tid & 63, w = uniform_int(tid >> 6);
-  const uint32_t pair = blockIdx.x, row_b = pair / static_cast<uint32_t>(p.H);
+  const int K = p.K, V = p.V;
+  // Workgroup ids go round the 8 XCDs: the column blocks of one (batch row, head, segment), which read the same rows of q
+  // and k, are 8 ids apart, on one XCD and its L2 at about the same time.
+  const uint32_t v_blocks = static_cast<uint32_t>((V + kColumns - 1) / kColumns);
+  const uint32_t blocks = v_blocks + (MODE == kState ? (K + kColumns - 1) / kColumns : 0), span = 8 * blocks;
+  const uint32_t group = blockIdx.x / span, in_group = blockIdx.x - group * span, item = group * 8 + in_group % 8;
+  const uint32_t nseg = static_cast<uint32_t>(p.nseg);
+  if (item >= static_cast<uint32_t>(p.batch) * p.H * nseg) return;
+  const uint32_t block = in_group / 8, pair = nseg == 1 ? item : item / nseg, seg = item - pair * nseg;
+  const bool ident = MODE == kState && block >= v_blocks;       // columns of the identity
+  const int col0 = kColumns * static_cast<int>(ident ? block - v_blocks : block), width = (ident ? K : V) - col0;
+  const uint32_t row_b = pair / static_cast<uint32_t>(p.H);
   const int64_t bh = pair, b = row_b;
   const int h = static_cast<int>(pair - row_b * static_cast<uint32_t>(p.H));
-  const int L = static_cast<int>(p.L), len = gd_length(p.lengths, static_cast<int>(p.L), b), K = p.K, V = p.V;
-  const int nchunks = (L + kQ - 1) / kQ, c_live = (len + kQ - 1) / kQ;   // chunks; those that hold a token
+  const int L = static_cast<int>(p.L), len = gd_length(p.lengths, L, b);
+  const int nchunks = (L + kQ - 1) / kQ, live = (len + kQ - 1) / kQ;   // chunks; those that hold a token
+  const int c_begin = static_cast<int>(seg) * p.seg_chunks, c_stop = least(c_begin + p.seg_chunks, nchunks);
+  const int c_end = least(c_stop, live), count = c_end > c_begin ? c_end - c_begin : 0;
+  if (STATE) {                                      // sums that nobody reads: of no chunks, and the last of each walk's
+    if (count == 0 || (BACK ? seg == 0 : c_end == live && !(ident && p.seg_mt))) return;
+  }
 
   ChunkRows<elem, RK, NW, BACK, MOVE, BACK> q_rows_in;
   ChunkRows<elem, RK, NW, true, MOVE, BACK> k_rows_in;
   ChunkRows<elem, RV, NW, false, MOVE, BACK> v_rows_in;
-  if constexpr (MODE != kSave) q_rows_in.start(static_cast<const elem*>(p.q) + b * p.qs[0] + (h / p.qdiv) * p.qs[2], p.qs[1], K, w, lane0);
+  if constexpr (SCORES)
+    q_rows_in.start(static_cast<const elem*>(p.q) + b * p.qs[0] + (h / p.qdiv) * p.qs[2], p.qs[1], K, w, lane0);
   k_rows_in.start(static_cast<const elem*>(p.k) + b * p.ks[0] + (h / p.kdiv) * p.ks[2], p.ks[1], K, w, lane0);
-  v_rows_in.start(static_cast<const elem*>(p.v) + b * p.vs[0] + (h / p.vdiv) * p.vs[2], p.vs[1], V, w, lane0);
-  const char* recs = (BACK ? p.rec_back : p.rec) + bh * nchunks * kRecord<ACT>;
-  auto present = [&](int c) { return len - c * kQ < kQ ? len - c * kQ : kQ; };
+  v_rows_in.start(static_cast<const elem*>(p.v) + b * p.vs[0] + (h / p.vdiv) * p.vs[2] + col0, p.vs[1],
+                  least(width, kColumns), w, lane0);
+  const char* recs = (BACK ? p.rec_back : p.rec) + bh * nchunks * kRecord<ACT, PR>;
+  auto present = [&](int c) { return least(len - c * kQ, kQ); };
   auto ask_k = [&](int c, int lane) __attribute__((always_inline)) {
     k_rows_in.template load<ALL>(sKK[c & 1], c, present(c), w, lane, tid);
-    if (w < 2)                                      // the record's vectors: 2 KB
-      load_to_lds(lds_address(reinterpret_cast<char*>(sVec[c & 1])) + w * 1024,
-                  recs + static_cast<int64_t>(c) * kRecord<ACT> + kTBytes<ACT> + w * 1024 + lane * 16);
+  };
+  auto ask_record = [&](int c, int lane) __attribute__((always_inline)) {
+    const uint32_t to = lds_address(sRec[AHEAD ? c & 1 : 0]);
+    const char* from = recs + static_cast<int64_t>(c) * kRecord<ACT, PR>;
+#pragma unroll
+    for (int i = 0; i < (kRec / 1024 + NW - 1) / NW; ++i)
+      if (kRec / 1024 % NW == 0 || w + i * NW < kRec / 1024) load_to_lds(to + (w + i * NW) * 1024, from, (w + i * NW) * 1024 + lane * 16);
   };
   auto ask_qv = [&](int c, int lane) __attribute__((always_inline)) {
-    if constexpr (MODE != kSave) q_rows_in.template load<ALL>(sQ, c, present(c), w, lane, tid);
-    v_rows_in.template load<ALL>(sV, c, present(c), w, lane, tid);
+    if constexpr (SCORES) q_rows_in.template load<ALL>(sQ, c, present(c), w, lane, tid);
+    if (!ident) v_rows_in.template load<ALL>(sV, c, present(c), w, lane, tid);
   };
   // Waits for this wave's part of chunk c's rows (and for everything else it asked for).
   auto arrived = [&](int c, int n, int lane) __attribute__((always_inline)) {
     __builtin_amdgcn_s_waitcnt(0x0f70);             // vmcnt(0); expcnt and lgkmcnt as they are
     if (n < kQ) {
       k_rows_in.clear(sKK[c & 1], n, w, lane);
-      if constexpr (MODE != kSave) q_rows_in.clear(sQ, n, w, lane);
+      if constexpr (SCORES) q_rows_in.clear(sQ, n, w, lane);
       v_rows_in.clear(sV, n, w, lane);
     }
   };
@@ -353,63 +466,56 @@ void gd_walk_kernel(GdArgs p) {
     if (!ALL) {                                     // columns that the loads leave alone
       k_rows_in.clear(sKK[0], 0, w, lane0);
       k_rows_in.clear(sKK[1], 0, w, lane0);
-      if constexpr (MODE != kSave) q_rows_in.clear(sQ, 0, w, lane0);
+      if constexpr (SCORES) q_rows_in.clear(sQ, 0, w, lane0);
       v_rows_in.clear(sV, 0, w, lane0);
       __builtin_amdgcn_s_waitcnt(0xc07f);           // lgkmcnt(0): before the loads into the same slots
     }
   }
-  const int c_first = BACK ? c_live - 1 : 0, c_step = BACK ? -1 : 1;
-  if (c_live > 0) {
+  const int c_first = BACK ? c_end - 1 : c_begin, c_step = BACK ? -1 : 1;
+  if (count > 0) {
     ask_k(c_first, lane0);
+    if (AHEAD) ask_record(c_first, lane0);
     ask_qv(c_first, lane0);
   }
 
-  // E[vt][t][u][e] is the entry k = 32 t + 8 g + 4 u + e, v = 16 (VT w + vt) + c16
-  const int g0 = lane0 >> 4, c0 = lane0 & 15;
-  f32x4_t E[VT][KT][2];
-  auto there = [&](int vt, int t, int u, int e) {
-    return ALL || (32 * t + 8 * g0 + 4 * u + e < K && 16 * (VT * w + vt) + c0 < V);
+  // E[t][u][e] is the entry k = 32 t + 8 g + 4 u + e, column 16 w + c16 of the block
+  const int g0 = lane0 >> 4, col = 16 * w + (lane0 & 15);
+  f32x4_t E[KT][2];
+  auto there = [&](int t, int u, int e) { return ALL || (32 * t + 8 * g0 + 4 * u + e < K && col < width); };
+  auto place = [&](int t, int u, int e) {           // in a state in memory
+    return static_cast<uint32_t>((32 * t + 8 * g0 + 4 * u + e) * V + col0 + col);
   };
-  auto place = [&](int vt, int t, int u, int e) {
-    return static_cast<uint32_t>((32 * t + 8 * g0 + 4 * u + e) * V + 16 * (VT * w + vt) + c0);
-  };
-  const float* src = p.carry ? p.carry + bh * static_cast<int64_t>(K) * V : nullptr;
-#pragma unroll
-  for (int vt = 0; vt < VT; ++vt)
+  auto each = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) E[vt][t][u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  if (src) {
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-    for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (there(vt, t, u, e)) E[vt][t][u][e] = src[place(vt, t, u, e)];
-  }
-  if (c_live > 0) arrived(c_first, present(c_first), lane0);
-  auto put_state = [&](float* dst) __attribute__((always_inline)) {
-#pragma unroll
-    for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (there(vt, t, u, e)) dst[place(vt, t, u, e)] = E[vt][t][u][e];
+        for (int e = 0; e < 4; ++e) f(t, u, e);
   };
+  const float* src = nullptr;
+  if constexpr (!STATE) {
+    if (nseg > 1) src = p.seg + (bh * nseg + seg) * static_cast<int64_t>(K) * V;
+    else if (p.carry) src = p.carry + bh * static_cast<int64_t>(K) * V;
+  }
+  each([&](int t, int u, int e) { E[t][u][e] = ident && 32 * t + 8 * g0 + 4 * u + e == col0 + col ? 1.0f : 0.0f; });
+  if (src)
+    each([&](int t, int u, int e) {
+      if (there(t, u, e)) E[t][u][e] = src[place(t, u, e)];
+    });
+  auto put_state = [&](float* dst) __attribute__((always_inline)) {
+    each([&](int t, int u, int e) {
+      if (there(t, u, e)) dst[place(t, u, e)] = E[t][u][e];
+    });
+  };
+  if (count > 0) arrived(c_first, present(c_first), lane0);
 
 #pragma unroll 1
-  for (int done = 0, c = c_first; done < c_live; ++done, c += c_step) {
+  for (int done = 0, c = c_first; done < count; ++done, c += c_step) {
     const int n = present(c);
-    const bool more = done + 1 < c_live;
-    if constexpr (MODE != kOut) {                   // the state that enters a stretch of p.every chunks
-      if (BACK ? done == 0 || (c + 1) % p.every == 0 : c % p.every == 0)
+    const bool more = done + 1 < count;
+    if constexpr (MODE == kSave || MODE == kBack) { // the state that enters a stretch of p.every chunks
+      if (BACK ? c + 1 == live || (c + 1) % p.every == 0 : c % p.every == 0)
         put_state(p.kept + (bh * ((nchunks + p.every - 1) / p.every) + c / p.every) * static_cast<int64_t>(K) * V);
     }
     // (opaque, so that the chunk's many LDS and memory addresses are formed here from the lane's number)
@@ -417,264 +523,190 @@ void gd_walk_kernel(GdArgs p) {
     asm volatile("" : "+v"(lane));
     const int g = lane >> 4, c16 = lane & 15;
     barrier_lds();                                  // the tiles of chunk c are complete
-    piece T[kT][NT];
-    {
-      const char* from = recs + static_cast<int64_t>(c) * kRecord<ACT> + lane * (kOne / 64);
-#pragma unroll
-      for (int x = 0; x < kT; ++x)
-#pragma unroll
-        for (int m = 0; m < NT; ++m) load_piece(from + (x * NT + m) * kOne, T[x][m]);
+    if (!AHEAD) ask_record(c, lane);
+    if (more) {
+      ask_k(c + c_step, lane);
+      if (AHEAD) ask_record(c + c_step, lane);
     }
-    if (more) ask_k(c + c_step, lane);
-    const float* vec = sVec[c & 1];
+    const char* rec = sRec[AHEAD ? c & 1 : 0];
+    const float* vec = reinterpret_cast<const float*>(rec + kTBytes<ACT>);
+    const char *t_in = rec + lane * (kOne / 64), *p_in = t_in + kTBytes<ACT> + kVecs * 256;   // operands of T, of the scores
     const uint32_t k_tile = lds_address(sKK[0]) + (c & 1) * (kQ * RK);
-    const uint32_t q_rows = O::template row_part<RK, BACK>(lds_address(sQ), BACK ? 8 * (c16 >> 2) + (c16 & 3) : c16, g);
-    const uint32_t k_rows = O::template row_part<RK, true>(k_tile, 8 * (c16 >> 2) + (c16 & 3), g);
+    const int perm_row = 8 * (c16 >> 2) + (c16 & 3);
+    const uint32_t q_rows = O::template row_part<RK, BACK>(lds_address(sQ), BACK ? perm_row : c16, g);
+    const uint32_t k_rows = O::template row_part<RK, true>(k_tile, perm_row, g);
     auto eight = [&](int which, int t, float (&x)[8]) __attribute__((always_inline)) {   // a vector's tokens 32 t + 8 g ..
       const float4 a = *reinterpret_cast<const float4*>(vec + which * 64 + 32 * t + 8 * g);
       const float4 d = *reinterpret_cast<const float4*>(vec + which * 64 + 32 * t + 8 * g + 4);
       x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = d.x; x[5] = d.y; x[6] = d.z; x[7] = d.w;
     };
+    // rows of the permuted tile (t, u), columns 32 y + 8 g ..
+    auto permuted = [&](uint32_t rows, int t, int u, int y) __attribute__((always_inline)) {
+      return O::row(rows + t * (32 * RK), (4 * PB * y) ^ (u ? swizzle<RK, kF32, true>(4) << 4 : 0), 4 * u * RK);
+    };
 
-    // ---- the scores, 16 rows by 32 tokens an operand.  Forwards operand x holds column j = 16 jt + c16 and tokens
-    // i = 32 t + 8 g + e, q_j.k_i; x = 0..3 are jt = x, t = 0, the others jt = x - 2, t = 1.  Backwards it is a left
-    // operand like T's: rows 32 t' + 8 (c / 4) + 4 u + c % 4, q_i.k_row; x = 0, 1 are t' = t = 0, 2, 3 t' = 1, t = 0,
-    // 4, 5 t' = t = 1, u = x % 2.
-    if constexpr (MODE != kSave) {
-#pragma unroll 1
-      for (int x = w; x < kT; x += NW) {
-        const int jt = x < 4 ? x : x - 2, t = x < 4 ? 0 : 1, two = x < 2 ? 0 : 1, one = x & 1;
-        const int j = BACK ? 32 * two + 8 * (c16 >> 2) + 4 * one + (c16 & 3) : 16 * jt + c16;
-        const uint32_t rows = BACK ? q_rows : k_rows;
-        f32x4_t s[2];
+    // ---- K E (rows token 32 t + 8 g + 4 u + e, column v) and Q E, transposed (rows v, column j = 16 jt + c16).  Products
+    // on different sums follow each other, here and below: one on the last's sum waits for it.
+    f32x4_t R[2][2], acc[4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) s[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int y = 0; y < KT; ++y) {
-          piece right;
-          if constexpr (BACK)
-            right = O::row(k_rows + two * (32 * RK), (4 * PB * y) ^ (one ? swizzle<RK, kF32, true>(4) << 4 : 0), one * (4 * RK));
-          else
-            right = O::row(q_rows + jt * (16 * RK), 4 * PB * y, 0);
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            s[u] = O::mma(O::row(rows + t * (32 * RK), (4 * PB * y) ^ (swizzle<RK, kF32, true>(4 * u) << 4), 4 * u * RK),
-                          right, s[u]);
-        }
-        float hi[8], lo[8], pv[8];
-        eight(kSumHi, t, hi);
-        eight(kSumLo, t, lo);
-        const float jhi = vec[kSumHi * 64 + j], jlo = vec[kSumLo * 64 + j];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float m = BACK ? exp2_pair(hi[e] - jhi, lo[e] - jlo) : exp2_pair(jhi - hi[e], jlo - lo[e]);
-          pv[e] = j >= 32 * t + 8 * g + e ? s[e / 4][e % 4] * (p.scale * m) : 0.0f;
-        }
-        piece ps[PT];
-        O::template split<PT>(pv, ps);
-#pragma unroll
-        for (int m = 0; m < PT; ++m) store_piece(sP + (x * PT + m) * kOne + lane * (kOne / 64), ps[m]);
-      }
-    }
-
-    // ---- K E (rows token 32 t + 8 g + 4 u + e, column v) and Q E, transposed (rows v, column j = 16 jt + c16)
-    f32x4_t R[VT][2][2], acc[VT][4];
-#pragma unroll
-    for (int vt = 0; vt < VT; ++vt) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) R[vt][t][u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int jt = 0; jt < 4; ++jt) acc[vt][jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+    for (int i = 0; i < 4; ++i) acc[i] = R[i / 2][i % 2] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int y = 0; y < KT; ++y) {
-      piece ef[VT][NT];
+      piece ef[NT], kf[4], qf[4];
+      const float x[8] = {E[y][0][0], E[y][0][1], E[y][0][2], E[y][0][3], E[y][1][0], E[y][1][1], E[y][1][2], E[y][1][3]};
+      O::template split<NT>(x, ef);
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) {
-        const float x[8] = {E[vt][y][0][0], E[vt][y][0][1], E[vt][y][0][2], E[vt][y][0][3],
-                            E[vt][y][1][0], E[vt][y][1][1], E[vt][y][1][2], E[vt][y][1][3]};
-        O::template split<NT>(x, ef[vt]);
+      for (int i = 0; i < 4; ++i) {
+        kf[i] = permuted(k_rows, i / 2, i % 2, y);
+        if constexpr (MODE == kOut) qf[i] = O::row(q_rows, 4 * PB * y, 16 * i * RK);
       }
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int m = NT - 1; m >= 0; --m) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const piece kf = O::row(k_rows + t * (32 * RK), (4 * PB * y) ^ (swizzle<RK, kF32, true>(4 * u) << 4), 4 * u * RK);
+        for (int i = 0; i < 4; ++i) R[i / 2][i % 2] = O::mma(kf[i], ef[m], R[i / 2][i % 2]);
+        if constexpr (MODE == kOut) {
+          if (m < OT) {
 #pragma unroll
-          for (int m = NT - 1; m >= 0; --m)
-#pragma unroll
-            for (int vt = 0; vt < VT; ++vt) R[vt][t][u] = O::mma(kf, ef[vt][m], R[vt][t][u]);
-        }
-      if constexpr (MODE == kOut) {
-#pragma unroll
-        for (int jt = 0; jt < 4; ++jt) {
-          const piece qf = O::row(q_rows, 4 * PB * y, 16 * jt * RK);
-#pragma unroll
-          for (int m = OT - 1; m >= 0; --m)
-#pragma unroll
-            for (int vt = 0; vt < VT; ++vt) acc[vt][jt] = O::mma(ef[vt][m], qf, acc[vt][jt]);
+            for (int i = 0; i < 4; ++i) acc[i] = O::mma(ef[m], qf[i], acc[i]);
+          }
         }
       }
     }
     // ---- the wave's own columns of v
-    piece vf[VT][2];
+    piece vf[2];
+    {
+      const uint32_t v_cols = O::template column_part<RV, false>(lds_address(sV), 16 * w, 4, lane);
 #pragma unroll
-    for (int vt = 0; vt < VT; ++vt) {
-      const uint32_t v_cols = O::template column_part<RV, false>(lds_address(sV), 16 * (VT * w + vt), 4, lane);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) vf[vt][t] = O::template column<RV, false>(v_cols, 0, 32 * t * RV);
+      for (int t = 0; t < 2; ++t) vf[t] = ident ? O::zero() : O::template column<RV, false>(v_cols, 0, 32 * t * RV);
     }
-    // (all of T is here before the next loads into LDS are asked for: a partial count of outstanding loads is not
-    // relied on where some go to LDS)
-    __builtin_amdgcn_s_waitcnt(0x0f70);
-#pragma unroll
-    for (int x = 0; x < kT; ++x)
-#pragma unroll
-      for (int m = 0; m < NT; ++m) {
-        if constexpr (kF32) asm volatile("" : "+v"(T[x][m].a.x), "+v"(T[x][m].a.y), "+v"(T[x][m].a.z), "+v"(T[x][m].a.w),
-                                              "+v"(T[x][m].b.x), "+v"(T[x][m].b.y), "+v"(T[x][m].b.z), "+v"(T[x][m].b.w));
-        else asm volatile("" : "+v"(T[x][m].x), "+v"(T[x][m].y), "+v"(T[x][m].z), "+v"(T[x][m].w));
-      }
-    barrier_lds();                                  // the scores are complete; the tiles of q and v are free
+    if (!AHEAD) __builtin_amdgcn_s_waitcnt(0x0f70); // the record is here
+    barrier_lds();                                  // ... of every wave; the tiles of q and v are free
     if constexpr (!BACK) {
       if (more) ask_qv(c + c_step, lane);
     }
 
-    // ---- X = V - exp(G) K E (backwards scale P^T D + exp(G_Q - G) K E), W = T X
+    // ---- X = V - exp(G) K E (backwards scale P^T D + exp(G_Q - G) K E)
     // Forwards, a value that is not finite must not reach earlier tokens' outputs through T's zeros: its column is cut there,
     // its outputs from that token on and its state are NaN.
-    float x[VT][2][8];
+    float x[2][8];
     float odd = 0.0f;
+    f32x4_t Z[2][2];
+    if constexpr (BACK) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) Z[i / 2][i % 2] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int m = NT - 1; m >= 0; --m) {
+        piece pf[kT];
+#pragma unroll
+        for (int i = 0; i < kT; ++i) load_piece(p_in + (i * NT + m) * kOne, pf[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Z[i / 2][i % 2] = O::mma(pf[i], vf[0], Z[i / 2][i % 2]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) Z[1][u] = O::mma(pf[4 + u], vf[1], Z[1][u]);
+      }
+    }
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       float with[8];
       eight(BACK ? kLast : kInto, t, with);
       if constexpr (BACK) {
-        f32x4_t Z[VT][2];
 #pragma unroll
-        for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) Z[vt][u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int from = 0; from <= t; ++from) {
-            piece pf[NT];
-#pragma unroll
-            for (int m = 0; m < NT; ++m)
-              load_piece(sP + ((2 * t + 2 * from + u) * NT + m) * kOne + lane * (kOne / 64), pf[m]);
-#pragma unroll
-            for (int m = NT - 1; m >= 0; --m)
-#pragma unroll
-              for (int vt = 0; vt < VT; ++vt) Z[vt][u] = O::mma(pf[m], vf[vt][from], Z[vt][u]);
-          }
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            x[vt][t][e] = __builtin_fmaf(with[e], R[vt][t][e / 4][e % 4], Z[vt][e / 4][e % 4]);
+        for (int e = 0; e < 8; ++e) x[t][e] = __builtin_fmaf(with[e], R[t][e / 4][e % 4], Z[t][e / 4][e % 4]);
       } else {
-        float beta[8];
+        O::unpack(vf[t], x[t]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[t][e] = __builtin_fmaf(-with[e], R[t][e / 4][e % 4], x[t][e]);
         if constexpr (MODE == kOut) {
+          float beta[8];
           eight(kBeta, t, beta);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) odd = __builtin_fmaf(beta[e], 0.0f, odd);
-        }
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-          O::unpack(vf[vt][t], x[vt][t]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[vt][t][e] = __builtin_fmaf(-with[e], R[vt][t][e / 4][e % 4], x[vt][t][e]);
-            if constexpr (MODE == kOut) odd = __builtin_fmaf(x[vt][t][e], 0.0f, odd);
-          }
+          for (int e = 0; e < 8; ++e) odd = __builtin_fmaf(x[t][e], 0.0f, __builtin_fmaf(beta[e], 0.0f, odd));
         }
       }
     }
     const bool bad = MODE == kOut && __builtin_amdgcn_ballot_w64(odd != odd) != 0;
-    int gone[VT];                                   // first token of the column that is not finite
-#pragma unroll
-    for (int vt = 0; vt < VT; ++vt) gone[vt] = kQ;
+    int gone = kQ;                                  // first token of the column that is not finite
     if (__builtin_expect(bad, 0)) {
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) {
+      for (int t = 0; t < 2; ++t) {
+        float beta[8];
+        eight(kBeta, t, beta);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          float beta[8];
-          eight(kBeta, t, beta);
+        for (int e = 0; e < 8; ++e)
+          if (!(fabsf(x[t][e]) < __builtin_huge_valf()) || !(fabsf(beta[e]) < __builtin_huge_valf()))
+            gone = least(gone, 32 * t + 8 * g + e);
+      }
+      gone = least(gone, __shfl_xor(gone, 16));
+      gone = least(gone, __shfl_xor(gone, 32));
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (!(fabsf(x[vt][t][e]) < __builtin_huge_valf()) || !(fabsf(beta[e]) < __builtin_huge_valf()))
-              gone[vt] = least(gone[vt], 32 * t + 8 * g + e);
-        }
-        gone[vt] = least(gone[vt], __shfl_xor(gone[vt], 16));
-        gone[vt] = least(gone[vt], __shfl_xor(gone[vt], 32));
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int e = 0; e < 8; ++e)
+          if (32 * t + 8 * g + e >= gone) x[t][e] = 0.0f;
+    }
+
+    // ---- W = T X, then U = beta W
+    f32x4_t U[2][2];
+    {
+      piece xf[2][NT];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (32 * t + 8 * g + e >= gone[vt]) x[vt][t][e] = 0.0f;
+      for (int t = 0; t < 2; ++t) O::template split<NT>(x[t], xf[t]);
+      f32x4_t s[kT];
+#pragma unroll
+      for (int i = 0; i < kT; ++i) s[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int m = NT - 1; m >= 0; --m) {           // (the products of terms that count at NT terms, largest last)
+        piece T[kT];
+#pragma unroll
+        for (int i = 0; i < kT; ++i) load_piece(t_in + (i * NT + m) * kOne, T[i]);
+#pragma unroll
+        for (int other = NT - 1 - m; other >= 0; --other)
+#pragma unroll
+          for (int i = 0; i < kT; ++i) s[i] = O::mma(T[i], xf[i / 4][other], s[i]);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        U[0][u] = s[u];
+        U[1][u] = s[2 + u] + s[4 + u];
       }
     }
-    f32x4_t U[VT][2][2];                            // (W, then U)
-    {
-      piece xf[VT][2][NT];
+    if constexpr (MODE == kSave || MODE == kBack) { // kept for the gradients of q and k (every column of the tiles)
+      float* w_out = p.w_out + ((bh * nchunks + c) * kQ) * p.w_stride + col0 + 16 * w + c16;
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) O::template split<NT>(x[vt][t], xf[vt][t]);
-#pragma unroll
-      for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const f32x4_t zero = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-          U[vt][0][u] = mma_terms<O, NT, NT>(T[u], xf[vt][0], zero);
-          U[vt][1][u] = mma_terms<O, NT, NT>(T[4 + u], xf[vt][1], mma_terms<O, NT, NT>(T[2 + u], xf[vt][0], zero));
+        for (int e = 0; e < 8; ++e) {
+          const int row = 32 * t + 8 * g + e;
+          w_out[(BACK ? kQ - 1 - row : row) * p.w_stride] = U[t][e / 4][e % 4];
         }
-    }
-    if constexpr (MODE != kOut) {                   // kept for the gradients of q and k (every column of the tiles)
-      float* w_out = p.w_out + ((bh * nchunks + c) * kQ) * VD + 16 * VT * w + c16;
-#pragma unroll
-      for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int row = 32 * t + 8 * g + e;
-            w_out[(BACK ? kQ - 1 - row : row) * VD + 16 * vt] = U[vt][t][e / 4][e % 4];
-          }
     }
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       float beta[8];
       eight(kBeta, t, beta);
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          U[vt][t][e / 4][e % 4] *= beta[e];
-          if (__builtin_expect(bad, 0)) {
-            if (32 * t + 8 * g + e >= gone[vt]) U[vt][t][e / 4][e % 4] = 0.0f;
-          }
-        }
+      for (int e = 0; e < 8; ++e) U[t][e / 4][e % 4] *= beta[e];
     }
-    if constexpr (BACK) {                           // dV, token by token
-      const int64_t row_stride = static_cast<int64_t>(p.H) * V;
-      const int64_t first = (b * L + static_cast<int64_t>(c) * kQ) * row_stride + static_cast<int64_t>(h) * V;
+    if (__builtin_expect(bad, 0)) {
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) {
-        const int col = 16 * (VT * w + vt) + c16;
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (32 * t + 8 * g + e >= gone) U[t][e / 4][e % 4] = 0.0f;
+    }
+    if constexpr (MODE == kBack) {                  // dV, token by token
+      const int64_t row_stride = static_cast<int64_t>(p.H) * V;
+      const int64_t first = (b * L + static_cast<int64_t>(c) * kQ) * row_stride + static_cast<int64_t>(h) * V + col0;
+      if (ALL || 16 * w + c16 < width) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int at = kQ - 1 - (32 * t + 8 * g + e);
-            if (at >= n || col >= V) continue;
-            const float y = U[vt][t][e / 4][e % 4];
-            if (p.o_f32) static_cast<float*>(p.o)[first + at * row_stride + col] = y;
-            else store_act<ACT>(p.o, first + at * row_stride + col, y);
+            const float y = U[t][e / 4][e % 4];
+            if (at >= n) continue;
+            if (p.o_f32) static_cast<float*>(p.o)[first + at * row_stride + 16 * w + c16] = y;
+            else store_act<ACT>(p.o, first + at * row_stride + 16 * w + c16, y);
           }
       }
     }
@@ -682,141 +714,120 @@ void gd_walk_kernel(GdArgs p) {
     // ---- outputs: exp(G) Q E and the scores' product with U on top
     if constexpr (MODE == kOut) {
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-      const float f = p.scale * vec[kInto * 64 + 16 * jt + c16];
+      for (int jt = 0; jt < 4; ++jt) {
+        const float f = p.scale * vec[kInto * 64 + 16 * jt + c16];
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[vt][jt][e] *= f;
-    }
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      piece uf[VT][OT];
-#pragma unroll
-      for (int vt = 0; vt < VT; ++vt) {
-        const float y[8] = {U[vt][t][0][0], U[vt][t][0][1], U[vt][t][0][2], U[vt][t][0][3],
-                            U[vt][t][1][0], U[vt][t][1][1], U[vt][t][1][2], U[vt][t][1][3]};
-        O::template split<OT>(y, uf[vt]);
+        for (int e = 0; e < 4; ++e) acc[jt][e] *= f;
       }
 #pragma unroll
-      for (int jt = 2 * t; jt < 4; ++jt) {
-        piece pf[OT];
+      for (int t = 0; t < 2; ++t) {
+        piece uf[OT], pf[4][OT];
+        const float y[8] = {U[t][0][0], U[t][0][1], U[t][0][2], U[t][0][3], U[t][1][0], U[t][1][1], U[t][1][2], U[t][1][3]};
+        O::template split<OT>(y, uf);
 #pragma unroll
-        for (int m = 0; m < OT; ++m) load_piece(sP + ((jt + 2 * t) * OT + m) * kOne + lane * (kOne / 64), pf[m]);
+        for (int jt = 2 * t; jt < 4; ++jt)
 #pragma unroll
-        for (int vt = 0; vt < VT; ++vt) acc[vt][jt] = mma_terms<O, OT, OT>(uf[vt], pf, acc[vt][jt]);
+          for (int m = 0; m < OT; ++m) load_piece(p_in + ((jt + 2 * t) * OT + m) * kOne, pf[jt][m]);
+#pragma unroll
+        for (int sum = OT - 1; sum >= 0; --sum)
+#pragma unroll
+          for (int m = 0; m <= sum; ++m)
+#pragma unroll
+            for (int jt = 2 * t; jt < 4; ++jt) acc[jt] = O::mma(uf[m], pf[jt][sum - m], acc[jt]);
       }
-    }
-    if (__builtin_expect(bad, 0)) {
-#pragma unroll
-      for (int vt = 0; vt < VT; ++vt)
+      if (__builtin_expect(bad, 0)) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {               // (the outputs' rows are the lanes' columns of x)
-          const int from = __shfl(gone[vt], 4 * g + e);
+          const int from = __shfl(gone, 4 * g + e);
 #pragma unroll
           for (int jt = 0; jt < 4; ++jt)
-            if (16 * jt + c16 >= from) acc[vt][jt][e] = __builtin_nanf("");
+            if (16 * jt + c16 >= from) acc[jt][e] = __builtin_nanf("");
         }
-    }
+      }
     }
 
-    // ---- the state: exp(G_Q) E + K^T (exp(G_Q - G) U)
+    // ---- the state: exp(G_Q) E + K^T (exp(G_Q - G) U), backwards exp(G_Q) E - K^T (exp(G) U) + Q^T (scale exp(G) D)
     const float whole = vec[kWhole * 64];
-#pragma unroll
-    for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-      for (int y = 0; y < KT; ++y)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) E[vt][y][u][e] *= whole;
+    each([&](int t, int u, int e) { E[t][u][e] *= whole; });
     const uint32_t k_cols = O::template column_part<RK, true>(k_tile, 0, 8, lane);
     const uint32_t q_cols = O::template column_part<RK, true>(lds_address(sQ), 0, 8, lane);   // (backwards)
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      float with[8];
+      float with[8], y[8];
       eight(BACK ? kInto : kLast, t, with);
-      piece wf[VT][NT], df[VT][NT];
+      piece wf[NT], df[NT];
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) {
-        float y[8];
+      for (int e = 0; e < 8; ++e) y[e] = (BACK ? -with[e] : with[e]) * U[t][e / 4][e % 4];
+      O::template split<NT>(y, wf);
+      if constexpr (BACK) {
+        O::unpack(vf[t], y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = (BACK ? -with[e] : with[e]) * U[vt][t][e / 4][e % 4];
-        O::template split<NT>(y, wf[vt]);
-        if constexpr (BACK) {
-          O::unpack(vf[vt][t], y);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] *= p.scale * with[e];
-          O::template split<NT>(y, df[vt]);
-        }
+        for (int e = 0; e < 8; ++e) y[e] *= p.scale * with[e];
+        O::template split<NT>(y, df);
       }
 #pragma unroll
-      for (int y = 0; y < KT; ++y)
+      for (int z = 0; z < KT; z += 2) {             // four tiles at a time
+        piece kf[4], qf[4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const piece kf =
-              O::template column<RK, true>(k_cols, (4 * PB * y) ^ O::half_flip(u), 32 * t * RK + O::half_offset(u));
+        for (int i = 0; i < 4; ++i) {
+          const int at = (4 * PB * (z + i / 2)) ^ O::half_flip(i % 2), offset = 32 * t * RK + O::half_offset(i % 2);
+          kf[i] = O::template column<RK, true>(k_cols, at, offset);
+          if constexpr (BACK) qf[i] = O::template column<RK, true>(q_cols, at, offset);
+        }
 #pragma unroll
-          for (int m = NT - 1; m >= 0; --m)
+        for (int m = NT - 1; m >= 0; --m) {
 #pragma unroll
-            for (int vt = 0; vt < VT; ++vt) E[vt][y][u] = O::mma(kf, wf[vt][m], E[vt][y][u]);
+          for (int i = 0; i < 4; ++i) E[z + i / 2][i % 2] = O::mma(kf[i], wf[m], E[z + i / 2][i % 2]);
           if constexpr (BACK) {
-            const piece qf =
-                O::template column<RK, true>(q_cols, (4 * PB * y) ^ O::half_flip(u), 32 * t * RK + O::half_offset(u));
 #pragma unroll
-            for (int m = NT - 1; m >= 0; --m)
-#pragma unroll
-              for (int vt = 0; vt < VT; ++vt) E[vt][y][u] = O::mma(qf, df[vt][m], E[vt][y][u]);
+            for (int i = 0; i < 4; ++i) E[z + i / 2][i % 2] = O::mma(qf[i], df[m], E[z + i / 2][i % 2]);
           }
         }
+      }
     }
     if constexpr (BACK) {
       barrier_lds();                                // the tiles of q and of the outputs' gradient are free
       if (more) ask_qv(c + c_step, lane);
     }
     if (__builtin_expect(bad, 0)) {
-#pragma unroll
-      for (int vt = 0; vt < VT; ++vt)
-        if (gone[vt] < kQ) {
-#pragma unroll
-          for (int y = 0; y < KT; ++y)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) E[vt][y][u][e] = __builtin_nanf("");
-        }
+      if (gone < kQ) each([&](int t, int u, int e) { E[t][u][e] = __builtin_nanf(""); });
     }
     arrived(c + c_step, more ? present(c + c_step) : kQ, lane);
 
+    // ---- the output rows to memory: lane (g, c) has 4 columns of token 16 jt + c
     if constexpr (MODE == kOut) {
-      // ---- the output rows to memory: lane (g, c) has 4 columns of token 16 jt + c
       auto four = [](const f32x4_t& a) __attribute__((always_inline)) {
         if constexpr (kF32) return make_float4(a[0], a[1], a[2], a[3]);
         else return make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
       };
       const int64_t row_stride = static_cast<int64_t>(p.H) * V;
-      elem* out = static_cast<elem*>(p.o) + (b * L + static_cast<int64_t>(c) * kQ) * row_stride + static_cast<int64_t>(h) * V;
+      const int v0 = 16 * w + 4 * g;
+      if (n == kQ && p.o_vec) {                     // a uniform address, the lane's offset, 16 rows' bytes
+        char* rows = static_cast<char*>(p.o) + ((b * L + static_cast<int64_t>(c) * kQ) * row_stride + static_cast<int64_t>(h) * V + col0) *
+                                                   static_cast<int64_t>(sizeof(elem));
+        const uint32_t step = static_cast<uint32_t>(row_stride) * sizeof(elem), off = c16 * step + v0 * sizeof(elem);
+        if (ALL || v0 < width) {
+#pragma unroll
+          for (int jt = 0; jt < 4; ++jt) *reinterpret_cast<decltype(four(acc[0]))*>(rows + (off + jt * 16 * step)) = four(acc[jt]);
+        }
+        continue;
+      }
+      elem* out = static_cast<elem*>(p.o) + (b * L + static_cast<int64_t>(c) * kQ) * row_stride + static_cast<int64_t>(h) * V +
+                  col0 + v0;
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
         const int row = 16 * jt + c16;
         if (c * kQ + row >= L) continue;
         elem* o = out + row * row_stride;
-        if (row >= n) {
+        if (row >= n) acc[jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        if (p.o_vec) {
+          if (ALL || v0 < width) *reinterpret_cast<decltype(four(acc[0]))*>(o) = four(acc[jt]);
+        } else {
 #pragma unroll
-          for (int vt = 0; vt < VT; ++vt) acc[vt][jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-          const int v0 = 16 * (VT * w + vt) + 4 * g;
-          if (p.o_vec) {
-            if (ALL || v0 < V) *reinterpret_cast<decltype(four(acc[0][0]))*>(o + v0) = four(acc[vt][jt]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (v0 + e >= V) continue;
-              if constexpr (kF32) o[v0 + e] = acc[vt][jt][e];
-              else o[v0 + e] = to_bf16(acc[vt][jt][e]);
-            }
+          for (int e = 0; e < 4; ++e) {
+            if (v0 + e >= width) continue;
+            if constexpr (kF32) o[e] = acc[jt][e];
+            else o[e] = to_bf16(acc[jt][e]);
           }
         }
       }
@@ -824,47 +835,143 @@ void gd_walk_kernel(GdArgs p) {
   }
 
   // tokens that are not there: zeros (forwards those of the last chunk have theirs)
-  if constexpr (MODE != kSave) {
-    for (int z = BACK ? len / kQ : c_live; z < nchunks; ++z) {
-      for (int i = tid; i < kQ * V; i += 64 * NW) {
-        const int64_t token = static_cast<int64_t>(z) * kQ + i / V;
+  if constexpr (MODE == kOut || MODE == kBack) {
+    const int from = BACK ? len / kQ : live;
+    for (int z = from > c_begin ? from : c_begin; z < c_stop; ++z) {
+      for (int i = tid; i < kQ * kColumns; i += 64 * NW) {
+        const int64_t token = static_cast<int64_t>(z) * kQ + i / kColumns;
         if (token >= L) break;
-        if (token < len) continue;
-        const int64_t at = ((b * L + token) * p.H + h) * V + i % V;
+        if (token < len || i % kColumns >= width) continue;
+        const int64_t at = ((b * L + token) * p.H + h) * V + col0 + i % kColumns;
         if (BACK && p.o_f32) static_cast<float*>(p.o)[at] = 0.0f;
         else static_cast<elem*>(p.o)[at] = elem(0);
       }
     }
   }
-  if (p.fin) put_state(p.fin + bh * static_cast<int64_t>(K) * V);
+  if constexpr (STATE) {
+    if (!ident) {
+      put_state(p.seg + (bh * nseg + seg) * static_cast<int64_t>(K) * V);
+    } else {                                        // whole tiles of M, and its transpose for the backward walk
+      float* m = p.seg_m + (bh * nseg + seg) * static_cast<int64_t>(KD * KD);
+      float* mt = p.seg_mt ? p.seg_mt + (bh * nseg + seg) * static_cast<int64_t>(KD * KD) : nullptr;
+      each([&](int t, int u, int e) {
+        const int k = 32 * t + 8 * g0 + 4 * u + e;
+        if (COLUMNS > KD && col >= KD) return;
+        m[k * KD + col0 + col] = E[t][u][e];
+        if (mt) mt[(col0 + col) * KD + k] = E[t][u][e];
+      });
+    }
+  } else if (p.fin) {
+    // forwards the segment of the last token that is there has the state after it, backwards the first segment
+    if (BACK ? seg == 0 : live == 0 ? seg == 0 : count > 0 && c_end == live) put_state(p.fin + bh * static_cast<int64_t>(K) * V);
+  }
 }
 
-template <typename ACT, int KD, int VD, int MOVE, bool ALL, int MODE>
+// The states that enter the segments, over what each made of none: forwards S = M S + N from the first on, backwards
+// F = M^T F + N from the last.  A wave owns 16 columns, a state's as above, through all segments; float32 products.
+template <int KD, bool BACK>
+__global__ __launch_bounds__(64) void gd_chain_kernel(GdArgs p) {
+  using O = Op<ActF32>;
+  constexpr int KT = KD / 32;
+  const int lane = threadIdx.x, g = lane >> 4, c16 = lane & 15, K = p.K, V = p.V, nseg = p.nseg;
+  const int64_t bh = blockIdx.x;
+  const int col = 16 * blockIdx.y + c16;
+  const int len = gd_length(p.lengths, static_cast<int>(p.L), blockIdx.x / static_cast<uint32_t>(p.H));
+  const int live = (len + kQ - 1) / kQ, count = (live + p.seg_chunks - 1) / p.seg_chunks;   // segments with tokens
+  f32x4_t S[KT][2];
+  auto each = [&](auto f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = 32 * t + 8 * g + 4 * u + e;
+          f(t, u, e, k < K && col < V, k * V + col);
+        }
+  };
+  const float* carry = p.carry ? p.carry + bh * static_cast<int64_t>(K) * V : nullptr;
+  each([&](int t, int u, int e, bool in, int at) { S[t][u][e] = carry && in ? carry[at] : 0.0f; });
+  const float* ms = (BACK ? p.seg_mt : p.seg_m) + bh * nseg * static_cast<int64_t>(KD * KD);
+  float* segs = p.seg + bh * nseg * static_cast<int64_t>(K) * V;
+  for (int i = 0; i < (count > 0 ? count : 1); ++i) {
+    const int s = BACK && count > 0 ? count - 1 - i : i;
+    float* at_s = segs + s * static_cast<int64_t>(K) * V;
+    f32x4_t next[KT][2];
+    const bool on = i + 1 < count;                  // (the last one's result is the walk's to find)
+    if (on) each([&](int t, int u, int e, bool in, int at) { next[t][u][e] = in ? at_s[at] : 0.0f; });
+    each([&](int t, int u, int e, bool in, int at) {
+      if (in) at_s[at] = S[t][u][e];
+    });
+    if (!on) break;
+    const float* m = ms + s * static_cast<int64_t>(KD * KD) + (8 * (c16 >> 2) + (c16 & 3)) * KD + 8 * g;
+#pragma unroll
+    for (int y = 0; y < KT; ++y) {
+      const float x[8] = {S[y][0][0], S[y][0][1], S[y][0][2], S[y][0][3], S[y][1][0], S[y][1][1], S[y][1][2], S[y][1][3]};
+      const F8 right = O::pack(x);
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          F8 left;
+          load_piece(reinterpret_cast<const char*>(m + (32 * t + 4 * u) * KD + 32 * y), left);
+          next[t][u] = O::mma(left, right, next[t][u]);
+        }
+    }
+    each([&](int t, int u, int e, bool, int) { S[t][u][e] = next[t][u][e]; });
+  }
+}
+
+template <typename ACT, int KD, int COLUMNS, int MOVE, bool ALL, int MODE, int PR>
+void launch_walk(const GdArgs& a, hipStream_t s) {
+  const int64_t items = (a.batch * a.H * a.nseg + 7) / 8 * 8;
+  const int64_t blocks = (a.V + COLUMNS - 1) / COLUMNS + (MODE == kState ? (a.K + COLUMNS - 1) / COLUMNS : 0);
+  hipLaunchKernelGGL((gd_walk_kernel<ACT, KD, COLUMNS, MOVE, ALL, MODE, PR>), dim3(static_cast<unsigned>(items * blocks)),
+                     dim3(4 * COLUMNS), 0, s, a);
+}
+
+template <typename ACT, int KD, int COLUMNS, int MOVE, bool ALL, int MODE>
 void launch_gd_t(const GdArgs& a, hipStream_t s) {
-  const int64_t nch = (a.L + kQ - 1) / kQ;
-  const int64_t all = a.batch * a.H * nch, most = 1 << 22;       // (a launch's threads are fewer than 2^32)
-  const dim3 chunks(static_cast<unsigned>(all < most ? all : most)), pairs(static_cast<unsigned>(a.batch * a.H));
-  hipLaunchKernelGGL((gd_prepare_kernel<ACT, KD, MOVE, MODE == kBack>), chunks, dim3(256), 0, s, a);
-  hipLaunchKernelGGL((gd_walk_kernel<ACT, KD, VD, MOVE, ALL, MODE>), pairs, dim3(4 * VD / kGdColumnTiles<ACT, VD>), 0, s, a);
+  constexpr bool BACK = MODE == kBack;
+  constexpr int PR = score_terms<ACT, MODE>();
+  if (a.nseg > 1) {
+    launch_walk<ACT, KD, COLUMNS, MOVE, ALL, BACK ? kBackState : kState, PR>(a, s);
+    const dim3 grid(static_cast<unsigned>(a.batch * a.H), static_cast<unsigned>((a.V + 15) / 16));
+    hipLaunchKernelGGL((gd_chain_kernel<KD, BACK>), grid, dim3(64), 0, s, a);
+  }
+  launch_walk<ACT, KD, COLUMNS, MOVE, ALL, MODE, PR>(a, s);
+}
+
+// Columns of a workgroup.  128 where every CU has work then: the rows of q and k and the record are read once for them.  64
+// where that leaves each workgroup a CU of its own, and for rows that do not move as whole vectors.
+bool wide(const GdArgs& a, int KD) {
+  return a.move == 16 && a.K == KD && a.V == 128 && a.batch * a.H * a.nseg > 128;
 }
 
 template <int MODE>
-void launch_gd_mode(const GdArgs& a, Dt dt, hipStream_t s) {
-  auto go = [&](auto act, auto kd, auto vd) {
+void launch_gd_mode(const GdArgs& args, Dt dt, hipStream_t s) {
+  GdArgs a = args;
+  const int64_t nch = (a.L + kQ - 1) / kQ;
+  a.seg_chunks = static_cast<int>((nch + a.nseg - 1) / a.nseg);
+  auto go = [&](auto act, auto kd) {
     using ACT = decltype(act);
-    constexpr int KD = decltype(kd)::value, VD = decltype(vd)::value;
-    if (a.move == 16 && a.K == KD && a.V == VD) launch_gd_t<ACT, KD, VD, 16, true, MODE>(a, s);
-    else if (a.move == 16) launch_gd_t<ACT, KD, VD, 16, false, MODE>(a, s);
-    else if (ACT::kBytes == 4 || a.move == 4) launch_gd_t<ACT, KD, VD, 4, false, MODE>(a, s);
-    else if constexpr (ACT::kBytes == 2) launch_gd_t<ACT, KD, VD, 0, false, MODE>(a, s);
+    constexpr int KD = decltype(kd)::value;
+    auto prepare = [&](auto move) {
+      const int64_t all = (a.batch * a.H * nch + 3) / 4, most = 1 << 22;   // (a launch's threads are fewer than 2^32)
+      hipLaunchKernelGGL((gd_prepare_kernel<ACT, KD, decltype(move)::value, MODE == kBack, score_terms<ACT, MODE>()>),
+                         dim3(static_cast<unsigned>(all < most ? all : most)), dim3(256), 0, s, a);
+    };
+    if (a.move == 16) prepare(std::integral_constant<int, 16>{});
+    else prepare(std::integral_constant<int, 0>{});
+    if (wide(a, KD)) launch_gd_t<ACT, KD, 128, 16, true, MODE>(a, s);
+    else if (a.move == 16 && a.K == KD && a.V % 64 == 0) launch_gd_t<ACT, KD, 64, 16, true, MODE>(a, s);
+    else if (a.move == 16) launch_gd_t<ACT, KD, 64, 16, false, MODE>(a, s);
+    else if (ACT::kBytes == 4 || a.move == 4) launch_gd_t<ACT, KD, 64, 4, false, MODE>(a, s);
+    else if constexpr (ACT::kBytes == 2) launch_gd_t<ACT, KD, 64, 0, false, MODE>(a, s);
   };
   auto shape = [&](auto act) {
-    constexpr std::integral_constant<int, 64> n64;
-    constexpr std::integral_constant<int, 128> n128;
-    if (a.K > 64 && a.V > 64) go(act, n128, n128);
-    else if (a.K > 64) go(act, n128, n64);
-    else if (a.V > 64) go(act, n64, n128);
-    else go(act, n64, n64);
+    if (a.K > 64) go(act, std::integral_constant<int, 128>{});
+    else go(act, std::integral_constant<int, 64>{});
   };
   if (dt == Dt::BF16) shape(ActBF16{});
   else shape(ActF32{});
@@ -872,7 +979,28 @@ void launch_gd_mode(const GdArgs& a, Dt dt, hipStream_t s) {
 
 }  // namespace
 
-int64_t gd_record_bytes(Dt dt) { return dt == Dt::BF16 ? kRecord<ActBF16> : kRecord<ActF32>; }
+GdRecords gd_records(Dt dt) {
+  auto of = [](auto act) {
+    using ACT = decltype(act);
+    return GdRecords{kRecord<ACT, score_terms<ACT, kOut>()>, kRecord<ACT, score_terms<ACT, kSave>()>,
+                     kRecord<ACT, score_terms<ACT, kBack>()>};
+  };
+  return dt == Dt::BF16 ? of(ActBF16{}) : of(ActF32{});
+}
+
+constexpr int kSegTarget = 256;
+
+// Segments per sequence.  The pre-pass walks V + K columns where the main pass walks V, so segments are worth it only
+// where few workgroups walk long sequences: up to 2 workgroups a CU, at least 4 of them, each 4 chunks or longer.  The count is
+// then derived back from the segment length, so that no segment is without a chunk.
+int gd_segments(int64_t batch, int64_t L, int64_t H, int64_t V) {
+  const int64_t workgroups = batch * H, nch = (L + kQ - 1) / kQ;
+  int64_t s = kSegTarget / (workgroups > 0 ? workgroups : 1);
+  if (s > nch / 4) s = nch / 4;
+  if (s < 4) return 1;
+  const int64_t per = (nch + s - 1) / s;
+  return static_cast<int>((nch + per - 1) / per);
+}
 
 hipError_t launch_gd(const GdArgs& a, Dt dt, hipStream_t s) {
   launch_gd_mode<kOut>(a, dt, s);

@@ -21,8 +21,8 @@ template <typename ACT>
 constexpr int kPieceBytes = ACT::kBytes == 2 ? 1024 : 2048;   // an operand of 64 lanes
 template <typename ACT>
 constexpr int kTBytes = kT * kTerms<ACT> * kPieceBytes<ACT>;
-template <typename ACT>
-constexpr int kRecord = kTBytes<ACT> + kVecs * 256;    // a chunk's T and vectors
+template <typename ACT, int PT>
+constexpr int kRecord = kTBytes<ACT> + kVecs * 256 + kT * PT * kPieceBytes<ACT>;   // a chunk's T, vectors and scores in PT terms
 
 // 2^(hi + lo) for |lo| far below 1: the sum of logarithms is kept as a float32 pair, so that a factor
 // exp(G_i - G_j) is as good as float32 where the sums themselves are in the hundreds.
@@ -59,10 +59,6 @@ __device__ __forceinline__ f32x4_t mma_terms(const typename O::piece (&a)[NA], c
       if (sum - i >= 0 && sum - i < NB) c = O::mma(a[i], b[sum - i], c);
   return c;
 }
-
-// A wave owns 16 VT columns.  VT = 2 at bfloat16, V > 64: each LDS read serves two columns' tiles.
-template <typename ACT, int VD>
-constexpr int kGdColumnTiles = 1;
 
 }  // namespace
 }  // namespace ssm

@@ -85,9 +85,9 @@ __device__ __forceinline__ void stage_terms(char* tiles, const float* src, int t
 
 // BACK: the second kernel, which adds the backward part of dk.
 template <typename ACT, int KD, int VD, bool BACK>
-__global__ __launch_bounds__((4 * KD / kGdColumnTiles<ACT, KD>), 1)
+__global__ __launch_bounds__(4 * KD, 1)
 void gd_qk_kernel(GdGradArgs p) {
-  constexpr int VT = kGdColumnTiles<ACT, KD>;
+  constexpr int VT = 1;
   using O = Op<ACT>;
   using elem = typename O::elem;
   using piece = typename O::piece;
@@ -184,7 +184,7 @@ void gd_qk_kernel(GdGradArgs p) {
     stage_terms<ACT, VD, NT, PW, THREADS>(sW[0], p.w + ((bh * nchunks + c) * kQ) * VD, tid);
     stage_terms<ACT, VD, NT, PY, THREADS>(sY[0], p.y + ((bh * nchunks + c) * kQ) * VD, tid);
     {
-      const float* from = reinterpret_cast<const float*>(p.rec + (bh * nchunks + c) * kRecord<ACT> + kTBytes<ACT>);
+      const float* from = reinterpret_cast<const float*>(p.rec + (bh * nchunks + c) * kRecord<ACT, 0> + kTBytes<ACT>);
       for (int i = tid; i < kVecs * 64; i += THREADS) vec[i] = from[i];
     }
     // the wave's own columns of k (and of q): tokens 32 t + 8 g + e of column c16
@@ -523,7 +523,7 @@ void gd_qk_kernel(GdGradArgs p) {
 template <typename ACT, int KD, int VD>
 void launch_qk_t(const GdGradArgs& a, hipStream_t s) {
   const int64_t nch = (a.L + kQ - 1) / kQ, stretches = (nch + a.every - 1) / a.every;
-  const dim3 grid(static_cast<unsigned>(a.batch * a.H * stretches)), block(4 * KD / kGdColumnTiles<ACT, KD>);
+  const dim3 grid(static_cast<unsigned>(a.batch * a.H * stretches)), block(4 * KD);
   hipLaunchKernelGGL((gd_qk_kernel<ACT, KD, VD, false>), grid, block, 0, s, a);
   hipLaunchKernelGGL((gd_qk_kernel<ACT, KD, VD, true>), grid, block, 0, s, a);
 }

@@ -356,23 +356,38 @@ ssm_status ssm_linear_attention_step(const float* state_in, float* state_out, co
 
 namespace {
 
-// Workspace of a gated delta call: the chunks' records.
+// Workspace of a gated delta call: the chunks' records, and of sequences in segments their states and matrices.
 struct GdPlan {
-  uint64_t rec_bytes = 0;
+  int nseg = 1;
+  uint64_t rec = 0, seg = 0, mat = 0;
   uint64_t total = 0;
 };
 
-bool gd_plan(int64_t batch, int64_t L, int64_t H, ssm_dtype dt, GdPlan* p) {
+bool gd_plan(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V, int64_t record, GdPlan* p) {
   if (batch == 0 || L == 0 || H == 0) return true;
-  const int64_t nch = (L + 63) / 64;
-  if (!bytes_of(static_cast<uint64_t>(ssm::gd_record_bytes(dt_of(dt))), &p->rec_bytes, batch, H, nch)) return false;
-  p->total = up256(p->rec_bytes);
+  const int64_t nch = (L + 63) / 64, side = K > 64 ? 128 : 64;
+  p->nseg = ssm::gd_segments(batch, L, H, V);
+  if (!bytes_of(static_cast<uint64_t>(record), &p->rec, batch, H, nch) ||
+      (p->nseg > 1 && (!bytes_of(4, &p->seg, batch, H, p->nseg, K, V) || !bytes_of(4, &p->mat, batch, H, p->nseg, side, side))))
+    return false;
+  p->total = up256(p->rec) + up256(p->seg) + up256(p->mat);
   return p->total <= kMaxBytes;
 }
 
+// Hands out a workspace piece by piece (none for no bytes).
+struct Taker {
+  char* at;
+  char* operator()(uint64_t bytes) {
+    char* p = at;
+    at += up256(bytes);
+    return bytes ? p : nullptr;
+  }
+  float* floats(uint64_t bytes) { return reinterpret_cast<float*>((*this)(bytes)); }
+};
+
 // ... of its gradient: the records of both walks, their rows of w and y, their states, and float32 parts.
 struct GdBwdPlan {
-  GdPlan fwd;
+  GdPlan fwd, back;
   uint64_t rows = 0, kept = 0;        // of one walk
   uint64_t dk = 0, dq = 0, dv = 0;    // dk's parts always, the others' of shared heads
   uint64_t total = 0;
@@ -380,14 +395,15 @@ struct GdBwdPlan {
 
 bool gd_bwd_plan(int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hv, int64_t K, int64_t V, ssm_dtype dt,
                  GdBwdPlan* p) {
-  if (!gd_plan(batch, L, H, dt, &p->fwd)) return false;
+  const ssm::GdRecords r = ssm::gd_records(dt_of(dt));
+  if (!gd_plan(batch, L, H, K, V, r.save, &p->fwd) || !gd_plan(batch, L, H, K, V, r.back, &p->back)) return false;
   if (batch == 0 || L == 0 || H == 0) return true;
   const int64_t nch = (L + 63) / 64, every = ssm::gd_every(batch, L, H);
   if (!bytes_of(4, &p->rows, batch, H, nch, 64, V > 64 ? 128 : 64) ||
       !bytes_of(4, &p->kept, batch, H, (nch + every - 1) / every, K, V) || !bytes_of(4, &p->dk, batch, L, H, K) ||
       (Hq != H && !bytes_of(4, &p->dq, batch, L, H, K)) || (Hv != H && !bytes_of(4, &p->dv, batch, L, H, V)))
     return false;
-  p->total = 2 * (p->fwd.total + up256(p->rows) + up256(p->kept)) + up256(p->dk) + up256(p->dq) + up256(p->dv);
+  p->total = p->fwd.total + p->back.total + 2 * (up256(p->rows) + up256(p->kept)) + up256(p->dk) + up256(p->dq) + up256(p->dv);
   return p->total <= kMaxBytes;
 }
 
@@ -414,7 +430,7 @@ extern "C" {
 size_t ssm_gated_delta_workspace_size(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V, ssm_dtype dt) {
   GdPlan p;
   if (check_gd_sizes(batch, L, H, H, H, H, K, V, dt) != SSM_OK) return 0;
-  return gd_plan(batch, L, H, dt, &p) ? p.total : 0;
+  return gd_plan(batch, L, H, K, V, ssm::gd_records(dt_of(dt)).out, &p) ? p.total : 0;
 }
 
 ssm_status ssm_gated_delta_fwd(const void* q, const void* k, const void* v, const int64_t* q_strides,
@@ -432,7 +448,7 @@ ssm_status ssm_gated_delta_fwd(const void* q, const void* k, const void* v, cons
   if (!make_view<3>(q_strides, {batch, L, Hq}, K, e, &t.q) || !make_view<3>(k_strides, {batch, L, Hk}, K, e, &t.k) ||
       !make_view<3>(v_strides, {batch, L, Hv}, V, e, &t.v) || !bytes_of(e, &out_bytes, batch, L, H, V) ||
       !bytes_of(4, &state_bytes, batch, H, K, V) || !bytes_of(4, &gate_bytes, batch, L, H) ||
-      !gd_plan(batch, L, H, dt, &plan))
+      !gd_plan(batch, L, H, K, V, ssm::gd_records(dt_of(dt)).out, &plan))
     return SSM_ERR_INVALID_ARG;
   if (out_bytes && (!q || !k || !v || !g || !beta || !out)) return SSM_ERR_INVALID_ARG;
   if (!aligned(q, e) || !aligned(k, e) || !aligned(v, e) || !aligned(out, e) || !aligned(g, 4) || !aligned(beta, 4) ||
@@ -456,7 +472,11 @@ ssm_status ssm_gated_delta_fwd(const void* q, const void* k, const void* v, cons
   for (int i = 0; i < 3; ++i) { a.qs[i] = t.q.stride[i]; a.ks[i] = t.k.stride[i]; a.vs[i] = t.v.stride[i]; }
   a.qdiv = static_cast<int>(H / Hq); a.kdiv = static_cast<int>(H / Hk); a.vdiv = static_cast<int>(H / Hv);
   a.g = g; a.beta = beta; a.lengths = lengths; a.carry = initial_state; a.fin = final_state; a.o = out;
-  a.rec = static_cast<char*>(workspace);
+  Taker take{static_cast<char*>(workspace)};
+  a.rec = take(plan.rec);
+  a.seg = take.floats(plan.seg);
+  a.seg_m = take.floats(plan.mat);
+  a.nseg = plan.nseg;
   a.batch = batch; a.L = L; a.H = static_cast<int>(H); a.K = static_cast<int>(K); a.V = static_cast<int>(V);
   a.scale = scale;
   a.move = least(least(row_move(q, t.q, K, e), row_move(k, t.k, K, e)), row_move(v, t.v, V, e));
@@ -518,12 +538,7 @@ ssm_status ssm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
   if (L == 0)
     return dinitial_state ? from_hip(ssm::launch_la_copy_state(dinitial_state, dfinal_state, batch * H * K * V, s))
                           : SSM_OK;
-  char* at = static_cast<char*>(workspace);
-  auto take = [&](uint64_t bytes) {
-    char* p = at;
-    at += up256(bytes);
-    return bytes ? p : nullptr;
-  };
+  Taker take{static_cast<char*>(workspace)};
   ssm::GdArgs a;
   a.q = q; a.k = k; a.v = v;
   for (int i = 0; i < 3; ++i) { a.qs[i] = t.q.stride[i]; a.ks[i] = t.k.stride[i]; a.vs[i] = t.v.stride[i]; }
@@ -532,22 +547,28 @@ ssm_status ssm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
   a.batch = batch; a.L = L; a.H = static_cast<int>(H); a.K = static_cast<int>(K); a.V = static_cast<int>(V);
   a.scale = scale;
   a.every = ssm::gd_every(batch, L, H);
-  a.rec = take(plan.fwd.rec_bytes);
-  a.rec_back = take(plan.fwd.rec_bytes);
-  a.w_out = reinterpret_cast<float*>(take(plan.rows));
-  a.kept = reinterpret_cast<float*>(take(plan.kept));
+  a.nseg = plan.fwd.nseg;
+  a.rec = take(plan.fwd.rec);
+  a.rec_back = take(plan.back.rec);
+  a.seg_m = take.floats(plan.fwd.mat);
+  a.seg_mt = take.floats(plan.fwd.mat);
+  a.seg = take.floats(plan.fwd.seg);
+  a.w_out = take.floats(plan.rows);
+  a.w_stride = V > 64 ? 128 : 64;
+  a.kept = take.floats(plan.kept);
   a.move = least(row_move(k, t.k, K, e), row_move(v, t.v, V, e));
   ssm::GdArgs r = a;
   r.v = dout;
   for (int i = 0; i < 3; ++i) r.vs[i] = t.d.stride[i];
   r.vdiv = 1;
   r.carry = dfinal_state; r.fin = dinitial_state;
-  r.w_out = reinterpret_cast<float*>(take(plan.rows));
-  r.kept = reinterpret_cast<float*>(take(plan.kept));
+  r.seg = take.floats(plan.fwd.seg);
+  r.w_out = take.floats(plan.rows);
+  r.kept = take.floats(plan.kept);
   r.move = least(least(row_move(q, t.q, K, e), row_move(k, t.k, K, e)), row_move(dout, t.d, V, e));
-  float* dk_part = reinterpret_cast<float*>(take(plan.dk));
-  float* dq_part = reinterpret_cast<float*>(take(plan.dq));
-  float* dv_part = reinterpret_cast<float*>(take(plan.dv));
+  float* dk_part = take.floats(plan.dk);
+  float* dq_part = take.floats(plan.dq);
+  float* dv_part = take.floats(plan.dv);
   r.o = dv_part ? static_cast<void*>(dv_part) : dv;
   r.o_f32 = dv_part != nullptr;
   hipError_t err = ssm::launch_gd_walks(a, r, dt_of(dt), s);

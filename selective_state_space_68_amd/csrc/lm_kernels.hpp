@@ -90,9 +90,13 @@ struct GdArgs {
   void* o = nullptr;                                     // [batch][L][H][V]
   int o_f32 = 0;                                         // (the gradient of a shared head of v) o is float32
   char *rec = nullptr, *rec_back = nullptr;              // a record for each chunk of each (batch row, head)
-  float* w_out = nullptr;                                // gradient walks: [batch * H][chunks][64][V as a tile has it]
+  float* w_out = nullptr;                                // gradient walks: [batch * H][chunks][64][w_stride]
+  int w_stride = 0;                                      // V in whole blocks of 64
   float* kept = nullptr;                                 // ... the state before every `every` chunks, [batch * H][..][K * V]
   int every = 1;
+  int nseg = 1, seg_chunks = 0;                          // segments of a sequence, and their chunks (set by the launch)
+  float* seg = nullptr;                                  // [batch * H][nseg][K * V]: states entering the segments
+  float *seg_m = nullptr, *seg_mt = nullptr;             // [batch * H][nseg][64 or 128 squared]; mt where a gradient needs it
   int64_t batch = 0, L = 0;
   int H = 0, K = 0, V = 0;
   float scale = 1.0f;
@@ -138,7 +142,11 @@ struct GdStepArgs {
 };
 hipError_t launch_gd_step(const GdStepArgs& a, Dt dt, hipStream_t s);
 
-int64_t gd_record_bytes(Dt dt);
+struct GdRecords {
+  int64_t out, save, back;                               // bytes of a chunk's record: forward pass, the gradient's walks
+};
+GdRecords gd_records(Dt dt);
+int gd_segments(int64_t batch, int64_t L, int64_t H, int64_t V);
 hipError_t launch_gd(const GdArgs& a, Dt dt, hipStream_t s);
 // The two walks of the gradient: forwards (v, carry: the inputs'), then backwards (v: the outputs' gradient, carry: the
 // final state's, o: dv, fin: the initial state's).
