@@ -12,14 +12,13 @@
 // g: a_t scales everything that passes from before t to t and after, so with r_j = exp(G_j) the state's scale, S / r,
 // r q and v / r carry all of it: d loss / d G_j = q_j.dq_j - v_j.dv_j, and dg_t is its sum over j >= t.  Summed over a
 // stretch only, onto <F, E> at its end: the sum over a long sequence would lose what a fast decay leaves of it.
-// v_j.dv_j = beta_j v_j.y_j = y_j.u_j - k_j.(the second part of dk_j), all of which is at hand.
 //
-// A workgroup walks one stretch; a wave owns 16 or 32 columns of E^T (of K), so that nothing is summed over waves but
-// the tokens' scalars.  Rows of D, W and Y lie in LDS (W and Y as terms, split once a workgroup).  q and k are
-// needed as a wave's own columns alone and come straight from memory.
+// A workgroup walks one stretch; a wave owns 16 columns of E^T (of K), so that only the tokens' scalars are summed over
+// waves.  Rows of D, W and Y lie in LDS, W and Y as terms, split once a workgroup; their dot products y.w and y.v are
+// taken on the way in.  A chunk's rows are asked for while the one before is worked on.
 //
-// Roundings (bfloat16 activations): forwards 24-bit operands, as g's and beta's gradients are float32; backwards, of
-// which only dk's bfloat16 sees anything, 16 bits.
+// Roundings (bfloat16 activations): what g's float32 gradient sees (dq, with the states that it is formed from) comes from
+// 24-bit operands; what only dk's bfloat16 sees from 16 bits.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -33,74 +32,57 @@ namespace {
 
 constexpr int kMostEvery = 16;
 
-// 64 rows of RB bytes into an LDS tile by 16 bytes a thread; rows past n and columns past `cols` are zeros.
-template <typename ELEM, int RB, bool PERM, int THREADS>
-__device__ __forceinline__ void stage_rows(char* tile, const ELEM* base, int64_t stride, int n, int cols, bool vec, int tid) {
-  constexpr int kSlots = RB / 16, kPer = 16 / sizeof(ELEM);
-  constexpr bool kF32 = sizeof(ELEM) == 4;
-  static_assert(kQ * kSlots % THREADS == 0, "");
-#pragma unroll
-  for (int j = 0; j < kQ * kSlots / THREADS; ++j) {
-    const int i = tid + j * THREADS, row = i / kSlots, slot = i % kSlots;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (row < n) {
-      const ELEM* at = base + row * stride + slot * kPer;
-      if (vec) {
-        if (slot * kPer < cols) x = *reinterpret_cast<const uint4*>(at);
-      } else {
-        ELEM v[kPer];
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) v[e] = slot * kPer + e < cols ? at[e] : ELEM(0);
-        x = __builtin_bit_cast(uint4, v);
-      }
-    }
-    *reinterpret_cast<uint4*>(tile + row * RB + ((slot ^ swizzle<RB, kF32, PERM>(row)) << 4)) = x;
-  }
-}
-
-// A float32 [64][WD] matrix into NT tiles of its terms.
-template <typename ACT, int WD, int NT, bool PERM, int THREADS>
-__device__ __forceinline__ void stage_terms(char* tiles, const float* src, int tid) {
-  using O = Op<ACT>;
-  constexpr int RB = WD * ACT::kBytes;
-  if constexpr (ACT::kBytes == 4) {
-    stage_rows<float, RB, PERM, THREADS>(tiles, src, WD, kQ, WD, true, tid);
+// Eight values of a row, of which `left` are there.
+template <typename ACT>
+__device__ __forceinline__ typename Op<ACT>::piece load8(const void* base, int64_t at, int left, bool vec) {
+  using elem = typename Op<ACT>::elem;
+  typename Op<ACT>::piece p = Op<ACT>::zero();
+  const elem* from = static_cast<const elem*>(base) + at;
+  if (vec) {
+    if (left > 0) load_piece(reinterpret_cast<const char*>(from), p);
   } else {
-    constexpr int kSlots = WD / 8;
-    static_assert(kQ * kSlots % THREADS == 0, "");
+    elem v[8];
 #pragma unroll
-    for (int j = 0; j < kQ * kSlots / THREADS; ++j) {
-      const int i = tid + j * THREADS, row = i / kSlots, slot = i % kSlots;
-      const float4 a = *reinterpret_cast<const float4*>(src + row * WD + slot * 8);
-      const float4 b = *reinterpret_cast<const float4*>(src + row * WD + slot * 8 + 4);
-      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      typename O::piece p[NT];
-      O::template split<NT>(v, p);
-#pragma unroll
-      for (int m = 0; m < NT; ++m)
-        *reinterpret_cast<uint4*>(tiles + m * (kQ * RB) + row * RB + ((slot ^ swizzle<RB, false, PERM>(row)) << 4)) = p[m];
-    }
+    for (int e = 0; e < 8; ++e) v[e] = e < left ? from[e] : elem(0);
+    p = __builtin_bit_cast(typename Op<ACT>::piece, v);
   }
+  return p;
+}
+// ... to columns 8 slot .. of an LDS tile's row.
+template <int RB, bool PERM>
+__device__ __forceinline__ void put8(char* tile, int row, int slot, const uint4& p) {
+  *reinterpret_cast<uint4*>(tile + row * RB + ((slot ^ swizzle<RB, false, PERM>(row)) << 4)) = p;
+}
+template <int RB, bool PERM>
+__device__ __forceinline__ void put8(char* tile, int row, int slot, const F8& p) {
+  const int flip = swizzle<RB, true, PERM>(row);
+  *reinterpret_cast<float4*>(tile + row * RB + (((2 * slot) ^ flip) << 4)) = p.a;
+  *reinterpret_cast<float4*>(tile + row * RB + (((2 * slot + 1) ^ flip) << 4)) = p.b;
 }
 
 // BACK: the second kernel, which adds the backward part of dk.
 template <typename ACT, int KD, int VD, bool BACK>
-__global__ __launch_bounds__(4 * KD, 1)
+__global__ __launch_bounds__(4 * KD, 2)
 void gd_qk_kernel(GdGradArgs p) {
-  constexpr int VT = 1;
   using O = Op<ACT>;
   using elem = typename O::elem;
   using piece = typename O::piece;
   constexpr bool kF32 = sizeof(elem) == 4;
-  constexpr int NW = KD / 16 / VT, THREADS = 64 * NW, NT = BACK ? kOutTerms<ACT> : kTerms<ACT>;
-  constexpr int RV = VD * static_cast<int>(sizeof(elem)), KT = VD / 32, PB = O::kPiece, kOne = kPieceBytes<ACT>;
+  constexpr int NW = KD / 16, THREADS = 64 * NW;
+  constexpr int OT = kOutTerms<ACT>, NT = BACK ? OT : kTerms<ACT>;      // terms of Y and N2; of W, E and N1
+  constexpr int RV = VD * static_cast<int>(sizeof(elem)), RK = KD * static_cast<int>(sizeof(elem));
+  constexpr int KT = VD / 32, PB = O::kPiece, kOne = kPieceBytes<ACT>;
   constexpr bool PW = !BACK, PY = BACK;             // whose rows are read as permuted ones
+  constexpr bool TILES = !kF32;                     // q and k by LDS (float32: no room; the waves read their own columns)
   __shared__ __attribute__((aligned(512))) char sD[kQ * RV];
   __shared__ __attribute__((aligned(512))) char sW[NT][kQ * RV];
-  __shared__ __attribute__((aligned(512))) char sY[NT][kQ * RV];
-  __shared__ __attribute__((aligned(512))) char sN[2][kT * NT * kOne];
+  __shared__ __attribute__((aligned(512))) char sY[OT][kQ * RV];
+  __shared__ __attribute__((aligned(512))) char sK[TILES ? kQ * RK : 16];
+  __shared__ __attribute__((aligned(512))) char sQ[TILES && BACK ? kQ * RK : 16];
+  __shared__ __attribute__((aligned(512))) char sN1[kT * NT * kOne];
+  __shared__ __attribute__((aligned(512))) char sN2[kT * OT * kOne];
   __shared__ __attribute__((aligned(16))) float vec[kVecs * 64];
-  __shared__ float sSum[NW][kQ], sDiag[kQ], sAll[BACK ? 1 : kMostEvery * kQ];
+  __shared__ float sSum[NW][kQ], sDot[2][kQ], sAll[BACK ? 1 : kMostEvery * kQ];
 
   const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6), g = lane >> 4, c16 = lane & 15;
   const int L = static_cast<int>(p.L), K = p.K, V = p.V;
@@ -113,6 +95,7 @@ void gd_qk_kernel(GdGradArgs p) {
   const int c_begin = static_cast<int>(s) * p.every, c_end = least(c_begin + p.every, c_live);
   const elem* qg = static_cast<const elem*>(p.q) + b * p.qs[0] + (h / p.qdiv) * p.qs[2];
   const elem* kg = static_cast<const elem*>(p.k) + b * p.ks[0] + (h / p.kdiv) * p.ks[2];
+  const elem* vg = static_cast<const elem*>(p.v) + b * p.vs[0] + (h / p.vdiv) * p.vs[2];
   const elem* dg = static_cast<const elem*>(p.d) + b * p.ds[0] + h * p.ds[2];
   const int64_t out_row = static_cast<int64_t>(p.H) * K;
   const int64_t out_base = b * L * out_row + static_cast<int64_t>(h) * K;
@@ -140,271 +123,352 @@ void gd_qk_kernel(GdGradArgs p) {
   }
   if (c_begin >= c_end) return;
 
-  // E[vt][y][u][e] is the entry v = 32 y + 8 g + 4 u + e, k = 16 (VT w + vt) + c16 (backwards of the gradient F)
-  f32x4_t E[VT][KT][2];
-  auto there = [&](int vt, int y, int u, int e) {
-    return 16 * (VT * w + vt) + c16 < K && 32 * y + 8 * g + 4 * u + e < V;
+  // ---- a chunk's rows, 8 columns at a time by the threads in turn, in registers on their way to LDS
+  constexpr int kV8 = VD / 8, kN = kQ * kV8 / THREADS, kK8 = KD / 8, kNK = kQ * kK8 / THREADS;
+  struct Rows {
+    F8 w[kN], y[kN];
+    piece d[kN], v[BACK ? 1 : kN], k[TILES ? kNK : 1], q[TILES && BACK ? kNK : 1];
+    float vec[(kVecs * 64 + THREADS - 1) / THREADS];
+  } in;
+  auto ask = [&](int c) __attribute__((always_inline)) {
+    const int n = least(len - c * kQ, kQ);
+    const int64_t t0 = static_cast<int64_t>(c) * kQ, rows = (bh * nchunks + c) * kQ;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int at = tid + i * THREADS, row = at / kV8, slot = at % kV8, left = row < n ? V - 8 * slot : 0;
+      load_piece(reinterpret_cast<const char*>(p.w + (rows + row) * VD + 8 * slot), in.w[i]);
+      load_piece(reinterpret_cast<const char*>(p.y + (rows + row) * VD + 8 * slot), in.y[i]);
+      in.d[i] = load8<ACT>(dg, (t0 + row) * p.ds[1] + 8 * slot, left, p.d_vec);
+      if constexpr (!BACK) in.v[i] = load8<ACT>(vg, (t0 + row) * p.vs[1] + 8 * slot, left, p.v_vec);
+    }
+    if constexpr (TILES) {
+#pragma unroll
+      for (int i = 0; i < kNK; ++i) {
+        const int at = tid + i * THREADS, row = at / kK8, slot = at % kK8, left = row < n ? K - 8 * slot : 0;
+        in.k[i] = load8<ACT>(kg, (t0 + row) * p.ks[1] + 8 * slot, left, p.k_vec);
+        if constexpr (BACK) in.q[i] = load8<ACT>(qg, (t0 + row) * p.qs[1] + 8 * slot, left, p.q_vec);
+      }
+    }
+    const float* from = reinterpret_cast<const float*>(p.rec + (bh * nchunks + c) * kRecord<ACT, 0> + kTBytes<ACT>);
+#pragma unroll
+    for (int i = 0; i < (kVecs * 64 + THREADS - 1) / THREADS; ++i) in.vec[i] = from[least(tid + i * THREADS, kVecs * 64 - 1)];
   };
-  auto place = [&](int vt, int y, int u, int e) {
-    return static_cast<uint32_t>((16 * (VT * w + vt) + c16) * V + 32 * y + 8 * g + 4 * u + e);
+  auto store = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int at = tid + i * THREADS, row = at / kV8, slot = at % kV8;
+      float x[8], y[8];
+      Op<ActF32>::unpack(in.w[i], x);
+      Op<ActF32>::unpack(in.y[i], y);
+      piece t[NT], o[OT];
+      O::template split<NT>(x, t);
+      O::template split<OT>(y, o);
+#pragma unroll
+      for (int m = 0; m < NT; ++m) put8<RV, PW>(sW[m], row, slot, t[m]);
+#pragma unroll
+      for (int m = 0; m < OT; ++m) put8<RV, PY>(sY[m], row, slot, o[m]);
+      put8<RV, BACK>(sD, row, slot, in.d[i]);
+      if constexpr (!BACK) {                        // y.w and y.v
+        float v[8], yw = 0.0f, yv = 0.0f;
+        O::unpack(in.v[i], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          yw = __builtin_fmaf(y[e], x[e], yw);
+          yv = __builtin_fmaf(y[e], v[e], yv);
+        }
+#pragma unroll
+        for (int d = 1; d < kV8; d *= 2) {
+          yw += __shfl_xor(yw, d);
+          yv += __shfl_xor(yv, d);
+        }
+        if (slot == 0) {
+          sDot[0][row] = yw;
+          sDot[1][row] = yv;
+        }
+      }
+    }
+    if constexpr (TILES) {
+#pragma unroll
+      for (int i = 0; i < kNK; ++i) {
+        const int at = tid + i * THREADS, row = at / kK8, slot = at % kK8;
+        put8<RK, false>(sK, row, slot, in.k[i]);
+        if constexpr (BACK) put8<RK, false>(sQ, row, slot, in.q[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < (kVecs * 64 + THREADS - 1) / THREADS; ++i)
+      if (tid + i * THREADS < kVecs * 64) vec[tid + i * THREADS] = in.vec[i];
+  };
+  auto chunk_of = [&](int done) { return BACK ? c_end - 1 - done : c_begin + done; };
+  ask(chunk_of(0));
+
+  // E[y][u][e] is the entry v = 32 y + 8 g + 4 u + e, k = 16 w + c16 (backwards of the gradient F)
+  const int col = 16 * w + c16;
+  f32x4_t E[KT][2];
+  auto each = [&](auto f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int y = 0; y < KT; ++y)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int v = 32 * y + 8 * g + 4 * u + e;
+          f(y, u, e, col < K && v < V, static_cast<uint32_t>(col * V + v));
+        }
   };
   {
     const float* src = (BACK ? p.kept_f : p.kept_e) + (bh * stretches + s) * static_cast<int64_t>(K) * V;
-#pragma unroll
-    for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-      for (int y = 0; y < KT; ++y)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) E[vt][y][u][e] = there(vt, y, u, e) ? src[place(vt, y, u, e)] : 0.0f;
+    each([&](int y, int u, int e, bool there, uint32_t at) { E[y][u][e] = there ? src[at] : 0.0f; });
   }
   const uint32_t tile_d = lds_address(sD), tile_w = lds_address(sW[0]), tile_y = lds_address(sY[0]);
   const int perm_row = 8 * (c16 >> 2) + (c16 & 3);
   const uint32_t d_rows = O::template row_part<RV, BACK>(tile_d, BACK ? perm_row : c16, g);
   const uint32_t w_rows = O::template row_part<RV, PW>(tile_w, BACK ? c16 : perm_row, g);
   const uint32_t y_rows = O::template row_part<RV, PY>(tile_y, BACK ? perm_row : c16, g);
-  // rows 16 jt + c16, or of the permuted tile (t, u)
-  auto natural = [&](uint32_t rows, int jt, int y, int m) { return O::row(rows + jt * (16 * RV), 4 * PB * y, m * (kQ * RV)); };
-  auto permuted = [&](uint32_t rows, int t, int u, int y, int m) {
-    return O::row(rows + t * (32 * RV), (4 * PB * y) ^ (swizzle<RV, kF32, true>(4 * u) << 4), 4 * u * RV + m * (kQ * RV));
+  // rows 16 jt + c16, or of the permuted tile (t, u), of term m
+  auto natural = [&](uint32_t rows, int jt, int y, int m) __attribute__((always_inline)) {
+    return O::row(rows + jt * (16 * RV), 4 * PB * y, m * (kQ * RV));
+  };
+  auto permuted = [&](uint32_t rows, int t, int u, int y, int m) __attribute__((always_inline)) {
+    return O::row(rows + t * (32 * RV), (4 * PB * y) ^ (u ? swizzle<RV, kF32, true>(4) << 4 : 0), 4 * u * RV + m * (kQ * RV));
   };
   auto eight = [&](int which, int t, float (&x)[8]) __attribute__((always_inline)) {
     const float4 a = *reinterpret_cast<const float4*>(vec + which * 64 + 32 * t + 8 * g);
     const float4 d = *reinterpret_cast<const float4*>(vec + which * 64 + 32 * t + 8 * g + 4);
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = d.x; x[5] = d.y; x[6] = d.z; x[7] = d.w;
   };
+  const f32x4_t zero = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
 #pragma unroll 1
   for (int done = 0; done < c_end - c_begin; ++done) {
-    const int c = BACK ? c_end - 1 - done : c_begin + done;
+    const int c = chunk_of(done);
     const int n = least(len - c * kQ, kQ);
     const int64_t t0 = static_cast<int64_t>(c) * kQ;
-    stage_rows<elem, RV, BACK, THREADS>(sD, dg + t0 * p.ds[1], p.ds[1], n, V, p.d_vec, tid);
-    stage_terms<ACT, VD, NT, PW, THREADS>(sW[0], p.w + ((bh * nchunks + c) * kQ) * VD, tid);
-    stage_terms<ACT, VD, NT, PY, THREADS>(sY[0], p.y + ((bh * nchunks + c) * kQ) * VD, tid);
-    {
-      const float* from = reinterpret_cast<const float*>(p.rec + (bh * nchunks + c) * kRecord<ACT, 0> + kTBytes<ACT>);
-      for (int i = tid; i < kVecs * 64; i += THREADS) vec[i] = from[i];
-    }
+    store();
+    __syncthreads();
+    if (done + 1 < c_end - c_begin) ask(chunk_of(done + 1));
     // the wave's own columns of k (and of q): tokens 32 t + 8 g + e of column c16
-    piece kf[VT][2], qf[VT][2];
-    auto columns = [&](const elem* base, int64_t stride, piece (&out)[VT][2]) __attribute__((always_inline)) {
+    piece kf[2], qf[2];
+    if constexpr (TILES) {
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) {
-        const int col = 16 * (VT * w + vt) + c16;
+      for (int t = 0; t < 2; ++t) {
+        kf[t] = O::template column<RK, false>(O::template column_part<RK, false>(lds_address(sK), 16 * w, 4, lane), 0, 32 * t * RK);
+        if constexpr (BACK)
+          qf[t] = O::template column<RK, false>(O::template column_part<RK, false>(lds_address(sQ), 16 * w, 4, lane), 0, 32 * t * RK);
+      }
+    } else {
+      auto columns = [&](const elem* base, int64_t stride, piece (&out)[2]) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          elem v[8];
+          elem x[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int row = 32 * t + 8 * g + e;
-            v[e] = row < n && col < K ? base[(t0 + row) * stride + col] : elem(0);
+            const elem y = base[(t0 + least(row, n - 1)) * stride + least(col, K - 1)];
+            x[e] = row < n && col < K ? y : elem(0);
           }
-          out[vt][t] = __builtin_bit_cast(piece, v);
+          out[t] = __builtin_bit_cast(piece, x);
         }
-      }
-    };
-    columns(kg, p.ks[1], kf);
-    if constexpr (BACK) columns(qg, p.qs[1], qf);
-    __syncthreads();
+      };
+      columns(kg, p.ks[1], kf);
+      if constexpr (BACK) columns(qg, p.qs[1], qf);
+    }
 
-    // ---- N1 and N2 in operand order.  Forwards as the scores: column j = 16 jt + c16, tokens i = 32 t + 8 g + e.
-    // Backwards column i, tokens j; i in the first half takes both halves of j, i in the second the second.
+    // ---- N1 and N2 in operand order, 16 rows by 32 tokens an operand.  Forwards as the scores: column j = 16 jt + c16, tokens
+    // i = 32 t + 8 g + e.  Backwards column i, tokens j; i in the first half takes both halves of j, i in the second the
+    // second.
 #pragma unroll 1
-    for (int z = w; z < 2 * kT; z += NW) {
-      const int second = z >= kT, x = second ? z - kT : z;
+    for (int x = w; x < kT; x += NW) {
       const int jt = x < 4 ? x : BACK ? x - 4 : x - 2, t = BACK ? (x < 4 ? 1 : 0) : (x < 4 ? 0 : 1);
-      f32x4_t a[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) a[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      f32x4_t a1[2] = {zero, zero}, a2[2] = {zero, zero};
 #pragma unroll
       for (int y = 0; y < KT; ++y) {
-        piece right[NT];
-        if (BACK || second) {                       // W, or Y
-#pragma unroll
-          for (int m = 0; m < NT; ++m) right[m] = natural(BACK ? w_rows : y_rows, jt, y, m);
-        } else {
-          right[0] = natural(d_rows, jt, y, 0);
-        }
+        piece wr[2][NT], yr[2][OT], dr[2];          // (of the permuted rows two tiles, of the others one)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          if constexpr (BACK) {
-            if (second) {
-              piece left[NT];
+          if (BACK) {
+            dr[u] = permuted(d_rows, t, u, y, 0);
 #pragma unroll
-              for (int m = 0; m < NT; ++m) left[m] = permuted(y_rows, t, u, y, m);
-              a[u] = mma_terms<O, NT, NT>(left, right, a[u]);
-            } else {
-              const piece left = permuted(d_rows, t, u, y, 0);
-#pragma unroll
-              for (int m = NT - 1; m >= 0; --m) a[u] = O::mma(left, right[m], a[u]);
-            }
+            for (int m = 0; m < OT; ++m) yr[u][m] = permuted(y_rows, t, u, y, m);
           } else {
-            piece left[NT];
 #pragma unroll
-            for (int m = 0; m < NT; ++m) left[m] = permuted(w_rows, t, u, y, m);
-            if (second) {
-              a[u] = mma_terms<O, NT, NT>(left, right, a[u]);
-            } else {
-#pragma unroll
-              for (int m = NT - 1; m >= 0; --m) a[u] = O::mma(left[m], right[0], a[u]);
-            }
+            for (int m = 0; m < NT; ++m) wr[u][m] = permuted(w_rows, t, u, y, m);
           }
         }
+        if (BACK) {
+#pragma unroll
+          for (int m = 0; m < NT; ++m) wr[0][m] = natural(w_rows, jt, y, m);
+        } else {
+          dr[0] = natural(d_rows, jt, y, 0);
+#pragma unroll
+          for (int m = 0; m < OT; ++m) yr[0][m] = natural(y_rows, jt, y, m);
+        }
+#pragma unroll
+        for (int m = NT - 1; m >= 0; --m) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) a1[u] = BACK ? O::mma(dr[u], wr[0][m], a1[u]) : O::mma(wr[u][m], dr[0], a1[u]);
+#pragma unroll
+          for (int o = OT - 1 - m; o >= 0; --o)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) a2[u] = BACK ? O::mma(yr[u][o], wr[0][m], a2[u]) : O::mma(wr[u][m], yr[0][o], a2[u]);
+        }
       }
-      const int col = 16 * jt + c16;                // forwards j, backwards i
-      float hi[8], lo[8], beta[8], v[8];
+      const int cc = 16 * jt + c16;                 // forwards j, backwards i
+      float hi[8], lo[8], beta[8], v1[8], v2[8];
       eight(kSumHi, t, hi);
       eight(kSumLo, t, lo);
       eight(kBeta, t, beta);
-      const float chi = vec[kSumHi * 64 + col], clo = vec[kSumLo * 64 + col], cbeta = vec[kBeta * 64 + col];
+      const float chi = vec[kSumHi * 64 + cc], clo = vec[kSumLo * 64 + cc], cbeta = vec[kBeta * 64 + cc];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int row = 32 * t + 8 * g + e;
         const float m = BACK ? exp2_pair(hi[e] - chi, lo[e] - clo) : exp2_pair(chi - hi[e], clo - lo[e]);
-        const float raw = a[e / 4][e % 4];
-        const bool in = BACK ? (second ? row > col : row >= col) : (second ? row < col : row <= col);
-        if (!BACK && second && row == col) sDiag[col] = raw;
-        const float f = second ? -(beta[e] * cbeta) * m : p.scale * (BACK ? cbeta : beta[e]) * m;
-        v[e] = in ? raw * f : 0.0f;
+        const float mi = m * (BACK ? cbeta : beta[e]), mj = BACK ? beta[e] : cbeta;     // beta of u_i, of y_j
+        v1[e] = (BACK ? row >= cc : row <= cc) ? a1[e / 4][e % 4] * (p.scale * mi) : 0.0f;
+        v2[e] = (BACK ? row > cc : row < cc) ? a2[e / 4][e % 4] * -(mj * mi) : 0.0f;
       }
-      piece out[NT];
-      O::template split<NT>(v, out);
+      piece o1[NT], o2[OT];
+      O::template split<NT>(v1, o1);
+      O::template split<OT>(v2, o2);
 #pragma unroll
-      for (int m = 0; m < NT; ++m) store_piece(sN[second] + (x * NT + m) * kOne + lane * (kOne / 64), out[m]);
+      for (int m = 0; m < NT; ++m) store_piece(sN1 + (x * NT + m) * kOne + lane * (kOne / 64), o1[m]);
+#pragma unroll
+      for (int m = 0; m < OT; ++m) store_piece(sN2 + (x * OT + m) * kOne + lane * (kOne / 64), o2[m]);
     }
 
-    // ---- the state's part, rows k, column j = 16 jt + c16: acc of D (and of Y), backwards of W
-    f32x4_t acc[VT][4], acy[VT][4];
+    // ---- the state's part, rows k, column j = 16 jt + c16: acc of D and acy of Y, backwards acc of W
+    f32x4_t acc[4], acy[4];
 #pragma unroll
-    for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-      for (int jt = 0; jt < 4; ++jt) acc[vt][jt] = acy[vt][jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int jt = 0; jt < 4; ++jt) acc[jt] = acy[jt] = zero;
 #pragma unroll
     for (int y = 0; y < KT; ++y) {
-      piece ef[VT][NT];
+      piece ef[NT];
+      const float x[8] = {E[y][0][0], E[y][0][1], E[y][0][2], E[y][0][3], E[y][1][0], E[y][1][1], E[y][1][2], E[y][1][3]};
+      O::template split<NT>(x, ef);
+      if constexpr (BACK) {
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) {
-        const float x[8] = {E[vt][y][0][0], E[vt][y][0][1], E[vt][y][0][2], E[vt][y][0][3],
-                            E[vt][y][1][0], E[vt][y][1][1], E[vt][y][1][2], E[vt][y][1][3]};
-        O::template split<NT>(x, ef[vt]);
-      }
+        for (int m = NT - 1; m >= 0; --m) {
+          piece r[4];
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt) {
-        piece r[NT];
+          for (int jt = 0; jt < 4; ++jt) r[jt] = natural(w_rows, jt, y, m);
 #pragma unroll
-        for (int m = 0; m < NT; ++m) r[m] = natural(BACK ? w_rows : y_rows, jt, y, m);
-        if constexpr (BACK) {
+          for (int o = NT - 1 - m; o >= 0; --o)
 #pragma unroll
-          for (int vt = 0; vt < VT; ++vt) acc[vt][jt] = mma_terms<O, NT, NT>(ef[vt], r, acc[vt][jt]);
-        } else {
-          const piece d = natural(d_rows, jt, y, 0);
+            for (int jt = 0; jt < 4; ++jt) acc[jt] = O::mma(ef[o], r[jt], acc[jt]);
+        }
+      } else {
+        piece d[4];
 #pragma unroll
-          for (int vt = 0; vt < VT; ++vt) {
-            acy[vt][jt] = mma_terms<O, NT, NT>(ef[vt], r, acy[vt][jt]);
+        for (int jt = 0; jt < 4; ++jt) d[jt] = natural(d_rows, jt, y, 0);
 #pragma unroll
-            for (int m = NT - 1; m >= 0; --m) acc[vt][jt] = O::mma(ef[vt][m], d, acc[vt][jt]);
-          }
+        for (int m = NT - 1; m >= 0; --m)
+#pragma unroll
+          for (int jt = 0; jt < 4; ++jt) acc[jt] = O::mma(ef[m], d[jt], acc[jt]);
+#pragma unroll
+        for (int m = OT - 1; m >= 0; --m) {
+          piece r[4];
+#pragma unroll
+          for (int jt = 0; jt < 4; ++jt) r[jt] = natural(y_rows, jt, y, m);
+#pragma unroll
+          for (int o = OT - 1 - m; o >= 0; --o)
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt) acy[jt] = O::mma(ef[o], r[jt], acy[jt]);
         }
       }
     }
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) {
-      const float beta = vec[kBeta * 64 + 16 * jt + c16];
-      const float f = BACK ? vec[kLast * 64 + 16 * jt + c16] * beta : p.scale * vec[kInto * 64 + 16 * jt + c16];
-      const float fy = -(beta * vec[kInto * 64 + 16 * jt + c16]);
+      const float beta = vec[kBeta * 64 + 16 * jt + c16], into = vec[kInto * 64 + 16 * jt + c16];
+      const float f = BACK ? vec[kLast * 64 + 16 * jt + c16] * beta : p.scale * into;
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt)
+      for (int e = 0; e < 4; ++e) {
+        acc[jt][e] *= f;
+        if constexpr (!BACK) acy[jt][e] *= -(beta * into);
+      }
+    }
+    // (q's values that meet dq, on their way)
+    float q_in[4][4];
+    if constexpr (!BACK) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          acc[vt][jt][e] *= f;
-          if constexpr (!BACK) acy[vt][jt][e] *= fy;
+      for (int jt = 0; jt < 4; ++jt) {
+        const int64_t at = (t0 + least(16 * jt + c16, n - 1)) * p.qs[1];
+        const int first = 16 * w + 4 * g;
+        if (p.q_four) {
+          if constexpr (kF32) {
+            const float4 y = *reinterpret_cast<const float4*>(qg + at + least(first, K - 4));
+            q_in[jt][0] = y.x; q_in[jt][1] = y.y; q_in[jt][2] = y.z; q_in[jt][3] = y.w;
+          } else {
+            const uint2 y = *reinterpret_cast<const uint2*>(qg + at + least(first, K - 4));
+            q_in[jt][0] = bf16_lo(y.x); q_in[jt][1] = bf16_hi(y.x); q_in[jt][2] = bf16_lo(y.y); q_in[jt][3] = bf16_hi(y.y);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q_in[jt][e] = load_act<ACT>(qg, at + least(first + e, K - 1));
         }
+      }
     }
     __syncthreads();                                // N1 and N2 are complete
 
     // ---- the chunk's own part
 #pragma unroll
-    for (int x = 0; x < kT; ++x) {
-      const int jt = x < 4 ? x : BACK ? x - 4 : x - 2, t = BACK ? (x < 4 ? 1 : 0) : (x < 4 ? 0 : 1);
+    for (int m = NT - 1; m >= 0; --m)
 #pragma unroll
-      for (int m = NT - 1; m >= 0; --m) {
-        piece n1, n2;
-        load_piece(sN[0] + (x * NT + m) * kOne + lane * (kOne / 64), n1);
-        load_piece(sN[1] + (x * NT + m) * kOne + lane * (kOne / 64), n2);
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-          if constexpr (BACK) {
-            acc[vt][jt] = O::mma(qf[vt][t], n1, acc[vt][jt]);
-            acc[vt][jt] = O::mma(kf[vt][t], n2, acc[vt][jt]);
-          } else {
-            acc[vt][jt] = O::mma(kf[vt][t], n1, acc[vt][jt]);
-            acy[vt][jt] = O::mma(kf[vt][t], n2, acy[vt][jt]);
-          }
+      for (int x = 0; x < kT; ++x) {
+        const int jt = x < 4 ? x : BACK ? x - 4 : x - 2, t = BACK ? (x < 4 ? 1 : 0) : (x < 4 ? 0 : 1);
+        piece n1;
+        load_piece(sN1 + (x * NT + m) * kOne + lane * (kOne / 64), n1);
+        acc[jt] = O::mma(BACK ? qf[t] : kf[t], n1, acc[jt]);
+        if (m < OT) {
+          piece n2;
+          load_piece(sN2 + (x * OT + m) * kOne + lane * (kOne / 64), n2);
+          if constexpr (BACK) acc[jt] = O::mma(kf[t], n2, acc[jt]);
+          else acy[jt] = O::mma(kf[t], n2, acy[jt]);
         }
       }
-    }
 
-    // ---- out: lane (g, c) has columns 4 g .. of token 16 jt + c
+    // ---- out: lane (g, c) has columns 16 w + 4 g .. of token 16 jt + c
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) {
-      const int row = 16 * jt + c16;
-      float sum = 0.0f;
+      const int row = 16 * jt + c16, first = 16 * w + 4 * g;
+      const int64_t at = out_base + (t0 + row) * out_row + first;
       if (row < n) {
-        const int64_t token = t0 + row;
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-          const int col = 16 * (VT * w + vt) + 4 * g;
-          const int64_t at = out_base + token * out_row + col;
-          if constexpr (BACK) {
-            if (p.part_vec) {
-              if (col < K) {
-                float4 y = *reinterpret_cast<const float4*>(p.dk_part + at);
-                y.x += acc[vt][jt][0]; y.y += acc[vt][jt][1]; y.z += acc[vt][jt][2]; y.w += acc[vt][jt][3];
-                if (p.dk_f32) *reinterpret_cast<float4*>(p.dk_part + at) = y;
-                else if constexpr (kF32) *reinterpret_cast<float4*>(static_cast<float*>(p.dk) + at) = y;
-                else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dk) + at) =
-                    make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-              }
+        if (p.part_vec) {
+          if (first < K) {
+            const f32x4_t& x = acc[jt];
+            float4 y = make_float4(x[0], x[1], x[2], x[3]);
+            if constexpr (BACK) {
+              const float4 z = *reinterpret_cast<const float4*>(p.dk_part + at);
+              y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
+              if (p.dk_f32) *reinterpret_cast<float4*>(p.dk_part + at) = y;
+              else if constexpr (kF32) *reinterpret_cast<float4*>(static_cast<float*>(p.dk) + at) = y;
+              else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dk) + at) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
             } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (col + e >= K) continue;
-                const float y = p.dk_part[at + e] + acc[vt][jt][e];
-                if (p.dk_f32) p.dk_part[at + e] = y;
-                else store_act<ACT>(p.dk, at + e, y);
-              }
+              if (p.dq_f32 || kF32) *reinterpret_cast<float4*>(static_cast<float*>(p.dq) + at) = y;
+              else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dq) + at) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+              const f32x4_t& z = acy[jt];
+              *reinterpret_cast<float4*>(p.dk_part + at) = make_float4(z[0], z[1], z[2], z[3]);
             }
-          } else {
+          }
+        } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (col + e >= K) continue;
-              sum = __builtin_fmaf(load_act<ACT>(qg, token * p.qs[1] + col + e), acc[vt][jt][e], sum);
-              sum = __builtin_fmaf(load_act<ACT>(kg, token * p.ks[1] + col + e), acy[vt][jt][e], sum);
-            }
-            if (p.part_vec) {
-              if (col < K) {
-                const f32x4_t& x = acc[vt][jt];
-                if (p.dq_f32 || kF32) *reinterpret_cast<float4*>(static_cast<float*>(p.dq) + at) = make_float4(x[0], x[1], x[2], x[3]);
-                else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dq) + at) =
-                    make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-                const f32x4_t& z = acy[vt][jt];
-                *reinterpret_cast<float4*>(p.dk_part + at) = make_float4(z[0], z[1], z[2], z[3]);
-              }
+          for (int e = 0; e < 4; ++e) {
+            if (first + e >= K) continue;
+            if constexpr (BACK) {
+              const float y = p.dk_part[at + e] + acc[jt][e];
+              if (p.dk_f32) p.dk_part[at + e] = y;
+              else store_act<ACT>(p.dk, at + e, y);
             } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (col + e >= K) continue;
-                if (p.dq_f32) static_cast<float*>(p.dq)[at + e] = acc[vt][jt][e];
-                else store_act<ACT>(p.dq, at + e, acc[vt][jt][e]);
-                p.dk_part[at + e] = acy[vt][jt][e];
-              }
+              if (p.dq_f32) static_cast<float*>(p.dq)[at + e] = acc[jt][e];
+              else store_act<ACT>(p.dq, at + e, acc[jt][e]);
+              p.dk_part[at + e] = acy[jt][e];
             }
           }
         }
       }
-      if constexpr (!BACK) {
+      if constexpr (!BACK) {                        // q.dq (its columns past K are zeros of k's)
+        float sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum = first + e < K ? __builtin_fmaf(q_in[jt][e], acc[jt][e], sum) : sum;
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
         if (g == 0) sSum[w][row] = sum;
@@ -412,61 +476,55 @@ void gd_qk_kernel(GdGradArgs p) {
     }
 
     // ---- the state
-    const float whole = vec[kWhole * 64];
-#pragma unroll
-    for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-      for (int y = 0; y < KT; ++y)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) E[vt][y][u][e] *= whole;
-    const uint32_t w_cols = O::template column_part<RV, PW>(tile_w, 0, 8, lane);
-    const uint32_t y_cols = O::template column_part<RV, PY>(tile_y, 0, 8, lane);
-    const uint32_t d_cols = O::template column_part<RV, BACK>(tile_d, 0, 8, lane);
     if (done + 1 < c_end - c_begin || !BACK) {      // (backwards the last is of no use)
+      const float whole = vec[kWhole * 64];
+      each([&](int y, int u, int e, bool, uint32_t) { E[y][u][e] *= whole; });
+      const uint32_t w_cols = O::template column_part<RV, PW>(tile_w, 0, 8, lane);
+      const uint32_t y_cols = O::template column_part<RV, PY>(tile_y, 0, 8, lane);
+      const uint32_t d_cols = O::template column_part<RV, BACK>(tile_d, 0, 8, lane);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         float with[8], beta[8], x[8];
         eight(BACK ? kInto : kLast, t, with);
         eight(kBeta, t, beta);
-        piece k_in[VT][NT], q_in[VT][NT];
+        piece k_in[NT], d_in[NT];
+        O::unpack(kf[t], x);
 #pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-          O::unpack(kf[vt][t], x);
+        for (int e = 0; e < 8; ++e) x[e] *= BACK ? -(with[e] * beta[e]) : with[e] * beta[e];
+        O::template split<NT>(x, k_in);
+        if constexpr (BACK) {
+          O::unpack(qf[t], x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= BACK ? -(with[e] * beta[e]) : with[e] * beta[e];
-          O::template split<NT>(x, k_in[vt]);
-          if constexpr (BACK) {
-            O::unpack(qf[vt][t], x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= with[e] * p.scale;
-            O::template split<NT>(x, q_in[vt]);
-          }
+          for (int e = 0; e < 8; ++e) x[e] *= with[e] * p.scale;
+          O::template split<NT>(x, d_in);
         }
 #pragma unroll
-        for (int y = 0; y < KT; ++y)
+        for (int z = 0; z < KT; z += 2) {           // four tiles at a time
+          auto columns = [&](uint32_t cols, auto perm, int m, piece (&out)[4]) __attribute__((always_inline)) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            auto column = [&](uint32_t cols, auto perm, int m) __attribute__((always_inline)) {
-              return O::template column<RV, decltype(perm)::value>(cols, (4 * PB * y) ^ O::half_flip(u),
-                                                                   32 * t * RV + O::half_offset(u) + m * (kQ * RV));
-            };
-            piece left[NT];
+            for (int i = 0; i < 4; ++i)
+              out[i] = O::template column<RV, decltype(perm)::value>(cols, (4 * PB * (z + i / 2)) ^ O::half_flip(i % 2),
+                                                                     32 * t * RV + O::half_offset(i % 2) + m * (kQ * RV));
+          };
 #pragma unroll
-            for (int m = 0; m < NT; ++m)
-              left[m] = BACK ? column(y_cols, std::integral_constant<bool, PY>{}, m)
-                             : column(w_cols, std::integral_constant<bool, PW>{}, m);
+          for (int m = NT - 1; m >= 0; --m) {
+            piece left[4];
+            if constexpr (BACK) columns(y_cols, std::integral_constant<bool, PY>{}, m, left);
+            else columns(w_cols, std::integral_constant<bool, PW>{}, m, left);
 #pragma unroll
-            for (int vt = 0; vt < VT; ++vt) E[vt][y][u] = mma_terms<O, NT, NT>(left, k_in[vt], E[vt][y][u]);
-            if constexpr (BACK) {
-              const piece d = column(d_cols, std::integral_constant<bool, BACK>{}, 0);
+            for (int o = NT - 1 - m; o >= 0; --o)
 #pragma unroll
-              for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-                for (int m = NT - 1; m >= 0; --m) E[vt][y][u] = O::mma(d, q_in[vt][m], E[vt][y][u]);
-            }
+              for (int i = 0; i < 4; ++i) E[z + i / 2][i % 2] = O::mma(left[i], k_in[o], E[z + i / 2][i % 2]);
           }
+          if constexpr (BACK) {
+            piece left[4];
+            columns(d_cols, std::integral_constant<bool, BACK>{}, 0, left);
+#pragma unroll
+            for (int o = NT - 1; o >= 0; --o)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) E[z + i / 2][i % 2] = O::mma(left[i], d_in[o], E[z + i / 2][i % 2]);
+          }
+        }
       }
     }
     __syncthreads();                                // the tiles are free, the tokens' sums complete
@@ -475,10 +533,10 @@ void gd_qk_kernel(GdGradArgs p) {
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NW; ++i) sum += sSum[i][tid];
-        sAll[done * kQ + tid] = __builtin_fmaf(-vec[kBeta * 64 + tid], sDiag[tid], sum);
-        p.dbeta[(b * L + t0 + tid) * p.H + h] = sDiag[tid];
+        sAll[done * kQ + tid] = __builtin_fmaf(-vec[kBeta * 64 + tid], sDot[1][tid], sum);
+        p.dbeta[(b * L + t0 + tid) * p.H + h] = sDot[0][tid];
       }
-      __syncthreads();
+      __syncthreads();                              // (before the next chunk's vectors and sums)
     }
   }
 
@@ -486,15 +544,9 @@ void gd_qk_kernel(GdGradArgs p) {
     // <F, E> at the end of the stretch, then the sums back over its tokens
     const float* f = p.kept_f + (bh * stretches + s) * static_cast<int64_t>(K) * V;
     float dot = 0.0f;
-#pragma unroll
-    for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-      for (int y = 0; y < KT; ++y)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (there(vt, y, u, e)) dot = __builtin_fmaf(f[place(vt, y, u, e)], E[vt][y][u][e], dot);
+    each([&](int y, int u, int e, bool there, uint32_t at) {
+      if (there) dot = __builtin_fmaf(f[at], E[y][u][e], dot);
+    });
     dot = wave_sum(dot);
     if (lane == 0) sSum[w][0] = dot;
     __syncthreads();

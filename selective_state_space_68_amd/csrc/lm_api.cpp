@@ -574,15 +574,21 @@ ssm_status ssm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
   hipError_t err = ssm::launch_gd_walks(a, r, dt_of(dt), s);
   if (err != hipSuccess) return from_hip(err);
   ssm::GdGradArgs x;
-  x.q = q; x.k = k; x.d = dout;
-  for (int i = 0; i < 3; ++i) { x.qs[i] = t.q.stride[i]; x.ks[i] = t.k.stride[i]; x.ds[i] = t.d.stride[i]; }
-  x.qdiv = a.qdiv; x.kdiv = a.kdiv;
+  x.q = q; x.k = k; x.v = v; x.d = dout;
+  for (int i = 0; i < 3; ++i) {
+    x.qs[i] = t.q.stride[i]; x.ks[i] = t.k.stride[i]; x.vs[i] = t.v.stride[i]; x.ds[i] = t.d.stride[i];
+  }
+  x.qdiv = a.qdiv; x.kdiv = a.kdiv; x.vdiv = a.vdiv;
   x.rec = a.rec; x.w = a.w_out; x.y = r.w_out; x.kept_e = a.kept; x.kept_f = r.kept; x.lengths = lengths;
   x.dq = dq_part ? static_cast<void*>(dq_part) : dq; x.dq_f32 = dq_part != nullptr;
   x.dk_part = dk_part; x.dk = dk; x.dk_f32 = Hk != H;
   x.dg = dg; x.dbeta = dbeta; x.batch = batch; x.L = L; x.H = a.H; x.K = a.K; x.V = a.V; x.every = a.every; x.scale = scale;
   x.carried = initial_state != nullptr;
+  x.q_vec = K % 8 == 0 && rows_aligned(q, t.q, e, 16);
+  x.k_vec = K % 8 == 0 && rows_aligned(k, t.k, e, 16);
+  x.v_vec = V % 8 == 0 && rows_aligned(v, t.v, e, 16);
   x.d_vec = V % 8 == 0 && rows_aligned(dout, t.d, e, 16);
+  x.q_four = K % 4 == 0 && rows_aligned(q, t.q, e, 4 * e);
   x.part_vec = K % 4 == 0 && aligned(x.dq, dq_part ? 16 : 4 * e) && (x.dk_f32 || aligned(dk, 4 * e));
   err = ssm::launch_gd_qk(x, dt_of(dt), s);
   ssm::LaSum sums[3];

@@ -105,9 +105,9 @@ struct GdArgs {
 };
 // The gradients of q, k, g and beta from what the walks left.
 struct GdGradArgs {
-  const void *q = nullptr, *k = nullptr, *d = nullptr;   // d: the outputs' gradient, [batch][L][H][V]
-  int64_t qs[3] = {}, ks[3] = {}, ds[3] = {};
-  int qdiv = 1, kdiv = 1;
+  const void *q = nullptr, *k = nullptr, *v = nullptr, *d = nullptr;   // d: the outputs' gradient, [batch][L][H][V]
+  int64_t qs[3] = {}, ks[3] = {}, vs[3] = {}, ds[3] = {};
+  int qdiv = 1, kdiv = 1, vdiv = 1;
   const char* rec = nullptr;
   const float *w = nullptr, *y = nullptr;                // w_out of the two walks
   const float *kept_e = nullptr, *kept_f = nullptr;      // kept of the two walks
@@ -121,7 +121,8 @@ struct GdGradArgs {
   float scale = 1.0f;
   int dq_f32 = 0, dk_f32 = 0;
   int carried = 0;                                       // there is an initial state
-  int d_vec = 0;                                         // rows of d move as 16 bytes
+  int q_vec = 0, k_vec = 0, v_vec = 0, d_vec = 0;        // rows move as 8 elements
+  int q_four = 0;                                        // rows of q move as 4 elements
   int part_vec = 0;                                      // rows of dq, dk and dk_part move as 4 elements
 };
 int gd_every(int64_t batch, int64_t L, int64_t H);
