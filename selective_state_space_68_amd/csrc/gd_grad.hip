@@ -32,21 +32,48 @@ namespace {
 
 constexpr int kMostEvery = 16;
 
-// Eight values of a row, of which `left` are there.
-template <typename ACT>
-__device__ __forceinline__ typename Op<ACT>::piece load8(const void* base, int64_t at, int left, bool vec) {
+// The sum over N = 8 or 16 neighbouring lanes: quads, then the quads of 8, then of 16.
+template <int N>
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp_mov<0xb1, 0xf, true>(0.0f, v);           // quad_perm [1, 0, 3, 2]
+  v += dpp_mov<0x4e, 0xf, true>(0.0f, v);           // quad_perm [2, 3, 0, 1]
+  v += dpp_mov<0x141, 0xf, true>(0.0f, v);          // row_half_mirror
+  if constexpr (N == 16) v += dpp_mov<0x140, 0xf, true>(0.0f, v);   // row_mirror
+  return v;
+}
+
+// Eight values of a row from memory.  Nothing is decided where they move as vectors: rows and columns that are not there
+// repeat the last ones (they are cleared on the way into LDS).
+template <bool VEC>
+using Offset = std::conditional_t<VEC, uint32_t, int64_t>;    // within a chunk's rows (vectors': of fewer than 2^32 bytes)
+template <typename ACT, bool VEC>
+__device__ __forceinline__ typename Op<ACT>::piece load8(const void* base, Offset<VEC> stride, int row, int n, int col, int width) {
   using elem = typename Op<ACT>::elem;
-  typename Op<ACT>::piece p = Op<ACT>::zero();
-  const elem* from = static_cast<const elem*>(base) + at;
-  if (vec) {
-    if (left > 0) load_piece(reinterpret_cast<const char*>(from), p);
+  const elem* at = static_cast<const elem*>(base);
+  const Offset<VEC> first = static_cast<Offset<VEC>>(least(row, n - 1)) * stride;
+  typename Op<ACT>::piece p;
+  if constexpr (VEC) {
+    load_piece(reinterpret_cast<const char*>(at + (first + least(col, width - 8))), p);
   } else {
     elem v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < left ? from[e] : elem(0);
+    for (int e = 0; e < 8; ++e) v[e] = at[first + least(col + e, width - 1)];
     p = __builtin_bit_cast(typename Op<ACT>::piece, v);
   }
   return p;
+}
+// The values of columns and rows that are there.
+template <typename ACT, bool VEC>
+__device__ __forceinline__ typename Op<ACT>::piece present(const typename Op<ACT>::piece& p, int row, int n, int col, int width) {
+  using elem = typename Op<ACT>::elem;
+  if constexpr (VEC) {
+    return row < n && col < width ? p : Op<ACT>::zero();
+  } else {
+    struct Eight { elem v[8]; } x = __builtin_bit_cast(Eight, p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x.v[e] = row < n && col + e < width ? x.v[e] : elem(0);
+    return __builtin_bit_cast(typename Op<ACT>::piece, x);
+  }
 }
 // ... to columns 8 slot .. of an LDS tile's row.
 template <int RB, bool PERM>
@@ -60,8 +87,9 @@ __device__ __forceinline__ void put8(char* tile, int row, int slot, const F8& p)
   *reinterpret_cast<float4*>(tile + row * RB + (((2 * slot + 1) ^ flip) << 4)) = p.b;
 }
 
-// BACK: the second kernel, which adds the backward part of dk.
-template <typename ACT, int KD, int VD, bool BACK>
+// BACK: the second kernel, which adds the backward part of dk.  VEC: rows of q, k, v and d move as 8 elements, those of dq and
+// dk as 4.
+template <typename ACT, int KD, int VD, bool VEC, bool BACK>
 __global__ __launch_bounds__(4 * KD, 2)
 void gd_qk_kernel(GdGradArgs p) {
   using O = Op<ACT>;
@@ -82,7 +110,8 @@ void gd_qk_kernel(GdGradArgs p) {
   __shared__ __attribute__((aligned(512))) char sN1[kT * NT * kOne];
   __shared__ __attribute__((aligned(512))) char sN2[kT * OT * kOne];
   __shared__ __attribute__((aligned(16))) float vec[kVecs * 64];
-  __shared__ float sSum[NW][kQ], sDot[2][kQ], sAll[BACK ? 1 : kMostEvery * kQ];
+  // the tokens' scalars, of this chunk and of the one before: parts of q.dq, y.w and y.v, beta
+  __shared__ float sSum[2][NW][kQ], sDot[2][3][kQ], sAll[BACK ? 1 : kMostEvery * kQ];
 
   const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6), g = lane >> 4, c16 = lane & 15;
   const int L = static_cast<int>(p.L), K = p.K, V = p.V;
@@ -105,13 +134,8 @@ void gd_qk_kernel(GdGradArgs p) {
     const int stop = least(L, (c_begin + p.every) * kQ), from = len > c_begin * kQ ? len : c_begin * kQ;
     for (int64_t i = tid; i < static_cast<int64_t>(stop - from) * K; i += THREADS) {
       const int64_t at = out_base + (from + i / K) * out_row + i % K;
-      if constexpr (BACK) {
-        if (!p.dk_f32) store_act<ACT>(p.dk, at, 0.0f);
-      } else {
-        if (p.dq_f32) static_cast<float*>(p.dq)[at] = 0.0f;
-        else store_act<ACT>(p.dq, at, 0.0f);
-        p.dk_part[at] = 0.0f;
-      }
+      if (BACK ? p.dk_f32 : p.dq_f32) static_cast<float*>(BACK ? p.dk : p.dq)[at] = 0.0f;
+      else store_act<ACT>(BACK ? p.dk : p.dq, at, 0.0f);
     }
     if constexpr (!BACK) {
       for (int i = tid; i < stop - from; i += THREADS) {
@@ -125,35 +149,47 @@ void gd_qk_kernel(GdGradArgs p) {
 
   // ---- a chunk's rows, 8 columns at a time by the threads in turn, in registers on their way to LDS
   constexpr int kV8 = VD / 8, kN = kQ * kV8 / THREADS, kK8 = KD / 8, kNK = kQ * kK8 / THREADS;
+  constexpr int kVecRegs = (kVecs * 64 + THREADS - 1) / THREADS;
   struct Rows {
     F8 w[kN], y[kN];
     piece d[kN], v[BACK ? 1 : kN], k[TILES ? kNK : 1], q[TILES && BACK ? kNK : 1];
-    float vec[(kVecs * 64 + THREADS - 1) / THREADS];
+    float vec[kVecRegs];
   } in;
-  auto ask = [&](int c) __attribute__((always_inline)) {
+  // in four parts, 0 to 3, spread over the chunk before: asked for at once, they keep the loads' unit busy for thousands of
+  // cycles while the waves wait for their turn
+  auto ask = [&](int c, int part) __attribute__((always_inline)) {
+    int id = tid;
+    asm volatile("" : "+v"(id));                    // (so that no address is kept over the loop)
     const int n = least(len - c * kQ, kQ);
     const int64_t t0 = static_cast<int64_t>(c) * kQ, rows = (bh * nchunks + c) * kQ;
+    const char *wc = reinterpret_cast<const char*>(p.w + rows * VD), *yc = reinterpret_cast<const char*>(p.y + rows * VD);
+    const elem *dc = dg + t0 * p.ds[1], *vc = vg + t0 * p.vs[1], *kc = kg + t0 * p.ks[1], *qc = qg + t0 * p.qs[1];
+    const Offset<VEC> dstep = static_cast<Offset<VEC>>(p.ds[1]), vstep = static_cast<Offset<VEC>>(p.vs[1]),
+                      kstep = static_cast<Offset<VEC>>(p.ks[1]), qstep = static_cast<Offset<VEC>>(p.qs[1]);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int at = tid + i * THREADS, row = at / kV8, slot = at % kV8, left = row < n ? V - 8 * slot : 0;
-      load_piece(reinterpret_cast<const char*>(p.w + (rows + row) * VD + 8 * slot), in.w[i]);
-      load_piece(reinterpret_cast<const char*>(p.y + (rows + row) * VD + 8 * slot), in.y[i]);
-      in.d[i] = load8<ACT>(dg, (t0 + row) * p.ds[1] + 8 * slot, left, p.d_vec);
-      if constexpr (!BACK) in.v[i] = load8<ACT>(vg, (t0 + row) * p.vs[1] + 8 * slot, left, p.v_vec);
+      const int at = id + i * THREADS, row = at / kV8, col = 8 * (at % kV8);
+      if (part == 0) load_piece(wc + static_cast<uint32_t>(32 * at), in.w[i]);
+      if (part == 1) load_piece(yc + static_cast<uint32_t>(32 * at), in.y[i]);
+      if (part == 2) {
+        in.d[i] = load8<ACT, VEC>(dc, dstep, row, n, col, V);
+        if constexpr (!BACK) in.v[i] = load8<ACT, VEC>(vc, vstep, row, n, col, V);
+      }
     }
+    if (part < 3) return;
     if constexpr (TILES) {
 #pragma unroll
       for (int i = 0; i < kNK; ++i) {
-        const int at = tid + i * THREADS, row = at / kK8, slot = at % kK8, left = row < n ? K - 8 * slot : 0;
-        in.k[i] = load8<ACT>(kg, (t0 + row) * p.ks[1] + 8 * slot, left, p.k_vec);
-        if constexpr (BACK) in.q[i] = load8<ACT>(qg, (t0 + row) * p.qs[1] + 8 * slot, left, p.q_vec);
+        const int at = id + i * THREADS, row = at / kK8, col = 8 * (at % kK8);
+        in.k[i] = load8<ACT, VEC>(kc, kstep, row, n, col, K);
+        if constexpr (BACK) in.q[i] = load8<ACT, VEC>(qc, qstep, row, n, col, K);
       }
     }
     const float* from = reinterpret_cast<const float*>(p.rec + (bh * nchunks + c) * kRecord<ACT, 0> + kTBytes<ACT>);
 #pragma unroll
-    for (int i = 0; i < (kVecs * 64 + THREADS - 1) / THREADS; ++i) in.vec[i] = from[least(tid + i * THREADS, kVecs * 64 - 1)];
+    for (int i = 0; i < kVecRegs; ++i) in.vec[i] = from[static_cast<uint32_t>(least(id + i * THREADS, kVecs * 64 - 1))];
   };
-  auto store = [&]() __attribute__((always_inline)) {
+  auto store = [&](int n, int which) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int at = tid + i * THREADS, row = at / kV8, slot = at % kV8;
@@ -167,23 +203,20 @@ void gd_qk_kernel(GdGradArgs p) {
       for (int m = 0; m < NT; ++m) put8<RV, PW>(sW[m], row, slot, t[m]);
 #pragma unroll
       for (int m = 0; m < OT; ++m) put8<RV, PY>(sY[m], row, slot, o[m]);
-      put8<RV, BACK>(sD, row, slot, in.d[i]);
+      put8<RV, BACK>(sD, row, slot, present<ACT, VEC>(in.d[i], row, n, 8 * slot, V));
       if constexpr (!BACK) {                        // y.w and y.v
         float v[8], yw = 0.0f, yv = 0.0f;
-        O::unpack(in.v[i], v);
+        O::unpack(present<ACT, VEC>(in.v[i], row, n, 8 * slot, V), v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           yw = __builtin_fmaf(y[e], x[e], yw);
           yv = __builtin_fmaf(y[e], v[e], yv);
         }
-#pragma unroll
-        for (int d = 1; d < kV8; d *= 2) {
-          yw += __shfl_xor(yw, d);
-          yv += __shfl_xor(yv, d);
-        }
+        yw = row_sum<kV8>(yw);
+        yv = row_sum<kV8>(yv);
         if (slot == 0) {
-          sDot[0][row] = yw;
-          sDot[1][row] = yv;
+          sDot[which][0][row] = yw;
+          sDot[which][1][row] = yv;
         }
       }
     }
@@ -191,16 +224,30 @@ void gd_qk_kernel(GdGradArgs p) {
 #pragma unroll
       for (int i = 0; i < kNK; ++i) {
         const int at = tid + i * THREADS, row = at / kK8, slot = at % kK8;
-        put8<RK, false>(sK, row, slot, in.k[i]);
-        if constexpr (BACK) put8<RK, false>(sQ, row, slot, in.q[i]);
+        put8<RK, false>(sK, row, slot, present<ACT, VEC>(in.k[i], row, n, 8 * slot, K));
+        if constexpr (BACK) put8<RK, false>(sQ, row, slot, present<ACT, VEC>(in.q[i], row, n, 8 * slot, K));
       }
     }
 #pragma unroll
-    for (int i = 0; i < (kVecs * 64 + THREADS - 1) / THREADS; ++i)
-      if (tid + i * THREADS < kVecs * 64) vec[tid + i * THREADS] = in.vec[i];
+    for (int i = 0; i < kVecRegs; ++i)
+      if (tid + i * THREADS < kVecs * 64) {
+        vec[tid + i * THREADS] = in.vec[i];
+        if (!BACK && (tid + i * THREADS) / 64 == kBeta) sDot[which][2][tid % 64] = in.vec[i];
+      }
+  };
+  // A chunk's tokens (one wave, when they are complete).
+  auto scalars = [&](int done) __attribute__((always_inline)) {
+    const int which = done & 1, t = (c_begin + done) * kQ + lane;
+    if (t >= len) return;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) sum += sSum[which][i][lane];
+    sAll[done * kQ + lane] = __builtin_fmaf(-sDot[which][2][lane], sDot[which][1][lane], sum);
+    p.dbeta[(b * L + t) * p.H + h] = sDot[which][0][lane];
   };
   auto chunk_of = [&](int done) { return BACK ? c_end - 1 - done : c_begin + done; };
-  ask(chunk_of(0));
+#pragma unroll
+  for (int part = 0; part < 4; ++part) ask(chunk_of(0), part);
 
   // E[y][u][e] is the entry v = 32 y + 8 g + 4 u + e, k = 16 w + c16 (backwards of the gradient F)
   const int col = 16 * w + c16;
@@ -244,9 +291,40 @@ void gd_qk_kernel(GdGradArgs p) {
     const int c = chunk_of(done);
     const int n = least(len - c * kQ, kQ);
     const int64_t t0 = static_cast<int64_t>(c) * kQ;
-    store();
+    store(n, done & 1);
     __syncthreads();
-    if (done + 1 < c_end - c_begin) ask(chunk_of(done + 1));
+    if (!BACK && done > 0 && w == NW - 1) scalars(done - 1);      // (the last waves have no part in N1 and N2)
+    // what meets dq and dk at the end (asked for before the next chunk's rows, which its arrival need not wait for)
+    const int first = 16 * w + 4 * g;               // this lane's columns of token 16 jt + c16 there
+    const uint32_t out_step = static_cast<uint32_t>(out_row);
+    const int64_t out_at = out_base + t0 * out_row;
+    float* part = p.dk_part + ((bh * nchunks + c) * NW + w) * 1024 + lane * 4;
+    float meet[4][4];
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+      const uint32_t row = static_cast<uint32_t>(least(16 * jt + c16, n - 1));
+      if constexpr (BACK) {                         // (dk's forward part, as this lane of the first kernel left it)
+        const float4 x = *reinterpret_cast<const float4*>(part + jt * 256);
+        meet[jt][0] = x.x; meet[jt][1] = x.y; meet[jt][2] = x.z; meet[jt][3] = x.w;
+      } else {                                      // (q)
+        const elem* from = qg + t0 * p.qs[1];
+        const Offset<VEC> at = row * static_cast<Offset<VEC>>(p.qs[1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) meet[jt][e] = 0.0f;
+        if constexpr (VEC && kF32) {
+          const float4 x = *reinterpret_cast<const float4*>(from + (at + least(first, K - 4)));
+          meet[jt][0] = x.x; meet[jt][1] = x.y; meet[jt][2] = x.z; meet[jt][3] = x.w;
+        } else if constexpr (VEC) {                 // (unpacked where it is used)
+          const float2 x = *reinterpret_cast<const float2*>(from + (at + least(first, K - 4)));
+          meet[jt][0] = x.x; meet[jt][1] = x.y;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) meet[jt][e] = load_act<ACT>(from, at + least(first + e, K - 1));
+        }
+      }
+    }
+    const bool more = done + 1 < c_end - c_begin;
+    if (more) ask(chunk_of(done + 1), 0);
     // the wave's own columns of k (and of q): tokens 32 t + 8 g + e of column c16
     piece kf[2], qf[2];
     if constexpr (TILES) {
@@ -336,6 +414,7 @@ void gd_qk_kernel(GdGradArgs p) {
       for (int m = 0; m < OT; ++m) store_piece(sN2 + (x * OT + m) * kOne + lane * (kOne / 64), o2[m]);
     }
 
+    if (more) ask(chunk_of(done + 1), 1);
     // ---- the state's part, rows k, column j = 16 jt + c16: acc of D and acy of Y, backwards acc of W
     f32x4_t acc[4], acy[4];
 #pragma unroll
@@ -386,27 +465,7 @@ void gd_qk_kernel(GdGradArgs p) {
         if constexpr (!BACK) acy[jt][e] *= -(beta * into);
       }
     }
-    // (q's values that meet dq, on their way)
-    float q_in[4][4];
-    if constexpr (!BACK) {
-#pragma unroll
-      for (int jt = 0; jt < 4; ++jt) {
-        const int64_t at = (t0 + least(16 * jt + c16, n - 1)) * p.qs[1];
-        const int first = 16 * w + 4 * g;
-        if (p.q_four) {
-          if constexpr (kF32) {
-            const float4 y = *reinterpret_cast<const float4*>(qg + at + least(first, K - 4));
-            q_in[jt][0] = y.x; q_in[jt][1] = y.y; q_in[jt][2] = y.z; q_in[jt][3] = y.w;
-          } else {
-            const uint2 y = *reinterpret_cast<const uint2*>(qg + at + least(first, K - 4));
-            q_in[jt][0] = bf16_lo(y.x); q_in[jt][1] = bf16_hi(y.x); q_in[jt][2] = bf16_lo(y.y); q_in[jt][3] = bf16_hi(y.y);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) q_in[jt][e] = load_act<ACT>(qg, at + least(first + e, K - 1));
-        }
-      }
-    }
+    if (more) ask(chunk_of(done + 1), 2);
     __syncthreads();                                // N1 and N2 are complete
 
     // ---- the chunk's own part
@@ -427,56 +486,63 @@ void gd_qk_kernel(GdGradArgs p) {
       }
 
     // ---- out: lane (g, c) has columns 16 w + 4 g .. of token 16 jt + c
+    if constexpr (!BACK) {                          // q.dq
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-      const int row = 16 * jt + c16, first = 16 * w + 4 * g;
-      const int64_t at = out_base + (t0 + row) * out_row + first;
-      if (row < n) {
-        if (p.part_vec) {
-          if (first < K) {
-            const f32x4_t& x = acc[jt];
-            float4 y = make_float4(x[0], x[1], x[2], x[3]);
-            if constexpr (BACK) {
-              const float4 z = *reinterpret_cast<const float4*>(p.dk_part + at);
-              y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
-              if (p.dk_f32) *reinterpret_cast<float4*>(p.dk_part + at) = y;
-              else if constexpr (kF32) *reinterpret_cast<float4*>(static_cast<float*>(p.dk) + at) = y;
-              else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dk) + at) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-            } else {
-              if (p.dq_f32 || kF32) *reinterpret_cast<float4*>(static_cast<float*>(p.dq) + at) = y;
-              else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dq) + at) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-              const f32x4_t& z = acy[jt];
-              *reinterpret_cast<float4*>(p.dk_part + at) = make_float4(z[0], z[1], z[2], z[3]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (first + e >= K) continue;
-            if constexpr (BACK) {
-              const float y = p.dk_part[at + e] + acc[jt][e];
-              if (p.dk_f32) p.dk_part[at + e] = y;
-              else store_act<ACT>(p.dk, at + e, y);
-            } else {
-              if (p.dq_f32) static_cast<float*>(p.dq)[at + e] = acc[jt][e];
-              else store_act<ACT>(p.dq, at + e, acc[jt][e]);
-              p.dk_part[at + e] = acy[jt][e];
-            }
-          }
+      for (int jt = 0; jt < 4; ++jt) {
+        if constexpr (VEC && !kF32) {
+          const uint32_t a = __builtin_bit_cast(uint32_t, meet[jt][0]), d = __builtin_bit_cast(uint32_t, meet[jt][1]);
+          meet[jt][0] = bf16_lo(a); meet[jt][1] = bf16_hi(a); meet[jt][2] = bf16_lo(d); meet[jt][3] = bf16_hi(d);
         }
-      }
-      if constexpr (!BACK) {                        // q.dq (its columns past K are zeros of k's)
         float sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum = first + e < K ? __builtin_fmaf(q_in[jt][e], acc[jt][e], sum) : sum;
+        for (int e = 0; e < 4; ++e) sum = first + e < K ? __builtin_fmaf(meet[jt][e], acc[jt][e], sum) : sum;
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
-        if (g == 0) sSum[w][row] = sum;
+        if (g == 0) sSum[done & 1][w][16 * jt + c16] = sum;
       }
     }
+    auto put = [&](auto* out, int jt, const float (&x)[4]) __attribute__((always_inline)) {
+      using OUT = std::remove_pointer_t<decltype(out)>;
+      const uint32_t at = static_cast<uint32_t>(16 * jt + c16) * out_step + first;
+      if constexpr (VEC) {
+        if constexpr (sizeof(OUT) == 4) *reinterpret_cast<float4*>(out + at) = make_float4(x[0], x[1], x[2], x[3]);
+        else *reinterpret_cast<uint2*>(out + at) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (first + e >= K) continue;
+          if constexpr (sizeof(OUT) == 4) out[at + e] = x[e];
+          else out[at + e] = to_bf16(x[e]);
+        }
+      }
+    };
+    auto put_act = [&](void* out, bool f32, int jt, const float (&x)[4]) __attribute__((always_inline)) {
+      if (f32 || kF32) put(static_cast<float*>(out) + out_at, jt, x);
+      else put(static_cast<uint16_t*>(out) + out_at, jt, x);
+    };
+    if (first < K) {
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt) {
+        if (16 * jt + c16 >= n) continue;
+        float x[4] = {acc[jt][0], acc[jt][1], acc[jt][2], acc[jt][3]};
+        if constexpr (BACK) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] += meet[jt][e];
+          put_act(p.dk, p.dk_f32, jt, x);
+        } else {
+          put_act(p.dq, p.dq_f32, jt, x);
+        }
+      }
+    }
+    if constexpr (!BACK) {
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt)
+        *reinterpret_cast<float4*>(part + jt * 256) = make_float4(acy[jt][0], acy[jt][1], acy[jt][2], acy[jt][3]);
+    }
 
+    if (more) ask(chunk_of(done + 1), 3);
     // ---- the state
-    if (done + 1 < c_end - c_begin || !BACK) {      // (backwards the last is of no use)
+    if (more || !BACK) {      // (backwards the last is of no use)
       const float whole = vec[kWhole * 64];
       each([&](int y, int u, int e, bool, uint32_t) { E[y][u][e] *= whole; });
       const uint32_t w_cols = O::template column_part<RV, PW>(tile_w, 0, 8, lane);
@@ -528,19 +594,10 @@ void gd_qk_kernel(GdGradArgs p) {
       }
     }
     __syncthreads();                                // the tiles are free, the tokens' sums complete
-    if constexpr (!BACK) {
-      if (tid < n) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NW; ++i) sum += sSum[i][tid];
-        sAll[done * kQ + tid] = __builtin_fmaf(-vec[kBeta * 64 + tid], sDot[1][tid], sum);
-        p.dbeta[(b * L + t0 + tid) * p.H + h] = sDot[0][tid];
-      }
-      __syncthreads();                              // (before the next chunk's vectors and sums)
-    }
   }
 
   if constexpr (!BACK) {
+    if (w == NW - 1) scalars(c_end - c_begin - 1);
     // <F, E> at the end of the stretch, then the sums back over its tokens
     const float* f = p.kept_f + (bh * stretches + s) * static_cast<int64_t>(K) * V;
     float dot = 0.0f;
@@ -548,12 +605,13 @@ void gd_qk_kernel(GdGradArgs p) {
       if (there) dot = __builtin_fmaf(f[at], E[y][u][e], dot);
     });
     dot = wave_sum(dot);
-    if (lane == 0) sSum[w][0] = dot;
+    __syncthreads();                                // (the sums have been read)
+    if (lane == 0) sSum[0][w][0] = dot;
     __syncthreads();
     if (w == 0) {
       double carry = 0.0;
 #pragma unroll
-      for (int i = 0; i < NW; ++i) carry += sSum[i][0];
+      for (int i = 0; i < NW; ++i) carry += sSum[0][i][0];
       const int first = c_begin * kQ, stop = least(len, c_end * kQ);
       for (int c = c_end - 1; c >= c_begin; --c) {
         const int t = c * kQ + lane;
@@ -576,8 +634,13 @@ template <typename ACT, int KD, int VD>
 void launch_qk_t(const GdGradArgs& a, hipStream_t s) {
   const int64_t nch = (a.L + kQ - 1) / kQ, stretches = (nch + a.every - 1) / a.every;
   const dim3 grid(static_cast<unsigned>(a.batch * a.H * stretches)), block(4 * KD);
-  hipLaunchKernelGGL((gd_qk_kernel<ACT, KD, VD, false>), grid, block, 0, s, a);
-  hipLaunchKernelGGL((gd_qk_kernel<ACT, KD, VD, true>), grid, block, 0, s, a);
+  auto go = [&](auto vec) {
+    constexpr bool VEC = decltype(vec)::value;
+    hipLaunchKernelGGL((gd_qk_kernel<ACT, KD, VD, VEC, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((gd_qk_kernel<ACT, KD, VD, VEC, true>), grid, block, 0, s, a);
+  };
+  if (a.vec) go(std::true_type{});
+  else go(std::false_type{});
 }
 
 }  // namespace

@@ -389,21 +389,22 @@ struct Taker {
 struct GdBwdPlan {
   GdPlan fwd, back;
   uint64_t rows = 0, kept = 0;        // of one walk
-  uint64_t dk = 0, dq = 0, dv = 0;    // dk's parts always, the others' of shared heads
+  uint64_t part = 0;                  // dk's forward part
+  uint64_t dk = 0, dq = 0, dv = 0;    // of shared heads
   uint64_t total = 0;
 };
 
-bool gd_bwd_plan(int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hv, int64_t K, int64_t V, ssm_dtype dt,
+bool gd_bwd_plan(int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv, int64_t K, int64_t V, ssm_dtype dt,
                  GdBwdPlan* p) {
   const ssm::GdRecords r = ssm::gd_records(dt_of(dt));
   if (!gd_plan(batch, L, H, K, V, r.save, &p->fwd) || !gd_plan(batch, L, H, K, V, r.back, &p->back)) return false;
   if (batch == 0 || L == 0 || H == 0) return true;
   const int64_t nch = (L + 63) / 64, every = ssm::gd_every(batch, L, H);
   if (!bytes_of(4, &p->rows, batch, H, nch, 64, V > 64 ? 128 : 64) ||
-      !bytes_of(4, &p->kept, batch, H, (nch + every - 1) / every, K, V) || !bytes_of(4, &p->dk, batch, L, H, K) ||
-      (Hq != H && !bytes_of(4, &p->dq, batch, L, H, K)) || (Hv != H && !bytes_of(4, &p->dv, batch, L, H, V)))
+      !bytes_of(4, &p->kept, batch, H, (nch + every - 1) / every, K, V) || !bytes_of(4, &p->part, batch, H, nch, 64, K > 64 ? 128 : 64) ||
+      (Hk != H && !bytes_of(4, &p->dk, batch, L, H, K)) || (Hq != H && !bytes_of(4, &p->dq, batch, L, H, K)) || (Hv != H && !bytes_of(4, &p->dv, batch, L, H, V)))
     return false;
-  p->total = p->fwd.total + p->back.total + 2 * (up256(p->rows) + up256(p->kept)) + up256(p->dk) + up256(p->dq) + up256(p->dv);
+  p->total = p->fwd.total + p->back.total + 2 * (up256(p->rows) + up256(p->kept)) + up256(p->part) + up256(p->dk) + up256(p->dq) + up256(p->dv);
   return p->total <= kMaxBytes;
 }
 
@@ -488,7 +489,7 @@ size_t ssm_gated_delta_bwd_workspace_size(int64_t batch, int64_t L, int64_t H, i
                                           int64_t K, int64_t V, ssm_dtype dt) {
   GdBwdPlan p;
   if (check_gd_bwd_sizes(batch, L, H, Hq, Hk, Hv, K, V, dt) != SSM_OK) return 0;
-  return gd_bwd_plan(batch, L, H, Hq, Hv, K, V, dt, &p) ? p.total : 0;
+  return gd_bwd_plan(batch, L, H, Hq, Hk, Hv, K, V, dt, &p) ? p.total : 0;
 }
 
 ssm_status ssm_gated_delta_bwd(const void* q, const void* k, const void* v, const void* dout, const int64_t* q_strides,
@@ -508,7 +509,7 @@ ssm_status ssm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
       !make_view<3>(v_strides, {batch, L, Hv}, V, e, &t.v) || !make_view<3>(dout_strides, {batch, L, H}, V, e, &t.d) ||
       !bytes_of(e, &qb, batch, L, Hq, K) || !bytes_of(e, &kb, batch, L, Hk, K) || !bytes_of(e, &vb, batch, L, Hv, V) ||
       !bytes_of(4, &state_bytes, batch, H, K, V) || !bytes_of(4, &gate_bytes, batch, L, H) ||
-      !gd_bwd_plan(batch, L, H, Hq, Hv, K, V, dt, &plan))
+      !gd_bwd_plan(batch, L, H, Hq, Hk, Hv, K, V, dt, &plan))
     return SSM_ERR_INVALID_ARG;
   if (qb && (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta)) return SSM_ERR_INVALID_ARG;
   if (!aligned(q, e) || !aligned(k, e) || !aligned(v, e) || !aligned(dout, e) || !aligned(dq, e) || !aligned(dk, e) ||
@@ -566,6 +567,7 @@ ssm_status ssm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
   r.w_out = take.floats(plan.rows);
   r.kept = take.floats(plan.kept);
   r.move = least(least(row_move(q, t.q, K, e), row_move(k, t.k, K, e)), row_move(dout, t.d, V, e));
+  float* part = take.floats(plan.part);
   float* dk_part = take.floats(plan.dk);
   float* dq_part = take.floats(plan.dq);
   float* dv_part = take.floats(plan.dv);
@@ -581,15 +583,10 @@ ssm_status ssm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
   x.qdiv = a.qdiv; x.kdiv = a.kdiv; x.vdiv = a.vdiv;
   x.rec = a.rec; x.w = a.w_out; x.y = r.w_out; x.kept_e = a.kept; x.kept_f = r.kept; x.lengths = lengths;
   x.dq = dq_part ? static_cast<void*>(dq_part) : dq; x.dq_f32 = dq_part != nullptr;
-  x.dk_part = dk_part; x.dk = dk; x.dk_f32 = Hk != H;
+  x.dk_part = part; x.dk = dk_part ? static_cast<void*>(dk_part) : dk; x.dk_f32 = dk_part != nullptr;
   x.dg = dg; x.dbeta = dbeta; x.batch = batch; x.L = L; x.H = a.H; x.K = a.K; x.V = a.V; x.every = a.every; x.scale = scale;
   x.carried = initial_state != nullptr;
-  x.q_vec = K % 8 == 0 && rows_aligned(q, t.q, e, 16);
-  x.k_vec = K % 8 == 0 && rows_aligned(k, t.k, e, 16);
-  x.v_vec = V % 8 == 0 && rows_aligned(v, t.v, e, 16);
-  x.d_vec = V % 8 == 0 && rows_aligned(dout, t.d, e, 16);
-  x.q_four = K % 4 == 0 && rows_aligned(q, t.q, e, 4 * e);
-  x.part_vec = K % 4 == 0 && aligned(x.dq, dq_part ? 16 : 4 * e) && (x.dk_f32 || aligned(dk, 4 * e));
+  x.vec = a.move == 16 && r.move == 16 && aligned(x.dq, dq_part ? 16 : 4 * e) && aligned(x.dk, dk_part ? 16 : 4 * e);
   err = ssm::launch_gd_qk(x, dt_of(dt), s);
   ssm::LaSum sums[3];
   int n = 0;

@@ -113,17 +113,15 @@ struct GdGradArgs {
   const float *kept_e = nullptr, *kept_f = nullptr;      // kept of the two walks
   const int32_t* lengths = nullptr;
   void* dq = nullptr;                                    // [batch][L][H][K]; dq_f32: float32 (partial sums of a shared head)
-  float* dk_part = nullptr;                              // [batch][L][H][K] float32
-  void* dk = nullptr;                                    // [batch][L][H][K]; dk_f32: the sum stays in dk_part
+  float* dk_part = nullptr;                              // dk's forward part, [batch * H][chunks][64 or 128 columns][64]
+  void* dk = nullptr;                                    // [batch][L][H][K]; dk_f32: float32, as dq
   float *dg = nullptr, *dbeta = nullptr;                 // [batch][L][H]
   int64_t batch = 0, L = 0;
   int H = 0, K = 0, V = 0, every = 1;
   float scale = 1.0f;
   int dq_f32 = 0, dk_f32 = 0;
   int carried = 0;                                       // there is an initial state
-  int q_vec = 0, k_vec = 0, v_vec = 0, d_vec = 0;        // rows move as 8 elements
-  int q_four = 0;                                        // rows of q move as 4 elements
-  int part_vec = 0;                                      // rows of dq, dk and dk_part move as 4 elements
+  int vec = 0;                                           // rows of q, k, v and d move as 8 elements, those of dq and dk as 4
 };
 int gd_every(int64_t batch, int64_t L, int64_t H);
 hipError_t launch_gd_qk(const GdGradArgs& a, Dt dt, hipStream_t s);
