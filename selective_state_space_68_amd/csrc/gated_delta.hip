@@ -92,29 +92,39 @@ __global__ __launch_bounds__(256, 2) void gd_prepare_kernel(GdArgs p) {
     const bool on = lane < n;
     const float g_in = on ? p.g[gate] : 0.0f, beta = on ? p.beta[gate] : 0.0f;
 
-    // columns 32 y + 8 g .. of a row as an operand's
+    // rows 32 t + 8 (c / 4) + 4 u + c % 4 as operands: columns 32 y + 8 g ..; rows and columns that are not there are zeros
     const elem* kg = static_cast<const elem*>(p.k) + b * p.ks[0] + (h / p.kdiv) * p.ks[2] + t0 * p.ks[1];
     const elem* qg = static_cast<const elem*>(p.q) + b * p.qs[0] + (h / p.qdiv) * p.qs[2] + t0 * p.qs[1];
-    auto load_row = [&](const elem* base, int64_t stride, int row, piece (&out)[KT]) __attribute__((always_inline)) {
-      const int at = token(row);
-      const elem* from = base + at * stride + 8 * g;
+    const int perm_row = 8 * (c16 >> 2) + (c16 & 3);
+    auto load_rows = [&](const elem* base, int64_t stride, int t, piece (&out)[2][KT]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int y = 0; y < KT; ++y) {
-        out[y] = O::zero();
-        if constexpr (MOVE == 16) {
-          if (at < n && 32 * y + 8 * g < p.K) load_piece(reinterpret_cast<const char*>(from + 32 * y), out[y]);
-        } else {
-          elem v[8];
+      for (int u = 0; u < 2; ++u) {
+        const int at = token(32 * t + 4 * u + perm_row);
+        const elem* from = base + least(at, n - 1) * stride;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = at < n && 32 * y + 8 * g + e < p.K ? from[32 * y + e] : elem(0);
-          out[y] = __builtin_bit_cast(piece, v);
+        for (int y = 0; y < KT; ++y) {
+          const int col = 32 * y + 8 * g;
+          if constexpr (MOVE == 16) {
+            load_piece(reinterpret_cast<const char*>(from + least(col, p.K - 8)), out[u][y]);
+            if (at >= n || col >= p.K) out[u][y] = O::zero();
+          } else {
+            elem v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const elem x = from[least(col + e, p.K - 1)];
+              v[e] = at < n && col + e < p.K ? x : elem(0);
+            }
+            out[u][y] = __builtin_bit_cast(piece, v);
+          }
         }
       }
     };
-    const int perm_row = 8 * (c16 >> 2) + (c16 & 3);
-    piece kp[2][2][KT];                             // rows 32 t + 8 (c / 4) + 4 u + c % 4
+    piece kp[2][2][KT], qp[2][2][KT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load_row(kg, p.ks[1], 32 * (i / 2) + 4 * (i % 2) + perm_row, kp[i / 2][i % 2]);
+    for (int t = 0; t < 2; ++t) {
+      load_rows(kg, p.ks[1], t, kp[t]);
+      if constexpr (PT > 0) load_rows(qg, p.qs[1], t, qp[t]);
+    }
 
     // the running sum of g, in units of log 2, from float64 as a pair of float32
     {
@@ -141,10 +151,9 @@ __global__ __launch_bounds__(256, 2) void gd_prepare_kernel(GdArgs p) {
     }
     wave_lds();
 
-    // A's and the scores' tiles: rows i = 32 t + 8 g + 4 u + e, column j, for i <= j.  Forwards column j = 16 jt + c16 of k and
-    // q; backwards j = 32 two + 8 (c / 4) + 4 one + c % 4 of k, with the rows of k and of q.  An entry of A that is not finite
-    // belongs to a token whose state and whose successors' are not either (the walk sees to those); as a zero it leaves
-    // the rows before alone.
+    // A's and the scores' tiles: rows i = 32 t + 8 g + 4 u + e, column j = 32 two + 8 (c / 4) + 4 one + c % 4, for i <= j.  The
+    // scores are q_j.k_i, backwards q_i.k_j.  An entry of A that is not finite belongs to a token whose state and whose
+    // successors' are not either (the walk sees to those); as a zero it leaves the rows before alone.
     auto tile = [&](int t, int j, const f32x4_t (&s1)[2], const f32x4_t (&s2)[2], int x) __attribute__((always_inline)) {
       const float jhi = sHi[j], jlo = sLo[j];
       float v[8];
@@ -173,14 +182,12 @@ __global__ __launch_bounds__(256, 2) void gd_prepare_kernel(GdArgs p) {
           store_piece(rec + kTBytes<ACT> + kVecs * 256 + (x * PT + m) * kOne + lane * (kOne / 64), ps[m]);
       }
     };
-    if constexpr (!BACK) {
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt) {
-        piece kn[KT], qn[KT];
-        load_row(kg, p.ks[1], 16 * jt + c16, kn);
-        if constexpr (PT > 0) load_row(qg, p.qs[1], 16 * jt + c16, qn);
+    for (int two = 0; two < 2; ++two)
 #pragma unroll
-        for (int t = 0; t <= jt / 2; ++t) {
+      for (int t = 0; t <= two; ++t)
+#pragma unroll
+        for (int one = 0; one < 2; ++one) {
           f32x4_t s1[2], s2[2];
 #pragma unroll
           for (int u = 0; u < 2; ++u) s1[u] = s2[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -188,36 +195,12 @@ __global__ __launch_bounds__(256, 2) void gd_prepare_kernel(GdArgs p) {
           for (int y = 0; y < KT; ++y)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              s1[u] = O::mma(kp[t][u][y], kn[y], s1[u]);
-              if constexpr (PT > 0) s2[u] = O::mma(kp[t][u][y], qn[y], s2[u]);
+              s1[u] = O::mma(kp[t][u][y], kp[two][one][y], s1[u]);
+              if constexpr (PT > 0)
+                s2[u] = BACK ? O::mma(qp[t][u][y], kp[two][one][y], s2[u]) : O::mma(kp[t][u][y], qp[two][one][y], s2[u]);
             }
-          tile(t, 16 * jt + c16, s1, s2, jt + 2 * t);
+          tile(t, 32 * two + 4 * one + perm_row, s1, s2, 2 * two + 2 * t + one);
         }
-      }
-    } else {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        piece qp[2][KT];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) load_row(qg, p.qs[1], 32 * t + 4 * u + perm_row, qp[u]);
-#pragma unroll
-        for (int two = t; two < 2; ++two)
-#pragma unroll
-          for (int one = 0; one < 2; ++one) {
-            f32x4_t s1[2], s2[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) s1[u] = s2[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int y = 0; y < KT; ++y)
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                s1[u] = O::mma(kp[t][u][y], kp[two][one][y], s1[u]);
-                s2[u] = O::mma(qp[u][y], kp[two][one][y], s2[u]);
-              }
-            tile(t, 32 * two + 4 * one + perm_row, s1, s2, 2 * two + 2 * t + one);
-          }
-      }
-    }
     wave_lds();
 
     // the inverses of the diagonal blocks of I + A, in place: 16 lanes a block, lane c16 solves for its column
@@ -429,7 +412,7 @@ void gd_walk_kernel(GdArgs p) {
     if (count == 0 || (BACK ? seg == 0 : c_end == live && !(ident && p.seg_mt))) return;
   }
 
-  ChunkRows<elem, RK, NW, BACK, MOVE, BACK> q_rows_in;
+  ChunkRows<elem, RK, NW, true, MOVE, BACK> q_rows_in;
   ChunkRows<elem, RK, NW, true, MOVE, BACK> k_rows_in;
   ChunkRows<elem, RV, NW, false, MOVE, BACK> v_rows_in;
   if constexpr (SCORES)
@@ -482,7 +465,7 @@ void gd_walk_kernel(GdArgs p) {
   const int g0 = lane0 >> 4, col = 16 * w + (lane0 & 15);
   f32x4_t E[KT][2];
   auto there = [&](int t, int u, int e) { return ALL || (32 * t + 8 * g0 + 4 * u + e < K && col < width); };
-  auto place = [&](int t, int u, int e) {           // in a state in memory
+  auto entry = [&](int t, int u, int e) {           // in a state in memory
     return static_cast<uint32_t>((32 * t + 8 * g0 + 4 * u + e) * V + col0 + col);
   };
   auto each = [&](auto f) __attribute__((always_inline)) {
@@ -501,11 +484,11 @@ void gd_walk_kernel(GdArgs p) {
   each([&](int t, int u, int e) { E[t][u][e] = ident && 32 * t + 8 * g0 + 4 * u + e == col0 + col ? 1.0f : 0.0f; });
   if (src)
     each([&](int t, int u, int e) {
-      if (there(t, u, e)) E[t][u][e] = src[place(t, u, e)];
+      if (there(t, u, e)) E[t][u][e] = src[entry(t, u, e)];
     });
   auto put_state = [&](float* dst) __attribute__((always_inline)) {
     each([&](int t, int u, int e) {
-      if (there(t, u, e)) dst[place(t, u, e)] = E[t][u][e];
+      if (there(t, u, e)) dst[entry(t, u, e)] = E[t][u][e];
     });
   };
   if (count > 0) arrived(c_first, present(c_first), lane0);
@@ -533,7 +516,7 @@ void gd_walk_kernel(GdArgs p) {
     const char *t_in = rec + lane * (kOne / 64), *p_in = t_in + kTBytes<ACT> + kVecs * 256;   // operands of T, of the scores
     const uint32_t k_tile = lds_address(sKK[0]) + (c & 1) * (kQ * RK);
     const int perm_row = 8 * (c16 >> 2) + (c16 & 3);
-    const uint32_t q_rows = O::template row_part<RK, BACK>(lds_address(sQ), BACK ? perm_row : c16, g);
+    const uint32_t q_rows = O::template row_part<RK, true>(lds_address(sQ), perm_row, g);
     const uint32_t k_rows = O::template row_part<RK, true>(k_tile, perm_row, g);
     auto eight = [&](int which, int t, float (&x)[8]) __attribute__((always_inline)) {   // a vector's tokens 32 t + 8 g ..
       const float4 a = *reinterpret_cast<const float4*>(vec + which * 64 + 32 * t + 8 * g);
@@ -545,8 +528,9 @@ void gd_walk_kernel(GdArgs p) {
       return O::row(rows + t * (32 * RK), (4 * PB * y) ^ (u ? swizzle<RK, kF32, true>(4) << 4 : 0), 4 * u * RK);
     };
 
-    // ---- K E (rows token 32 t + 8 g + 4 u + e, column v) and Q E, transposed (rows v, column j = 16 jt + c16).  Products
+    // ---- K E (rows token 32 t + 8 g + 4 u + e, column v) and Q E, transposed (rows v, column j = place(jt)).  Products
     // on different sums follow each other, here and below: one on the last's sum waits for it.
+    auto place = [&](int jt) { return 32 * (jt / 2) + 4 * (jt % 2) + perm_row; };     // token of column c16 of tile jt
     f32x4_t R[2][2], acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = R[i / 2][i % 2] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -558,7 +542,7 @@ void gd_walk_kernel(GdArgs p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         kf[i] = permuted(k_rows, i / 2, i % 2, y);
-        if constexpr (MODE == kOut) qf[i] = O::row(q_rows, 4 * PB * y, 16 * i * RK);
+        if constexpr (MODE == kOut) qf[i] = permuted(q_rows, i / 2, i % 2, y);
       }
 #pragma unroll
       for (int m = NT - 1; m >= 0; --m) {
@@ -715,7 +699,7 @@ void gd_walk_kernel(GdArgs p) {
     if constexpr (MODE == kOut) {
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
-        const float f = p.scale * vec[kInto * 64 + 16 * jt + c16];
+        const float f = p.scale * vec[kInto * 64 + place(jt)];
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[jt][e] *= f;
       }
@@ -741,7 +725,7 @@ void gd_walk_kernel(GdArgs p) {
           const int from = __shfl(gone, 4 * g + e);
 #pragma unroll
           for (int jt = 0; jt < 4; ++jt)
-            if (16 * jt + c16 >= from) acc[jt][e] = __builtin_nanf("");
+            if (place(jt) >= from) acc[jt][e] = __builtin_nanf("");
         }
       }
     }
@@ -794,7 +778,7 @@ void gd_walk_kernel(GdArgs p) {
     }
     arrived(c + c_step, more ? present(c + c_step) : kQ, lane);
 
-    // ---- the output rows to memory: lane (g, c) has 4 columns of token 16 jt + c
+    // ---- the output rows to memory: lane (g, c) has 4 columns of token place(jt)
     if constexpr (MODE == kOut) {
       auto four = [](const f32x4_t& a) __attribute__((always_inline)) {
         if constexpr (kF32) return make_float4(a[0], a[1], a[2], a[3]);
@@ -805,10 +789,10 @@ void gd_walk_kernel(GdArgs p) {
       if (n == kQ && p.o_vec) {                     // a uniform address, the lane's offset, 16 rows' bytes
         char* rows = static_cast<char*>(p.o) + ((b * L + static_cast<int64_t>(c) * kQ) * row_stride + static_cast<int64_t>(h) * V + col0) *
                                                    static_cast<int64_t>(sizeof(elem));
-        const uint32_t step = static_cast<uint32_t>(row_stride) * sizeof(elem), off = c16 * step + v0 * sizeof(elem);
+        const uint32_t step = static_cast<uint32_t>(row_stride) * sizeof(elem), off = v0 * sizeof(elem);
         if (ALL || v0 < width) {
 #pragma unroll
-          for (int jt = 0; jt < 4; ++jt) *reinterpret_cast<decltype(four(acc[0]))*>(rows + (off + jt * 16 * step)) = four(acc[jt]);
+          for (int jt = 0; jt < 4; ++jt) *reinterpret_cast<decltype(four(acc[0]))*>(rows + (off + place(jt) * step)) = four(acc[jt]);
         }
         continue;
       }
@@ -816,7 +800,7 @@ void gd_walk_kernel(GdArgs p) {
                   col0 + v0;
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
-        const int row = 16 * jt + c16;
+        const int row = place(jt);
         if (c * kQ + row >= L) continue;
         elem* o = out + row * row_stride;
         if (row >= n) acc[jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -868,57 +852,59 @@ void gd_walk_kernel(GdArgs p) {
 }
 
 // The states that enter the segments, over what each made of none: forwards S = M S + N from the first on, backwards
-// F = M^T F + N from the last.  A wave owns 16 columns, a state's as above, through all segments; float32 products.
+// F = M^T F + N from the last.  A workgroup takes 16 columns through all segments, wave w rows 32 w .. of them; the state
+// goes round in operand order through LDS.  Float32 products.
 template <int KD, bool BACK>
-__global__ __launch_bounds__(64) void gd_chain_kernel(GdArgs p) {
+__global__ __launch_bounds__(2 * KD) void gd_chain_kernel(GdArgs p) {
   using O = Op<ActF32>;
   constexpr int KT = KD / 32;
-  const int lane = threadIdx.x, g = lane >> 4, c16 = lane & 15, K = p.K, V = p.V, nseg = p.nseg;
+  __shared__ __attribute__((aligned(16))) F8 sS[2][KT][64];
+  const int lane = threadIdx.x & 63, w = uniform_int(threadIdx.x >> 6), g = lane >> 4, c16 = lane & 15;
+  const int K = p.K, V = p.V, nseg = p.nseg;
   const int64_t bh = blockIdx.x;
   const int col = 16 * blockIdx.y + c16;
   const int len = gd_length(p.lengths, static_cast<int>(p.L), blockIdx.x / static_cast<uint32_t>(p.H));
   const int live = (len + kQ - 1) / kQ, count = (live + p.seg_chunks - 1) / p.seg_chunks;   // segments with tokens
-  f32x4_t S[KT][2];
+  float S[8];                                       // rows 32 w + 8 g + e, column c16
   auto each = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int k = 32 * t + 8 * g + 4 * u + e;
-          f(t, u, e, k < K && col < V, k * V + col);
-        }
+    for (int e = 0; e < 8; ++e) {
+      const int k = 32 * w + 8 * g + e;
+      f(e, k < K && col < V, k * V + col);
+    }
   };
   const float* carry = p.carry ? p.carry + bh * static_cast<int64_t>(K) * V : nullptr;
-  each([&](int t, int u, int e, bool in, int at) { S[t][u][e] = carry && in ? carry[at] : 0.0f; });
+  each([&](int e, bool in, int at) { S[e] = carry && in ? carry[at] : 0.0f; });
   const float* ms = (BACK ? p.seg_mt : p.seg_m) + bh * nseg * static_cast<int64_t>(KD * KD);
   float* segs = p.seg + bh * nseg * static_cast<int64_t>(K) * V;
   for (int i = 0; i < (count > 0 ? count : 1); ++i) {
     const int s = BACK && count > 0 ? count - 1 - i : i;
     float* at_s = segs + s * static_cast<int64_t>(K) * V;
-    f32x4_t next[KT][2];
     const bool on = i + 1 < count;                  // (the last one's result is the walk's to find)
-    if (on) each([&](int t, int u, int e, bool in, int at) { next[t][u][e] = in ? at_s[at] : 0.0f; });
-    each([&](int t, int u, int e, bool in, int at) {
-      if (in) at_s[at] = S[t][u][e];
+    f32x4_t next[2];
+    F8 m[2][KT];
+    if (on) {
+      each([&](int e, bool in, int at) { next[e / 4][e % 4] = in ? at_s[at] : 0.0f; });
+      const float* from = ms + s * static_cast<int64_t>(KD * KD) + (32 * w + 8 * (c16 >> 2) + (c16 & 3)) * KD + 8 * g;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int y = 0; y < KT; ++y) load_piece(reinterpret_cast<const char*>(from + 4 * u * KD + 32 * y), m[u][y]);
+    }
+    each([&](int e, bool in, int at) {
+      if (in) at_s[at] = S[e];
     });
     if (!on) break;
-    const float* m = ms + s * static_cast<int64_t>(KD * KD) + (8 * (c16 >> 2) + (c16 & 3)) * KD + 8 * g;
+    sS[i & 1][w][lane] = O::pack(S);
+    __syncthreads();                                // (the other buffer was read before)
 #pragma unroll
     for (int y = 0; y < KT; ++y) {
-      const float x[8] = {S[y][0][0], S[y][0][1], S[y][0][2], S[y][0][3], S[y][1][0], S[y][1][1], S[y][1][2], S[y][1][3]};
-      const F8 right = O::pack(x);
+      const F8 right = sS[i & 1][y][lane];
 #pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          F8 left;
-          load_piece(reinterpret_cast<const char*>(m + (32 * t + 4 * u) * KD + 32 * y), left);
-          next[t][u] = O::mma(left, right, next[t][u]);
-        }
+      for (int u = 0; u < 2; ++u) next[u] = O::mma(m[u][y], right, next[u]);
     }
-    each([&](int t, int u, int e, bool, int) { S[t][u][e] = next[t][u][e]; });
+#pragma unroll
+    for (int e = 0; e < 8; ++e) S[e] = next[e / 4][e % 4];
   }
 }
 
@@ -937,7 +923,7 @@ void launch_gd_t(const GdArgs& a, hipStream_t s) {
   if (a.nseg > 1) {
     launch_walk<ACT, KD, COLUMNS, MOVE, ALL, BACK ? kBackState : kState, PR>(a, s);
     const dim3 grid(static_cast<unsigned>(a.batch * a.H), static_cast<unsigned>((a.V + 15) / 16));
-    hipLaunchKernelGGL((gd_chain_kernel<KD, BACK>), grid, dim3(64), 0, s, a);
+    hipLaunchKernelGGL((gd_chain_kernel<KD, BACK>), grid, dim3(2 * KD), 0, s, a);
   }
   launch_walk<ACT, KD, COLUMNS, MOVE, ALL, MODE, PR>(a, s);
 }

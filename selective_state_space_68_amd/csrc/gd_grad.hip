@@ -157,8 +157,8 @@ void gd_qk_kernel(GdGradArgs p) {
   } in;
   // in four parts, 0 to 3, spread over the chunk before: asked for at once, they keep the loads' unit busy for thousands of
   // cycles while the waves wait for their turn
-  auto ask = [&](int c, int part) __attribute__((always_inline)) {
-    int id = tid;
+  auto ask = [&](int c, int part, bool wanted) __attribute__((always_inline)) {
+    int id = wanted ? tid : 0;
     asm volatile("" : "+v"(id));                    // (so that no address is kept over the loop)
     const int n = least(len - c * kQ, kQ);
     const int64_t t0 = static_cast<int64_t>(c) * kQ, rows = (bh * nchunks + c) * kQ;
@@ -247,7 +247,7 @@ void gd_qk_kernel(GdGradArgs p) {
   };
   auto chunk_of = [&](int done) { return BACK ? c_end - 1 - done : c_begin + done; };
 #pragma unroll
-  for (int part = 0; part < 4; ++part) ask(chunk_of(0), part);
+  for (int part = 0; part < 4; ++part) ask(chunk_of(0), part, true);
 
   // E[y][u][e] is the entry v = 32 y + 8 g + 4 u + e, k = 16 w + c16 (backwards of the gradient F)
   const int col = 16 * w + c16;
@@ -324,7 +324,9 @@ void gd_qk_kernel(GdGradArgs p) {
       }
     }
     const bool more = done + 1 < c_end - c_begin;
-    if (more) ask(chunk_of(done + 1), 0);
+    // (the last chunk asks for one place: after a load on one side of a branch every wait is for all loads)
+    const int next = chunk_of(more ? done + 1 : done);
+    ask(next, 0, more);
     // the wave's own columns of k (and of q): tokens 32 t + 8 g + e of column c16
     piece kf[2], qf[2];
     if constexpr (TILES) {
@@ -414,7 +416,7 @@ void gd_qk_kernel(GdGradArgs p) {
       for (int m = 0; m < OT; ++m) store_piece(sN2 + (x * OT + m) * kOne + lane * (kOne / 64), o2[m]);
     }
 
-    if (more) ask(chunk_of(done + 1), 1);
+    ask(next, 1, more);
     // ---- the state's part, rows k, column j = 16 jt + c16: acc of D and acy of Y, backwards acc of W
     f32x4_t acc[4], acy[4];
 #pragma unroll
@@ -465,7 +467,7 @@ void gd_qk_kernel(GdGradArgs p) {
         if constexpr (!BACK) acy[jt][e] *= -(beta * into);
       }
     }
-    if (more) ask(chunk_of(done + 1), 2);
+    ask(next, 2, more);
     __syncthreads();                                // N1 and N2 are complete
 
     // ---- the chunk's own part
@@ -540,7 +542,7 @@ void gd_qk_kernel(GdGradArgs p) {
         *reinterpret_cast<float4*>(part + jt * 256) = make_float4(acy[jt][0], acy[jt][1], acy[jt][2], acy[jt][3]);
     }
 
-    if (more) ask(chunk_of(done + 1), 3);
+    ask(next, 3, more);
     // ---- the state
     if (more || !BACK) {      // (backwards the last is of no use)
       const float whole = vec[kWhole * 64];
