@@ -32,16 +32,6 @@ namespace {
 
 constexpr int kMostEvery = 16;
 
-// The sum over N = 8 or 16 neighbouring lanes: quads, then the quads of 8, then of 16.
-template <int N>
-__device__ __forceinline__ float row_sum(float v) {
-  v += dpp_mov<0xb1, 0xf, true>(0.0f, v);           // quad_perm [1, 0, 3, 2]
-  v += dpp_mov<0x4e, 0xf, true>(0.0f, v);           // quad_perm [2, 3, 0, 1]
-  v += dpp_mov<0x141, 0xf, true>(0.0f, v);          // row_half_mirror
-  if constexpr (N == 16) v += dpp_mov<0x140, 0xf, true>(0.0f, v);   // row_mirror
-  return v;
-}
-
 // Eight values of a row from memory.  Nothing is decided where they move as vectors: rows and columns that are not there
 // repeat the last ones (they are cleared on the way into LDS).
 template <bool VEC>

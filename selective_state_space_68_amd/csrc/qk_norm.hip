@@ -40,7 +40,8 @@ __device__ __forceinline__ void store4(void* p, int64_t i, const float (&v)[4]) 
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
-// sin and cos of position * frequency.
+// sin and cos of position * frequency.  (The hardware's sine of turns for bfloat16 rows saved 1 of 128 us: 16384 x 40 heads of
+// 128, gradient.)
 __device__ __forceinline__ void turn_of(double position, float frequency, float* s, float* c) {
   double turns = position * static_cast<double>(frequency) * 0.15915494309189535;      // over 2 pi
   turns -= __builtin_rint(turns);
@@ -153,8 +154,9 @@ struct Row {
       for (int m = 0; m < 2; ++m) x[i][m] = w && any && col[i][m] >= 0 ? w[col[i][m]] : 1.0f;
   }
   static __device__ __forceinline__ float sum(float v) {
-#pragma unroll
-    for (int d = 1; d < G; d *= 2) v += __shfl_xor(v, d);
+    if constexpr (G == 64) return wave_sum(v);
+    v = row_sum<G == 8 ? 8 : 16>(v);
+    if constexpr (G == 32) v += __shfl_xor(v, 16);
     return v;
   }
 };
@@ -188,25 +190,28 @@ __global__ __launch_bounds__(kThreads) void qk_norm_kernel(QkArgs p) {
     const int first = static_cast<int>(item - token * p.split);
     const int64_t b = p.batch == 1 ? 0 : token / p.L, t = token - b * p.L;
     row.turns(p, at.lane, token);
-    for (int h = first; h < p.Hq + p.Hk; h += p.split) {
-      const bool key = h >= p.Hq;
-      const int head = key ? h - p.Hq : h;
-      const int64_t* st = key ? p.ks : p.qs;
-      float x[R::N][2];
-      row.load(key ? p.k : p.q, b * st[0] + t * st[1] + head * st[2], x);
-      float ss = 0.0f;
+    auto heads = [&](int h, int count, const void* in, const int64_t (&st)[3], const float (&wt)[R::N][2], void* out)
+                     __attribute__((always_inline)) {
+      const int64_t base = b * st[0] + t * st[1], to = token * count;
+      for (; h < count; h += p.split) {
+        float x[R::N][2];
+        row.load(in, base + h * st[2], x);
+        float ss = 0.0f;
 #pragma unroll
-      for (int i = 0; i < R::N; ++i) ss = __builtin_fmaf(x[i][0], x[i][0], __builtin_fmaf(x[i][1], x[i][1], ss));
-      ss = R::sum(ss);
-      const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, p.inv_count, p.eps));
+        for (int i = 0; i < R::N; ++i) ss = __builtin_fmaf(x[i][0], x[i][0], __builtin_fmaf(x[i][1], x[i][1], ss));
+        ss = R::sum(ss);
+        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, p.inv_count, p.eps));
 #pragma unroll
-      for (int i = 0; i < R::N; ++i) {
-        const float a = x[i][0] * r * (key ? wk[i][0] : wq[i][0]), d = x[i][1] * r * (key ? wk[i][1] : wq[i][1]);
-        x[i][0] = __builtin_fmaf(a, row.c[i], -d * row.s[i]);
-        x[i][1] = __builtin_fmaf(d, row.c[i], a * row.s[i]);
+        for (int i = 0; i < R::N; ++i) {
+          const float a = x[i][0] * r * wt[i][0], d = x[i][1] * r * wt[i][1];
+          x[i][0] = __builtin_fmaf(a, row.c[i], -d * row.s[i]);
+          x[i][1] = __builtin_fmaf(d, row.c[i], a * row.s[i]);
+        }
+        row.store(out, (to + h) * p.K, x);
       }
-      row.store(key ? p.ko : p.qo, (token * (key ? p.Hk : p.Hq) + head) * p.K, x);
-    }
+      return h - count;                             // (the first of the next tensor's heads)
+    };
+    heads(heads(first, p.Hq, p.q, p.qs, wq, p.qo), p.Hk, p.k, p.ks, wk, p.ko);
   }
 }
 
@@ -227,39 +232,41 @@ __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkArgs p) {
     const int first = static_cast<int>(item - token * p.split);
     const int64_t b = p.batch == 1 ? 0 : token / p.L, t = token - b * p.L;
     row.turns(p, at.lane, token);
-    for (int h = first; h < p.Hq + p.Hk; h += p.split) {
-      const bool key = h >= p.Hq;
-      const int head = key ? h - p.Hq : h;
-      const int64_t *st = key ? p.ks : p.qs, *ds = key ? p.dks : p.dqs;
-      float x[R::N][2], y[R::N][2];
-      row.load(key ? p.k : p.q, b * st[0] + t * st[1] + head * st[2], x);
-      row.load(key ? p.dko : p.dqo, b * ds[0] + t * ds[1] + head * ds[2], y);
-      float ss = 0.0f;
+    auto heads = [&](int h, int count, const void* in, const int64_t (&st)[3], const void* grad, const int64_t (&ds)[3],
+                     const float (&wt)[R::N][2], float (&dw)[R::N][2], void* out) __attribute__((always_inline)) {
+      const int64_t base = b * st[0] + t * st[1], dbase = b * ds[0] + t * ds[1], to = token * count;
+      for (; h < count; h += p.split) {
+        float x[R::N][2], y[R::N][2];
+        row.load(in, base + h * st[2], x);
+        row.load(grad, dbase + h * ds[2], y);
+        float ss = 0.0f;
 #pragma unroll
-      for (int i = 0; i < R::N; ++i) ss = __builtin_fmaf(x[i][0], x[i][0], __builtin_fmaf(x[i][1], x[i][1], ss));
-      ss = R::sum(ss);
-      const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, p.inv_count, p.eps));
-      float dot = 0.0f;
+        for (int i = 0; i < R::N; ++i) ss = __builtin_fmaf(x[i][0], x[i][0], __builtin_fmaf(x[i][1], x[i][1], ss));
+        ss = R::sum(ss);
+        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, p.inv_count, p.eps));
+        float dot = 0.0f;
 #pragma unroll
-      for (int i = 0; i < R::N; ++i) {
-        const float a = __builtin_fmaf(y[i][0], row.c[i], y[i][1] * row.s[i]);       // dn: turned back
-        const float d = __builtin_fmaf(y[i][1], row.c[i], -y[i][0] * row.s[i]);
-        x[i][0] *= r;
-        x[i][1] *= r;
-        const float da = a * x[i][0], dd = d * x[i][1];
-        if (key) { dwk[i][0] += da; dwk[i][1] += dd; }
-        else { dwq[i][0] += da; dwq[i][1] += dd; }
-        y[i][0] = a * (key ? wk[i][0] : wq[i][0]);
-        y[i][1] = d * (key ? wk[i][1] : wq[i][1]);
-        dot = __builtin_fmaf(y[i][0], x[i][0], __builtin_fmaf(y[i][1], x[i][1], dot));
+        for (int i = 0; i < R::N; ++i) {
+          const float a = __builtin_fmaf(y[i][0], row.c[i], y[i][1] * row.s[i]);       // dn: turned back
+          const float d = __builtin_fmaf(y[i][1], row.c[i], -y[i][0] * row.s[i]);
+          x[i][0] *= r;
+          x[i][1] *= r;
+          dw[i][0] = __builtin_fmaf(a, x[i][0], dw[i][0]);
+          dw[i][1] = __builtin_fmaf(d, x[i][1], dw[i][1]);
+          y[i][0] = a * wt[i][0];
+          y[i][1] = d * wt[i][1];
+          dot = __builtin_fmaf(y[i][0], x[i][0], __builtin_fmaf(y[i][1], x[i][1], dot));
+        }
+        dot = R::sum(dot) * p.inv_count;
+#pragma unroll
+        for (int i = 0; i < R::N; ++i)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) y[i][m] = r * __builtin_fmaf(-x[i][m], dot, y[i][m]);
+        row.store(out, (to + h) * p.K, y);
       }
-      dot = R::sum(dot) * p.inv_count;
-#pragma unroll
-      for (int i = 0; i < R::N; ++i)
-#pragma unroll
-        for (int m = 0; m < 2; ++m) y[i][m] = r * __builtin_fmaf(-x[i][m], dot, y[i][m]);
-      row.store(key ? p.ko : p.qo, (token * (key ? p.Hk : p.Hq) + head) * p.K, y);
-    }
+      return h - count;
+    };
+    heads(heads(first, p.Hq, p.q, p.qs, p.dqo, p.dqs, wq, dwq, p.qo), p.Hk, p.k, p.ks, p.dko, p.dks, wk, dwk, p.ko);
   }
   constexpr int kGroups = kThreads / G;
 #pragma unroll
@@ -321,12 +328,14 @@ void launch_t(const QkArgs& a, dim3 grid, hipStream_t s) {
   else go(wave, std::integral_constant<int, 4>{}, std::false_type{});
 }
 
-// Groups of lanes for a token's heads, and workgroups.
+// Groups of lanes for a token's heads, and workgroups.  A group's angles cost more than a row, so it takes as many heads as leave
+// enough groups: 16384 x 40 heads of 128, rotated, gradient: 120 us with 2 groups a token, 124 with one, 127 with 5, 135 with
+// 10.  (Twice the workgroups: 6 % more; half: 25 %.)
 dim3 plan(QkArgs* a, int64_t most) {
   const int64_t tokens = a->batch * a->L;
   const int heads = a->Hq + a->Hk, groups = groups_of(*a);
   int split = 1;
-  while (split < heads && (tokens * split < 8192 || heads / split > 8)) ++split;
+  while (split < heads && tokens * split < 32768) ++split;
   a->split = split;
   const int64_t blocks = (tokens * split + groups - 1) / groups;
   return dim3(static_cast<unsigned>(blocks < most ? blocks : most));
