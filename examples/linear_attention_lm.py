@@ -1,6 +1,6 @@
-"""A small language model of linear attention blocks, trained and then served, on one GPU.
+"""A small language model of linear attention or gated delta rule blocks, trained and then served, on one GPU.
 
-    python examples/linear_attention_lm.py [--steps 80] [--batch 16] [--length 256] [--serve 8]
+    python examples/linear_attention_lm.py [--mixer delta] [--steps 80] [--batch 16] [--length 256] [--serve 8]
 
 Every block is
 
@@ -8,7 +8,9 @@ Every block is
     h = h + t W_out;          y = norm(h)   (the norm in front of the next block)
 
 where the attention, both norms, the gate and the residual sum run as the library's kernels, forward and backward, and the
-projections are matrix products.  Training shows one step of each; serving runs prompts of unequal lengths at once, keeps
+projections are matrix products.  With --mixer delta, the projection also gives each head a decay and a writing strength for
+every token, queries and keys are rotated by position and scaled to length 1, and the gated delta rule takes the
+attention's place.  Training shows one step of each; serving runs prompts of unequal lengths at once, keeps
 every sequence's states in a pool, and continues them token by token from the pool's slots.  The data are synthetic: a
 random permutation of the vocabulary is followed with probability 0.9, else a token is drawn at random.
 """
@@ -36,6 +38,33 @@ class LinearAttention(torch.autograd.Function):
         q, k, v, log_decay = ctx.saved_tensors
         g = ssm.linear_attention_bwd(q, k, v, log_decay, dout)
         return g["dq"], g["dk"], g["dv"], None
+
+
+class UnitHeads(torch.autograd.Function):
+    """Queries and keys rotated by their positions, of length 1."""
+    @staticmethod
+    def forward(ctx, q, k, inv_freq):
+        ctx.save_for_backward(q, k, inv_freq)
+        return ssm.qk_norm_fwd(q, k, norm="l2", inv_freq=inv_freq)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        q, k, inv_freq = ctx.saved_tensors
+        g = ssm.qk_norm_bwd(q, k, dq, dk, norm="l2", inv_freq=inv_freq)
+        return g["dq"], g["dk"], None
+
+
+class GatedDelta(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta):
+        ctx.save_for_backward(q, k, v, g, beta)
+        return ssm.gated_delta_fwd(q, k, v, g, beta, return_final_state=False)[0]
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, g, beta = ctx.saved_tensors
+        d = ssm.gated_delta_bwd(q, k, v, g, beta, dout)
+        return d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"]
 
 
 class GatedHeadNorm(torch.autograd.Function):
@@ -69,13 +98,14 @@ class AddNorm(torch.autograd.Function):
 
 
 class Model(torch.nn.Module):
-    def __init__(self, vocab=256, dim=256, heads=4, layers=2, device="cuda"):
+    def __init__(self, vocab=256, dim=256, heads=4, layers=2, device="cuda", mixer="attention"):
         super().__init__()
-        self.vocab, self.dim, self.heads, self.layers = vocab, dim, heads, layers
+        self.vocab, self.dim, self.heads, self.layers, self.mixer = vocab, dim, heads, layers, mixer
         par = lambda *s, std: torch.nn.Parameter(torch.randn(*s, device=device) * std)
         one = lambda: torch.nn.Parameter(torch.ones(dim, device=device))
         self.embed = par(vocab, dim, std=1.0)
-        self.w_in = torch.nn.ParameterList([par(dim, 4 * dim, std=dim ** -0.5) for _ in range(layers)])
+        gates = 2 * heads if mixer == "delta" else 0
+        self.w_in = torch.nn.ParameterList([par(dim, 4 * dim + gates, std=dim ** -0.5) for _ in range(layers)])
         self.w_out = torch.nn.ParameterList([par(dim, dim, std=(2 * layers * dim) ** -0.5) for _ in range(layers)])
         self.head_norm = torch.nn.ParameterList([one() for _ in range(layers)])
         self.norm = torch.nn.ParameterList([one() for _ in range(layers + 1)])
@@ -83,12 +113,19 @@ class Model(torch.nn.Module):
         # the heads forget at rates from 2^-2 to 2^-2-heads
         rates = torch.log1p(-(2.0 ** -(2.0 + torch.arange(heads, dtype=torch.float32))))
         self.register_buffer("log_decay", rates.to(device))
+        pairs = torch.arange(dim // heads // 2, dtype=torch.float32)
+        self.register_buffer("inv_freq", (10000.0 ** (-2.0 * pairs / (dim // heads))).to(device))
 
     def project(self, y, layer):
         """q, k, v [..., heads, dim / heads] and gate [..., dim]: views of one product."""
-        z = (y @ self.w_in[layer].to(y.dtype)).unflatten(-1, (4, self.dim))
-        q, k, v = (z[..., i, :].unflatten(-1, (self.heads, -1)) for i in range(3))
-        return q, k, v, z[..., 3, :]
+        z = y @ self.w_in[layer].to(y.dtype)
+        four = z[..., :4 * self.dim].unflatten(-1, (4, self.dim))
+        q, k, v = (four[..., i, :].unflatten(-1, (self.heads, -1)) for i in range(3))
+        if self.mixer == "delta":
+            raw = z[..., 4 * self.dim:].float()
+            g = self.log_decay * nnf.softplus(raw[..., :self.heads])
+            return q, k, v, four[..., 3, :], g.contiguous(), torch.sigmoid(raw[..., self.heads:]).contiguous()
+        return q, k, v, four[..., 3, :]
 
     def logits(self, y):
         return (y @ self.unembed.to(y.dtype)).float()
@@ -99,8 +136,11 @@ class Model(torch.nn.Module):
         h = torch.zeros(x.shape, device=x.device)
         for i in range(self.layers):
             h, y = AddNorm.apply(x, h, self.norm[i])
-            q, k, v, gate = self.project(y, i)
-            o = LinearAttention.apply(q, k, v, self.log_decay)
+            q, k, v, gate, *gates = self.project(y, i)
+            if self.mixer == "delta":
+                o = GatedDelta.apply(*UnitHeads.apply(q, k, self.inv_freq), v, *gates)
+            else:
+                o = LinearAttention.apply(q, k, v, self.log_decay)
             x = GatedHeadNorm.apply(o.flatten(-2), gate, self.head_norm[i], self.heads) @ self.w_out[i].to(x.dtype)
         h, y = AddNorm.apply(x, h, self.norm[-1])
         return self.logits(y)
@@ -111,14 +151,14 @@ class Model(torch.nn.Module):
         return [torch.zeros(slots, self.heads, d, d, device=self.log_decay.device) for _ in range(self.layers)]
 
     def serve(self, tokens, mix):
-        """Logits for tokens [..., length or none]; mix(layer, q, k, v) is the attention of a prompt or of a token."""
+        """Logits for tokens [..., length or none]; mix(layer, q, k, v, ...) is the attention of a prompt or of a token."""
         x = self.embed[tokens].bfloat16()
         h = torch.zeros(x.shape, device=x.device)
         y = torch.empty_like(x)
         for i in range(self.layers):
             ssm.block_norm_fwd(x, h, pre_weight=self.norm[i], h=h, y=y)           # h in place
-            q, k, v, gate = self.project(y, i)
-            o = mix(i, q, k, v).flatten(-2)
+            q, k, v, gate, *gates = self.project(y, i)
+            o = mix(i, q, k, v, *gates).flatten(-2)
             t = ssm.block_norm_fwd(o, gate=gate, post_weight=self.head_norm[i], groups=self.heads)[0]
             x = t @ self.w_out[i].to(x.dtype)
         ssm.block_norm_fwd(x, h, pre_weight=self.norm[-1], h=h, y=y)
@@ -127,17 +167,25 @@ class Model(torch.nn.Module):
     @torch.no_grad()
     def prefill(self, tokens, lengths, pool, slots):
         """Prompts [batch, length] of `lengths` tokens each; their states go to the pool's `slots`."""
-        def mix(i, q, k, v):
-            o, state = ssm.linear_attention_fwd(q, k, v, self.log_decay, lengths=lengths)
+        def mix(i, q, k, v, *gates):
+            if self.mixer == "delta":
+                q, k = ssm.qk_norm_fwd(q, k, norm="l2", inv_freq=self.inv_freq)
+                o, state = ssm.gated_delta_fwd(q, k, v, *gates, lengths=lengths)
+            else:
+                o, state = ssm.linear_attention_fwd(q, k, v, self.log_decay, lengths=lengths)
             pool[i][slots.long()] = state
             return o
         return self.serve(tokens, mix)
 
     @torch.no_grad()
-    def step(self, tokens, pool, slots):
-        """One token for every row; a row whose slot is -1 is idle."""
-        return self.serve(tokens, lambda i, q, k, v: ssm.linear_attention_step(pool[i], q, k, v, self.log_decay,
-                                                                               slots=slots))
+    def step(self, tokens, pool, slots, positions=None):
+        """One token for every row; a row whose slot is -1 is idle.  positions [batch] int32: the tokens' (mixer "delta")."""
+        def mix(i, q, k, v, *gates):
+            if self.mixer == "delta":
+                q, k = ssm.qk_norm_fwd(q, k, norm="l2", inv_freq=self.inv_freq, positions=positions)
+                return ssm.gated_delta_step(pool[i], q, k, v, *gates, slots=slots)
+            return ssm.linear_attention_step(pool[i], q, k, v, self.log_decay, slots=slots)
+        return self.serve(tokens, mix)
 
 
 def batch_of(permutation, batch, length, generator):
@@ -178,10 +226,10 @@ def generate(model, prompts, lengths, new_tokens):
     logits = model.prefill(prompts, lengths.int(), pool, slots)
     last = logits[torch.arange(batch, device=prompts.device), lengths.long() - 1]
     out, seen = [], []
-    for _ in range(new_tokens):
+    for i in range(new_tokens):
         out.append(last.argmax(-1))
         seen.append(last)
-        last = model.step(out[-1], pool, slots)
+        last = model.step(out[-1], pool, slots, (lengths + i).int())
     return torch.stack(out, 1), torch.stack(seen, 1)
 
 
@@ -189,9 +237,10 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     for name, value in (("steps", 80), ("batch", 16), ("length", 256), ("serve", 8)):
         ap.add_argument(f"--{name}", type=int, default=value)
+    ap.add_argument("--mixer", choices=("attention", "delta"), default="attention")
     args = ap.parse_args()
     torch.manual_seed(0)
-    model = Model()
+    model = Model(mixer=args.mixer)
     start = time.time()
     losses, permutation = train(model, args.steps, args.batch, args.length)
     best = -0.9 * math.log(0.9 + 0.1 / model.vocab) - 0.1 * math.log(0.1 / model.vocab)
