@@ -979,7 +979,7 @@ constexpr int kSegTarget = 256;
 // Segments per sequence.  The pre-pass walks V + K columns where the main pass walks V, so segments are worth it only
 // where few workgroups walk long sequences: up to 2 workgroups a CU, at least 4 of them, each 4 chunks or longer.  The count is
 // then derived back from the segment length, so that no segment is without a chunk.
-int gd_segments(int64_t batch, int64_t L, int64_t H, int64_t V) {
+int gd_segments(int64_t batch, int64_t L, int64_t H) {
   const int64_t workgroups = batch * H, nch = (L + kQ - 1) / kQ;
   int64_t s = kSegTarget / (workgroups > 0 ? workgroups : 1);
   if (s > nch / 4) s = nch / 4;

@@ -101,7 +101,7 @@ void gd_qk_kernel(GdGradArgs p) {
   __shared__ __attribute__((aligned(512))) char sN2[kT * OT * kOne];
   __shared__ __attribute__((aligned(16))) float vec[kVecs * 64];
   // the tokens' scalars, of this chunk and of the one before: parts of q.dq, y.w and y.v, beta
-  __shared__ float sSum[2][NW][kQ], sDot[2][3][kQ], sAll[BACK ? 1 : kMostEvery * kQ];
+  __shared__ float sSum[2][NW][kQ], sDot[2][3][kQ];
 
   const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6), g = lane >> 4, c16 = lane & 15;
   const int L = static_cast<int>(p.L), K = p.K, V = p.V;
@@ -225,15 +225,16 @@ void gd_qk_kernel(GdGradArgs p) {
         if (!BACK && (tid + i * THREADS) / 64 == kBeta) sDot[which][2][tid % 64] = in.vec[i];
       }
   };
-  // A chunk's tokens (one wave, when they are complete).
+  // A chunk's tokens (one wave, when they are complete): dbeta, and in dg's place what the sums at the end are of.
   auto scalars = [&](int done) __attribute__((always_inline)) {
     const int which = done & 1, t = (c_begin + done) * kQ + lane;
     if (t >= len) return;
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NW; ++i) sum += sSum[which][i][lane];
-    sAll[done * kQ + lane] = __builtin_fmaf(-sDot[which][2][lane], sDot[which][1][lane], sum);
-    p.dbeta[(b * L + t) * p.H + h] = sDot[which][0][lane];
+    const int64_t at = (b * L + t) * p.H + h;
+    p.dg[at] = __builtin_fmaf(-sDot[which][2][lane], sDot[which][1][lane], sum);
+    p.dbeta[at] = sDot[which][0][lane];
   };
   auto chunk_of = [&](int done) { return BACK ? c_end - 1 - done : c_begin + done; };
 #pragma unroll
@@ -597,17 +598,18 @@ void gd_qk_kernel(GdGradArgs p) {
       if (there) dot = __builtin_fmaf(f[at], E[y][u][e], dot);
     });
     dot = wave_sum(dot);
-    __syncthreads();                                // (the sums have been read)
+    __syncthreads();                                // (the sums have been read, the tokens' parts are in memory)
     if (lane == 0) sSum[0][w][0] = dot;
     __syncthreads();
     if (w == 0) {
       double carry = 0.0;
 #pragma unroll
       for (int i = 0; i < NW; ++i) carry += sSum[0][i][0];
-      const int first = c_begin * kQ, stop = least(len, c_end * kQ);
+      const int stop = least(len, c_end * kQ);
       for (int c = c_end - 1; c >= c_begin; --c) {
         const int t = c * kQ + lane;
-        double x = t < stop ? static_cast<double>(sAll[t - first]) : 0.0;
+        float* at = p.dg + (b * L + least(t, stop - 1)) * p.H + h;
+        double x = t < stop ? static_cast<double>(*at) : 0.0;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
           const double after = __shfl_down(x, d);
@@ -616,7 +618,7 @@ void gd_qk_kernel(GdGradArgs p) {
         x += carry;
         carry = __shfl(x, 0);
         // (the first token of a sequence without a state has nothing to scale)
-        if (t < stop) p.dg[(b * L + t) * p.H + h] = t == 0 && !p.carried ? 0.0f : static_cast<float>(x);
+        if (t < stop) *at = t == 0 && !p.carried ? 0.0f : static_cast<float>(x);
       }
     }
   }
@@ -637,10 +639,22 @@ void launch_qk_t(const GdGradArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Chunks between two kept states: enough stretches for the chip several times over, few states to write and read.
-int gd_every(int64_t batch, int64_t L, int64_t H) {
-  const int64_t e = batch * H * ((L + kQ - 1) / kQ) / 1024;
-  return e < 1 ? 1 : e > kMostEvery ? kMostEvery : static_cast<int>(e);
+// Chunks between two kept states.  A workgroup of gd_qk_kernel has a CU to itself (the smallest two share one), and a stretch costs its chunks and about as
+// much as kStart more for its start (its states, its first rows): the least of that over the chip's rounds.
+int gd_every(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V, Dt dt) {
+  const int64_t places = dt == Dt::F32 && K <= 64 && V <= 64 ? 512 : 256;
+  constexpr double kStart = 1.5;
+  const int64_t pairs = batch * H, nch = (L + kQ - 1) / kQ;
+  int best = 1;
+  double least_cost = 0.0;
+  for (int e = 1; e <= kMostEvery; ++e) {
+    const int64_t rounds = (pairs * ((nch + e - 1) / e) + places - 1) / places;
+    const double cost = static_cast<double>(rounds) * (e + kStart);
+    if (e > 1 && cost >= least_cost) continue;
+    best = e;
+    least_cost = cost;
+  }
+  return best;
 }
 
 hipError_t launch_gd_qk(const GdGradArgs& a, Dt dt, hipStream_t s) {

@@ -366,7 +366,7 @@ struct GdPlan {
 bool gd_plan(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V, int64_t record, GdPlan* p) {
   if (batch == 0 || L == 0 || H == 0) return true;
   const int64_t nch = (L + 63) / 64, side = K > 64 ? 128 : 64;
-  p->nseg = ssm::gd_segments(batch, L, H, V);
+  p->nseg = ssm::gd_segments(batch, L, H);
   if (!bytes_of(static_cast<uint64_t>(record), &p->rec, batch, H, nch) ||
       (p->nseg > 1 && (!bytes_of(4, &p->seg, batch, H, p->nseg, K, V) || !bytes_of(4, &p->mat, batch, H, p->nseg, side, side))))
     return false;
@@ -399,7 +399,7 @@ bool gd_bwd_plan(int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk, in
   const ssm::GdRecords r = ssm::gd_records(dt_of(dt));
   if (!gd_plan(batch, L, H, K, V, r.save, &p->fwd) || !gd_plan(batch, L, H, K, V, r.back, &p->back)) return false;
   if (batch == 0 || L == 0 || H == 0) return true;
-  const int64_t nch = (L + 63) / 64, every = ssm::gd_every(batch, L, H);
+  const int64_t nch = (L + 63) / 64, every = ssm::gd_every(batch, L, H, K, V, dt_of(dt));
   if (!bytes_of(4, &p->rows, batch, H, nch, 64, V > 64 ? 128 : 64) ||
       !bytes_of(4, &p->kept, batch, H, (nch + every - 1) / every, K, V) || !bytes_of(4, &p->part, batch, H, nch, 64, K > 64 ? 128 : 64) ||
       (Hk != H && !bytes_of(4, &p->dk, batch, L, H, K)) || (Hq != H && !bytes_of(4, &p->dq, batch, L, H, K)) || (Hv != H && !bytes_of(4, &p->dv, batch, L, H, V)))
@@ -547,7 +547,7 @@ ssm_status ssm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
   a.g = g; a.beta = beta; a.lengths = lengths; a.carry = initial_state;
   a.batch = batch; a.L = L; a.H = static_cast<int>(H); a.K = static_cast<int>(K); a.V = static_cast<int>(V);
   a.scale = scale;
-  a.every = ssm::gd_every(batch, L, H);
+  a.every = ssm::gd_every(batch, L, H, K, V, dt_of(dt));
   a.nseg = plan.fwd.nseg;
   a.rec = take(plan.fwd.rec);
   a.rec_back = take(plan.back.rec);

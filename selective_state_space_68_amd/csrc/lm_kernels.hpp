@@ -123,7 +123,7 @@ struct GdGradArgs {
   int carried = 0;                                       // there is an initial state
   int vec = 0;                                           // rows of q, k, v and d move as 8 elements, those of dq and dk as 4
 };
-int gd_every(int64_t batch, int64_t L, int64_t H);
+int gd_every(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V, Dt dt);
 hipError_t launch_gd_qk(const GdGradArgs& a, Dt dt, hipStream_t s);
 
 struct GdStepArgs {
@@ -145,7 +145,7 @@ struct GdRecords {
   int64_t out, save, back;                               // bytes of a chunk's record: forward pass, the gradient's walks
 };
 GdRecords gd_records(Dt dt);
-int gd_segments(int64_t batch, int64_t L, int64_t H, int64_t V);
+int gd_segments(int64_t batch, int64_t L, int64_t H);
 hipError_t launch_gd(const GdArgs& a, Dt dt, hipStream_t s);
 // The two walks of the gradient: forwards (v, carry: the inputs'), then backwards (v: the outputs' gradient, carry: the
 // final state's, o: dv, fin: the initial state's).

@@ -40,6 +40,12 @@ __device__ __forceinline__ void store4(void* p, int64_t i, const float (&v)[4]) 
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
+// 1 / sqrt(x).  The hardware's root takes numbers below 2^-126 for 0: small ones are scaled.
+__device__ __forceinline__ float inverse_root(float x) {
+  const bool small = x < 0x1p-100f;
+  return __builtin_amdgcn_rsqf(small ? x * 0x1p100f : x) * (small ? 0x1p50f : 1.0f);
+}
+
 // sin and cos of position * frequency.  (The hardware's sine of turns for bfloat16 rows saved 1 of 128 us: 16384 x 40 heads of
 // 128, gradient.)
 __device__ __forceinline__ void turn_of(double position, float frequency, float* s, float* c) {
@@ -99,9 +105,9 @@ struct Row {
       return x < p.rotary / 2 ? x : -1;
     }
   }
-  __device__ __forceinline__ void turns(const QkArgs& p, int lane, int64_t token) {
+  __device__ __forceinline__ void turns(const QkArgs& p, int lane, int64_t token, int64_t t) {
     if (!p.rotary) return;
-    const double position = static_cast<double>(p.positions ? p.positions[token] : static_cast<int32_t>(token % p.L));
+    const double position = static_cast<double>(p.positions ? p.positions[token] : static_cast<int32_t>(t));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int pair = pair_of(p, lane, i);
@@ -174,6 +180,10 @@ struct Place {
     items = p.batch * p.L * p.split;
     step = static_cast<int64_t>(gridDim.x) * kGroups;
   }
+  // a / b, for a below `items` and b no larger (32-bit where they are: a 64-bit division is 500 cycles)
+  __device__ __forceinline__ int64_t over(int64_t a, int64_t b) const {
+    return items < (int64_t(1) << 32) ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+  }
 };
 
 template <typename ACT, int G, int NI, bool VEC>
@@ -186,10 +196,10 @@ __global__ __launch_bounds__(kThreads) void qk_norm_kernel(QkArgs p) {
   row.weights(p.qw, wq);
   row.weights(p.kw, wk);
   for (int64_t item = at.item; item < at.items; item += at.step) {
-    const int64_t token = p.split == 1 ? item : item / p.split;
+    const int64_t token = p.split == 1 ? item : at.over(item, p.split);
     const int first = static_cast<int>(item - token * p.split);
-    const int64_t b = p.batch == 1 ? 0 : token / p.L, t = token - b * p.L;
-    row.turns(p, at.lane, token);
+    const int64_t b = p.batch == 1 ? 0 : at.over(token, p.L), t = token - b * p.L;
+    row.turns(p, at.lane, token, t);
     auto heads = [&](int h, int count, const void* in, const int64_t (&st)[3], const float (&wt)[R::N][2], void* out)
                      __attribute__((always_inline)) {
       const int64_t base = b * st[0] + t * st[1], to = token * count;
@@ -200,7 +210,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_kernel(QkArgs p) {
 #pragma unroll
         for (int i = 0; i < R::N; ++i) ss = __builtin_fmaf(x[i][0], x[i][0], __builtin_fmaf(x[i][1], x[i][1], ss));
         ss = R::sum(ss);
-        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, p.inv_count, p.eps));
+        const float r = inverse_root(__builtin_fmaf(ss, p.inv_count, p.eps));
 #pragma unroll
         for (int i = 0; i < R::N; ++i) {
           const float a = x[i][0] * r * wt[i][0], d = x[i][1] * r * wt[i][1];
@@ -228,10 +238,10 @@ __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkArgs p) {
 #pragma unroll
   for (int i = 0; i < R::N; ++i) dwq[i][0] = dwq[i][1] = dwk[i][0] = dwk[i][1] = 0.0f;
   for (int64_t item = at.item; item < at.items; item += at.step) {
-    const int64_t token = p.split == 1 ? item : item / p.split;
+    const int64_t token = p.split == 1 ? item : at.over(item, p.split);
     const int first = static_cast<int>(item - token * p.split);
-    const int64_t b = p.batch == 1 ? 0 : token / p.L, t = token - b * p.L;
-    row.turns(p, at.lane, token);
+    const int64_t b = p.batch == 1 ? 0 : at.over(token, p.L), t = token - b * p.L;
+    row.turns(p, at.lane, token, t);
     auto heads = [&](int h, int count, const void* in, const int64_t (&st)[3], const void* grad, const int64_t (&ds)[3],
                      const float (&wt)[R::N][2], float (&dw)[R::N][2], void* out) __attribute__((always_inline)) {
       const int64_t base = b * st[0] + t * st[1], dbase = b * ds[0] + t * ds[1], to = token * count;
@@ -243,7 +253,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkArgs p) {
 #pragma unroll
         for (int i = 0; i < R::N; ++i) ss = __builtin_fmaf(x[i][0], x[i][0], __builtin_fmaf(x[i][1], x[i][1], ss));
         ss = R::sum(ss);
-        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, p.inv_count, p.eps));
+        const float r = inverse_root(__builtin_fmaf(ss, p.inv_count, p.eps));
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < R::N; ++i) {
@@ -334,8 +344,8 @@ void launch_t(const QkArgs& a, dim3 grid, hipStream_t s) {
 dim3 plan(QkArgs* a, int64_t most) {
   const int64_t tokens = a->batch * a->L;
   const int heads = a->Hq + a->Hk, groups = groups_of(*a);
-  int split = 1;
-  while (split < heads && tokens * split < 32768) ++split;
+  const int64_t wanted = (32768 + tokens - 1) / tokens;
+  const int split = static_cast<int>(wanted < heads ? wanted : heads);
   a->split = split;
   const int64_t blocks = (tokens * split + groups - 1) / groups;
   return dim3(static_cast<unsigned>(blocks < most ? blocks : most));

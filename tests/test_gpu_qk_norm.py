@@ -185,6 +185,15 @@ def test_zero_rows_and_no_tokens():
     assert not out["dq_weight"].any() and not out["dk_weight"].any()
 
 
+@pytest.mark.parametrize("K", [64, 50])
+def test_small_rows_without_eps(K):
+    # a mean square of 10^-38 is below 2^-126; its parts are rounded to 2^-149, so that it is off by 7e-8 more than counted above
+    gen = torch.Generator().manual_seed(4)
+    q = torch.randn(1, 9, 3, K, generator=gen) * 1e-19
+    got, _ = _ssm().qk_norm_fwd(q.cuda(), eps=0.0)
+    _check(got, ref.qk_norm(q, None, eps=0.0), "rows of 1e-19", sums=1.01)
+
+
 def test_gradient_differences():
     """A step of 2^-8 along a direction in float32: the outputs move by the gradient's products, to the step's own square."""
     ssm = _ssm()
