@@ -6,7 +6,8 @@
 // and backwards, with dn = dy turned back:  dw = sum over rows of dn x r,   dx = r (w dn - x r m),  m = the mean, or the
 // sum, of w dn x r over the row.
 //
-// Every value is read and written once: the kernels are bound by memory.  A row is held by 8 to 64 lanes of a wave, 8 values
+// Every value is read and written once: the kernels are bound by memory (bfloat16 heads of 128: 8192 x 40 without rotation 27 us, 6.1 TB/s;
+// gradient of 16384 x 40, rotated, 107 us, 4.7 TB/s, half the vector unit's time).  A row is held by 8 to 64 lanes of a wave, 8 values
 // each; a lane has both members of its pairs, so nothing but the row's sum crosses lanes.  A group of lanes takes
 // several heads of its token, so that its angles, whose sines and cosines cost more than a row's norm, are formed
 // once for all of them: in float64 up to the turn's fraction (position 10^6 leaves 4 bits of a float32 angle), in float32

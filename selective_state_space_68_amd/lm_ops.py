@@ -394,6 +394,10 @@ def gated_delta_step(state, q_t, k_t, v_t, g_t, beta_t, scale=None, *, slots=Non
     return out
 
 
+def _packed_like(t):
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _outputs(given, like, spec) -> dict:
     """Output tensors by name: the caller's where given (checked), else new ones; None where not computed."""
     got = {}
@@ -475,9 +479,9 @@ def qk_norm_fwd(q, k=None, q_weight=None, k_weight=None, *, norm="rms", eps=1e-6
     qs = _token_strides(q, "q", act, dev)
     ks = None if k is None else _token_strides(k, "k", act, dev)
     if q_out is None:
-        q_out = q.new_empty(q.shape)
+        q_out = _packed_like(q)
     if k_out is None and k is not None:
-        k_out = k.new_empty(k.shape)
+        k_out = _packed_like(k)
     _run(_entry("ssm_qk_norm_fwd"), dev,
          q.data_ptr(), None if k is None else k.data_ptr(), qs, ks, _ptr(q_weight, "q_weight", F32, dev),
          _ptr(k_weight, "k_weight", F32, dev), _ptr(inv_freq, "inv_freq", F32, dev),
@@ -513,9 +517,14 @@ def qk_norm_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, *, norm="rms
     dt = _dt(act)
     qs, dqs = _token_strides(q, "q", act, dev), _token_strides(dq_out, "dq_out", act, dev)
     ks, dks = (None, None) if k is None else (_token_strides(k, "k", act, dev), _token_strides(dk_out, "dk_out", act, dev))
-    grads = _outputs(out, q, {"dq": (q.shape, act, True), "dk": (None if k is None else k.shape, act, k is not None),
-                              "dq_weight": ((K,), F32, q_weight is not None),
-                              "dk_weight": ((K,), F32, k_weight is not None)})
+    if out is None:
+        grads = {"dq": _packed_like(q), "dk": None if k is None else _packed_like(k),
+                 "dq_weight": None if q_weight is None else torch.empty_like(q_weight),
+                 "dk_weight": None if k_weight is None else torch.empty_like(k_weight)}
+    else:
+        grads = _outputs(out, q, {"dq": (q.shape, act, True), "dk": (None if k is None else k.shape, act, k is not None),
+                                  "dq_weight": ((K,), F32, q_weight is not None),
+                                  "dk_weight": ((K,), F32, k_weight is not None)})
     need = 0 if q_weight is None and k_weight is None else qk_norm_bwd_workspace_size(K)
     ws, ws_ptr, ws_bytes = _scratch(workspace, need, q)
     _run(_entry("ssm_qk_norm_bwd"), dev,
