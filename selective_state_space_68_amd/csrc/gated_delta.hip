@@ -81,11 +81,14 @@ __global__ __launch_bounds__(256, 2) void gd_prepare_kernel(GdArgs p) {
   __shared__ __attribute__((aligned(16))) float blocks[4][10 * kBlock];
   __shared__ __attribute__((aligned(16))) float vectors[4][3][kQ];              // G in two parts, beta
 
-  const int lane = threadIdx.x & 63, w = uniform_int(threadIdx.x >> 6), g = lane >> 4, c16 = lane & 15;
+  const int w = uniform_int(threadIdx.x >> 6);
   float *A = blocks[w], *sHi = vectors[w][0], *sLo = vectors[w][1], *sB = vectors[w][2];
   const uint32_t nch = static_cast<uint32_t>((p.L + kQ - 1) / kQ), all = static_cast<uint32_t>(p.batch) * p.H * nch;
   auto token = [](int row) { return BACK ? kQ - 1 - row : row; };               // (its own inverse)
   for (uint32_t item = blockIdx.x * 4 + w; item < all; item += gridDim.x * 4) {
+    int lane = lane_id();                           // (opaque: what follows from it is formed here, not kept in spilled registers)
+    asm volatile("" : "+v"(lane));
+    const int g = lane >> 4, c16 = lane & 15;
     const uint32_t pair = item / nch, c = item - pair * nch;
     const uint32_t row_b = pair / static_cast<uint32_t>(p.H);
     const int h = static_cast<int>(pair - row_b * static_cast<uint32_t>(p.H));
@@ -124,12 +127,10 @@ __global__ __launch_bounds__(256, 2) void gd_prepare_kernel(GdArgs p) {
         }
       }
     };
-    piece kp[2][2][KT], qp[2][2][KT];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      load_rows(kg, p.ks[1], t, kp[t]);
-      if constexpr (PT > 0) load_rows(qg, p.qs[1], t, qp[t]);
-    }
+    piece kp[2][2][KT], qp[2][KT];                  // of q a half at a time
+    load_rows(kg, p.ks[1], 0, kp[0]);
+    if constexpr (PT > 0) load_rows(qg, p.qs[1], 0, qp);
+    load_rows(kg, p.ks[1], 1, kp[1]);
 
     // the running sum of g, in units of log 2, from float64 as a pair of float32
     {
@@ -188,11 +189,15 @@ __global__ __launch_bounds__(256, 2) void gd_prepare_kernel(GdArgs p) {
       }
     };
 #pragma unroll
-    for (int two = 0; two < 2; ++two)
+    for (int half = 0; half < 2; ++half) {          // (q's: columns, backwards rows)
+      if constexpr (PT > 0) {
+        if (half) load_rows(qg, p.qs[1], 1, qp);
+      }
 #pragma unroll
-      for (int t = 0; t <= two; ++t)
+      for (int other = BACK ? half : 0; other < (BACK ? 2 : half + 1); ++other)
 #pragma unroll
         for (int one = 0; one < 2; ++one) {
+          const int two = BACK ? other : half, t = BACK ? half : other;
           f32x4_t s1[2], s2[2];
 #pragma unroll
           for (int u = 0; u < 2; ++u) s1[u] = s2[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -202,10 +207,11 @@ __global__ __launch_bounds__(256, 2) void gd_prepare_kernel(GdArgs p) {
             for (int u = 0; u < 2; ++u) {
               s1[u] = O::mma(kp[t][u][y], kp[two][one][y], s1[u]);
               if constexpr (PT > 0)
-                s2[u] = BACK ? O::mma(qp[t][u][y], kp[two][one][y], s2[u]) : O::mma(kp[t][u][y], qp[two][one][y], s2[u]);
+                s2[u] = BACK ? O::mma(qp[u][y], kp[two][one][y], s2[u]) : O::mma(kp[t][u][y], qp[one][y], s2[u]);
             }
           tile(t, 32 * two + 4 * one + perm_row, s1, s2, 2 * two + 2 * t + one);
         }
+    }
     wave_lds();
 
     // the inverses of the diagonal blocks of I + A, in place: 16 lanes a block, lane c16 solves for its column

@@ -20,7 +20,7 @@ constexpr int kThreads = 256;
 // CPT: consecutive columns per thread (4: rows of states move as vectors).  N: rows of a thread at most.
 template <typename ACT, int CPT, int N>
 __global__ __launch_bounds__(kThreads) void gd_step_kernel(GdStepArgs p) {
-  __shared__ float sq[kLaMaxDim], sk[kLaMaxDim], su[kLaMaxDim];
+  __shared__ float sq[kLaMaxDim], sk[kLaMaxDim], su[kLaMaxDim], s_qk;
   __shared__ __attribute__((aligned(16))) float part[2][kThreads * CPT];
   const int tid = threadIdx.x;
   const int K = p.K, V = p.V;
@@ -62,6 +62,12 @@ __global__ __launch_bounds__(kThreads) void gd_step_kernel(GdStepArgs p) {
   const float v = tid < V ? load_act<ACT>(p.v, v0 + tid) : 0.0f;
   const float a = expf(p.g[bh]), beta = p.beta[bh];
   __syncthreads();
+  if (tid < 64) {                                   // q.k (a thread that adds it up for itself waits for LDS K times)
+    float qk = tid < K ? sq[tid] * sk[tid] : 0.0f;
+    if (tid + 64 < K) qk = __builtin_fmaf(sq[tid + 64], sk[tid + 64], qk);
+    qk = wave_sum(qk);
+    if (tid == 0) s_qk = qk;
+  }
   if (mine) {
     float kS[CPT], qS[CPT];
 #pragma unroll
@@ -85,12 +91,12 @@ __global__ __launch_bounds__(kThreads) void gd_step_kernel(GdStepArgs p) {
   }
   __syncthreads();
   if (tid < V) {
-    float kS = 0.0f, qS = 0.0f, qk = 0.0f;
+    float kS = 0.0f, qS = 0.0f;
+    const float qk = s_qk;
     for (int r = 0; r < rows; ++r) {
       kS += part[0][r * V + tid];
       qS += part[1][r * V + tid];
     }
-    for (int r = 0; r < K; ++r) qk = __builtin_fmaf(sq[r], sk[r], qk);
     const float u = beta * __builtin_fmaf(-a, kS, v);
     su[tid] = u;
     store_act<ACT>(p.o, o0 + tid, p.scale * __builtin_fmaf(a, qS, qk * u));
