@@ -248,24 +248,24 @@ def linear_attention_step(state, q_t, k_t, v_t, log_decay, scale=None, *, slots=
     return out
 
 
-def _gates(g, beta, lead):
-    """Checks g and beta [*lead, H]; returns H."""
-    _dims(g, "g", len(lead) + 1)
-    _is(g, "g", (*lead, g.shape[-1]))
-    _is(beta, "beta", g.shape)
-    if beta is None:
-        raise ValueError("beta must be a tensor")
-    return g.shape[-1]
-
-
 def _delta_shapes(q, k, v, g, beta, n: int):
     """Checks q, k, v [..., heads, width] of n dimensions and g, beta [..., H]; as _attention_shapes."""
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         _dims(t, name, n)
+    _dims(g, "g", n - 1)
     *lead, Hq, K = q.shape
-    Hk, (Hv, V), H = k.shape[-2], v.shape[-2:], _gates(g, beta, lead)
-    _is(k, "k", (*lead, Hk, K))
-    _is(v, "v", (*lead, Hv, V))
+    *k_lead, Hk, k_width = k.shape
+    *v_lead, Hv, V = v.shape
+    *g_lead, H = g_shape = g.shape
+    if k_lead != lead or k_width != K:
+        _shape(k, "k", (*lead, Hk, K))
+    if v_lead != lead:
+        _shape(v, "v", (*lead, Hv, V))
+    if g_lead != lead:
+        _shape(g, "g", (*lead, H))
+    if beta is None:
+        raise ValueError("beta must be a tensor")
+    _is(beta, "beta", g_shape)
     for heads, name in ((Hq, "q"), (Hk, "k"), (Hv, "v")):
         if heads < 1 or H % heads:
             raise ValueError(f"{name} has {heads} heads, which does not divide g's {H}")
