@@ -115,6 +115,11 @@ __global__ __launch_bounds__(256, 2) void gd_prepare_kernel(GdArgs p) {
           if constexpr (MOVE == 16) {
             load_piece(reinterpret_cast<const char*>(from + least(col, p.K - 8)), out[u][y]);
             if (at >= n || col >= p.K) out[u][y] = O::zero();
+          } else if constexpr (MOVE == 4) {         // (the last columns come at the end of 8 that are there)
+            const int start = least(col, p.K - 8);
+            load_words(reinterpret_cast<const char*>(from + start), out[u][y]);
+            if (32 * y + 32 > p.K) drop_first(out[u][y], least(col - start, 7));
+            if (at >= n || col >= p.K) out[u][y] = O::zero();
           } else {
             elem v[8];
 #pragma unroll
@@ -327,6 +332,16 @@ struct ChunkRows {
       }
     } else if constexpr (MOVE == 4) {
       constexpr int kWords = RB / 4, kAll = kQ * RB / 256 / NW;
+      if constexpr (kWords >= 64) {                 // an instruction is of one row: what follows from the row is scalar
+        constexpr int kPer = kWords / 64;
+#pragma unroll 4
+        for (int i = 0; i < kAll; ++i) {
+          const int at = w * kAll + i, row = at / kPer;
+          const uint32_t byte = static_cast<uint32_t>((256 * (at % kPer) + 4 * lane) ^ (swizzle<RB, kF32, PERM>(row) << 4));
+          if (static_cast<int>(byte) < cols) load_word_to_lds(tile + at * 256, from + clamped(row, n) * bytes, byte);
+        }
+        return;
+      }
 #pragma unroll 4
       for (int i = 0; i < kAll; ++i) {
         const int word = (w * kAll + i) * 64 + lane, row = word / kWords;
@@ -961,6 +976,7 @@ void launch_gd_mode(const GdArgs& args, Dt dt, hipStream_t s) {
                          dim3(static_cast<unsigned>(all < most ? all : most)), dim3(256), 0, s, a);
     };
     if (a.move == 16) prepare(std::integral_constant<int, 16>{});
+    else if (a.move == 4 && a.K >= 8) prepare(std::integral_constant<int, 4>{});
     else prepare(std::integral_constant<int, 0>{});
     if (wide(a, KD)) launch_gd_t<ACT, KD, 128, 16, true, MODE>(a, s);
     else if (a.move == 16 && a.K == KD && a.V % 64 == 0) launch_gd_t<ACT, KD, 64, 16, true, MODE>(a, s);

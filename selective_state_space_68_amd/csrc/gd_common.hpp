@@ -48,6 +48,37 @@ __device__ __forceinline__ void load_piece(const char* at, F8& p) {
   p.b = reinterpret_cast<const float4*>(at)[1];
 }
 
+// ... from 4-byte words (the hardware's loads of 16 bytes need no more)
+typedef uint32_t words_t __attribute__((ext_vector_type(4), aligned(4)));
+__device__ __forceinline__ void load_words(const char* at, uint4& p) {
+  const words_t x = *reinterpret_cast<const words_t*>(at);
+  p = make_uint4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void load_words(const char* at, F8& p) {
+  p.a = __builtin_bit_cast(float4, reinterpret_cast<const words_t*>(at)[0]);
+  p.b = __builtin_bit_cast(float4, reinterpret_cast<const words_t*>(at)[1]);
+}
+// Elements by .. of a piece, zeros behind them (by: 0 .. 7).
+__device__ __forceinline__ void drop_first(uint4& p, int by) {
+  uint32_t x[5] = {p.x, p.y, p.z, p.w, 0u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = by & 4 ? (i < 2 ? x[i + 2] : 0u) : x[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = by & 2 ? x[i + 1] : x[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = by & 1 ? x[i] >> 16 | x[i + 1] << 16 : x[i];
+  p = make_uint4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void drop_first(F8& p, int by) {
+  float x[8] = {p.a.x, p.a.y, p.a.z, p.a.w, p.b.x, p.b.y, p.b.z, p.b.w};
+#pragma unroll
+  for (int d = 4; d > 0; d /= 2)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = by & d ? (i + d < 8 ? x[i + d < 8 ? i + d : 0] : 0.0f) : x[i];
+  p.a = make_float4(x[0], x[1], x[2], x[3]);
+  p.b = make_float4(x[4], x[5], x[6], x[7]);
+}
+
 // The sum of products of two values in N terms each, of those terms that count at N terms (largest last).
 template <typename O, int NA, int NB>
 __device__ __forceinline__ f32x4_t mma_terms(const typename O::piece (&a)[NA], const typename O::piece (&b)[NB], f32x4_t c) {

@@ -36,18 +36,20 @@ namespace {
 
 constexpr int kMostEvery = 16;
 
-// Eight values of a row from memory.  Nothing is decided where they move as vectors: rows and columns that are not there
-// repeat the last ones (they are cleared on the way into LDS).
-template <bool VEC>
-using Offset = std::conditional_t<VEC, uint32_t, int64_t>;    // within a chunk's rows (vectors': of fewer than 2^32 bytes)
-template <typename ACT, bool VEC>
-__device__ __forceinline__ typename Op<ACT>::piece load8(const void* base, Offset<VEC> stride, int row, int n, int col, int width) {
+// Eight values of a row from memory, MOVE bytes being the unit in which rows move (16, 4, or 0: element by element).  Nothing is decided
+// where they move as vectors or words: rows and columns that are not there repeat the last ones (they are cleared on the way into LDS).
+template <int MOVE>
+using Offset = std::conditional_t<MOVE == 16, uint32_t, int64_t>;    // within a chunk's rows (vectors': of fewer than 2^32 bytes)
+template <typename ACT, int MOVE>
+__device__ __forceinline__ typename Op<ACT>::piece load8(const void* base, Offset<MOVE> stride, int row, int n, int col, int width) {
   using elem = typename Op<ACT>::elem;
   const elem* at = static_cast<const elem*>(base);
-  const Offset<VEC> first = static_cast<Offset<VEC>>(least(row, n - 1)) * stride;
+  const Offset<MOVE> first = static_cast<Offset<MOVE>>(least(row, n - 1)) * stride;
   typename Op<ACT>::piece p;
-  if constexpr (VEC) {
+  if constexpr (MOVE == 16) {
     load_piece(reinterpret_cast<const char*>(at + (first + least(col, width - 8))), p);
+  } else if constexpr (MOVE == 4) {
+    load_words(reinterpret_cast<const char*>(at + (first + least(col, width - 8))), p);
   } else {
     elem v[8];
 #pragma unroll
@@ -57,10 +59,12 @@ __device__ __forceinline__ typename Op<ACT>::piece load8(const void* base, Offse
   return p;
 }
 // The values of columns and rows that are there.
-template <typename ACT, bool VEC>
-__device__ __forceinline__ typename Op<ACT>::piece present(const typename Op<ACT>::piece& p, int row, int n, int col, int width) {
+template <typename ACT, int MOVE>
+__device__ __forceinline__ typename Op<ACT>::piece present(typename Op<ACT>::piece p, int row, int n, int col, int width) {
   using elem = typename Op<ACT>::elem;
-  if constexpr (VEC) {
+  if constexpr (MOVE == 4)
+    if (width % 8) drop_first(p, least(col - least(col, width - 8), 7));
+  if constexpr (MOVE != 0) {
     return row < n && col < width ? p : Op<ACT>::zero();
   } else {
     struct Eight { elem v[8]; } x = __builtin_bit_cast(Eight, p);
@@ -81,9 +85,9 @@ __device__ __forceinline__ void put8(char* tile, int row, int slot, const F8& p)
   *reinterpret_cast<float4*>(tile + row * RB + (((2 * slot + 1) ^ flip) << 4)) = p.b;
 }
 
-// BACK: the second kernel, which adds the backward part of dk.  VEC: rows of q, k, v and d move as 8 elements, those of dq and
-// dk as 4.
-template <typename ACT, int KD, int VD, bool VEC, bool BACK>
+// BACK: the second kernel, which adds the backward part of dk.  MOVE: the unit in which rows of q, k, v and d move; with 16, those of dq
+// and dk move as 4 elements.
+template <typename ACT, int KD, int VD, int MOVE, bool BACK>
 __global__ __launch_bounds__(4 * KD, 2)
 void gd_qk_kernel(GdGradArgs p) {
   using O = Op<ACT>;
@@ -94,6 +98,7 @@ void gd_qk_kernel(GdGradArgs p) {
   constexpr int OT = kOutTerms<ACT>, NT = BACK ? OT : kTerms<ACT>;      // terms of Y and N2; of W, E and N1
   constexpr int RV = VD * static_cast<int>(sizeof(elem)), RK = KD * static_cast<int>(sizeof(elem));
   constexpr int KT = VD / 32, PB = O::kPiece, kOne = kPieceBytes<ACT>;
+  constexpr bool VEC = MOVE == 16;
   constexpr bool PW = !BACK, PY = BACK;             // whose rows are read as permuted ones
   constexpr bool TILES = !kF32;                     // q and k by LDS (float32: no room; the waves read their own columns)
   __shared__ __attribute__((aligned(512))) char sD[kQ * RV];
@@ -158,16 +163,16 @@ void gd_qk_kernel(GdGradArgs p) {
     const int64_t t0 = static_cast<int64_t>(c) * kQ, rows = (bh * nchunks + c) * kQ;
     const char *wc = reinterpret_cast<const char*>(p.w + rows * VD), *yc = reinterpret_cast<const char*>(p.y + rows * VD);
     const elem *dc = dg + t0 * p.ds[1], *vc = vg + t0 * p.vs[1], *kc = kg + t0 * p.ks[1], *qc = qg + t0 * p.qs[1];
-    const Offset<VEC> dstep = static_cast<Offset<VEC>>(p.ds[1]), vstep = static_cast<Offset<VEC>>(p.vs[1]),
-                      kstep = static_cast<Offset<VEC>>(p.ks[1]), qstep = static_cast<Offset<VEC>>(p.qs[1]);
+    const Offset<MOVE> dstep = static_cast<Offset<MOVE>>(p.ds[1]), vstep = static_cast<Offset<MOVE>>(p.vs[1]),
+                      kstep = static_cast<Offset<MOVE>>(p.ks[1]), qstep = static_cast<Offset<MOVE>>(p.qs[1]);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int at = id + i * THREADS, row = at / kV8, col = 8 * (at % kV8);
       if (part == 0) load_piece(wc + static_cast<uint32_t>(32 * at), in.w[i]);
       if (part == 1) load_piece(yc + static_cast<uint32_t>(32 * at), in.y[i]);
       if (part == 2) {
-        in.d[i] = load8<ACT, VEC>(dc, dstep, row, n, col, V);
-        if constexpr (!BACK) in.v[i] = load8<ACT, VEC>(vc, vstep, row, n, col, V);
+        in.d[i] = load8<ACT, MOVE>(dc, dstep, row, n, col, V);
+        if constexpr (!BACK) in.v[i] = load8<ACT, MOVE>(vc, vstep, row, n, col, V);
       }
     }
     if (part < 3) return;
@@ -175,8 +180,8 @@ void gd_qk_kernel(GdGradArgs p) {
 #pragma unroll
       for (int i = 0; i < kNK; ++i) {
         const int at = id + i * THREADS, row = at / kK8, col = 8 * (at % kK8);
-        in.k[i] = load8<ACT, VEC>(kc, kstep, row, n, col, K);
-        if constexpr (BACK) in.q[i] = load8<ACT, VEC>(qc, qstep, row, n, col, K);
+        in.k[i] = load8<ACT, MOVE>(kc, kstep, row, n, col, K);
+        if constexpr (BACK) in.q[i] = load8<ACT, MOVE>(qc, qstep, row, n, col, K);
       }
     }
     const float* from = reinterpret_cast<const float*>(p.rec + (bh * nchunks + c) * kRecord<ACT, 0> + kTBytes<ACT>);
@@ -197,10 +202,10 @@ void gd_qk_kernel(GdGradArgs p) {
       for (int m = 0; m < NT; ++m) put8<RV, PW>(sW[m], row, slot, t[m]);
 #pragma unroll
       for (int m = 0; m < OT; ++m) put8<RV, PY>(sY[m], row, slot, o[m]);
-      put8<RV, BACK>(sD, row, slot, present<ACT, VEC>(in.d[i], row, n, 8 * slot, V));
+      put8<RV, BACK>(sD, row, slot, present<ACT, MOVE>(in.d[i], row, n, 8 * slot, V));
       if constexpr (!BACK) {                        // y.w and y.v
         float v[8], yw = 0.0f, yv = 0.0f;
-        O::unpack(present<ACT, VEC>(in.v[i], row, n, 8 * slot, V), v);
+        O::unpack(present<ACT, MOVE>(in.v[i], row, n, 8 * slot, V), v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           yw = __builtin_fmaf(y[e], x[e], yw);
@@ -218,8 +223,8 @@ void gd_qk_kernel(GdGradArgs p) {
 #pragma unroll
       for (int i = 0; i < kNK; ++i) {
         const int at = tid + i * THREADS, row = at / kK8, slot = at % kK8;
-        put8<RK, false>(sK, row, slot, present<ACT, VEC>(in.k[i], row, n, 8 * slot, K));
-        if constexpr (BACK) put8<RK, false>(sQ, row, slot, present<ACT, VEC>(in.q[i], row, n, 8 * slot, K));
+        put8<RK, false>(sK, row, slot, present<ACT, MOVE>(in.k[i], row, n, 8 * slot, K));
+        if constexpr (BACK) put8<RK, false>(sQ, row, slot, present<ACT, MOVE>(in.q[i], row, n, 8 * slot, K));
       }
     }
 #pragma unroll
@@ -303,7 +308,7 @@ void gd_qk_kernel(GdGradArgs p) {
         meet[jt][0] = x.x; meet[jt][1] = x.y; meet[jt][2] = x.z; meet[jt][3] = x.w;
       } else {                                      // (q)
         const elem* from = qg + t0 * p.qs[1];
-        const Offset<VEC> at = row * static_cast<Offset<VEC>>(p.qs[1]);
+        const Offset<MOVE> at = row * static_cast<Offset<MOVE>>(p.qs[1]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) meet[jt][e] = 0.0f;
         if constexpr (VEC && kF32) {
@@ -632,13 +637,14 @@ template <typename ACT, int KD, int VD>
 void launch_qk_t(const GdGradArgs& a, hipStream_t s) {
   const int64_t nch = (a.L + kQ - 1) / kQ, stretches = (nch + a.every - 1) / a.every;
   const dim3 grid(static_cast<unsigned>(a.batch * a.H * stretches)), block(4 * KD);
-  auto go = [&](auto vec) {
-    constexpr bool VEC = decltype(vec)::value;
-    hipLaunchKernelGGL((gd_qk_kernel<ACT, KD, VD, VEC, false>), grid, block, 0, s, a);
-    hipLaunchKernelGGL((gd_qk_kernel<ACT, KD, VD, VEC, true>), grid, block, 0, s, a);
+  auto go = [&](auto move) {
+    constexpr int MOVE = decltype(move)::value;
+    hipLaunchKernelGGL((gd_qk_kernel<ACT, KD, VD, MOVE, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((gd_qk_kernel<ACT, KD, VD, MOVE, true>), grid, block, 0, s, a);
   };
-  if (a.vec) go(std::true_type{});
-  else go(std::false_type{});
+  if (a.move == 16) go(std::integral_constant<int, 16>{});
+  else if (a.move == 4 && a.K >= 8 && a.V >= 8) go(std::integral_constant<int, 4>{});
+  else go(std::integral_constant<int, 0>{});
 }
 
 }  // namespace

@@ -234,6 +234,12 @@ __device__ __forceinline__ void load_word_to_lds(uint32_t tile, const char* src)
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, off"
                :: "s"(m0), "v"(src) : "memory");
 }
+// ... from a uniform address and the lane's offset
+__device__ __forceinline__ void load_word_to_lds(uint32_t tile, const char* src, uint32_t off) {
+  const int m0 = uniform_int(static_cast<int>(tile));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2"
+               :: "s"(m0), "v"(off), "s"(src) : "memory");
+}
 
 // Clears rows n.. of the slots that this wave's loads filled.
 template <int RB, int NW>

@@ -586,7 +586,8 @@ ssm_status ssm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
   x.dk_part = part; x.dk = dk_part ? static_cast<void*>(dk_part) : dk; x.dk_f32 = dk_part != nullptr;
   x.dg = dg; x.dbeta = dbeta; x.batch = batch; x.L = L; x.H = a.H; x.K = a.K; x.V = a.V; x.every = a.every; x.scale = scale;
   x.carried = initial_state != nullptr;
-  x.vec = a.move == 16 && r.move == 16 && aligned(x.dq, dq_part ? 16 : 4 * e) && aligned(x.dk, dk_part ? 16 : 4 * e);
+  x.move = least(a.move, r.move);
+  if (x.move == 16 && !(aligned(x.dq, dq_part ? 16 : 4 * e) && aligned(x.dk, dk_part ? 16 : 4 * e))) x.move = 4;
   err = ssm::launch_gd_qk(x, dt_of(dt), s);
   ssm::LaSum sums[3];
   int n = 0;

@@ -121,7 +121,7 @@ struct GdGradArgs {
   float scale = 1.0f;
   int dq_f32 = 0, dk_f32 = 0;
   int carried = 0;                                       // there is an initial state
-  int vec = 0;                                           // rows of q, k, v and d move as 8 elements, those of dq and dk as 4
+  int move = 0;                                          // bytes in which rows of q, k, v and d move (16, 4, 0: an element); 16: those of dq and dk as 4 elements
 };
 int gd_every(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V, Dt dt);
 hipError_t launch_gd_qk(const GdGradArgs& a, Dt dt, hipStream_t s);

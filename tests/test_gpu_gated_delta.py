@@ -147,6 +147,22 @@ def test_gradient(B, L, H, K, V, heads, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("K,V", [(12, 10), (66, 126), (6, 12), (12, 6), (126, 66), (10, 62)])
+def test_words(K, V, dtype):
+    """Rows that move as words: their last columns are read with those before them."""
+    lengths = [70, 130]
+    t, s0, df = ref.inputs(2, 130, 2, K, V, dtype, (1, 2, 2), seed=K)
+    want, wfin = _want(t, K ** -0.5, s0, lengths)
+    wg = ref.delta_grad(*t.values(), K ** -0.5, None, df, lengths)
+    for x in ("q", "k", "v", "do"):
+        t[x][0, 70:] = float("nan")
+    out, fin = _forward(t, s0, lengths)
+    _check(out, want, OUT[dtype], "out")
+    _check(fin, wfin, STATE, "final_state")
+    _check_grads(_gradient(t, None, df, lengths), wg, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_absent_tokens_hold_anything(dtype):
     B, L, H, K, V = 6, 150, 3, 64, 72
     lengths = [150, 0, 1, 64, 65, 149]
