@@ -217,3 +217,35 @@ def test_deterministic():
     run = lambda: ssm.qk_norm_bwd(d["q"], d["k"], d["dq"], d["dk"], d["qw"], d["kw"], inv_freq=freq.cuda(), positions=positions.cuda())
     a, b = run(), run()
     assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_views_past_32_bits_of_elements():
+    """Tokens 2^30 elements apart: the bits of packed copies."""
+    t, freq, positions = _case(1, 3, 2, 1, 64, BF16, 64, seed=6)
+    space = torch.empty(2 ** 31 + 4096, dtype=BF16, device="cuda")
+
+    def far(x, at):
+        v = space.as_strided(x.shape, (x[0].numel(), 2 ** 30, x.shape[-1], 1), at)
+        return v.copy_(x.cuda())
+
+    q, k, dq, dk = (far(t[n], 512 * i) for i, n in enumerate(("q", "k", "dq", "dk")))
+    ssm, named = _ssm(), dict(inv_freq=freq.cuda(), positions=positions.cuda())
+    weights = t["qw"].cuda(), t["kw"].cuda()
+    for x, y in zip(ssm.qk_norm_fwd(q, k, *weights, **named),
+                    ssm.qk_norm_fwd(t["q"].cuda(), t["k"].cuda(), *weights, **named)):
+        assert torch.equal(x, y)
+    a = ssm.qk_norm_bwd(q, k, dq, dk, *weights, **named)
+    b = ssm.qk_norm_bwd(*(t[n].cuda() for n in ("q", "k", "dq", "dk")), *weights, **named)
+    assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_outputs_past_32_bits_of_elements():
+    L = 2 ** 20 + 33
+    q = torch.randn(1, L, 1, 64, device="cuda", dtype=BF16, generator=torch.Generator("cuda").manual_seed(5)).expand(1, L, 32, 64)
+    freq = torch.linspace(1.0, 0.001, 32, device="cuda")
+    out, _ = _ssm().qk_norm_fwd(q, norm="l2", inv_freq=freq)
+    assert out.numel() > 2 ** 31
+    for at in (0, 2 ** 19, L - 40):
+        pos = torch.arange(at, at + 40, dtype=torch.int32, device="cuda")[None]
+        part, _ = _ssm().qk_norm_fwd(q[:, at:at + 40], norm="l2", inv_freq=freq, positions=pos)
+        assert torch.equal(part, out[:, at:at + 40])
