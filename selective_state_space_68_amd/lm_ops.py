@@ -23,6 +23,7 @@ F32 = torch.float32
 BF16 = torch.bfloat16
 _I32 = torch.int32
 _Tensor = torch.Tensor
+_INTS = tuple(ctypes.c_int64 * n for n in range(5))
 
 # The checks of a call run before every launch and are most of a small call's time on the
 # host, so the passing case is a few comparisons; a failing one goes on to say what is wrong.
@@ -76,9 +77,10 @@ def _strides(t, name: str, dtype, index: int):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.is_contiguous() or t.numel() == 0:
         return None
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    *strides, last = t.stride()
+    if last != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must have a contiguous last axis")
-    return (ctypes.c_int64 * (t.dim() - 1))(*t.stride()[:-1])
+    return _INTS[len(strides)](*strides)
 
 
 def _run(fn, index: int, *args) -> None:
@@ -386,16 +388,25 @@ def gated_delta_step(state, q_t, k_t, v_t, g_t, beta_t, scale=None, *, slots=Non
     state_ptr = _ptr(state, "state", F32, dev)
     if out is None:
         out = q_t.new_empty((batch, H, V))
+        out_ptr = out.data_ptr()
+    else:
+        out_ptr = _ptr(out, "out", act, dev)
     _run(_entry("ssm_gated_delta_step"), dev,
          state_ptr, state_ptr if out_state is None else _ptr(out_state, "out_state", F32, dev),
          q_t.data_ptr(), k_t.data_ptr(), v_t.data_ptr(), qs, ks, vs, _ptr(g_t, "g_t", F32, dev),
          _ptr(beta_t, "beta_t", F32, dev), K ** -0.5 if scale is None else float(scale),
-         _ptr(slots, "slots", _I32, dev), _ptr(out, "out", act, dev), batch, states, H, Hq, Hk, Hv, K, V, dt)
+         _ptr(slots, "slots", _I32, dev), out_ptr, batch, states, H, Hq, Hk, Hv, K, V, dt)
     return out
 
 
 def _packed_like(t):
-    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _new_like(t):
+    """A packed tensor like t, and its pointer."""
+    new = _packed_like(t)
+    return new, new.data_ptr()
 
 
 def _outputs(given, like, spec) -> dict:
@@ -421,7 +432,7 @@ def _token_strides(t, name: str, dtype, index: int):
     strides = _strides(t, name, dtype, index)
     if strides is None or t.dim() == 4:
         return strides
-    return (ctypes.c_int64 * 3)(0, *strides)
+    return _INTS[3](0, *strides)
 
 
 def _qk_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions):
@@ -431,9 +442,10 @@ def _qk_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions):
     *lead, Hq, K = q.shape
     Hk = 0
     if k is not None:
-        _dims(k, "k", q.dim())
-        Hk = k.shape[-2]
-        _is(k, "k", (*lead, Hk, K))
+        _dims(k, "k", len(lead) + 2)
+        *k_lead, Hk, k_width = k.shape
+        if k_lead != lead or k_width != K:
+            _shape(k, "k", (*lead, Hk, K))
     elif k_weight is not None:
         raise ValueError("k_weight is given without k")
     _is(q_weight, "q_weight", (K,))
@@ -478,14 +490,16 @@ def qk_norm_fwd(q, k=None, q_weight=None, k_weight=None, *, norm="rms", eps=1e-6
     dt = _dt(act)
     qs = _token_strides(q, "q", act, dev)
     ks = None if k is None else _token_strides(k, "k", act, dev)
-    if q_out is None:
-        q_out = _packed_like(q)
-    if k_out is None and k is not None:
-        k_out = _packed_like(k)
+    q_out, qo_ptr = (_new_like(q) if q_out is None else (q_out, _ptr(q_out, "q_out", act, dev)))
+    if k is None:
+        k_ptr = ko_ptr = None
+    else:
+        k_ptr = k.data_ptr()
+        k_out, ko_ptr = (_new_like(k) if k_out is None else (k_out, _ptr(k_out, "k_out", act, dev)))
     _run(_entry("ssm_qk_norm_fwd"), dev,
-         q.data_ptr(), None if k is None else k.data_ptr(), qs, ks, _ptr(q_weight, "q_weight", F32, dev),
+         q.data_ptr(), k_ptr, qs, ks, _ptr(q_weight, "q_weight", F32, dev),
          _ptr(k_weight, "k_weight", F32, dev), _ptr(inv_freq, "inv_freq", F32, dev),
-         _ptr(positions, "positions", _I32, dev), _ptr(q_out, "q_out", act, dev), _ptr(k_out, "k_out", act, dev),
+         _ptr(positions, "positions", _I32, dev), qo_ptr, ko_ptr,
          batch, L, Hq, Hk, K, rotary, int(bool(interleaved)), kind, float(eps), dt)
     return q_out, k_out
 
