@@ -68,7 +68,7 @@ __device__ __forceinline__ void wave_lds() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 }
 
-// One wave a chunk: 8 waves a CU that never wait for each other (4 waves on a chunk met at 7 barriers: 4 x 2048, 40 heads of 128,
+// One wave a chunk: 8 waves a CU (12 for heads of 64) that never wait for each other (4 waves on a chunk met at 7 barriers: 4 x 2048, 40 heads of 128,
 // 69 us without the scores, 67 with them now).  Rows come straight from memory in operand order.
 // BACK: the rows are the chunk's tokens from its last place to its first, as the backward walk takes them; its matrix is
 // the same with M_ji k_i.k_j for M_ij k_i.k_j.  PT: the scores' terms (0: not wanted).

@@ -8,7 +8,7 @@
 //     o = scale (a S^T q + (q.k) u)
 // needs no second look at the new state.  A lane owns 4 consecutive columns of every `rows`-th row; the rows' parts
 // are added up through LDS in one order.  256 sequences of 40 heads, 128 x 128: 259 us, 5.2 TB/s, a copy's rate; one sequence of 24
-// heads, 64 x 64: 5.5 us of latency.
+// heads, 64 x 64: 5.2 us of latency.
 #include "device_common.hpp"
 #include "lm_kernels.hpp"
 
