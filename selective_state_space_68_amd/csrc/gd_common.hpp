@@ -11,7 +11,9 @@ namespace {
 constexpr int kT = 6;                     // operands of T (and of the scores): 16 rows by 32 tokens, where it is not zero
 constexpr int kVecs = 8;                  // vectors of 64 floats in a chunk's record
 enum { kInto = 0, kLast, kBeta, kSumHi, kSumLo, kWhole };   // exp(G), exp(G_Q - G), beta, G in two parts, exp(G_Q)
-constexpr double kMinGate = -4096.0;      // 2^kMinGate == 0; sums of 64 of these and their differences stay finite
+// The least logarithm of a decay (of base 2): 2^kMinGate is 0 in float32.  No lower, as the sum over a chunk with many decays
+// of 0 has to stay small for exp2_pair.
+constexpr double kMinGate = -160.0;
 
 template <typename ACT>
 constexpr int kTerms = ACT::kBytes == 2 ? 3 : 1;       // operand terms of what the state depends on
@@ -24,8 +26,9 @@ constexpr int kTBytes = kT * kTerms<ACT> * kPieceBytes<ACT>;
 template <typename ACT, int PT>
 constexpr int kRecord = kTBytes<ACT> + kVecs * 256 + kT * PT * kPieceBytes<ACT>;   // a chunk's T, vectors and scores in PT terms
 
-// 2^(hi + lo) for |lo| far below 1: the sum of logarithms is kept as a float32 pair, so that a factor
-// exp(G_i - G_j) is as good as float32 where the sums themselves are in the hundreds.
+// 2^(hi + lo), of first order in lo: the sum of logarithms is kept as a float32 pair, so that a factor exp(G_i - G_j) is as
+// good as float32 where the sums themselves are in the thousands.  With a decay of 0 at every other token of a chunk they reach
+// 32 x 160 < 2^13, where a difference's lo is up to 2^-11 and what is left out (lo log 2)^2 / 2 = 2^-24.
 __device__ __forceinline__ float exp2_pair(float hi, float lo) {
   const float e = exp2_hw(hi);
   return __builtin_fmaf(e, lo * kLn2, e);
