@@ -566,8 +566,9 @@ ssm_status ssm_linear_attention_step(
  * With float32 activations every product is in float32.  With bfloat16, q, k and v enter the products as they are;
  * what the state depends on enters them as three bfloat16 terms (24 bits) and what only outputs depend on as two (16
  * bits); sums and the state are float32.  A NaN or infinity in a token that is there reaches its own and later
- * outputs (as a NaN) and no earlier one.  Errors as there.  Deterministic; which states are asked for and how rows
- * are aligned change no result.
+ * outputs (as a NaN) and no earlier one; so does a product beta k.k' of finite keys that passes float32's range, from
+ * the later of its two tokens on.  Errors as there.  Deterministic; which states are asked for and how rows are aligned
+ * change no result.
  */
 size_t ssm_gated_delta_workspace_size(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V, ssm_dtype dt);
 
@@ -584,7 +585,8 @@ ssm_status ssm_gated_delta_fwd(
  *   dg, dbeta     : out, [batch][L][H] float32 (0 for absent tokens)
  *   workspace     : >= ssm_gated_delta_bwd_workspace_size(...) bytes, for every call with tokens
  *   batch * H * ceil(L / 64) <= 2^26
- * A NaN or infinity makes gradients of its (batch row, head) NaN, of earlier tokens and of other columns too.
+ * A NaN, an infinity or such a product of keys makes gradients of its (batch row, head) NaN, of earlier tokens and of
+ * other columns too.
  * Deterministic.
  */
 size_t ssm_gated_delta_bwd_workspace_size(int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv,

@@ -163,27 +163,48 @@ __global__ __launch_bounds__(256, 2) void gd_prepare_kernel(GdArgs p) {
     wave_lds();
 
     // A's and the scores' tiles: rows i = 32 t + 8 g + 4 u + e, column j = 32 two + 8 (c / 4) + 4 one + c % 4, for i <= j.  The
-    // scores are q_j.k_i, backwards q_i.k_j.  An entry of A that is not finite belongs to a token whose state and whose
-    // successors' are not either (the walk sees to those); as a zero it leaves the rows before alone.
+    // scores are q_j.k_i, backwards q_i.k_j.  An entry of A that is not finite (finite keys may have such a product) belongs to a
+    // token that is not finite, nor are its successors: for outputs it is a zero, which leaves the rows before alone, and the
+    // record says from where on the walk has to make up for it; in the gradient's records it stays.  Behind a decay of 0 or
+    // a beta of 0 there is nothing that a key could meet.
+    constexpr bool CUT = !BACK && PT > 0;
+    int odd = kQ;
     auto tile = [&](int t, int j, const f32x4_t (&s1)[2], const f32x4_t (&s2)[2], int x) __attribute__((always_inline)) {
       const float jhi = sHi[j], jlo = sLo[j];
-      float v[8];
+      float v[8], a[8], poison = 0.0f;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int i0 = 32 * t + 8 * g + 4 * u;
         const float4 hi = *reinterpret_cast<const float4*>(sHi + i0), lo = *reinterpret_cast<const float4*>(sLo + i0);
         const float4 be = *reinterpret_cast<const float4*>(sB + i0);
         const float ihi[4] = {hi.x, hi.y, hi.z, hi.w}, ilo[4] = {lo.x, lo.y, lo.z, lo.w}, ib[4] = {be.x, be.y, be.z, be.w};
-        float a[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float m = BACK ? exp2_pair(ihi[e] - jhi, ilo[e] - jlo) : exp2_pair(jhi - ihi[e], jlo - ilo[e]);
-          a[e] = ib[e] * (m * s1[u][e]);
-          if (i0 + e >= j || !(fabsf(a[e]) < __builtin_huge_valf())) a[e] = 0.0f;
+          a[4 * u + e] = i0 + e < j ? ib[e] * (m * s1[u][e]) : 0.0f;
+          poison = __builtin_fmaf(a[4 * u + e], 0.0f, poison);
           if constexpr (PT > 0) v[4 * u + e] = i0 + e <= j ? s2[u][e] * (p.scale * m) : 0.0f;
         }
+      }
+      if (__builtin_expect(__builtin_amdgcn_ballot_w64(poison != poison) != 0, 0)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int at = 32 * t + 8 * g + i;
+          const float m = BACK ? exp2_pair(sHi[at] - jhi, sLo[at] - jlo) : exp2_pair(jhi - sHi[at], jlo - sLo[at]);
+          if (fabsf(a[i]) < __builtin_huge_valf()) continue;
+          if (m == 0.0f || sB[at] == 0.0f) a[i] = 0.0f;
+          else if (CUT) {
+            a[i] = 0.0f;
+            odd = least(odd, j);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i0 = 32 * t + 8 * g + 4 * u;
         if (i0 / 16 <= j / 16)
-          *reinterpret_cast<float4*>(A + block_at(j / 16, i0 / 16) + j % 16 * kRow + i0 % 16) = make_float4(a[0], a[1], a[2], a[3]);
+          *reinterpret_cast<float4*>(A + block_at(j / 16, i0 / 16) + j % 16 * kRow + i0 % 16) =
+              make_float4(a[4 * u], a[4 * u + 1], a[4 * u + 2], a[4 * u + 3]);
       }
       if constexpr (PT > 0) {
         piece ps[PT];
@@ -216,6 +237,15 @@ __global__ __launch_bounds__(256, 2) void gd_prepare_kernel(GdArgs p) {
             }
           tile(t, 32 * two + 4 * one + perm_row, s1, s2, 2 * two + 2 * t + one);
         }
+    }
+    if constexpr (CUT) {
+      float* vec = reinterpret_cast<float*>(rec + kTBytes<ACT>);
+      if (__builtin_expect(__builtin_amdgcn_ballot_w64(odd < kQ) != 0, 0)) {
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) odd = least(odd, __shfl_xor(odd, d));
+        vec[kWhole * 64 + lane] = __builtin_nanf("");
+      }
+      vec[kFirstOdd * 64 + lane] = static_cast<float>(odd);
     }
     wave_lds();
 
@@ -597,9 +627,10 @@ void gd_walk_kernel(GdArgs p) {
 
     // ---- X = V - exp(G) K E (backwards scale P^T D + exp(G_Q - G) K E)
     // Forwards, a value that is not finite must not reach earlier tokens' outputs through T's zeros: its column is cut there,
-    // its outputs from that token on and its state are NaN.
+    // its outputs from that token on and its state are NaN.  So are all columns from a token on whose row of A is not
+    // finite (the pre-pass of segments has its NaN from exp(G_Q)).
     float x[2][8];
-    float odd = 0.0f;
+    float odd = MODE == kOut ? 0.0f * vec[kWhole * 64] : 0.0f;
     f32x4_t Z[2][2];
     if constexpr (BACK) {
 #pragma unroll
@@ -637,6 +668,7 @@ void gd_walk_kernel(GdArgs p) {
     const bool bad = MODE == kOut && __builtin_amdgcn_ballot_w64(odd != odd) != 0;
     int gone = kQ;                                  // first token of the column that is not finite
     if (__builtin_expect(bad, 0)) {
+      gone = static_cast<int>(vec[kFirstOdd * 64]);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         float beta[8];

@@ -10,7 +10,9 @@ namespace {
 
 constexpr int kT = 6;                     // operands of T (and of the scores): 16 rows by 32 tokens, where it is not zero
 constexpr int kVecs = 8;                  // vectors of 64 floats in a chunk's record
-enum { kInto = 0, kLast, kBeta, kSumHi, kSumLo, kWhole };   // exp(G), exp(G_Q - G), beta, G in two parts, exp(G_Q)
+// exp(G), exp(G_Q - G), beta, G in two parts, exp(G_Q); in every entry the first token whose row of A is not finite, or 64 (outputs'
+// records; exp(G_Q) is NaN there)
+enum { kInto = 0, kLast, kBeta, kSumHi, kSumLo, kWhole, kFirstOdd };
 // The least logarithm of a decay (of base 2): 2^kMinGate is 0 in float32.  No lower, as the sum over a chunk with many decays
 // of 0 has to stay small for exp2_pair.
 constexpr double kMinGate = -160.0;
