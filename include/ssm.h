@@ -582,9 +582,12 @@ ssm_status ssm_gated_delta_fwd(
 /*
  * The gradients of sum(dout * out) + sum(dfinal_state * final_state) of ssm_gated_delta_fwd.  dout, dfinal_state,
  * dq, dk, dv and dinitial_state are as in ssm_linear_attention_bwd;
- *   dg, dbeta     : out, [batch][L][H] float32 (0 for absent tokens)
+ *   dg, dbeta     : out, [batch][L][H] float32 (0 for absent tokens; dg is 0 where the decay is)
  *   workspace     : >= ssm_gated_delta_bwd_workspace_size(...) bytes, for every call with tokens
  *   batch * H * ceil(L / 64) <= 2^26
+ * With bfloat16 activations what dq, dv, dbeta and the states come from enters the products as three bfloat16 terms (24
+ * bits), as forwards; the gradient of v under its key and what passes out of a chunk, in dk and in dg of chunks with a
+ * decay below 0.42, as two (16 bits).  dg is good to about 1e-5 of its own size for any decay, fast ones too.
  * A NaN, an infinity or such a product of keys makes gradients of its (batch row, head) NaN, of earlier tokens and of
  * other columns too.
  * Deterministic.

@@ -141,6 +141,7 @@ __global__ __launch_bounds__(256, 2) void gd_prepare_kernel(GdArgs p) {
     {
       double G = static_cast<double>(g_in) * 1.4426950408889634;
       G = G < kMinGate ? kMinGate : G;              // (NaN passes through)
+      const bool fast = __builtin_amdgcn_ballot_w64(G < kFastGate) != 0, strong = __builtin_amdgcn_ballot_w64(G < kStrongGate) != 0;
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
         const double before = __shfl_up(G, d);
@@ -157,7 +158,12 @@ __global__ __launch_bounds__(256, 2) void gd_prepare_kernel(GdArgs p) {
       vec[kBeta * 64 + row] = beta;
       vec[kSumHi * 64 + row] = hi;
       vec[kSumLo * 64 + row] = lo;
-      vec[kWhole * 64 + row] = __shfl(into, 63);
+      const float whole = __shfl(into, 63);
+      vec[kWhole * 64 + row] = whole;
+      if constexpr (!BACK && PT == 0) {
+        const bool last = left <= kQ;               // (the gradient of the state behind it is the caller's, of any size)
+        vec[kPace * 64 + row] = !fast ? kSlow : whole < nothing(strong) ? kFast : strong || last ? kFastThrough : kSlow;
+      }
       sHi[row] = hi; sLo[row] = lo; sB[row] = beta;
     }
     wave_lds();

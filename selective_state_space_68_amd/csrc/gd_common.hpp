@@ -11,8 +11,14 @@ namespace {
 constexpr int kT = 6;                     // operands of T (and of the scores): 16 rows by 32 tokens, where it is not zero
 constexpr int kVecs = 8;                  // vectors of 64 floats in a chunk's record
 // exp(G), exp(G_Q - G), beta, G in two parts, exp(G_Q); in every entry the first token whose row of A is not finite, or 64 (outputs'
-// records; exp(G_Q) is NaN there)
-enum { kInto = 0, kLast, kBeta, kSumHi, kSumLo, kWhole, kFirstOdd };
+// records; exp(G_Q) is NaN there); in the gradient's records what gd_grad.hip needs for g: the chunk's pace in the first entry, in
+// the second the sum of what its tokens have from before it, in the third, of a stretch's last chunk, <F, E> behind it
+enum { kInto = 0, kLast, kBeta, kSumHi, kSumLo, kWhole, kFirstOdd, kPace };
+// A chunk's pace: every decay at least 2^kFastGate; or one is less, and exp(G_Q) below `nothing` (what passes through the whole chunk
+// is too little to be seen in a gradient) or above.
+enum { kSlow = 0, kFast, kFastThrough };
+constexpr double kFastGate = -1.25, kStrongGate = -3.0;
+__device__ __forceinline__ float nothing(bool strong) { return strong ? 0x1p-48f : 0x1p-32f; }   // a decay is below 2^kStrongGate
 // The least logarithm of a decay (of base 2): 2^kMinGate is 0 in float32.  No lower, as the sum over a chunk with many decays
 // of 0 has to stay small for exp2_pair.
 constexpr double kMinGate = -160.0;

@@ -9,20 +9,31 @@
 //          = -beta_j exp(G_j) E y_j + sum_{i<j} N2_ji k_i,                               N2_ji = -beta_j M_ji y_j.u_i
 //     and the first (backwards) = exp(G_Q - G_i) F u_i + sum_{j>=i} N1_ji q_j + sum_{j>i} N2_ji k_j
 //     dbeta_j = y_j.w_j
-// g: a_t scales everything that passes from before t to t and after, so with r_j = exp(G_j) the state's scale, S / r,
-// r q and v / r carry all of it: d loss / d G_j = q_j.dq_j - v_j.dv_j, and dg_t is its sum over j >= t.  Summed over a
-// stretch only, onto <F, E> at its end: the sum over a long sequence would lose what a fast decay leaves of it.
+// g: dg_t is what passes token t, from tokens and states before it to tokens and states from it on; each part carries a_t.
+// In a chunk of slow decays it is a sum over later tokens: a_t scales everything that passes, so with r_j = exp(G_j) the
+// state's scale, S / r, r q and v / r carry all of it: d loss / d G_j = q_j.dq_j - v_j.dv_j, and dg_t is its sum over j >= t in
+// the stretch, in float64, onto <F, E> at its end.  Both dots hold what token j has of itself, which a fast decay leaves
+// dg_t far below: at g = -5 the float32 terms' roundings were 1e-3 of dg, at -12 all of it.  So in a chunk with a decay below
+// 2^kFastGate = 0.42 the parts are summed, none of which a token has of itself:
+//     dg_t = exp(G_Q) <F, E> + sum_{j>=t} from_j + sum_{i<t<=j} (N1_ji q_j.k_i + N2_ji k_j.k_i) + sum_{i<t} to_i,
+//     from_j = q_j.(scale exp(G_j) E d_j) + k_j.(-beta_j exp(G_j) E y_j),   to_i = k_i.(exp(G_Q - G_i) F u_i),
+// with E before the chunk and F behind it; from_j and the sum over pairs come with dq, to_i with the rest of dk.  <F, E> takes both
+// states at once: the first kernel leaves E in memory for the second, where exp(G_Q) is not too small to be seen and
+// either a decay is below 1/8 or F is the caller's; else the chunk counts as slow.  Errors of dg against its own size at g = -1 to
+// -20 and at single decays of exp(-3) to exp(-30) in slow heads: below 1e-5; a decay of 0 has 0.  The two kernels of the case
+// below, whose heads range from slow to fast, took 778 us with sums over later tokens alone and take 839 (float32, 2 x 2047, 24
+// heads of 64: 190 and 225).
 //
 // A workgroup walks one stretch; a wave owns 16 columns of E^T (of K), so that only the tokens' scalars are summed over
 // waves.  Rows of D, W and Y lie in LDS, W and Y as terms, split once a workgroup; their dot products y.w and y.v are
 // taken on the way in.  A chunk's rows are asked for while the one before is worked on.
 //
-// What bounds it: 8 x 2048 tokens, 32 heads of 128, bfloat16: 456 us and 328, 3.5 and 4.2 TB/s (1.6 and 1.4 GB: W and Y as float32 rows are
-// half of it) with the matrix units busy for a third of the time: its one workgroup a CU (142 KB of LDS) reads, multiplies and meets at
-// three barriers a chunk.
+// What bounds it: 8 x 2048 tokens, 32 heads of 128, bfloat16: 492 us and 348, 3.3 and 4.0 TB/s (1.6 and 1.4 GB: W and Y as float32 rows are
+// half of it) with the matrix units busy for a third of the time: its one workgroup a CU (155 and 145 KB of LDS) reads, multiplies and
+// meets at three barriers a chunk.
 //
-// Roundings (bfloat16 activations): what g's float32 gradient sees (dq, with the states that it is formed from) comes from
-// 24-bit operands; what only dk's bfloat16 sees from 16 bits.
+// Roundings (bfloat16 activations): what g's float32 gradient sees of dq, with the states that it is formed from, comes from
+// 24-bit operands; what dk's bfloat16 sees, and g through k in chunks of fast decays, from 16 bits (y and F u: 2^-17 an operand).
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -111,6 +122,10 @@ void gd_qk_kernel(GdGradArgs p) {
   __shared__ __attribute__((aligned(16))) float vec[kVecs * 64];
   // the tokens' scalars, of this chunk and of the one before: parts of q.dq, y.w and y.v, beta
   __shared__ float sSum[2][NW][kQ], sDot[2][3][kQ];
+  // of chunks with fast decays: what passes tokens from one of the chunk to another, by operand, and from the first half into
+  // tokens of the second; products of the two states
+  __shared__ __attribute__((aligned(16))) float sPass[BACK ? 1 : 2][kT][32];
+  __shared__ float sOver[BACK ? 1 : 2][32], sThrough[2][NW];
 
   const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6), g = lane >> 4, c16 = lane & 15;
   const int L = static_cast<int>(p.L), K = p.K, V = p.V;
@@ -234,18 +249,73 @@ void gd_qk_kernel(GdGradArgs p) {
         if (!BACK && (tid + i * THREADS) / 64 == kBeta) sDot[which][2][tid % 64] = in.vec[i];
       }
   };
-  // A chunk's tokens (one wave, when they are complete): dbeta, and in dg's place what the sums at the end are of.
-  auto scalars = [&](int done) __attribute__((always_inline)) {
-    const int which = done & 1, t = (c_begin + done) * kQ + lane;
-    if (t >= len) return;
+  auto chunk_of = [&](int done) { return BACK ? c_end - 1 - done : c_begin + done; };
+  auto suffix = [&](auto x) __attribute__((always_inline)) {          // the sum over this lane and those after it
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const auto after = __shfl_down(x, d);
+      if (lane + d < 64) x += after;
+    }
+    return x;
+  };
+  // A chunk's tokens (one wave, when they are complete).  The first kernel: dbeta, and in dg's place its part of what passes
+  // a token, or the terms that the sum over later tokens is of.
+  auto scalars = [&](int done, int pace) __attribute__((always_inline)) {
+    const int which = done & 1, c = chunk_of(done), t = c * kQ + lane;
+    const bool on = t < len;
+    const int64_t at = (b * L + (on ? t : len - 1)) * p.H + h;
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NW; ++i) sum += sSum[which][i][lane];
-    const int64_t at = (b * L + t) * p.H + h;
-    p.dg[at] = __builtin_fmaf(-sDot[which][2][lane], sDot[which][1][lane], sum);
-    p.dbeta[at] = sDot[which][0][lane];
+    if (pace == kSlow) {
+      sum = __builtin_fmaf(-sDot[which][2][lane], sDot[which][1][lane], sum);
+    } else {
+      const float (&pass)[kT][32] = sPass[BACK ? 0 : which];
+      sum = suffix(on ? sum : 0.0f);
+      if (lane == 0) reinterpret_cast<float*>(p.rec + (bh * nchunks + c) * kRecord<ACT, 0> + kTBytes<ACT>)[kPace * 64 + 1] = sum;
+      const float over = suffix(lane >= 32 && on ? sOver[BACK ? 0 : which][lane & 31] : 0.0f);
+      sum += lane < 32 ? (pass[0][lane] + pass[1][lane]) + (pass[2][lane] + pass[3][lane])
+                       : (pass[4][lane & 31] + pass[5][lane & 31]) + over;
+    }
+    if (on) {
+      p.dg[at] = sum;
+      p.dbeta[at] = sDot[which][0][lane];
+    }
   };
-  auto chunk_of = [&](int done) { return BACK ? c_end - 1 - done : c_begin + done; };
+  // The second kernel: dg.  carry: what passes from the tokens before this chunk's end to those behind it.
+  double carry = 0.0;
+  float gate_whole = 0.0f, gate_into = 0.0f, gate_part = 0.0f;        // exp(G_Q), the sum of from_j, the first kernel's part of dg
+  auto gate_at = [&](int done, int lane) { return p.dg + (b * L + least(chunk_of(done) * kQ + lane, len - 1)) * p.H + h; };
+  auto gates = [&](int done, int pace) __attribute__((always_inline)) {
+    const int which = done & 1, t = chunk_of(done) * kQ + lane;
+    const bool on = t < len;
+    float x = gate_part;
+    if (pace == kSlow) {
+      const double sum = suffix(on ? static_cast<double>(x) : 0.0) + carry;
+      carry = __shfl(sum, 0);
+      x = static_cast<float>(sum);
+    } else {
+      float out = 0.0f, through = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        out += sSum[which][i][lane];
+        if (pace == kFastThrough) through += sThrough[which][i];
+      }
+      if (!on) out = 0.0f;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const float before = __shfl_up(out, d);
+        if (lane >= d) out += before;
+      }
+      const float before = __shfl_up(out, 1);       // of the tokens before this one
+      if (lane > 0) x += before;
+      through *= gate_whole;
+      x += through;
+      carry = static_cast<double>(through) + gate_into;
+    }
+    // (the first token of a sequence without a state has nothing to scale)
+    if (on) *gate_at(done, lane) = t == 0 && !p.carried ? 0.0f : x;
+  };
 #pragma unroll
   for (int part = 0; part < 4; ++part) ask(chunk_of(0), part, true);
 
@@ -286,6 +356,7 @@ void gd_qk_kernel(GdGradArgs p) {
   };
   const f32x4_t zero = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
+  int pace = kSlow;
 #pragma unroll 1
   for (int done = 0; done < c_end - c_begin; ++done) {
     const int c = chunk_of(done);
@@ -293,7 +364,47 @@ void gd_qk_kernel(GdGradArgs p) {
     const int64_t t0 = static_cast<int64_t>(c) * kQ;
     store(n, done & 1);
     __syncthreads();
-    if (!BACK && done > 0 && w == NW - 1) scalars(done - 1);      // (the last waves have no part in N1 and N2)
+    if (done > 0 && w == NW - 1) {                  // (the last waves have no part in N1 and N2)
+      if constexpr (BACK) gates(done - 1, pace);
+      else scalars(done - 1, pace);
+    }
+    pace = uniform_int(static_cast<int>(vec[kPace * 64]));
+    if constexpr (BACK) {
+      gate_whole = vec[kWhole * 64];
+      gate_into = vec[kPace * 64 + 1];
+      gate_part = *gate_at(done, w == NW - 1 ? lane : 0);
+      if (done == 0) carry = vec[kPace * 64 + 2];
+    }
+    // the state before a chunk, as the first kernel's threads have it
+    float4* before = reinterpret_cast<float4*>(p.through + (bh * nchunks + c) * (KD * VD)) + tid;
+    if constexpr (BACK) {
+      if (pace == kFastThrough) {
+        float dot = 0.0f;
+#pragma unroll
+        for (int y = 0; y < KT; ++y)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float4 x = before[(2 * y + u) * THREADS];
+            const f32x4_t& f = E[y][u];
+            dot = __builtin_fmaf(x.x, f[0], __builtin_fmaf(x.y, f[1], __builtin_fmaf(x.z, f[2], __builtin_fmaf(x.w, f[3], dot))));
+          }
+        dot = wave_sum(dot);
+        if (lane == 0) sThrough[done & 1][w] = dot;
+      }
+    }
+    // (rows 16 jt + c16 of q for what passes through the chunk's tokens)
+    constexpr int kOps = (kT + NW - 1) / NW;
+    piece qn[TILES && !BACK ? kOps : 1][KD / 32];
+    if constexpr (TILES && !BACK) {
+#pragma unroll
+      for (int o = 0; o < kOps; ++o) {
+        const int x = w + o * NW, row = 16 * (x < 4 ? x : x - 2) + c16;
+        const bool wanted = pace != kSlow && x < kT;
+#pragma unroll
+        for (int y = 0; y < KD / 32; ++y)
+          qn[o][y] = load8<ACT, MOVE>(qg + t0 * p.qs[1], static_cast<Offset<MOVE>>(p.qs[1]), wanted ? row : 0, n, wanted ? 32 * y + 8 * g : 0, K);
+      }
+    }
     // what meets dq and dk at the end (asked for before the next chunk's rows, which its arrival need not wait for)
     const int first = 16 * w + 4 * g;               // this lane's columns of token 16 jt + c16 there
     const uint32_t out_step = static_cast<uint32_t>(out_row);
@@ -326,7 +437,7 @@ void gd_qk_kernel(GdGradArgs p) {
     const bool more = done + 1 < c_end - c_begin;
     // (the last chunk asks for one place: after a load on one side of a branch every wait is for all loads)
     const int next = chunk_of(more ? done + 1 : done);
-    ask(next, 0, more);
+    if (TILES || BACK) ask(next, 0, more);
     // the wave's own columns of k (and of q): tokens 32 t + 8 g + e of column c16
     piece kf[2], qf[2];
     if constexpr (TILES) {
@@ -407,6 +518,69 @@ void gd_qk_kernel(GdGradArgs p) {
         v1[e] = (BACK ? row >= cc : row <= cc) ? a1[e / 4][e % 4] * (p.scale * mi) : 0.0f;
         v2[e] = (BACK ? row > cc : row < cc) ? a2[e / 4][e % 4] * -(mj * mi) : 0.0f;
       }
+      if constexpr (!BACK) {
+        if (pace != kSlow) {
+          // what token j has of token i through the chunk: N1_ji q_j.k_i + N2_ji k_j.k_i, for i < j
+          f32x4_t b1[2] = {zero, zero}, b2[2] = {zero, zero};
+          if constexpr (TILES) {
+            const uint32_t tile_k = lds_address(sK);
+            const uint32_t kn = O::template row_part<RK, false>(tile_k, cc, g);
+            const uint32_t kp = O::template row_part<RK, false>(tile_k, 32 * t + perm_row, g);
+#pragma unroll
+            for (int y = 0; y < KD / 32; ++y) {
+              const piece qj = present<ACT, MOVE>(kOps > 1 && x >= NW ? qn[kOps - 1][y] : qn[0][y], cc, n, 32 * y + 8 * g, K);
+              const piece kj = O::row(kn, 4 * PB * y, 0);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const piece ki = O::row(kp, (4 * PB * y) ^ (u ? swizzle<RK, kF32, false>(4) << 4 : 0), 4 * u * RK);
+                b1[u] = O::mma(ki, qj, b1[u]);
+                b2[u] = O::mma(ki, kj, b2[u]);
+              }
+            }
+          } else {
+            const elem *qc = qg + t0 * p.qs[1], *kc = kg + t0 * p.ks[1];
+#pragma unroll 1
+            for (int y = 0; y < KD / 32; ++y) {
+              auto eight_of = [&](const elem* base, int64_t stride, int row) __attribute__((always_inline)) {
+                const int at = 32 * y + 8 * g;
+                return present<ACT, MOVE>(load8<ACT, MOVE>(base, static_cast<Offset<MOVE>>(stride), row, n, at, K), row, n, at, K);
+              };
+              const piece qj = eight_of(qc, p.qs[1], cc), kj = eight_of(kc, p.ks[1], cc);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const piece ki = eight_of(kc, p.ks[1], 32 * t + 4 * u + perm_row);
+                b1[u] = O::mma(ki, qj, b1[u]);
+                b2[u] = O::mma(ki, kj, b2[u]);
+              }
+            }
+          }
+          // summed over i before a token and j from it on: over the lane's tokens i, those of the lanes before, the columns
+          float before[8], sum = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            before[e] = sum;
+            const float x = __builtin_fmaf(v1[e], b1[e / 4][e % 4], v2[e] * b2[e / 4][e % 4]);
+            sum += 32 * t + 8 * g + e < cc ? x : 0.0f;
+          }
+#pragma unroll
+          for (int d = 16; d < 64; d *= 2) {
+            const float x = __shfl_up(sum, d);
+            if (lane >= d) sum += x;
+          }
+          const float lanes = __shfl_up(sum, 16);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float x = 32 * t + 8 * g + e <= cc ? before[e] + (g > 0 ? lanes : 0.0f) : 0.0f;
+            before[e] = row_sum<16>(x);
+          }
+          float* to = sPass[done & 1][x] + 8 * g;
+          if (c16 == 0) {
+            *reinterpret_cast<float4*>(to) = make_float4(before[0], before[1], before[2], before[3]);
+            *reinterpret_cast<float4*>(to + 4) = make_float4(before[4], before[5], before[6], before[7]);
+          }
+          if (g == 3 && (x == 2 || x == 3)) sOver[done & 1][cc - 32] = sum;
+        }
+      }
       piece o1[NT], o2[OT];
       O::template split<NT>(v1, o1);
       O::template split<OT>(v2, o2);
@@ -416,6 +590,7 @@ void gd_qk_kernel(GdGradArgs p) {
       for (int m = 0; m < OT; ++m) store_piece(sN2 + (x * OT + m) * kOne + lane * (kOne / 64), o2[m]);
     }
 
+    if (!TILES && !BACK) ask(next, 0, more);        // (N's loads would wait for these)
     ask(next, 1, more);
     // ---- the state's part, rows k, column j = 16 jt + c16: acc of D and acy of Y, backwards acc of W
     f32x4_t acc[4], acy[4];
@@ -467,6 +642,43 @@ void gd_qk_kernel(GdGradArgs p) {
         if constexpr (!BACK) acy[jt][e] *= -(beta * into);
       }
     }
+    if (pace != kSlow) {
+      // what passes into a token from before the chunk, q.dq and k.dk of the state's parts; backwards out of the chunk from it
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt) {
+        const int row = 16 * jt + c16;
+        float kx[4], sum = 0.0f;
+        if constexpr (TILES) {
+          const uint2 x = *reinterpret_cast<const uint2*>(sK + row * RK + ((2 * first) ^ (swizzle<RK, false, false>(row) << 4)));
+          kx[0] = bf16_lo(x.x); kx[1] = bf16_hi(x.x); kx[2] = bf16_lo(x.y); kx[3] = bf16_hi(x.y);
+        } else {
+          const elem* from = kg + (t0 + least(row, n - 1)) * p.ks[1];
+          if constexpr (VEC) {
+            const float4 x = *reinterpret_cast<const float4*>(from + least(first, K - 4));
+            kx[0] = x.x; kx[1] = x.y; kx[2] = x.z; kx[3] = x.w;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) kx[e] = load_act<ACT>(from, least(first + e, K - 1));
+          }
+        }
+        if constexpr (BACK) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum = first + e < K ? __builtin_fmaf(kx[e], acc[jt][e], sum) : sum;
+        } else {
+          float qx[4] = {meet[jt][0], meet[jt][1], meet[jt][2], meet[jt][3]};
+          if constexpr (VEC && !kF32) {
+            const uint32_t a = __builtin_bit_cast(uint32_t, qx[0]), d = __builtin_bit_cast(uint32_t, qx[1]);
+            qx[0] = bf16_lo(a); qx[1] = bf16_hi(a); qx[2] = bf16_lo(d); qx[3] = bf16_hi(d);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sum = first + e < K ? __builtin_fmaf(qx[e], acc[jt][e], __builtin_fmaf(kx[e], acy[jt][e], sum)) : sum;
+        }
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (g == 0) sSum[done & 1][w][row] = sum;
+      }
+    }
     ask(next, 2, more);
     __syncthreads();                                // N1 and N2 are complete
 
@@ -488,7 +700,7 @@ void gd_qk_kernel(GdGradArgs p) {
       }
 
     // ---- out: lane (g, c) has columns 16 w + 4 g .. of token 16 jt + c
-    if constexpr (!BACK) {                          // q.dq
+    if (!BACK && pace == kSlow) {                   // q.dq
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
         if constexpr (VEC && !kF32) {
@@ -545,6 +757,14 @@ void gd_qk_kernel(GdGradArgs p) {
     ask(next, 3, more);
     // ---- the state
     if (more || !BACK) {      // (backwards the last is of no use)
+      if constexpr (!BACK) {
+        if (pace == kFastThrough) {
+#pragma unroll
+          for (int y = 0; y < KT; ++y)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) before[(2 * y + u) * THREADS] = make_float4(E[y][u][0], E[y][u][1], E[y][u][2], E[y][u][3]);
+        }
+      }
       const float whole = vec[kWhole * 64];
       each([&](int y, int u, int e, bool, uint32_t) { E[y][u][e] *= whole; });
       const uint32_t w_cols = O::template column_part<RV, PW>(tile_w, 0, 8, lane);
@@ -598,37 +818,24 @@ void gd_qk_kernel(GdGradArgs p) {
     __syncthreads();                                // the tiles are free, the tokens' sums complete
   }
 
-  if constexpr (!BACK) {
-    if (w == NW - 1) scalars(c_end - c_begin - 1);
-    // <F, E> at the end of the stretch, then the sums back over its tokens
+  if constexpr (BACK) {
+    if (w == NW - 1) gates(c_end - c_begin - 1, pace);
+  } else {
+    if (w == NW - 1) scalars(c_end - c_begin - 1, pace);
+    // <F, E> at the end of the stretch
     const float* f = p.kept_f + (bh * stretches + s) * static_cast<int64_t>(K) * V;
     float dot = 0.0f;
     each([&](int y, int u, int e, bool there, uint32_t at) {
       if (there) dot = __builtin_fmaf(f[at], E[y][u][e], dot);
     });
     dot = wave_sum(dot);
-    __syncthreads();                                // (the sums have been read, the tokens' parts are in memory)
-    if (lane == 0) sSum[0][w][0] = dot;
+    if (lane == 0) sThrough[0][w] = dot;
     __syncthreads();
-    if (w == 0) {
-      double carry = 0.0;
+    if (tid == 0) {
+      float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NW; ++i) carry += sSum[0][i][0];
-      const int stop = least(len, c_end * kQ);
-      for (int c = c_end - 1; c >= c_begin; --c) {
-        const int t = c * kQ + lane;
-        float* at = p.dg + (b * L + least(t, stop - 1)) * p.H + h;
-        double x = t < stop ? static_cast<double>(*at) : 0.0;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-          const double after = __shfl_down(x, d);
-          if (lane + d < 64) x += after;
-        }
-        x += carry;
-        carry = __shfl(x, 0);
-        // (the first token of a sequence without a state has nothing to scale)
-        if (t < stop) *at = t == 0 && !p.carried ? 0.0f : static_cast<float>(x);
-      }
+      for (int i = 0; i < NW; ++i) sum += sThrough[0][i];
+      reinterpret_cast<float*>(p.rec + (bh * nchunks + c_end - 1) * kRecord<ACT, 0> + kTBytes<ACT>)[kPace * 64 + 2] = sum;
     }
   }
 }

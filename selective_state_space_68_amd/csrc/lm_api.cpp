@@ -390,6 +390,7 @@ struct GdBwdPlan {
   GdPlan fwd, back;
   uint64_t rows = 0, kept = 0;        // of one walk
   uint64_t part = 0;                  // dk's forward part
+  uint64_t back_rec = 0;              // the backward walk's records, and after it the states that pass through chunks
   uint64_t dk = 0, dq = 0, dv = 0;    // of shared heads
   uint64_t total = 0;
 };
@@ -402,9 +403,11 @@ bool gd_bwd_plan(int64_t batch, int64_t L, int64_t H, int64_t Hq, int64_t Hk, in
   const int64_t nch = (L + 63) / 64, every = ssm::gd_every(batch, L, H, K, V, dt_of(dt));
   if (!bytes_of(4, &p->rows, batch, H, nch, 64, V > 64 ? 128 : 64) ||
       !bytes_of(4, &p->kept, batch, H, (nch + every - 1) / every, K, V) || !bytes_of(4, &p->part, batch, H, nch, 64, K > 64 ? 128 : 64) ||
+      !bytes_of(4, &p->back_rec, batch, H, nch, K > 64 ? 128 : 64, V > 64 ? 128 : 64) ||
       (Hk != H && !bytes_of(4, &p->dk, batch, L, H, K)) || (Hq != H && !bytes_of(4, &p->dq, batch, L, H, K)) || (Hv != H && !bytes_of(4, &p->dv, batch, L, H, V)))
     return false;
-  p->total = p->fwd.total + p->back.total + 2 * (up256(p->rows) + up256(p->kept)) + up256(p->part) + up256(p->dk) + up256(p->dq) + up256(p->dv);
+  if (p->back_rec < p->back.rec) p->back_rec = p->back.rec;
+  p->total = p->fwd.total + (p->back.total - up256(p->back.rec)) + up256(p->back_rec) + 2 * (up256(p->rows) + up256(p->kept)) + up256(p->part) + up256(p->dk) + up256(p->dq) + up256(p->dv);
   return p->total <= kMaxBytes;
 }
 
@@ -550,7 +553,7 @@ ssm_status ssm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
   a.every = ssm::gd_every(batch, L, H, K, V, dt_of(dt));
   a.nseg = plan.fwd.nseg;
   a.rec = take(plan.fwd.rec);
-  a.rec_back = take(plan.back.rec);
+  a.rec_back = take(plan.back_rec);
   a.seg_m = take.floats(plan.fwd.mat);
   a.seg_mt = take.floats(plan.fwd.mat);
   a.seg = take.floats(plan.fwd.seg);
@@ -581,7 +584,7 @@ ssm_status ssm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
     x.qs[i] = t.q.stride[i]; x.ks[i] = t.k.stride[i]; x.vs[i] = t.v.stride[i]; x.ds[i] = t.d.stride[i];
   }
   x.qdiv = a.qdiv; x.kdiv = a.kdiv; x.vdiv = a.vdiv;
-  x.rec = a.rec; x.w = a.w_out; x.y = r.w_out; x.kept_e = a.kept; x.kept_f = r.kept; x.lengths = lengths;
+  x.rec = a.rec; x.through = reinterpret_cast<float*>(a.rec_back); x.w = a.w_out; x.y = r.w_out; x.kept_e = a.kept; x.kept_f = r.kept; x.lengths = lengths;
   x.dq = dq_part ? static_cast<void*>(dq_part) : dq; x.dq_f32 = dq_part != nullptr;
   x.dk_part = part; x.dk = dk_part ? static_cast<void*>(dk_part) : dk; x.dk_f32 = dk_part != nullptr;
   x.dg = dg; x.dbeta = dbeta; x.batch = batch; x.L = L; x.H = a.H; x.K = a.K; x.V = a.V; x.every = a.every; x.scale = scale;

@@ -108,7 +108,8 @@ struct GdGradArgs {
   const void *q = nullptr, *k = nullptr, *v = nullptr, *d = nullptr;   // d: the outputs' gradient, [batch][L][H][V]
   int64_t qs[3] = {}, ks[3] = {}, vs[3] = {}, ds[3] = {};
   int qdiv = 1, kdiv = 1, vdiv = 1;
-  const char* rec = nullptr;
+  char* rec = nullptr;
+  float* through = nullptr;                              // states before chunks of which a part passes through, [batch * H][chunks][..]
   const float *w = nullptr, *y = nullptr;                // w_out of the two walks
   const float *kept_e = nullptr, *kept_f = nullptr;      // kept of the two walks
   const int32_t* lengths = nullptr;
