@@ -247,17 +247,6 @@ __device__ __forceinline__ float wave_sum(float v) {
   return wave_lane63(v);
 }
 
-// The sum over N = 8 or 16 neighbouring lanes: quads, then the quads of 8, then of 16.
-template <int N>
-__device__ __forceinline__ float row_sum(float v) {
-  static_assert(N == 8 || N == 16, "");
-  v += dpp_mov<0xb1, 0xf, true>(0.0f, v);           // quad_perm [1, 0, 3, 2]
-  v += dpp_mov<0x4e, 0xf, true>(0.0f, v);           // quad_perm [2, 3, 0, 1]
-  v += dpp_mov<0x141, 0xf, true>(0.0f, v);          // row_half_mirror
-  if constexpr (N == 16) v += dpp_mov<0x140, 0xf, true>(0.0f, v);   // row_mirror
-  return v;
-}
-
 __device__ __forceinline__ float lane_value(float v, int l) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
 }

@@ -40,6 +40,7 @@
 #include "gd_common.hpp"
 #include "la_tiles.hpp"
 #include "lm_kernels.hpp"
+#include "row_sum.hpp"
 #include "scan_common.hpp"
 
 namespace ssm {

@@ -15,6 +15,7 @@
 // groups in LDS, and over workgroups by a second kernel, in one order.
 #include "device_common.hpp"
 #include "lm_kernels.hpp"
+#include "row_sum.hpp"
 
 namespace ssm {
 namespace {
