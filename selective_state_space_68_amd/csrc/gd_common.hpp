@@ -90,17 +90,5 @@ __device__ __forceinline__ void drop_first(F8& p, int by) {
   p.b = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// The sum of products of two values in N terms each, of those terms that count at N terms (largest last).
-template <typename O, int NA, int NB>
-__device__ __forceinline__ f32x4_t mma_terms(const typename O::piece (&a)[NA], const typename O::piece (&b)[NB], f32x4_t c) {
-  constexpr int most = NA > NB ? NA : NB;
-#pragma unroll
-  for (int sum = most - 1; sum >= 0; --sum)
-#pragma unroll
-    for (int i = 0; i < NA; ++i)
-      if (sum - i >= 0 && sum - i < NB) c = O::mma(a[i], b[sum - i], c);
-  return c;
-}
-
 }  // namespace
 }  // namespace ssm

@@ -170,7 +170,6 @@ struct QkArgs {
   int vec = 0;                                           // rows move as pieces of 4 elements
   int split = 1;
 };
-constexpr int kQkMaxDim = 256;
 int qk_norm_parts();                                     // most workgroups that sum the weights' gradients
 hipError_t launch_qk_norm(const QkArgs& a, Dt dt, hipStream_t s);
 hipError_t launch_qk_norm_bwd(const QkArgs& a, Dt dt, hipStream_t s);
