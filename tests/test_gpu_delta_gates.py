@@ -119,6 +119,25 @@ def test_resets_in_a_slow_head(at, reset, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("K,V,L,carried", [(64, 64, 150, True), (128, 128, 200, False), (100, 36, 65, True)])
+def test_strengths_head_by_head(K, V, L, carried, dtype):
+    """beta's gradient, y.w of float32 rows from 24-bit operands in either type, against the size of its own head's."""
+    import selective_state_space_68_amd as ssm
+    H = len(RATES)
+    t, s0, df = ref.inputs(2, L, H, K, V, dtype, (H, 1, 2), seed=L + V)
+    t["g"] = torch.tensor(RATES) * (0.9 + 0.2 * torch.rand(2, L, H, generator=torch.Generator().manual_seed(L)))
+    s0, df = (s0, df) if carried else (None, None)
+    want = ref.delta_grad(*t.values(), K ** -0.5, s0, df)["dbeta"]
+    got = ssm.gated_delta_bwd(*(t[n].cuda() for n in ("q", "k", "v", "g", "beta", "do")),
+                              initial_state=None if s0 is None else s0.cuda(),
+                              dfinal_state=None if df is None else df.cuda())["dbeta"]
+    for b in range(2):
+        for h, rate in enumerate(RATES):
+            size = want[b, :, h].abs() + want[b, :, h].square().mean().sqrt()
+            _check(got[b, :, h], want[b, :, h], size, BOUND[F32], f"{b} {rate}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_ragged_rows(dtype):
     """Chunks of one token and of none, NaN in absent ones."""
     L, H, lengths = 200, 4, [200, 0, 1, 64, 65, 129]
