@@ -24,10 +24,11 @@
 // float32's accuracy over any number of tokens.  What only the outputs see (E and U in front of them, and the
 // scores) has two terms, 16 bits, so that the output's own rounding is the one that counts.
 //
-// What bounds it (bfloat16, heads of 128): the walk by its products, of which the terms make 24 MFLOP a chunk of 128 columns: 4 x 2048
-// tokens, 40 heads: 201 us, 6.3 a chunk, 3.8 TFLOP/s on each of the 160 CUs that have a (batch row, head); a large library
-// product reaches 5.0 a CU.  The prepared records by memory: 67 us there for 254 MB, 3.8 TB/s (131072 tokens, 20 heads: 522 us,
-// 5.9 TB/s).  A sequence of few heads by both in turn: segments.  The shortest prompts by latency, 10 us a kernel.
+// What bounds it (bfloat16, heads of 128): the walk by the chain of a chunk, K E, T X, U and K^T U one after the other with two
+// barriers and a wait for the next chunk's tiles: 4 x 2048 tokens, 40 heads: 201 us, 6.3 a chunk (24 MFLOP with the terms) on each of
+// the 160 CUs that have a (batch row, head), the matrix units busy for 0.44 of it; a workgroup of half the columns, and so half the
+// products, still takes 0.78 of the time.  The prepared records by memory: 67 us there for 254 MB, 3.8 TB/s (131072 tokens, 20
+// heads: 522 us, 5.9 TB/s).  A sequence of few heads by both in turn: segments.  The shortest prompts by latency, 10 us a kernel.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -995,7 +996,8 @@ void launch_gd_t(const GdArgs& a, hipStream_t s) {
 // Columns of a workgroup.  128 where more than half of the CUs have work then: the rows of q and k and the record are read once for
 // them, and two waves a SIMD hide each other's waits.  64 where that leaves each workgroup a CU of its own, and for rows that
 // do not move as whole vectors.  2048 tokens, heads of 128, us with 128 and with 64 columns: bfloat16, 80 pairs of batch row and head 213 and
-// 167, 120 pairs 237 and 198, 160 pairs 260 and 341; float32, 80 pairs 679 and 486, 160 pairs 767 and 917; 256 pairs, gradient, 1452 and 1613.
+// 167, 120 pairs 237 and 198, 160 pairs 260 and 341 (two rounds: two workgroups of about 120 KB of LDS do not fit a CU); float32, 80 pairs
+// 679 and 486, 160 pairs 767 and 917; 256 pairs, gradient, 1431 and 1568.
 bool wide(const GdArgs& a, int KD) {
   return a.move == 16 && a.K == KD && a.V == 128 && a.batch * a.H * a.nseg > 128;
 }
@@ -1048,7 +1050,7 @@ constexpr int kSegTarget = 256;
 // longer.  The count is then derived back from the segment length, so that no segment is without a chunk.
 // us with targets of 128, 256 and 512 and without segments, bfloat16, heads of 128: 131072 tokens, 20 heads: 3351, 3200, 3130, 8967;
 // 8192 tokens, 32 heads: 351, 336, 392, 582; 4096, 40: 287, 232, 286, 289; 2048, 20: 95, 110, 111, 145; 8192, 64: 638, 618, 655, 639;
-// float32 gradient, 2 x 2047, 24 heads of 64: 668, 503, 525, 670.  Two segments (16384 tokens, 100 heads) 2111 for 1409 without.
+// float32 gradient, 2 x 2047, 24 heads of 64: 675, 509, 535, 677.  Two segments (16384 tokens, 100 heads) 2111 for 1409 without.
 int gd_segments(int64_t batch, int64_t L, int64_t H) {
   const int64_t workgroups = batch * H, nch = (L + kQ - 1) / kQ;
   int64_t s = kSegTarget / (workgroups > 0 ? workgroups : 1);

@@ -21,14 +21,14 @@
 // states at once: the first kernel leaves E in memory for the second, where exp(G_Q) is not too small to be seen and
 // either a decay is below 1/8 or F is the caller's; else the chunk counts as slow.  Errors of dg against its own size at g = -1 to
 // -20 and at single decays of exp(-3) to exp(-30) in slow heads: below 1e-5; a decay of 0 has 0.  The two kernels of the case
-// below, whose heads range from slow to fast, took 778 us with sums over later tokens alone and take 839 (float32, 2 x 2047, 24
-// heads of 64: 190 and 225).
+// below, whose heads range from slow to fast, took 793 us with sums over later tokens alone and take 839 (float32, 2 x 2047, 24
+// heads of 64: 190 and 223).
 //
 // A workgroup walks one stretch; a wave owns 16 columns of E^T (of K), so that only the tokens' scalars are summed over
 // waves.  Rows of D, W and Y lie in LDS, W and Y as terms, split once a workgroup; their dot products y.w and y.v are
 // taken on the way in.  A chunk's rows are asked for while the one before is worked on.
 //
-// What bounds it: 8 x 2048 tokens, 32 heads of 128, bfloat16: 492 us and 348, 3.3 and 4.0 TB/s (1.6 and 1.4 GB: W and Y as float32 rows are
+// What bounds it: 8 x 2048 tokens, 32 heads of 128, bfloat16: 492 us and 347, 3.2 and 4.1 TB/s (1.6 and 1.4 GB: W and Y as float32 rows are
 // half of it) with the matrix units busy for a third of the time: its one workgroup a CU (155 and 145 KB of LDS) reads, multiplies and
 // meets at three barriers a chunk.
 //
@@ -859,8 +859,8 @@ void launch_qk_t(const GdGradArgs& a, hipStream_t s) {
 
 // Chunks between two kept states.  A workgroup of gd_qk_kernel has a CU to itself (the smallest two share one), and a stretch costs its chunks and about as
 // much as kStart more for its start (its states, its first rows): the least of that over the chip's rounds.  us, against a fixed 1024
-// stretches and against one chunk a stretch: bfloat16, heads of 128: 8 x 2048, 32 heads 1380, 1436, 2369; 2 x 2048, 32 heads 571, 692, 837; 3 x 1777, 17
-// heads 476, 650; float32, 4 x 2048, 24 heads of 128 1850, 2040, 2162; of 64 860, 1011, 1011.
+// stretches and against one chunk a stretch: bfloat16, heads of 128: 8 x 2048, 32 heads 1436, 1477, 2423; 2 x 2048, 32 heads 571, 688, 831; 3 x 1777, 17
+// heads 478, 547, 661; float32, 4 x 2048, 24 heads of 128 1950, 2151, 2238; of 64 945, 988, 964.
 int gd_every(int64_t batch, int64_t L, int64_t H, int64_t K, int64_t V, Dt dt) {
   const int64_t places = dt == Dt::F32 && K <= 64 && V <= 64 ? 512 : 256;
   constexpr double kStart = 1.5;
