@@ -587,7 +587,8 @@ ssm_status ssm_gated_delta_fwd(
  *   batch * H * ceil(L / 64) <= 2^26
  * With bfloat16 activations what dq, dv, dbeta and the states come from enters the products as three bfloat16 terms (24
  * bits), as forwards; the gradient of v under its key and what passes out of a chunk, in dk and in dg of chunks with a
- * decay below 0.42, as two (16 bits).  dg is good to about 1e-5 of its own size for any decay, fast ones too.
+ * decay below 0.42, as two (16 bits).  dg is good to about 1e-5 of the size of its head's, however fast the decays are,
+ * and at a fast decay among slow ones of its own.
  * A NaN, an infinity or such a product of keys makes gradients of its (batch row, head) NaN, of earlier tokens and of
  * other columns too.
  * Deterministic.
